@@ -17,6 +17,19 @@ from .binding import (  # noqa: F401
     muon_tall_giveups,
     muon_tall_poll_limit, muon_timing_enable, muon_timing_read, tensor_desc)
 
+# The transformer-block operators need torch at import; the optimizer's C ABI
+# does not, so they are looked up on first use.
+_BLOCK = ("norm_fwd", "norm_bwd", "residual_norm")
+
+
+def __getattr__(name: str):
+    if name in _BLOCK:
+        from . import block
+        for n in _BLOCK:
+            globals()[n] = getattr(block, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
 
 class MuonSession:
     """One muon_ctx plus the torch-allocated state buffer it lives in.

@@ -1,0 +1,238 @@
+"""PyTorch entry points of the transformer-block operators declared in
+include/muon_block.h: the fused residual norm, softmax attention and the gated
+feed-forward block.
+
+``norm_fwd`` / ``norm_bwd``, ``attn_fwd`` / ``attn_bwd`` and ``ffn_fwd`` /
+``ffn_bwd`` are one call of the library each: they check devices, types and
+shapes, take outputs and workspace from PyTorch's allocator and enqueue the
+kernels on the current stream of the tensors' device.  Nothing is copied or
+made contiguous behind the caller's back: a layout that the kernels cannot
+read raises.  Tensors made on another stream need the caller's wait (and
+``record_stream``), as with PyTorch's own operators.  All six may be captured
+into a HIP graph.
+
+``residual_norm``, ``attention`` and ``gated_ffn`` wrap them for autograd.  To
+capture a training step into a graph, call the forward and backward functions
+themselves: an autograd graph that shares leaves with a captured backward pass
+must not be alive during the capture.
+"""
+
+from __future__ import annotations
+
+import ctypes
+import struct
+
+import torch
+
+from .binding import MUON_OK, MuonError, lib
+
+NORM_KINDS = {"none": 0, "rms": 1, "layer": 2}
+ACTS = {"silu": 0, "gelu": 1}
+BLOCK_EXPORTED = ("muon_block_last_error", "muon_norm_fwd", "muon_norm_bwd_workspace", "muon_norm_bwd")
+
+_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+# The argument structures of muon_block.h, packed field by field (a few
+# microseconds where a ctypes.Structure of some 120 fields takes ten times that).
+_MAT, _HEADS = "Pqqqii", "Pqqq"
+NORM_ARGS = struct.Struct("@qqqiiff" + 9 * _MAT + "P" + 9 * _MAT)
+ATTN_ARGS = struct.Struct("@qqqiiiiqfiPP" + 4 * _HEADS + "P" + 4 * _HEADS)
+FFN_ARGS = struct.Struct("@qqqii" + 11 * _MAT)
+_NO_MAT, _NO_HEADS = (0,) * 6, (0,) * 4
+
+_READY = None
+
+
+def _lib():
+    global _READY
+    if _READY is None:
+        L = lib()
+        L.muon_block_last_error.restype = ctypes.c_char_p
+        void, size = ctypes.c_void_p, ctypes.c_size_t
+        for name in BLOCK_EXPORTED[1:]:
+            f = getattr(L, name)
+            f.restype = ctypes.c_int
+            if name.endswith("_workspace"):
+                f.argtypes = [ctypes.c_char_p, ctypes.POINTER(size)]
+            elif name == "muon_norm_fwd":
+                f.argtypes = [ctypes.c_char_p, void]
+            else:
+                f.argtypes = [ctypes.c_char_p, void, size, void]
+        _READY = L
+    return _READY
+
+
+def _check(status: int) -> None:
+    if status != MUON_OK:
+        raise MuonError(status, _lib().muon_block_last_error().decode())
+
+
+def _call(name: str, args: bytes, device, workspace: bool = True) -> None:
+    L = _lib()
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _call(name, args, device, workspace)
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if not workspace:
+        _check(getattr(L, name)(args, stream))
+        return
+    need = ctypes.c_size_t(0)
+    _check(getattr(L, name + "_workspace")(args, need))
+    ws = torch.empty(need.value, dtype=torch.uint8, device=device) if need.value else None
+    _check(getattr(L, name)(args, ws.data_ptr() if need.value else None, need.value, stream))
+
+
+def _device(first, *others):
+    """The device that all the tensors are on; they may be None."""
+    d = first.device
+    if d.type != "cuda":
+        raise ValueError("tensors must be on a GPU")
+    for t in others:
+        if t is not None and t.device != d:
+            raise ValueError(f"tensors on {d} and {t.device}")
+    return d
+
+
+def _mat(t, rows: int, cols: int):
+    """Descriptor of a tensor as rows x cols: its last dimension contiguous,
+    the others one run of evenly spaced rows."""
+    if t is None:
+        return _NO_MAT
+    dt = _TYPES.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    if t.is_contiguous():
+        if t.numel() != rows * cols or t.shape[-1] != cols:
+            raise ValueError(f"shape {tuple(t.shape)} where {rows} x {cols} is wanted")
+        return t.data_ptr(), rows, cols, cols, dt, 0
+    shape, stride = t.shape, t.stride()
+    if t.numel() != rows * cols or shape[-1] != cols:
+        raise ValueError(f"shape {tuple(shape)} where {rows} x {cols} is wanted")
+    if cols > 1 and stride[-1] != 1:
+        raise ValueError("the last dimension must be contiguous")
+    ld, span = None, 0
+    for n, s in zip(reversed(shape[:-1]), reversed(stride[:-1])):
+        if n == 1:
+            continue
+        if ld is None:
+            ld, span = s, s * n
+        elif s != span:
+            raise ValueError(f"rows are not evenly spaced: shape {tuple(shape)}, strides {tuple(stride)}")
+        else:
+            span = s * n
+    if ld is None:
+        ld = cols
+    if ld < cols:
+        raise ValueError("rows overlap")
+    return t.data_ptr(), rows, cols, ld, dt, 0
+
+
+# ------------------------------------------------------------ residual norm
+def _norm_shape(x):
+    """(rows, cols, rows of one sample) of (samples, rows, cols) or (rows, cols)."""
+    if x.dim() not in (2, 3):
+        raise ValueError(f"(rows, cols) or (samples, rows, cols) is wanted: got {tuple(x.shape)}")
+    rows = x.shape[:-1].numel()
+    return rows, x.shape[-1], x.shape[-2]
+
+
+def _norm_kinds(post: str, pre: str):
+    if post not in NORM_KINDS or pre not in NORM_KINDS:
+        raise ValueError(f"norm kinds are {sorted(NORM_KINDS)}: got {post!r}, {pre!r}")
+    return NORM_KINDS[post], NORM_KINDS[pre]
+
+
+def norm_fwd(resid, h=None, gate=None, post_weight=None, pre_weight=None, scale=None, shift=None, *,
+             post: str = "none", pre: str = "layer", alpha: float = 1.0, eps: float = 1e-6):
+    """resid_out = resid + alpha gate N_post(h) post_weight;
+    y = N_pre(resid_out) pre_weight (1 + scale) + shift.
+
+    resid, h: (samples, rows, cols) or (rows, cols), fp32 or bf16 each; gate,
+    scale, shift: (samples, cols); weights: (cols).  post, pre: "none", "rms"
+    or "layer".  Returns (resid_out, y, stats): resid_out is resid where h is
+    None; y has h's type (resid's where h is None) and is None where pre is
+    "none" and nothing modulates it; stats (rows, 4) is what norm_bwd reads."""
+    dev = _device(resid, h, gate, post_weight, pre_weight, scale, shift)
+    rows, cols, group = _norm_shape(resid)
+    k_post, k_pre = _norm_kinds(post, pre)
+    if h is not None and h.shape != resid.shape:
+        raise ValueError(f"h {tuple(h.shape)} and resid {tuple(resid.shape)}")
+    want_y = k_pre != 0 or pre_weight is not None or scale is not None or shift is not None
+    out = resid if h is None else torch.empty(resid.shape, dtype=resid.dtype, device=dev)
+    y = torch.empty(resid.shape, dtype=(resid if h is None else h).dtype, device=dev) if want_y else None
+    stats = torch.empty((rows, 4), dtype=torch.float32, device=dev)
+    if rows == 0 or cols == 0:
+        return out, y, stats
+    groups = rows // group
+    args = NORM_ARGS.pack(
+        rows, cols, group, k_post, k_pre, alpha, eps,
+        *_mat(resid, rows, cols), *_mat(h, rows, cols), *(_mat(out, rows, cols) if h is not None else _NO_MAT),
+        *_mat(y, rows, cols), *_mat(gate, groups, cols), *_mat(scale, groups, cols), *_mat(shift, groups, cols),
+        *_mat(post_weight, 1, cols), *_mat(pre_weight, 1, cols), stats.data_ptr(), *(9 * _NO_MAT))
+    _call("muon_norm_fwd", args, dev, workspace=False)
+    return out, y, stats
+
+
+def norm_bwd(d_resid_out, d_y, resid_out, h, stats, gate=None, post_weight=None, pre_weight=None, scale=None,
+             shift=None, *, post: str = "none", pre: str = "layer", alpha: float = 1.0, eps: float = 1e-6):
+    """Gradients of norm_fwd's inputs, as a dict with the keys resid, h, gate,
+    post_weight, pre_weight, scale and shift (None for what was None).
+
+    d_resid_out, d_y: gradients of norm_fwd's first two results (either may be
+    None: zero); resid_out and stats are its results, the rest its arguments."""
+    x = resid_out
+    dev = _device(x, d_resid_out, d_y, h, stats, gate, post_weight, pre_weight, scale, shift)
+    rows, cols, group = _norm_shape(x)
+    k_post, k_pre = _norm_kinds(post, pre)
+    if stats.dtype != torch.float32 or not stats.is_contiguous() or stats.shape != (rows, 4):
+        raise ValueError("stats is norm_fwd's third result")
+    if d_y is None and (k_pre != 0 or pre_weight is not None or scale is not None or shift is not None):
+        d_y = torch.zeros(x.shape, dtype=(x if h is None else h).dtype, device=dev)
+    d_h = None if h is None else torch.empty(h.shape, dtype=h.dtype, device=dev)
+    d_resid = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    vectors = [None if t is None else torch.empty(t.shape, dtype=t.dtype, device=dev)
+               for t in (gate, scale, shift, post_weight, pre_weight)]
+    if rows == 0 or cols == 0:
+        for t in vectors:
+            if t is not None:
+                t.zero_()
+    else:
+        groups = rows // group
+        m = [_mat(t, groups if i < 3 else 1, cols) for i, t in enumerate((gate, scale, shift, post_weight, pre_weight))]
+        dm = [_mat(t, groups if i < 3 else 1, cols) for i, t in enumerate(vectors)]
+        args = NORM_ARGS.pack(
+            rows, cols, group, k_post, k_pre, alpha, eps,
+            *_NO_MAT, *_mat(h, rows, cols), *_mat(x, rows, cols), *_NO_MAT, *m[0], *m[1], *m[2], *m[3], *m[4],
+            stats.data_ptr(), *_mat(d_resid_out, rows, cols), *_mat(d_y, rows, cols), *_mat(d_resid, rows, cols),
+            *_mat(d_h, rows, cols), *dm[0], *dm[1], *dm[2], *dm[3], *dm[4])
+        _call("muon_norm_bwd", args, dev)
+    return {"resid": d_resid, "h": d_h, "gate": vectors[0], "post_weight": vectors[3], "pre_weight": vectors[4],
+            "scale": vectors[1], "shift": vectors[2]}
+
+
+class _ResidualNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, resid, h, gate, post_weight, pre_weight, scale, shift, how):
+        out, y, stats = norm_fwd(resid, h, gate, post_weight, pre_weight, scale, shift, **how)
+        if h is None:
+            out = resid.view_as(resid)
+        ctx.how = how
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(out, h, stats, gate, post_weight, pre_weight, scale, shift)
+        return out, y
+
+    @staticmethod
+    def backward(ctx, d_out, d_y):
+        out, h, stats, gate, post_weight, pre_weight, scale, shift = ctx.saved_tensors
+        if d_out is None and d_y is None:
+            return (None,) * 8
+        d_out = None if d_out is None else d_out.contiguous()
+        d_y = None if d_y is None else d_y.contiguous()
+        g = norm_bwd(d_out, d_y, out, h, stats, gate, post_weight, pre_weight, scale, shift, **ctx.how)
+        return (g["resid"], g["h"], g["gate"], g["post_weight"], g["pre_weight"], g["scale"], g["shift"], None)
+
+
+def residual_norm(resid, h=None, gate=None, post_weight=None, pre_weight=None, scale=None, shift=None, *,
+                  post: str = "none", pre: str = "layer", alpha: float = 1.0, eps: float = 1e-6):
+    """norm_fwd for autograd; returns (resid_out, y)."""
+    return _ResidualNorm.apply(resid, h, gate, post_weight, pre_weight, scale, shift,
+                               {"post": post, "pre": pre, "alpha": alpha, "eps": eps})

@@ -1,0 +1,215 @@
+// Host side of the transformer-block operators (muon_block.h): argument
+// checks, workspace sizes and the launch of each call.  No device memory is
+// allocated and nothing is synchronised.  No function here throws: the only
+// state is a fixed buffer of error text per thread.
+#include "../../include/muon_block.h"
+#include "block_internal.h"
+
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+
+using namespace muon;
+
+namespace {
+
+thread_local char g_text[256] = "";
+
+muon_status fail(muon_status st, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_text, sizeof g_text, fmt, ap);
+  va_end(ap);
+  return st;
+}
+
+#define CHECK(x)                              \
+  do {                                        \
+    const muon_status st_ = (x);              \
+    if (st_ != MUON_OK) return st_;           \
+  } while (0)
+
+constexpr int64_t kMaxRows = int64_t(1) << 40;
+// Row strides stay below 2^22 values so that the rows of one tile can be
+// addressed with 32-bit byte offsets.
+constexpr int64_t kMaxLd = int64_t(1) << 22;
+
+size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
+
+size_t type_size(int32_t dt) { return dt == MUON_F32 ? 4 : 2; }
+
+bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+// A present matrix: shape, type (dt < 0: F32 or BF16), stride, alignment.
+muon_status check_mat(const char* name, const muon_tensor& t, int64_t rows, int64_t cols, int32_t dt) {
+  if (!t.ptr) return fail(MUON_E_ARG, "%s is missing", name);
+  if (t.rows != rows || t.cols != cols || t.reserved != 0)
+    return fail(MUON_E_SHAPE, "%s: %lld x %lld where %lld x %lld is wanted", name, (long long)t.rows,
+                (long long)t.cols, (long long)rows, (long long)cols);
+  if ((t.dtype != MUON_F32 && t.dtype != MUON_BF16) || (dt >= 0 && t.dtype != dt))
+    return fail(MUON_E_DTYPE, "%s: dtype %d", name, t.dtype);
+  if (t.ld < cols || t.ld > kMaxLd)
+    return fail(MUON_E_ALIGN, "%s: ld %lld for %lld columns", name, (long long)t.ld, (long long)cols);
+  if (!aligned(t.ptr, type_size(t.dtype))) return fail(MUON_E_ALIGN, "%s: pointer not aligned to its type", name);
+  return MUON_OK;
+}
+
+muon_status check_opt(const char* name, const muon_tensor& t, int64_t rows, int64_t cols, int32_t dt) {
+  return t.ptr ? check_mat(name, t, rows, cols, dt) : MUON_OK;
+}
+
+muon_status check_workspace(void* ws, size_t have, size_t need) {
+  if (need == 0) return MUON_OK;
+  if (!ws || have < need) return fail(MUON_E_WORKSPACE, "workspace of %zu bytes where %zu are needed", ws ? have : 0, need);
+  if (!aligned(ws, 256)) return fail(MUON_E_ALIGN, "workspace not 256-byte aligned");
+  return MUON_OK;
+}
+
+muon_status launched(const char* what, hipError_t e) {
+  if (e == hipSuccess) return MUON_OK;
+  return fail(MUON_E_HIP, "%s: %s", what, hipGetErrorString(e));
+}
+
+// ---- residual norm ----------------------------------------------------------
+muon_status norm_dims(const muon_norm_args* a) {
+  if (!a) return fail(MUON_E_ARG, "args is NULL");
+  if (a->rows < 0 || a->rows > kMaxRows || a->cols < 1 || a->cols > kNormMaxCols)
+    return fail(MUON_E_SHAPE, "rows %lld, cols %lld (1 .. %d)", (long long)a->rows, (long long)a->cols, kNormMaxCols);
+  if (a->group_rows < 1 || a->rows % a->group_rows)
+    return fail(MUON_E_SHAPE, "group_rows %lld does not divide rows %lld", (long long)a->group_rows, (long long)a->rows);
+  if (a->post_kind < 0 || a->post_kind > 2 || a->pre_kind < 0 || a->pre_kind > 2)
+    return fail(MUON_E_ARG, "unknown norm kind");
+  if (!std::isfinite(a->alpha) || !(a->eps >= 0.f) || !std::isfinite(a->eps))
+    return fail(MUON_E_ARG, "alpha and eps must be finite, eps >= 0");
+  // one workgroup per 64 columns and group in the sums' launch, per row in the forward's
+  if (a->rows / a->group_rows * ((a->cols + 63) / 64) > 0x7fffffff || a->rows > 0x7fffffff)
+    return fail(MUON_E_SHAPE, "too many rows for one call");
+  return MUON_OK;
+}
+
+muon_status norm_vectors(const muon_norm_args* a) {
+  const int64_t g = a->rows / a->group_rows;
+  CHECK(check_opt("gate", a->gate, g, a->cols, -1));
+  CHECK(check_opt("scale", a->scale, g, a->cols, -1));
+  CHECK(check_opt("shift", a->shift, g, a->cols, -1));
+  CHECK(check_opt("post_weight", a->post_weight, 1, a->cols, -1));
+  CHECK(check_opt("pre_weight", a->pre_weight, 1, a->cols, -1));
+  if (!a->h.ptr && (a->gate.ptr || a->post_weight.ptr || a->post_kind != MUON_NORM_NONE))
+    return fail(MUON_E_ARG, "gate, post_weight and a post norm need h");
+  if (a->rows > 0 && (!a->stats || !aligned(a->stats, 16))) return fail(a->stats ? MUON_E_ALIGN : MUON_E_ARG, "stats is missing or not 16-byte aligned");
+  return MUON_OK;
+}
+
+NormMat norm_mat(const muon_tensor& t) { return NormMat{t.ptr, t.ld, t.dtype, 0}; }
+
+// Whether eight columns can move at once: whole groups of eight, 16-byte
+// aligned rows of every matrix and vector that the kernels read that way.
+bool norm_vec(const muon_norm_args* a) {
+  if (a->cols % 8) return false;
+  const muon_tensor* all[] = {&a->resid, &a->h, &a->resid_out, &a->y, &a->gate, &a->scale, &a->shift, &a->post_weight,
+                              &a->pre_weight, &a->d_resid_out, &a->d_y, &a->d_resid, &a->d_h};
+  for (const muon_tensor* t : all)
+    if (t->ptr && (t->ld % 8 || !aligned(t->ptr, 16))) return false;
+  return true;
+}
+
+NormDev norm_dev(const muon_norm_args* a) {
+  NormDev d{};
+  d.rows = a->rows; d.group_rows = a->group_rows; d.cols = int32_t(a->cols);
+  d.post_kind = a->post_kind; d.pre_kind = a->pre_kind; d.alpha = a->alpha; d.eps = a->eps;
+  d.resid = norm_mat(a->resid); d.h = norm_mat(a->h); d.resid_out = norm_mat(a->resid_out); d.y = norm_mat(a->y);
+  d.gate = norm_mat(a->gate); d.scale = norm_mat(a->scale); d.shift = norm_mat(a->shift);
+  d.post_weight = norm_mat(a->post_weight); d.pre_weight = norm_mat(a->pre_weight);
+  d.stats = a->stats;
+  d.d_resid_out = norm_mat(a->d_resid_out); d.d_y = norm_mat(a->d_y);
+  d.d_resid = norm_mat(a->d_resid); d.d_h = norm_mat(a->d_h);
+  d.d_gate = norm_mat(a->d_gate); d.d_scale = norm_mat(a->d_scale); d.d_shift = norm_mat(a->d_shift);
+  d.d_post_weight = norm_mat(a->d_post_weight); d.d_pre_weight = norm_mat(a->d_pre_weight);
+  d.splits = 1;
+  return d;
+}
+
+bool norm_sums(const muon_norm_args* a) {
+  return a->d_gate.ptr || a->d_scale.ptr || a->d_shift.ptr || a->d_post_weight.ptr || a->d_pre_weight.ptr;
+}
+
+size_t norm_bwd_bytes(const muon_norm_args* a) {
+  if (!norm_sums(a) || a->rows == 0) return 0;
+  const int64_t g = a->rows / a->group_rows;
+  const size_t part = align_up(size_t(g) * norm_splits(g, a->group_rows) * kNormSums * size_t(a->cols) * 4);
+  const bool weights = g > 1 && (a->d_post_weight.ptr || a->d_pre_weight.ptr);
+  return part + (weights ? align_up(size_t(g) * 2 * size_t(a->cols) * 4) : 0);
+}
+
+}  // namespace
+
+extern "C" {
+
+const char* muon_block_last_error(void) { return g_text; }
+
+muon_status muon_norm_fwd(const muon_norm_args* a, void* hip_stream) {
+  CHECK(norm_dims(a));
+  CHECK(norm_vectors(a));
+  if (a->rows == 0) return MUON_OK;
+  const int64_t n = a->rows, d = a->cols;
+  CHECK(check_mat("resid", a->resid, n, d, -1));
+  if (a->h.ptr) {
+    CHECK(check_mat("h", a->h, n, d, -1));
+    CHECK(check_mat("resid_out", a->resid_out, n, d, a->resid.dtype));
+  }
+  if (a->pre_kind != MUON_NORM_NONE || a->y.ptr) CHECK(check_mat("y", a->y, n, d, a->h.ptr ? a->h.dtype : -1));
+  if (!a->y.ptr && (a->scale.ptr || a->shift.ptr || a->pre_weight.ptr)) return fail(MUON_E_ARG, "scale, shift and pre_weight need y");
+  NormDev dev = norm_dev(a);
+  if (!a->h.ptr) dev.resid_out = dev.resid;
+  return launched("muon_norm_fwd", launch_norm_fwd(static_cast<hipStream_t>(hip_stream), dev, norm_vec(a)));
+}
+
+muon_status muon_norm_bwd_workspace(const muon_norm_args* a, size_t* bytes) {
+  if (!bytes) return fail(MUON_E_ARG, "bytes is NULL");
+  CHECK(norm_dims(a));
+  *bytes = norm_bwd_bytes(a);
+  return MUON_OK;
+}
+
+muon_status muon_norm_bwd(const muon_norm_args* a, void* ws, size_t ws_bytes, void* hip_stream) {
+  CHECK(norm_dims(a));
+  CHECK(norm_vectors(a));
+  const int64_t n = a->rows, d = a->cols, g = n / a->group_rows;
+  const bool sums = norm_sums(a);
+  CHECK(check_opt("d_gate", a->d_gate, g, d, a->gate.ptr ? a->gate.dtype : -1));
+  CHECK(check_opt("d_scale", a->d_scale, g, d, a->scale.ptr ? a->scale.dtype : -1));
+  CHECK(check_opt("d_shift", a->d_shift, g, d, a->shift.ptr ? a->shift.dtype : -1));
+  CHECK(check_opt("d_post_weight", a->d_post_weight, 1, d, a->post_weight.ptr ? a->post_weight.dtype : -1));
+  CHECK(check_opt("d_pre_weight", a->d_pre_weight, 1, d, a->pre_weight.ptr ? a->pre_weight.dtype : -1));
+  if ((a->d_gate.ptr || a->d_post_weight.ptr) && !a->h.ptr) return fail(MUON_E_ARG, "d_gate and d_post_weight need h");
+  if (n == 0 && sums) return fail(MUON_E_SHAPE, "no rows: the vectors' gradients have none to be summed over");
+  if (n == 0) return MUON_OK;
+  CHECK(check_mat("d_resid", a->d_resid, n, d, -1));
+  const int32_t rt = a->d_resid.dtype;
+  CHECK(check_opt("d_resid_out", a->d_resid_out, n, d, rt));
+  if (a->h.ptr) {
+    CHECK(check_mat("h", a->h, n, d, -1));
+    CHECK(check_mat("d_h", a->d_h, n, d, a->h.dtype));
+  }
+  if (a->d_y.ptr) {
+    CHECK(check_mat("d_y", a->d_y, n, d, a->h.ptr ? a->h.dtype : -1));
+    CHECK(check_mat("resid_out", a->resid_out, n, d, rt));
+  } else if (a->pre_kind != MUON_NORM_NONE || a->d_scale.ptr || a->d_shift.ptr || a->d_pre_weight.ptr) {
+    return fail(MUON_E_ARG, "d_y is missing");
+  }
+  const size_t need = norm_bwd_bytes(a);
+  CHECK(check_workspace(ws, ws_bytes, need));
+  NormDev dev = norm_dev(a);
+  dev.resid_out.dt = rt;
+  dev.splits = norm_splits(g, a->group_rows);
+  dev.split_rows = int32_t((a->group_rows + dev.splits - 1) / dev.splits);
+  if (sums) {
+    dev.part = static_cast<float*>(ws);
+    if (g > 1 && (a->d_post_weight.ptr || a->d_pre_weight.ptr))
+      dev.gsum = reinterpret_cast<float*>(static_cast<char*>(ws) +
+                                          align_up(size_t(g) * dev.splits * kNormSums * size_t(d) * 4));
+  }
+  return launched("muon_norm_bwd", launch_norm_bwd(static_cast<hipStream_t>(hip_stream), dev, norm_vec(a), sums));
+}
+
+}  // extern "C"

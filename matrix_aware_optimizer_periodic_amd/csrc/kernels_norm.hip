@@ -1,0 +1,396 @@
+// Fused residual norm: the end of one transformer sub-block and the start of
+// the next, forward and backward.
+//
+//   p = N_post(h) w_post;  r' = r + alpha gate_b p;
+//   y = N_pre(r') w_pre (1 + scale_b) + shift_b          (b: the row's sample)
+//
+// Bound by memory: forward reads r and h and writes r' and y once, backward
+// reads r', h, dr' and dy and writes dr and dh once.  One row is held in the
+// registers of one wave (up to 512 columns) or of one workgroup, eight
+// columns per thread, so that the two norms' statistics (mean first, then the
+// centred squares, both fp32) cost no second pass over memory.
+//
+// Backward, with xhat and hhat the normalised rows and g = dy w_pre (1 + scale_b):
+//
+//   dr = dr' + rstd_r (g - [mean g] - xhat mean(g xhat))
+//   dh = rstd_h (u - [mean u] - hhat mean(u hhat)),  u = alpha gate_b w_post dr
+//
+// (bracketed terms for LayerNorm only), and three column sums per sample,
+//   S1 = sum dy xhat,  S2 = sum dr hhat,  S3 = sum dy,
+// give all five vector gradients, because what multiplies them does not
+// change along the rows of one sample:
+//   dscale = w_pre S1, dshift = S3, dgate = alpha w_post S2,
+//   dw_pre = sum_b (1 + scale_b) S1, dw_post = sum_b alpha gate_b S2.
+// A workgroup keeps the three sums of its share of one sample's rows in
+// registers and writes them once; a second kernel adds the shares in order
+// (no atomics).
+#include "block_device.h"
+
+namespace muon {
+namespace {
+
+constexpr int kMaxWaves = 16;
+
+// Sums of N values over the row's threads.  One wave per row: shuffles only.
+// Otherwise one LDS exchange; `buf` alternates between two halves so that a
+// row needs one barrier per sum.
+template <int N, bool WAVE>
+__device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[2][kMaxWaves], int& phase, int nwaves) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = wave_sum(v[k]);
+  if constexpr (!WAVE) {
+    const int w = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) red[phase][k][w] = v[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      float s = 0.f;
+      for (int i = 0; i < nwaves; ++i) s += red[phase][k][i];
+      v[k] = s;
+    }
+    phase ^= 1;
+  }
+}
+
+// Columns of chunk c of this thread: VEC from col(c), none past the row.
+// tid counts the threads of a row.
+template <int VEC>
+__device__ __forceinline__ int col_of(int c, int tid, int nthreads) { return (c * nthreads + tid) * VEC; }
+
+// Mean and 1 / deviation of a row held in v (zeros past its end).
+template <int VEC, int NC, bool WAVE>
+__device__ __forceinline__ void row_stats(const float (&v)[NC][VEC], int kind, int cols, float inv, float eps,
+                                          int tid, int nt, float (*red)[2][kMaxWaves], int& phase, float& mean,
+                                          float& rstd) {
+  mean = 0.f;
+  rstd = 1.f;
+  if (kind == 0) return;
+  if (kind == 2) {
+    float s[1] = {0.f};
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) s[0] += v[c][k];
+    row_sum<1, WAVE>(s, red, phase, nt >> 6);
+    mean = s[0] * inv;
+  }
+  float q[1] = {0.f};
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    if (col_of<VEC>(c, tid, nt) < cols) {
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) { const float d = v[c][k] - mean; q[0] = fmaf(d, d, q[0]); }
+    }
+  }
+  row_sum<1, WAVE>(q, red, phase, nt >> 6);
+  rstd = 1.0f / sqrtf(fmaf(q[0], inv, eps));
+}
+
+// One row per wave (WAVE: four rows per workgroup) or per workgroup.
+template <typename TR, typename TH, int VEC, int NC, bool WAVE>
+__global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_fwd_kernel(NormDev a) {
+  __shared__ float red[2][2][kMaxWaves];
+  const int tid = WAVE ? threadIdx.x & 63 : threadIdx.x;
+  const int nt = WAVE ? 64 : blockDim.x;
+  const int64_t row = WAVE ? int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  if (row >= a.rows) return;          // WAVE: whole waves, no barrier follows
+  int phase = 0;
+  const int64_t grp = row / a.group_rows;
+  const float inv = 1.0f / float(a.cols);
+  float r[NC][VEC], h[NC][VEC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int col = col_of<VEC>(c, tid, nt);
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) { r[c][k] = 0.f; h[c][k] = 0.f; }
+    if (col < a.cols) {
+      load_vals<TR, VEC>(a.resid.p, row * a.resid.ld + col, r[c]);
+      if (a.h.p) load_vals<TH, VEC>(a.h.p, row * a.h.ld + col, h[c]);
+    }
+  }
+  float mh = 0.f, rh = 1.f, mr, rr;
+  if (a.h.p) {
+    row_stats<VEC, NC, WAVE>(h, a.post_kind, a.cols, inv, a.eps, tid, nt, red, phase, mh, rh);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int col = col_of<VEC>(c, tid, nt);
+      if (col >= a.cols) continue;
+      float w[VEC], g[VEC];
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) { w[k] = 1.f; g[k] = 1.f; }
+      if (a.post_weight.p) load_any<VEC>(a.post_weight.p, a.post_weight.dt, col, w);
+      if (a.gate.p) load_any<VEC>(a.gate.p, a.gate.dt, grp * a.gate.ld + col, g);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) r[c][k] = fmaf(a.alpha * g[k], (h[c][k] - mh) * rh * w[k], r[c][k]);
+      store_vals<TR, VEC>(a.resid_out.p, row * a.resid_out.ld + col, r[c]);
+    }
+  }
+  row_stats<VEC, NC, WAVE>(r, a.pre_kind, a.cols, inv, a.eps, tid, nt, red, phase, mr, rr);
+  if (a.y.p) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int col = col_of<VEC>(c, tid, nt);
+      if (col >= a.cols) continue;
+      float w[VEC], sc[VEC], sh[VEC];
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) { w[k] = 1.f; sc[k] = 0.f; sh[k] = 0.f; }
+      if (a.pre_weight.p) load_any<VEC>(a.pre_weight.p, a.pre_weight.dt, col, w);
+      if (a.scale.p) load_any<VEC>(a.scale.p, a.scale.dt, grp * a.scale.ld + col, sc);
+      if (a.shift.p) load_any<VEC>(a.shift.p, a.shift.dt, grp * a.shift.ld + col, sh);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) w[k] = fmaf((r[c][k] - mr) * rr * w[k], 1.f + sc[k], sh[k]);
+      store_vals<TH, VEC>(a.y.p, row * a.y.ld + col, w);
+    }
+  }
+  if (tid == 0 && a.stats) {
+    *as_global(reinterpret_cast<f32x2_t*>(a.stats + row * 4)) = f32x2_t{mh, rh};
+    *as_global(reinterpret_cast<f32x2_t*>(a.stats + row * 4 + 2)) = f32x2_t{mr, rr};
+  }
+}
+
+// One share of one sample's rows per wave (WAVE: four shares per workgroup)
+// or per workgroup; share = group * splits + split.
+template <typename TR, typename TH, int VEC, int NC, bool WAVE>
+__global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_bwd_kernel(NormDev a, int64_t shares) {
+  __shared__ float red[2][2][kMaxWaves];
+  const int tid = WAVE ? threadIdx.x & 63 : threadIdx.x;
+  const int nt = WAVE ? 64 : blockDim.x;
+  const int64_t share = WAVE ? int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  if (share >= shares) return;
+  int phase = 0;
+  const int64_t grp = share / a.splits;
+  const int64_t first = grp * a.group_rows + (share - grp * a.splits) * int64_t(a.split_rows);
+  const int64_t end = min(first + a.split_rows, (grp + 1) * a.group_rows);
+  const float inv = 1.0f / float(a.cols);
+  const bool have_h = a.h.p != nullptr;
+  const float kpre = a.pre_kind == 2 ? inv : 0.f, kpost = a.post_kind == 2 ? inv : 0.f;
+  const float npre = a.pre_kind ? inv : 0.f, npost = a.post_kind ? inv : 0.f;
+  // what multiplies dy and dr in this share's columns, and its sums
+  float wy[NC][VEC], wr[NC][VEC], s1[NC][VEC], s2[NC][VEC], s3[NC][VEC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int col = col_of<VEC>(c, tid, nt);
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) { wy[c][k] = 1.f; wr[c][k] = a.alpha; s1[c][k] = s2[c][k] = s3[c][k] = 0.f; }
+    if (col >= a.cols) continue;
+    float t[VEC];
+    if (a.pre_weight.p) load_any<VEC>(a.pre_weight.p, a.pre_weight.dt, col, wy[c]);
+    if (a.scale.p) {
+      load_any<VEC>(a.scale.p, a.scale.dt, grp * a.scale.ld + col, t);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) wy[c][k] *= 1.f + t[k];
+    }
+    if (a.post_weight.p) {
+      load_any<VEC>(a.post_weight.p, a.post_weight.dt, col, t);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) wr[c][k] *= t[k];
+    }
+    if (a.gate.p) {
+      load_any<VEC>(a.gate.p, a.gate.dt, grp * a.gate.ld + col, t);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) wr[c][k] *= t[k];
+    }
+  }
+  for (int64_t row = first; row < end; ++row) {
+    const f32x4_t st = *as_global(reinterpret_cast<const f32x4_t*>(a.stats + row * 4));
+    float x[NC][VEC], dy[NC][VEC], dr[NC][VEC], h[NC][VEC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int col = col_of<VEC>(c, tid, nt);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) x[c][k] = dy[c][k] = dr[c][k] = h[c][k] = 0.f;
+      if (col < a.cols) {
+        if (a.d_y.p) {
+          load_vals<TR, VEC>(a.resid_out.p, row * a.resid_out.ld + col, x[c]);
+          load_vals<TH, VEC>(a.d_y.p, row * a.d_y.ld + col, dy[c]);
+        }
+        if (a.d_resid_out.p) load_vals<TR, VEC>(a.d_resid_out.p, row * a.d_resid_out.ld + col, dr[c]);
+        if (have_h) load_vals<TH, VEC>(a.h.p, row * a.h.ld + col, h[c]);
+      }
+    }
+    if (a.d_y.p) {
+      float t[2] = {0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        if (col_of<VEC>(c, tid, nt) >= a.cols) continue;
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+          x[c][k] = (x[c][k] - st[2]) * st[3];
+          s3[c][k] += dy[c][k];
+          s1[c][k] = fmaf(dy[c][k], x[c][k], s1[c][k]);
+          dy[c][k] *= wy[c][k];
+          t[0] += dy[c][k];
+          t[1] = fmaf(dy[c][k], x[c][k], t[1]);
+        }
+      }
+      row_sum<2, WAVE>(t, red, phase, nt >> 6);
+      t[0] *= kpre;
+      t[1] *= npre;
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) dr[c][k] = fmaf(st[3], dy[c][k] - t[0] - x[c][k] * t[1], dr[c][k]);
+    }
+    float t[2] = {0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int col = col_of<VEC>(c, tid, nt);
+      if (col >= a.cols) continue;
+      store_vals<TR, VEC>(a.d_resid.p, row * a.d_resid.ld + col, dr[c]);
+      if (have_h) {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+          h[c][k] = (h[c][k] - st[0]) * st[1];
+          s2[c][k] = fmaf(dr[c][k], h[c][k], s2[c][k]);
+          dr[c][k] *= wr[c][k];
+          t[0] += dr[c][k];
+          t[1] = fmaf(dr[c][k], h[c][k], t[1]);
+        }
+      }
+    }
+    if (!have_h) continue;
+    if (a.post_kind) row_sum<2, WAVE>(t, red, phase, nt >> 6);
+    t[0] *= kpost;
+    t[1] *= npost;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int col = col_of<VEC>(c, tid, nt);
+      if (col >= a.cols) continue;
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) dr[c][k] = st[1] * (dr[c][k] - t[0] - h[c][k] * t[1]);
+      store_vals<TH, VEC>(a.d_h.p, row * a.d_h.ld + col, dr[c]);
+    }
+  }
+  if (!a.part) return;
+  float* o = a.part + share * int64_t(kNormSums) * a.cols;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int col = col_of<VEC>(c, tid, nt);
+    if (col >= a.cols) continue;
+    store_vals<float, VEC>(o, col, s1[c]);
+    store_vals<float, VEC>(o, int64_t(a.cols) + col, s2[c]);
+    store_vals<float, VEC>(o, 2 * int64_t(a.cols) + col, s3[c]);
+  }
+}
+
+// Sums over `n` rows, `stride` floats apart, of 64 columns per workgroup:
+// 16 threads per column take every 16th row, then their sums are added in
+// order.  The result is in the threads of the first wave.
+template <int N>
+__device__ __forceinline__ void col_sums(const float* p, int64_t n, int64_t stride, int64_t next, int col, int cols,
+                                         float (&v)[N], float (*red)[16][64]) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = 0.f;
+  if (col < cols) {
+    for (int64_t i = w; i < n; i += 16)
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[k] += *as_global(p + i * stride + k * next + col);
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k) red[k][w][lane] = v[k];
+  __syncthreads();
+  if (w == 0) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      v[k] = 0.f;
+      for (int i = 0; i < 16; ++i) v[k] += red[k][i][lane];
+    }
+  }
+}
+
+__global__ __launch_bounds__(1024) void norm_sums_kernel(NormDev a, int64_t groups) {
+  __shared__ float red[kNormSums][16][64];
+  const int tiles = (a.cols + 63) / 64;
+  const int64_t grp = blockIdx.x / unsigned(tiles);
+  const int col = int(blockIdx.x % unsigned(tiles)) * 64 + (threadIdx.x & 63);
+  float s[kNormSums];
+  col_sums<kNormSums>(a.part + grp * a.splits * kNormSums * int64_t(a.cols), a.splits, kNormSums * int64_t(a.cols),
+                      a.cols, col, a.cols, s, red);
+  if (threadIdx.x >= 64 || col >= a.cols) return;
+  const float wp = a.pre_weight.p ? load_any1(a.pre_weight.p, a.pre_weight.dt, col) : 1.f;
+  const float wo = a.post_weight.p ? load_any1(a.post_weight.p, a.post_weight.dt, col) : 1.f;
+  if (a.d_scale.p) store_any1(a.d_scale.p, a.d_scale.dt, grp * a.d_scale.ld + col, wp * s[0]);
+  if (a.d_gate.p) store_any1(a.d_gate.p, a.d_gate.dt, grp * a.d_gate.ld + col, a.alpha * wo * s[1]);
+  if (a.d_shift.p) store_any1(a.d_shift.p, a.d_shift.dt, grp * a.d_shift.ld + col, s[2]);
+  const float sc = a.scale.p ? load_any1(a.scale.p, a.scale.dt, grp * a.scale.ld + col) : 0.f;
+  const float g = a.gate.p ? load_any1(a.gate.p, a.gate.dt, grp * a.gate.ld + col) : 1.f;
+  const float dp = (1.f + sc) * s[0], dq = a.alpha * g * s[1];
+  if (groups == 1) {
+    if (a.d_pre_weight.p) store_any1(a.d_pre_weight.p, a.d_pre_weight.dt, col, dp);
+    if (a.d_post_weight.p) store_any1(a.d_post_weight.p, a.d_post_weight.dt, col, dq);
+  } else if (a.gsum) {
+    *as_global(a.gsum + grp * 2 * a.cols + col) = dp;
+    *as_global(a.gsum + (grp * 2 + 1) * a.cols + col) = dq;
+  }
+}
+
+__global__ __launch_bounds__(1024) void norm_weights_kernel(NormDev a, int64_t groups) {
+  __shared__ float red[2][16][64];
+  const int col = int(blockIdx.x) * 64 + (threadIdx.x & 63);
+  float s[2];
+  col_sums<2>(a.gsum, groups, 2 * int64_t(a.cols), a.cols, col, a.cols, s, red);
+  if (threadIdx.x >= 64 || col >= a.cols) return;
+  if (a.d_pre_weight.p) store_any1(a.d_pre_weight.p, a.d_pre_weight.dt, col, s[0]);
+  if (a.d_post_weight.p) store_any1(a.d_post_weight.p, a.d_post_weight.dt, col, s[1]);
+}
+
+// Threads per row and chunks per thread: eight columns per thread while a
+// row fits 1024 threads, single columns where a row is not whole aligned
+// groups of eight.
+struct Shape { int threads; int nc; bool wave; };
+Shape shape_of(int cols, bool vec) {
+  const int per = (cols + (vec ? 8 : 1) - 1) / (vec ? 8 : 1);   // thread columns of a row
+  const int nc = vec ? (per <= 1024 ? 1 : 2) : (per <= 4096 ? 4 : 16);
+  const int threads = ((per + nc - 1) / nc + 63) / 64 * 64;
+  return {threads, nc, threads == 64 && nc == (vec ? 1 : 4)};
+}
+
+#define NORM_KERNEL(K, TR, TH)                                                                       \
+  (vec ? (sh.wave ? K<TR, TH, 8, 1, true> : sh.nc == 1 ? K<TR, TH, 8, 1, false> : K<TR, TH, 8, 2, false>) \
+       : (sh.wave ? K<TR, TH, 1, 4, true> : sh.nc == 4 ? K<TR, TH, 1, 4, false> : K<TR, TH, 1, 16, false>))
+#define NORM_PICK(K)                                                                   \
+  (a.resid_out.dt ? (hdt ? NORM_KERNEL(K, uint16_t, uint16_t) : NORM_KERNEL(K, uint16_t, float)) \
+                  : (hdt ? NORM_KERNEL(K, float, uint16_t) : NORM_KERNEL(K, float, float)))
+
+}  // namespace
+
+int norm_splits(int64_t groups, int64_t group_rows) {
+  // About 512 shares in all (two workgroups on each of 256 CUs), of at least
+  // eight rows: a share costs one write and one read of its column sums.
+  const int64_t want = (512 + groups - 1) / groups;
+  const int64_t most = (group_rows + 7) / 8;
+  const int64_t n = want < most ? want : most;
+  return int(n < 1 ? 1 : n);
+}
+
+hipError_t launch_norm_fwd(hipStream_t s, const NormDev& a, bool vec) {
+  const Shape sh = shape_of(a.cols, vec);
+  const int hdt = a.h.p ? a.h.dt : a.y.dt;
+  auto* k = NORM_PICK(norm_fwd_kernel);
+  const int64_t grid = sh.wave ? (a.rows + 3) / 4 : a.rows;
+  hipLaunchKernelGGL(k, dim3(unsigned(grid)), dim3(sh.wave ? 256 : sh.threads), 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_norm_bwd(hipStream_t s, const NormDev& a, bool vec, bool sums) {
+  const Shape sh = shape_of(a.cols, vec);
+  const int hdt = a.h.p ? a.h.dt : a.d_y.dt;
+  const int64_t groups = a.rows / a.group_rows, shares = groups * a.splits;
+  auto* k = NORM_PICK(norm_bwd_kernel);
+  const int64_t grid = sh.wave ? (shares + 3) / 4 : shares;
+  hipLaunchKernelGGL(k, dim3(unsigned(grid)), dim3(sh.wave ? 256 : sh.threads), 0, s, a, shares);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !sums) return e;
+  const unsigned tiles = unsigned((a.cols + 63) / 64);
+  hipLaunchKernelGGL(norm_sums_kernel, dim3(unsigned(tiles * groups)), dim3(1024), 0, s, a, groups);
+  e = hipGetLastError();
+  if (e != hipSuccess || groups == 1 || !(a.d_pre_weight.p || a.d_post_weight.p)) return e;
+  hipLaunchKernelGGL(norm_weights_kernel, dim3(tiles), dim3(1024), 0, s, a, groups);
+  return hipGetLastError();
+}
+
+}  // namespace muon
