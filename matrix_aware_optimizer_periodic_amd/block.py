@@ -28,7 +28,8 @@ from .binding import MUON_OK, MuonError, lib
 
 NORM_KINDS = {"none": 0, "rms": 1, "layer": 2}
 ACTS = {"silu": 0, "gelu": 1}
-BLOCK_EXPORTED = ("muon_block_last_error", "muon_norm_fwd", "muon_norm_bwd_workspace", "muon_norm_bwd")
+BLOCK_EXPORTED = ("muon_block_last_error", "muon_norm_fwd", "muon_norm_bwd_workspace", "muon_norm_bwd",
+                  "muon_attn_fwd_workspace", "muon_attn_fwd", "muon_attn_bwd_workspace", "muon_attn_bwd")
 
 _TYPES = {torch.float32: 0, torch.bfloat16: 1}
 # The argument structures of muon_block.h, packed field by field (a few
@@ -236,3 +237,94 @@ def residual_norm(resid, h=None, gate=None, post_weight=None, pre_weight=None, s
     """norm_fwd for autograd; returns (resid_out, y)."""
     return _ResidualNorm.apply(resid, h, gate, post_weight, pre_weight, scale, shift,
                                {"post": post, "pre": pre, "alpha": alpha, "eps": eps})
+
+
+# ---------------------------------------------------------------- attention
+def _heads(t, name: str):
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: bf16 is wanted, got {t.dtype}")
+    b, n, h, d = t.shape
+    sb, sl, sh, sd = t.stride()
+    if sd != 1 and d > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    # the stride of a dimension of one says nothing
+    return t.data_ptr(), sb if b > 1 else 0, sl if n > 1 else 0, sh if h > 1 else 0
+
+
+def _attn_dims(q, k, v, q_lens, k_lens, scale):
+    if q.dim() != 4 or k.dim() != 4 or v.shape != k.shape or q.shape[0] != k.shape[0] or q.shape[3] != k.shape[3]:
+        raise ValueError(f"(batch, len, heads, dim) each: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}")
+    for name, t in (("q_lens", q_lens), ("k_lens", k_lens)):
+        if t is None:
+            continue
+        if t.dtype != torch.int32:
+            raise TypeError(f"{name}: int32 is wanted, got {t.dtype}")
+        if t.shape != (q.shape[0],) or not t.is_contiguous():
+            raise ValueError(f"{name}: one length per sample is wanted")
+    b, m, h, d = q.shape
+    return b, m, k.shape[1], h, k.shape[2], d, float(d) ** -0.5 if scale is None else float(scale)
+
+
+def _ptr(t) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def attn_fwd(q, k, v, *, causal: bool = False, offset: int = 0, q_lens=None, k_lens=None, scale: float | None = None):
+    """Softmax attention: q (batch, q_len, heads, dim), k and v (batch, k_len,
+    kv_heads, dim), bf16, any strides that are multiples of eight with the last
+    dimension contiguous (slices of a packed projection are fine); dim a
+    multiple of 8 up to 128; kv_heads divides heads.
+
+    q_lens, k_lens: int32 (batch,) on the GPU, how many of a sample's queries
+    and keys are there.  causal: query i sees key j for j <= i + offset.
+    scale: dim ** -0.5 where None.  Returns o (batch, q_len, heads, dim) bf16
+    and lse (batch, heads, q_len) fp32; a query that sees no key has o = 0 and
+    lse = -inf."""
+    dev = _device(q, k, v, q_lens, k_lens)
+    b, m, n, h, g, d, scale = _attn_dims(q, k, v, q_lens, k_lens, scale)
+    o = torch.empty((b, m, h, d), dtype=torch.bfloat16, device=dev)
+    lse = torch.empty((b, h, m), dtype=torch.float32, device=dev)
+    args = ATTN_ARGS.pack(b, m, n, h, g, d, int(causal), offset, scale, 0, _ptr(q_lens), _ptr(k_lens),
+                          *_heads(q, "q"), *_heads(k, "k"), *_heads(v, "v"), *_heads(o, "o"), lse.data_ptr(),
+                          *(4 * _NO_HEADS))
+    _call("muon_attn_fwd", args, dev)
+    return o, lse
+
+
+def attn_bwd(d_o, q, k, v, o, lse, *, causal: bool = False, offset: int = 0, q_lens=None, k_lens=None,
+             scale: float | None = None):
+    """Gradients (d_q, d_k, d_v) of attn_fwd's o, from d_o and what attn_fwd
+    took and gave; contiguous, zero past the lengths."""
+    dev = _device(q, d_o, k, v, o, lse, q_lens, k_lens)
+    b, m, n, h, g, d, scale = _attn_dims(q, k, v, q_lens, k_lens, scale)
+    if d_o.shape != q.shape or o.shape != q.shape or lse.shape != (b, h, m):
+        raise ValueError(f"d_o {tuple(d_o.shape)}, o {tuple(o.shape)}, lse {tuple(lse.shape)} for q {tuple(q.shape)}")
+    if lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError("lse is attn_fwd's second result")
+    d_q, d_k, d_v = (torch.empty(t.shape, dtype=torch.bfloat16, device=dev) for t in (q, k, v))
+    args = ATTN_ARGS.pack(b, m, n, h, g, d, int(causal), offset, scale, 0, _ptr(q_lens), _ptr(k_lens),
+                          *_heads(q, "q"), *_heads(k, "k"), *_heads(v, "v"), *_heads(o, "o"), lse.data_ptr(),
+                          *_heads(d_o, "d_o"), *_heads(d_q, "d_q"), *_heads(d_k, "d_k"), *_heads(d_v, "d_v"))
+    _call("muon_attn_bwd", args, dev)
+    return d_q, d_k, d_v
+
+
+class _Attention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, how):
+        o, lse = attn_fwd(q, k, v, **how)
+        ctx.how = how
+        ctx.save_for_backward(q, k, v, o, lse)
+        return o
+
+    @staticmethod
+    def backward(ctx, d_o):
+        q, k, v, o, lse = ctx.saved_tensors
+        return (*attn_bwd(d_o.contiguous(), q, k, v, o, lse, **ctx.how), None)
+
+
+def attention(q, k, v, *, causal: bool = False, offset: int = 0, q_lens=None, k_lens=None,
+              scale: float | None = None):
+    """attn_fwd for autograd; returns o."""
+    return _Attention.apply(q, k, v, {"causal": causal, "offset": offset, "q_lens": q_lens, "k_lens": k_lens,
+                                      "scale": scale})

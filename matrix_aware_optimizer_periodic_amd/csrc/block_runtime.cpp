@@ -141,6 +141,61 @@ size_t norm_bwd_bytes(const muon_norm_args* a) {
   return part + (weights ? align_up(size_t(g) * 2 * size_t(a->cols) * 4) : 0);
 }
 
+// ---- attention ----------------------------------------------------------------
+muon_status attn_dims(const muon_attn_args* a) {
+  if (!a) return fail(MUON_E_ARG, "args is NULL");
+  if (a->batch < 0 || a->q_len < 0 || a->k_len < 0 || a->heads < 1 || a->kv_heads < 1 || a->heads % a->kv_heads)
+    return fail(MUON_E_SHAPE, "batch %lld, lengths %lld and %lld, heads %d over %d", (long long)a->batch,
+                (long long)a->q_len, (long long)a->k_len, a->heads, a->kv_heads);
+  if (a->dim < 8 || a->dim > 128 || a->dim % 8) return fail(MUON_E_SHAPE, "dim %d: a multiple of 8 up to 128", a->dim);
+  if ((a->causal != 0 && a->causal != 1) || a->reserved != 0) return fail(MUON_E_ARG, "causal is 0 or 1, reserved 0");
+  if (!std::isfinite(a->scale) || !(a->scale > 0.f)) return fail(MUON_E_ARG, "scale must be positive and finite");
+  // 32-bit row, key and workgroup numbers
+  const int64_t group = a->heads / a->kv_heads, top = 1 << 30;
+  if (a->batch > 1 << 20 || a->q_len > top || a->k_len > top || a->q_len * group > top ||
+      ((a->q_len * group + 127) / 128 + 1) * a->batch * a->kv_heads > top / 512 * 64 ||
+      ((a->k_len + 127) / 128) * a->batch * a->kv_heads > top)
+    return fail(MUON_E_SHAPE, "too many rows for one call");
+  return MUON_OK;
+}
+
+muon_status attn_heads(const char* name, const muon_heads& t) {
+  if (!t.ptr) return fail(MUON_E_ARG, "%s is missing", name);
+  if (!aligned(t.ptr, 16)) return fail(MUON_E_ALIGN, "%s: pointer not 16-byte aligned", name);
+  if (t.stride_batch % 8 || t.stride_len % 8 || t.stride_head % 8)
+    return fail(MUON_E_ALIGN, "%s: strides must be multiples of 8 values", name);
+  if (t.stride_batch < 0 || t.stride_len < 0 || t.stride_head < 0 || t.stride_len > kMaxLd)
+    return fail(MUON_E_SHAPE, "%s: stride out of range", name);
+  return MUON_OK;
+}
+
+HeadsDev heads_dev(const muon_heads& t) { return HeadsDev{t.ptr, t.stride_batch, t.stride_len, t.stride_head}; }
+
+AttnDev attn_dev(const muon_attn_args* a) {
+  AttnDev d{};
+  d.batch = int32_t(a->batch); d.q_len = int32_t(a->q_len); d.k_len = int32_t(a->k_len);
+  d.heads = a->heads; d.kv_heads = a->kv_heads; d.dim = a->dim; d.causal = a->causal; d.scale = a->scale;
+  const int64_t far = int64_t(1) << 31;      // beyond every length
+  d.offset = a->offset > far ? far : a->offset < -far ? -far : a->offset;
+  d.q_lens = a->q_lens; d.k_lens = a->k_lens;
+  d.q = heads_dev(a->q); d.k = heads_dev(a->k); d.v = heads_dev(a->v); d.o = heads_dev(a->o);
+  d.lse = a->lse;
+  d.d_o = heads_dev(a->d_o); d.d_q = heads_dev(a->d_q); d.d_k = heads_dev(a->d_k); d.d_v = heads_dev(a->d_v);
+  int keys = 0;
+  d.splits = attn_splits(d, &keys);
+  d.split_keys = keys;
+  return d;
+}
+
+size_t attn_lines(const AttnDev& d) { return size_t(d.batch) * d.heads * d.q_len; }
+
+size_t attn_fwd_bytes(const AttnDev& d) {
+  if (d.splits <= 1 || attn_lines(d) == 0) return 0;
+  return align_up(attn_lines(d) * d.splits * d.dim * 4) + align_up(attn_lines(d) * d.splits * 4);
+}
+
+size_t attn_bwd_bytes(const AttnDev& d) { return 2 * align_up(attn_lines(d) * 4); }
+
 }  // namespace
 
 extern "C" {
@@ -210,6 +265,62 @@ muon_status muon_norm_bwd(const muon_norm_args* a, void* ws, size_t ws_bytes, vo
                                           align_up(size_t(g) * dev.splits * kNormSums * size_t(d) * 4));
   }
   return launched("muon_norm_bwd", launch_norm_bwd(static_cast<hipStream_t>(hip_stream), dev, norm_vec(a), sums));
+}
+
+muon_status muon_attn_fwd_workspace(const muon_attn_args* a, size_t* bytes) {
+  if (!bytes) return fail(MUON_E_ARG, "bytes is NULL");
+  CHECK(attn_dims(a));
+  *bytes = attn_fwd_bytes(attn_dev(a));
+  return MUON_OK;
+}
+
+muon_status muon_attn_fwd(const muon_attn_args* a, void* ws, size_t ws_bytes, void* hip_stream) {
+  CHECK(attn_dims(a));
+  if (a->batch == 0 || a->q_len == 0) return MUON_OK;
+  CHECK(attn_heads("q", a->q));
+  if (a->k_len > 0) {
+    CHECK(attn_heads("k", a->k));
+    CHECK(attn_heads("v", a->v));
+  }
+  CHECK(attn_heads("o", a->o));
+  if (!a->lse || !aligned(a->lse, 4)) return fail(MUON_E_ARG, "lse is missing or not aligned");
+  AttnDev d = attn_dev(a);
+  CHECK(check_workspace(ws, ws_bytes, attn_fwd_bytes(d)));
+  if (d.splits > 1) {
+    d.part_o = static_cast<float*>(ws);
+    d.part_lse = reinterpret_cast<float*>(static_cast<char*>(ws) + align_up(attn_lines(d) * d.splits * d.dim * 4));
+  }
+  return launched("muon_attn_fwd", launch_attn_fwd(static_cast<hipStream_t>(hip_stream), d));
+}
+
+muon_status muon_attn_bwd_workspace(const muon_attn_args* a, size_t* bytes) {
+  if (!bytes) return fail(MUON_E_ARG, "bytes is NULL");
+  CHECK(attn_dims(a));
+  *bytes = attn_bwd_bytes(attn_dev(a));
+  return MUON_OK;
+}
+
+muon_status muon_attn_bwd(const muon_attn_args* a, void* ws, size_t ws_bytes, void* hip_stream) {
+  CHECK(attn_dims(a));
+  if (a->batch == 0 || (a->q_len == 0 && a->k_len == 0)) return MUON_OK;
+  if (a->q_len > 0) {
+    CHECK(attn_heads("q", a->q));
+    CHECK(attn_heads("o", a->o));
+    CHECK(attn_heads("d_o", a->d_o));
+    CHECK(attn_heads("d_q", a->d_q));
+    if (!a->lse || !aligned(a->lse, 4)) return fail(MUON_E_ARG, "lse is missing or not aligned");
+  }
+  if (a->k_len > 0) {
+    CHECK(attn_heads("k", a->k));
+    CHECK(attn_heads("v", a->v));
+    CHECK(attn_heads("d_k", a->d_k));
+    CHECK(attn_heads("d_v", a->d_v));
+  }
+  AttnDev d = attn_dev(a);
+  CHECK(check_workspace(ws, ws_bytes, attn_bwd_bytes(d)));
+  d.part_lse = static_cast<float*>(ws);
+  d.delta = reinterpret_cast<float*>(static_cast<char*>(ws) + align_up(attn_lines(d) * 4));
+  return launched("muon_attn_bwd", launch_attn_bwd(static_cast<hipStream_t>(hip_stream), d));
 }
 
 }  // extern "C"

@@ -1,0 +1,626 @@
+// Softmax attention, forward and backward, on bf16 matrix cores.
+//
+//   s = scale q k^T (keys that a query sees), p = softmax(s), o = p v
+//   delta_i = do_i . o_i,  ds = p (do v^T - delta)
+//   dv = p^T do,  dq = scale ds k,  dk = scale ds^T q
+//
+// One pass over the keys with a running maximum and sum per query; nothing of
+// size q_len x k_len is stored, and the backward pass recomputes p from q, k
+// and the logarithm of the sum.  Bound by the matrix cores (4 D operations per
+// visible pair forward, 14 D backward here: the scores and do v^T are formed
+// in both backward kernels, so that neither needs atomics), for one query by
+// reading the keys and values.
+//
+// Every product is arranged so that the scores stay in registers between the
+// two products they sit between: the first product leaves a lane with one
+// query (or key) and four consecutive keys (or queries) at a time, and as the
+// second product's operand those are k indices, whose order is free as long
+// as the other operand follows it.  That other operand is read from LDS
+// through the transposing read, four consecutive k of one column at a time,
+// in just that order.  So probabilities never go through LDS.
+//
+// LDS rows hold 64 or 128 values; 16-byte chunk c of row r is stored at chunk
+// c ^ x(r).  The row reads (32 rows at one chunk) and the transposed reads
+// (four rows at a 64-byte block) then both go to distinct banks.
+//
+// Rows of the forward and dq kernels are the (query, head) pairs that share a
+// key head, the heads of one query next to each other: grouped heads and few
+// queries share the key tiles of one workgroup.
+#include "block_mfma.h"
+
+namespace muon {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kTile = 64;        // keys (dq, forward) or queries (dk, dv) per LDS tile
+constexpr int kRowsWg = 128;     // rows per workgroup: four waves of 32
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32, 64); }
+
+// Head geometry: DB blocks of 32 dims; LDS rows of PITCH 16-byte chunks.
+template <int DB>
+struct Geo {
+  static constexpr int KS = 2 * DB;                 // 16-deep steps over the head's dims
+  static constexpr int PITCH = DB <= 2 ? 8 : 16;
+  static constexpr int ROWB = PITCH * 16;           // bytes of a row
+  static constexpr int TILEB = kTile * ROWB;
+  static constexpr int DMA = TILEB / 1024 / 4;      // per wave and tile
+  static __device__ __forceinline__ int swz(int row) {
+    return PITCH == 16 ? ((row & 3) << 2) | ((row >> 2) & 3) : (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
+  }
+};
+
+// Moves one tile of kTile rows, `stride` values apart, into LDS.  What is past
+// `there` rows or past dim values reads as zero.
+template <int DB>
+struct TileMove {
+  unsigned voff[Geo<DB>::DMA];
+  int row0;
+  int chunk;
+  bool dim_ok;
+  __device__ __forceinline__ TileMove(int64_t stride, int dim, int wave, int lane) {
+    constexpr int P = Geo<DB>::PITCH;
+    row0 = wave * (64 / P) + lane / P;
+    chunk = (lane % P) ^ Geo<DB>::swz(row0);
+    dim_ok = chunk * 8 < dim;
+#pragma unroll
+    for (int i = 0; i < Geo<DB>::DMA; ++i)
+      voff[i] = dim_ok ? unsigned(int64_t(row0 + i * (256 / P)) * stride * 2 + chunk * 16) : kBufNone;
+  }
+  __device__ __forceinline__ void issue(const uint16_t* tile, int there, unsigned lds, int wave) const {
+    const u32x4_t r = buffer_at(tile);
+#pragma unroll
+    for (int i = 0; i < Geo<DB>::DMA; ++i)
+      dma16(r, lds + unsigned(wave + 4 * i) * 1024u,
+            row0 + i * (256 / Geo<DB>::PITCH) < there ? voff[i] : kBufNone);
+  }
+};
+
+// Fragments straight from global memory: one row per lane, 8 values from
+// 16 ks + 8 half.
+template <int DB>
+__device__ __forceinline__ void load_rows(u32x4_t (&f)[2 * DB], const uint16_t* row, bool ok, int dim, int half) {
+#pragma unroll
+  for (int ks = 0; ks < 2 * DB; ++ks) {
+    const int d = ks * 16 + half * 8;
+    f[ks] = u32x4_t{0, 0, 0, 0};
+    if (ok && d < dim) f[ks] = *as_global(reinterpret_cast<const u32x4_t*>(row + d));
+  }
+}
+
+// Byte offsets of this lane's reads within a tile: row reads (32 rows of one
+// chunk) and transposed reads (A operand: dims down, k across).
+template <int DB>
+struct TileRead {
+  unsigned row[2 * DB];       // + 32 rows per block
+  unsigned tr[DB][2];         // + 16 rows per k step
+  __device__ __forceinline__ TileRead(int lane) {
+    using G = Geo<DB>;
+    const int l = lane & 31, half = lane >> 5;
+#pragma unroll
+    for (int ks = 0; ks < 2 * DB; ++ks) row[ks] = unsigned(l * G::ROWB + (((2 * ks + half) ^ G::swz(l)) << 4));
+    const int s = lane & 15;
+#pragma unroll
+    for (int db = 0; db < DB; ++db)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int r = 4 * half + 8 * u + (s >> 2);
+        const int c = 4 * db + 2 * ((lane >> 4) & 1) + ((s & 3) >> 1);
+        tr[db][u] = unsigned(r * G::ROWB + ((c ^ G::swz(r)) << 4) + (s & 1) * 8);
+      }
+  }
+  __device__ __forceinline__ u32x4_t rows(const unsigned char* t, int ks, int block) const {
+    return lds_read16(t, row[ks] + unsigned(block * 32 * Geo<DB>::ROWB));
+  }
+  __device__ __forceinline__ u32x4_t cols(const unsigned char* t, int db, int step) const {
+    const u32x2_t a = lds_read_tr(t, tr[db][0] + unsigned(step * 16 * Geo<DB>::ROWB));
+    const u32x2_t b = lds_read_tr(t, tr[db][1] + unsigned(step * 16 * Geo<DB>::ROWB));
+    return u32x4_t{a[0], a[1], b[0], b[1]};
+  }
+};
+
+// Eight results of a product as the next product's operand.
+__device__ __forceinline__ u32x4_t pack8(const f32x16_t& s, int from) {
+  return u32x4_t{pack_bf16x2(s[from], s[from + 1]), pack_bf16x2(s[from + 2], s[from + 3]),
+                 pack_bf16x2(s[from + 4], s[from + 5]), pack_bf16x2(s[from + 6], s[from + 7])};
+}
+
+// Result block -> one row of global memory per lane: dims 32 db + 8 g + 4 half
+// .. + 3 of every g.
+template <int DB>
+__device__ __forceinline__ void store_rows(const f32x16_t (&acc)[DB], float mul, uint16_t* row, int dim, int half) {
+#pragma unroll
+  for (int db = 0; db < DB; ++db)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int d = 32 * db + 8 * g + 4 * half;
+      if (d < dim)
+        *as_global(reinterpret_cast<u32x2_t*>(row + d)) =
+            u32x2_t{pack_bf16x2(acc[db][4 * g] * mul, acc[db][4 * g + 1] * mul),
+                    pack_bf16x2(acc[db][4 * g + 2] * mul, acc[db][4 * g + 3] * mul)};
+    }
+}
+
+__device__ __forceinline__ int clamp_len(const int32_t* lens, int b, int most) {
+  return lens ? min(max(lens[b], 0), most) : most;
+}
+
+// Which rows a workgroup of the forward or dq kernel has, and what they see.
+struct Rows {
+  int b, kvh, group, q_here, k_here;
+  int row0;                  // first row of the workgroup
+  int qi, head;              // this lane's query and head
+  bool ok;                   // the lane's row is inside the tensor
+  bool live;                 // ... and inside the sample's length
+  int see;                   // keys that the lane's row sees: 0 .. see - 1
+};
+
+__device__ __forceinline__ int seen(const AttnDev& a, int qi, int k_here) {
+  if (!a.causal) return k_here;
+  const int64_t n = int64_t(qi) + a.offset + 1;
+  return int(max(int64_t(0), min(int64_t(k_here), n)));
+}
+
+__device__ __forceinline__ Rows rows_of(const AttnDev& a, unsigned item, unsigned blocks, int wave, int lane) {
+  Rows r;
+  // Later rows see more keys under a causal border: they go first.
+  const unsigned blk = blocks - 1 - item % blocks, bh = item / blocks;
+  r.b = int(bh) / a.kv_heads;
+  r.kvh = int(bh) % a.kv_heads;
+  r.group = a.heads / a.kv_heads;
+  r.q_here = clamp_len(a.q_lens, r.b, a.q_len);
+  r.k_here = clamp_len(a.k_lens, r.b, a.k_len);
+  r.row0 = int(blk) * kRowsWg;
+  const int row = r.row0 + wave * 32 + (lane & 31);
+  r.qi = row / r.group;
+  r.head = r.kvh * r.group + row % r.group;
+  r.ok = r.qi < a.q_len;
+  r.live = r.qi < r.q_here;
+  r.see = r.live ? seen(a, r.qi, r.k_here) : 0;
+  return r;
+}
+
+__device__ __forceinline__ int wave_max(int v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = max(v, __shfl_xor(v, o, 64));
+  return __builtin_amdgcn_readfirstlane(v);
+}
+
+// Keys that the last of the workgroup's rows sees (the most of any).
+__device__ __forceinline__ int seen_most(const AttnDev& a, const Rows& r) {
+  const int last = min((r.row0 + kRowsWg - 1) / r.group, r.q_here - 1);
+  return last < r.row0 / r.group ? 0 : seen(a, last, r.k_here);
+}
+
+// ---------------------------------------------------------------------------
+// Forward.  Per tile of 64 keys: s^T = k q^T (a lane has one row, half of the
+// keys), running maximum and sum, o^T += v^T p^T.  The maximum that the
+// exponents are taken against follows the running one only when that has
+// grown by more than 2^8 (the result does not depend on it), so that the
+// accumulators are rarely rescaled.
+template <int DB, bool SPLIT>
+__global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnDev a, unsigned items, unsigned blocks) {
+  using G = Geo<DB>;
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[4 * G::TILEB];   // two of k, two of v
+  const int lane = threadIdx.x & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const unsigned id = xcd_item(blockIdx.x, items);
+  const unsigned split = SPLIT ? id % unsigned(a.splits) : 0;
+  const Rows r = rows_of(a, SPLIT ? id / unsigned(a.splits) : id, blocks, wave, lane);
+  const int first = SPLIT ? int(split) * a.split_keys : 0;
+  const int end = SPLIT ? min(seen_most(a, r), first + a.split_keys) : seen_most(a, r);
+  const int tiles = end > first ? (end - first + kTile - 1) / kTile : 0;
+
+  u32x4_t q[2 * DB];
+  const uint16_t* qrow = static_cast<const uint16_t*>(a.q.p) + r.b * a.q.sb + r.qi * a.q.sl + r.head * a.q.sh;
+  load_rows<DB>(q, qrow, r.live, a.dim, half);
+  const uint16_t* kbase = static_cast<const uint16_t*>(a.k.p) + r.b * a.k.sb + r.kvh * a.k.sh + first * a.k.sl;
+  const uint16_t* vbase = static_cast<const uint16_t*>(a.v.p) + r.b * a.v.sb + r.kvh * a.v.sh + first * a.v.sl;
+  const TileMove<DB> mk(a.k.sl, a.dim, wave, lane), mv(a.v.sl, a.dim, wave, lane);
+  const TileRead<DB> rd(lane);
+  const unsigned lds = lds_offset(smem);
+  auto fetch = [&](int t) {
+    const unsigned at = lds + unsigned(t & 1) * 2u * G::TILEB;
+    mk.issue(kbase + int64_t(t) * kTile * a.k.sl, r.k_here - first - t * kTile, at, wave);
+    mv.issue(vbase + int64_t(t) * kTile * a.v.sl, r.k_here - first - t * kTile, at + G::TILEB, wave);
+  };
+
+  f32x16_t o[DB];
+#pragma unroll
+  for (int db = 0; db < DB; ++db) o[db] = (f32x16_t)(0.f);
+  const float c = a.scale * kLog2e;
+  float top = -INFINITY, top_c = 0.f, sum = 0.f;
+  const int wave_see = wave_max(r.see), wave_all = -wave_max(r.ok ? -r.see : -0x7fffffff);
+
+  if (tiles > 0) fetch(0);
+  for (int t = 0; t < tiles; ++t) {
+    wait_vm<0>();
+    barrier();
+    if (t + 1 < tiles) fetch(t + 1);
+    const int key0 = first + t * kTile;
+    if (key0 >= wave_see) continue;
+    const unsigned char* kt = smem + (t & 1) * 2 * G::TILEB;
+    const unsigned char* vt = kt + G::TILEB;
+    f32x16_t s[2];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      s[kb] = (f32x16_t)(0.f);
+#pragma unroll
+      for (int ks = 0; ks < G::KS; ++ks) s[kb] = mfma32(rd.rows(kt, ks, kb), q[ks], s[kb]);
+    }
+    if (key0 + kTile > wave_all) {
+      const int n = r.see - key0 - 4 * half;
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+          if (32 * kb + 8 * (v >> 2) + (v & 3) >= n) s[kb][v] = -INFINITY;
+    }
+    float m = s[0][0];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) m = fmaxf(m, s[kb][v]);
+    m = fmaxf(m, other_half(m));
+    if (__any((m - top) * c > 8.f)) {        // also where top is -inf and m is not
+      const float to = fmaxf(top, m);
+      const float f = to == -INFINITY ? 1.f : exp2_fast((top - to) * c);
+      top = to;
+      top_c = to == -INFINITY ? 0.f : to * c;
+      sum *= f;
+#pragma unroll
+      for (int db = 0; db < DB; ++db)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) o[db][v] *= f;
+    }
+    u32x4_t p[4];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        s[kb][v] = exp2_fast(fmaf(s[kb][v], c, -top_c));
+        sum += s[kb][v];
+      }
+      p[2 * kb] = pack8(s[kb], 0);
+      p[2 * kb + 1] = pack8(s[kb], 8);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int db = 0; db < DB; ++db) o[db] = mfma32(rd.cols(vt, db, j), p[j], o[db]);
+  }
+  sum += other_half(sum);
+  const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+  const float lse = sum == 0.f ? -INFINITY : fmaf(top, a.scale, __builtin_amdgcn_logf(sum) * kLn2);
+  if (!r.ok) return;
+  const int64_t line = (int64_t(r.b) * a.heads + r.head) * a.q_len + r.qi;
+  if constexpr (SPLIT) {
+    const int64_t at = int64_t(split) * a.batch * a.heads * a.q_len + line;
+    float* po = a.part_o + at * a.dim;
+#pragma unroll
+    for (int db = 0; db < DB; ++db)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int d = 32 * db + 8 * g + 4 * half;
+        if (d < a.dim)
+          *as_global(reinterpret_cast<f32x4_t*>(po + d)) = f32x4_t{o[db][4 * g] * inv, o[db][4 * g + 1] * inv,
+                                                                   o[db][4 * g + 2] * inv, o[db][4 * g + 3] * inv};
+      }
+    if (half == 0) *as_global(a.part_lse + at) = lse;
+  } else {
+    store_rows<DB>(o, inv, static_cast<uint16_t*>(a.o.p) + r.b * a.o.sb + r.qi * a.o.sl + r.head * a.o.sh, a.dim, half);
+    if (half == 0) *as_global(a.lse + line) = lse;
+  }
+}
+
+// Joins the key ranges of one row: weights exp(lse_i - lse) add up to 1.
+// Sixteen lanes per row, eight dims each.
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnDev a) {
+  const int64_t lines = int64_t(a.batch) * a.heads * a.q_len;
+  const int64_t line = int64_t(blockIdx.x) * 16 + (threadIdx.x >> 4);
+  if (line >= lines) return;
+  const int d = (threadIdx.x & 15) * 8;
+  float top = -INFINITY;
+  for (int i = 0; i < a.splits; ++i) top = fmaxf(top, *as_global(a.part_lse + i * lines + line));
+  float sum = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (top != -INFINITY) {
+    for (int i = 0; i < a.splits; ++i) {
+      const float w = exp2_fast((*as_global(a.part_lse + i * lines + line) - top) * kLog2e);
+      sum += w;
+      if (d < a.dim && w != 0.f) {
+        float t[8];
+        load_vals<float, 8>(a.part_o, (i * lines + line) * a.dim + d, t);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[k] = fmaf(w, t[k], o[k]);
+      }
+    }
+  }
+  const int qi = int(line % a.q_len);
+  const int64_t bh = line / a.q_len;
+  if (d < a.dim) {
+    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) o[k] *= inv;
+    store_vals<uint16_t, 8>(a.o.p, (bh / a.heads) * a.o.sb + qi * a.o.sl + (bh % a.heads) * a.o.sh + d, o);
+  }
+  if (d == 0) *as_global(a.lse + line) = sum == 0.f ? -INFINITY : top + __builtin_amdgcn_logf(sum) * kLn2;
+}
+
+// ---------------------------------------------------------------------------
+// dq, and per row delta = do . o and the exponent's offset for the dk, dv
+// kernel.  Per tile of 64 keys, 32 at a time: s^T = k q^T, dp^T = v do^T,
+// ds^T = p^T (dp^T - delta), dq^T += k^T ds^T.
+template <int DB>
+__global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnDev a, unsigned items, unsigned blocks) {
+  using G = Geo<DB>;
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[4 * G::TILEB];
+  const int lane = threadIdx.x & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Rows r = rows_of(a, xcd_item(blockIdx.x, items), blocks, wave, lane);
+  const int end = seen_most(a, r);
+  const int tiles = (end + kTile - 1) / kTile;
+
+  u32x4_t q[2 * DB], g[2 * DB];
+  load_rows<DB>(q, static_cast<const uint16_t*>(a.q.p) + r.b * a.q.sb + r.qi * a.q.sl + r.head * a.q.sh, r.live, a.dim,
+                half);
+  load_rows<DB>(g, static_cast<const uint16_t*>(a.d_o.p) + r.b * a.d_o.sb + r.qi * a.d_o.sl + r.head * a.d_o.sh, r.live,
+                a.dim, half);
+  float delta = 0.f;
+  {
+    u32x4_t o[2 * DB];
+    load_rows<DB>(o, static_cast<const uint16_t*>(a.o.p) + r.b * a.o.sb + r.qi * a.o.sl + r.head * a.o.sh, r.live,
+                  a.dim, half);
+    // The diagonal of o do^T, summed in the same order as do v^T below: where
+    // a row's o is one row of v (one key), dp - delta is then exactly 0.
+    f32x16_t s = (f32x16_t)(0.f);
+#pragma unroll
+    for (int ks = 0; ks < G::KS; ++ks) s = mfma32(o[ks], g[ks], s);
+#pragma unroll
+    for (int v = 0; v < 16; ++v)
+      if (8 * (v >> 2) + 4 * half + (v & 3) == (lane & 31)) delta = s[v];
+    delta += other_half(delta);
+  }
+  // A row that sees nothing gets the offset +inf: its probabilities are 0.
+  const int64_t line = (int64_t(r.b) * a.heads + r.head) * a.q_len + r.qi;
+  float lse = INFINITY;
+  if (r.live) {
+    lse = *as_global(a.lse + line);
+    lse = lse == -INFINITY ? INFINITY : lse * kLog2e;
+  }
+  if (r.see == 0) { lse = INFINITY; delta = 0.f; }
+  if (r.ok && half == 0) {
+    *as_global(a.part_lse + line) = lse;
+    *as_global(a.delta + line) = delta;
+  }
+
+  const uint16_t* kbase = static_cast<const uint16_t*>(a.k.p) + r.b * a.k.sb + r.kvh * a.k.sh;
+  const uint16_t* vbase = static_cast<const uint16_t*>(a.v.p) + r.b * a.v.sb + r.kvh * a.v.sh;
+  const TileMove<DB> mk(a.k.sl, a.dim, wave, lane), mv(a.v.sl, a.dim, wave, lane);
+  const TileRead<DB> rd(lane);
+  const unsigned lds = lds_offset(smem);
+  auto fetch = [&](int t) {
+    const unsigned at = lds + unsigned(t & 1) * 2u * G::TILEB;
+    mk.issue(kbase + int64_t(t) * kTile * a.k.sl, r.k_here - t * kTile, at, wave);
+    mv.issue(vbase + int64_t(t) * kTile * a.v.sl, r.k_here - t * kTile, at + G::TILEB, wave);
+  };
+  f32x16_t acc[DB];
+#pragma unroll
+  for (int db = 0; db < DB; ++db) acc[db] = (f32x16_t)(0.f);
+  const float c = a.scale * kLog2e;
+  const int wave_see = wave_max(r.see), wave_all = -wave_max(r.ok ? -r.see : -0x7fffffff);
+
+  if (tiles > 0) fetch(0);
+  for (int t = 0; t < tiles; ++t) {
+    wait_vm<0>();
+    barrier();
+    if (t + 1 < tiles) fetch(t + 1);
+    const int key0 = t * kTile;
+    if (key0 >= wave_see) continue;
+    const unsigned char* kt = smem + (t & 1) * 2 * G::TILEB;
+    const unsigned char* vt = kt + G::TILEB;
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      f32x16_t s = (f32x16_t)(0.f), dp = (f32x16_t)(0.f);
+#pragma unroll
+      for (int ks = 0; ks < G::KS; ++ks) {
+        s = mfma32(rd.rows(kt, ks, kb), q[ks], s);
+        dp = mfma32(rd.rows(vt, ks, kb), g[ks], dp);
+      }
+      if (key0 + 32 * kb + 32 > wave_all) {
+        const int n = r.see - key0 - 32 * kb - 4 * half;
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+          if (8 * (v >> 2) + (v & 3) >= n) s[v] = -INFINITY;
+      }
+#pragma unroll
+      for (int v = 0; v < 16; ++v) s[v] = exp2_fast(fmaf(s[v], c, -lse)) * (dp[v] - delta);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const u32x4_t ds = pack8(s, 8 * j);
+#pragma unroll
+        for (int db = 0; db < DB; ++db) acc[db] = mfma32(rd.cols(kt, db, 2 * kb + j), ds, acc[db]);
+      }
+    }
+  }
+  if (r.ok)
+    store_rows<DB>(acc, a.scale, static_cast<uint16_t*>(a.d_q.p) + r.b * a.d_q.sb + r.qi * a.d_q.sl + r.head * a.d_q.sh,
+                   a.dim, half);
+}
+
+// ---------------------------------------------------------------------------
+// dk and dv: 32 keys per wave, whose k and v rows stay in registers as the
+// first products' operands.  Over the heads of the group and tiles of 64
+// queries, 32 at a time: s = q k^T, dp = do v^T (a lane has one key), then
+// dv^T += do^T p, dk^T += q^T ds.
+template <int DB>
+__global__ __launch_bounds__(256, 2) void attn_dkv_kernel(AttnDev a, unsigned items, unsigned blocks) {
+  using G = Geo<DB>;
+  constexpr int BUF = 2 * G::TILEB + 2 * kTile * 4;     // q, do, offsets, deltas
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[2 * BUF];
+  const int lane = threadIdx.x & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const unsigned item = xcd_item(blockIdx.x, items);
+  const unsigned bh = item / blocks;
+  const int b = int(bh) / a.kv_heads, kvh = int(bh) % a.kv_heads, group = a.heads / a.kv_heads;
+  const int q_here = clamp_len(a.q_lens, b, a.q_len), k_here = clamp_len(a.k_lens, b, a.k_len);
+  const int key0 = int(item % blocks) * kRowsWg;
+  const int wkey = key0 + wave * 32, key = wkey + (lane & 31);
+  // First query that sees the workgroup's (wave's, lane's) first key.
+  const int64_t border = a.causal ? -a.offset : int64_t(-0x7fffffff);
+  auto first_query = [&](int k) { return int(max(int64_t(0), min(int64_t(q_here), int64_t(k) + border))); };
+  const int tile0 = first_query(key0) / kTile, tile_end = (q_here + kTile - 1) / kTile;
+  const int per_head = key0 < k_here && tile_end > tile0 && first_query(key0) < q_here ? tile_end - tile0 : 0;
+  const int tiles = per_head * group;
+  const int wave_first = first_query(wkey), wave_all = first_query(wkey + 31), mine = first_query(key);
+
+  u32x4_t kf[2 * DB], vf[2 * DB];
+  load_rows<DB>(kf, static_cast<const uint16_t*>(a.k.p) + b * a.k.sb + key * a.k.sl + kvh * a.k.sh, key < k_here,
+                a.dim, half);
+  load_rows<DB>(vf, static_cast<const uint16_t*>(a.v.p) + b * a.v.sb + key * a.v.sl + kvh * a.v.sh, key < k_here,
+                a.dim, half);
+  const TileMove<DB> mq(a.q.sl, a.dim, wave, lane), mg(a.d_o.sl, a.dim, wave, lane);
+  const TileRead<DB> rd(lane);
+  const unsigned lds = lds_offset(smem);
+  auto fetch = [&](int t) {
+    const int head = kvh * group + t / per_head, q0 = (tile0 + t % per_head) * kTile;
+    const unsigned at = lds + unsigned(t & 1) * BUF;
+    mq.issue(static_cast<const uint16_t*>(a.q.p) + b * a.q.sb + head * a.q.sh + q0 * a.q.sl, q_here - q0, at, wave);
+    mg.issue(static_cast<const uint16_t*>(a.d_o.p) + b * a.d_o.sb + head * a.d_o.sh + q0 * a.d_o.sl, q_here - q0,
+             at + G::TILEB, wave);
+    const int64_t line = (int64_t(b) * a.heads + head) * a.q_len + q0;
+    const unsigned off = lane < q_here - q0 ? unsigned(lane) * 4u : kBufNone;
+    if (wave == 0) dma4(buffer_at(a.part_lse + line), at + 2 * G::TILEB, off);
+    if (wave == 1) dma4(buffer_at(a.delta + line), at + 2 * G::TILEB + kTile * 4, off);
+  };
+  f32x16_t dk[DB], dv[DB];
+#pragma unroll
+  for (int db = 0; db < DB; ++db) dk[db] = dv[db] = (f32x16_t)(0.f);
+  const float c = a.scale * kLog2e;
+
+  if (tiles > 0) fetch(0);
+  for (int t = 0; t < tiles; ++t) {
+    wait_vm<0>();
+    barrier();
+    if (t + 1 < tiles) fetch(t + 1);
+    const int q0 = (tile0 + t % per_head) * kTile;
+    const unsigned char* qt = smem + (t & 1) * BUF;
+    const unsigned char* gt = qt + G::TILEB;
+    const float* lt = reinterpret_cast<const float*>(gt + G::TILEB);
+#pragma unroll
+    for (int qb = 0; qb < 2; ++qb) {
+      if (q0 + 32 * qb + 32 <= wave_first || q0 + 32 * qb >= q_here || wkey >= k_here) continue;
+      f32x16_t s = (f32x16_t)(0.f);
+#pragma unroll
+      for (int ks = 0; ks < G::KS; ++ks) s = mfma32(rd.rows(qt, ks, qb), kf[ks], s);
+      if (q0 + 32 * qb < wave_all) {
+        const int n = mine - q0 - 32 * qb - 4 * half;
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+          if (8 * (v >> 2) + (v & 3) < n) s[v] = -INFINITY;
+      }
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x4_t l = *(const MUON_LOCAL f32x4_t*)(const MUON_LOCAL float*)(lt + 32 * qb + 8 * g + 4 * half);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[4 * g + k] = exp2_fast(fmaf(s[4 * g + k], c, -l[k]));
+      }
+      f32x16_t dp = (f32x16_t)(0.f);
+#pragma unroll
+      for (int ks = 0; ks < G::KS; ++ks) dp = mfma32(rd.rows(gt, ks, qb), vf[ks], dp);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const u32x4_t p = pack8(s, 8 * j);
+#pragma unroll
+        for (int db = 0; db < DB; ++db) dv[db] = mfma32(rd.cols(gt, db, 2 * qb + j), p, dv[db]);
+      }
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x4_t l = *(const MUON_LOCAL f32x4_t*)(const MUON_LOCAL float*)(lt + kTile + 32 * qb + 8 * g + 4 * half);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[4 * g + k] *= dp[4 * g + k] - l[k];
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const u32x4_t ds = pack8(s, 8 * j);
+#pragma unroll
+        for (int db = 0; db < DB; ++db) dk[db] = mfma32(rd.cols(qt, db, 2 * qb + j), ds, dk[db]);
+      }
+    }
+  }
+  if (key >= a.k_len) return;
+  const bool there = key < k_here;   // a key past the length has no gradient
+  if (!there) {
+#pragma unroll
+    for (int db = 0; db < DB; ++db) dk[db] = dv[db] = (f32x16_t)(0.f);
+  }
+  store_rows<DB>(dk, a.scale, static_cast<uint16_t*>(a.d_k.p) + b * a.d_k.sb + key * a.d_k.sl + kvh * a.d_k.sh, a.dim,
+                 half);
+  store_rows<DB>(dv, 1.f, static_cast<uint16_t*>(a.d_v.p) + b * a.d_v.sb + key * a.d_v.sl + kvh * a.d_v.sh, a.dim,
+                 half);
+}
+
+unsigned row_blocks(const AttnDev& a) {
+  const int64_t rows = int64_t(a.q_len) * (a.heads / a.kv_heads);
+  return unsigned((rows + kRowsWg - 1) / kRowsWg);
+}
+
+#define BY_DIM(K, ...)                                                                            \
+  (a.dim <= 32 ? K<1 __VA_ARGS__> : a.dim <= 64 ? K<2 __VA_ARGS__> : a.dim <= 96 ? K<3 __VA_ARGS__> \
+                                                                                 : K<4 __VA_ARGS__>)
+#define COMMA ,
+
+}  // namespace
+
+int attn_splits(const AttnDev& a, int* split_keys) {
+  // Two workgroups fit on each of 256 CUs.  With fewer than half of that,
+  // the keys are divided, in ranges of at least four tiles.
+  const int64_t items = int64_t(row_blocks(a)) * a.batch * a.kv_heads;
+  const int tiles = (a.k_len + kTile - 1) / kTile;
+  int64_t n = 1;
+  if (items > 0 && items < 256) {
+    n = 512 / items;
+    if (n > tiles / 4) n = tiles / 4;
+    if (n < 1) n = 1;
+  }
+  const int per = int((tiles + n - 1) / n);
+  *split_keys = per * kTile;
+  return tiles == 0 ? 1 : (tiles + per - 1) / per;
+}
+
+hipError_t launch_attn_fwd(hipStream_t s, const AttnDev& a) {
+  const unsigned blocks = row_blocks(a);
+  const unsigned items = blocks * unsigned(a.batch) * unsigned(a.kv_heads) * unsigned(a.splits);
+  if (a.splits == 1) {
+    auto* k = BY_DIM(attn_fwd_kernel, COMMA false);
+    hipLaunchKernelGGL(k, dim3(items), dim3(256), 0, s, a, items, blocks);
+    return hipGetLastError();
+  }
+  auto* k = BY_DIM(attn_fwd_kernel, COMMA true);
+  hipLaunchKernelGGL(k, dim3(items), dim3(256), 0, s, a, items, blocks);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t lines = int64_t(a.batch) * a.heads * a.q_len;
+  hipLaunchKernelGGL(attn_join_kernel, dim3(unsigned((lines + 15) / 16)), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_attn_bwd(hipStream_t s, const AttnDev& a) {
+  const unsigned bh = unsigned(a.batch) * unsigned(a.kv_heads);
+  if (a.q_len > 0) {
+    const unsigned blocks = row_blocks(a), items = blocks * bh;
+    auto* k = BY_DIM(attn_dq_kernel, );
+    hipLaunchKernelGGL(k, dim3(items), dim3(256), 0, s, a, items, blocks);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (a.k_len > 0) {
+    const unsigned blocks = unsigned((a.k_len + kRowsWg - 1) / kRowsWg), items = blocks * bh;
+    auto* k = BY_DIM(attn_dkv_kernel, );
+    hipLaunchKernelGGL(k, dim3(items), dim3(256), 0, s, a, items, blocks);
+    return hipGetLastError();
+  }
+  return hipSuccess;
+}
+
+}  // namespace muon

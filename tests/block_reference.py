@@ -61,3 +61,30 @@ def norm_block(resid, h, gate, post_weight, pre_weight, scale, shift, post, pre,
     if shift is not None:
         y = y + vec(shift)
     return r, y
+
+
+def attention(q, k, v, causal=False, offset=0, q_lens=None, k_lens=None, scale=None):
+    """(o, lse) of (batch, len, heads, dim) tensors, float64, one sample and
+    head at a time over what is there."""
+    b, m, h, d = q.shape
+    n, g = k.shape[1], k.shape[2]
+    scale = d ** -0.5 if scale is None else scale
+    o = torch.zeros((b, m, h, d), dtype=torch.float64, device=q.device)
+    lse = torch.full((b, h, m), float("-inf"), dtype=torch.float64, device=q.device)
+    for i in range(b):
+        mi = m if q_lens is None else min(max(int(q_lens[i]), 0), m)
+        ni = n if k_lens is None else min(max(int(k_lens[i]), 0), n)
+        if mi == 0 or ni == 0:
+            continue
+        see = torch.ones((mi, ni), dtype=torch.bool, device=q.device)
+        if causal:
+            rows = torch.arange(mi, device=q.device)[:, None]
+            see = torch.arange(ni, device=q.device)[None, :] <= rows + offset
+        some = see.any(1)
+        for j in range(h):
+            kj = j * g // h
+            s = (q[i, :mi, j] @ k[i, :ni, kj].T * scale).masked_fill(~see, -1e300)
+            p = torch.softmax(s, dim=1) * some[:, None]
+            o[i, :mi, j] = p @ v[i, :ni, kj]
+            lse[i, j, :mi] = torch.where(some, torch.logsumexp(s, dim=1), float("-inf"))
+    return o, lse
