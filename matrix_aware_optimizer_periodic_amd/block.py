@@ -29,7 +29,8 @@ from .binding import MUON_OK, MuonError, lib
 NORM_KINDS = {"none": 0, "rms": 1, "layer": 2}
 ACTS = {"silu": 0, "gelu": 1}
 BLOCK_EXPORTED = ("muon_block_last_error", "muon_norm_fwd", "muon_norm_bwd_workspace", "muon_norm_bwd",
-                  "muon_attn_fwd_workspace", "muon_attn_fwd", "muon_attn_bwd_workspace", "muon_attn_bwd")
+                  "muon_attn_fwd_workspace", "muon_attn_fwd", "muon_attn_bwd_workspace", "muon_attn_bwd",
+                  "muon_ffn_fwd_workspace", "muon_ffn_fwd", "muon_ffn_bwd_workspace", "muon_ffn_bwd")
 
 _TYPES = {torch.float32: 0, torch.bfloat16: 1}
 # The argument structures of muon_block.h, packed field by field (a few
@@ -328,3 +329,78 @@ def attention(q, k, v, *, causal: bool = False, offset: int = 0, q_lens=None, k_
     """attn_fwd for autograd; returns o."""
     return _Attention.apply(q, k, v, {"causal": causal, "offset": offset, "q_lens": q_lens, "k_lens": k_lens,
                                       "scale": scale})
+
+
+# ------------------------------------------------------- gated feed-forward
+def _ffn_dims(x, w_gate, w_up, w_down, act: str):
+    if act not in ACTS:
+        raise ValueError(f"act is one of {sorted(ACTS)}: got {act!r}")
+    for name, t in (("x", x), ("w_gate", w_gate), ("w_up", w_up), ("w_down", w_down)):
+        if t.dtype != torch.bfloat16:
+            raise TypeError(f"{name}: bf16 is wanted, got {t.dtype}")
+    if w_gate.dim() != 2 or x.dim() < 1:
+        raise ValueError("x is (..., cols), the weights are matrices")
+    hidden, cols = w_gate.shape
+    if x.shape[-1] != cols or w_up.shape != (hidden, cols) or w_down.shape != (cols, hidden):
+        raise ValueError(f"x {tuple(x.shape)}, w_gate {tuple(w_gate.shape)}, w_up {tuple(w_up.shape)}, "
+                         f"w_down {tuple(w_down.shape)}")
+    return x.shape[:-1].numel(), cols, hidden
+
+
+def ffn_fwd(x, w_gate, w_up, w_down, *, act: str = "silu", save: bool = True):
+    """y = (act(x w_gate^T) * (x w_up^T)) w_down^T, bf16 with fp32 sums.
+
+    x (..., cols); w_gate, w_up (hidden, cols); w_down (cols, hidden); cols and
+    hidden multiples of 8.  act: "silu", or "gelu" in its tanh form.  Returns
+    (y, gu): gu (rows, 2 hidden) holds both projections for ffn_bwd, None where
+    save is false."""
+    dev = _device(x, w_gate, w_up, w_down)
+    rows, cols, hidden = _ffn_dims(x, w_gate, w_up, w_down, act)
+    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    gu = torch.empty((rows, 2 * hidden), dtype=x.dtype, device=dev) if save else None
+    if rows == 0:
+        return y, gu
+    args = FFN_ARGS.pack(rows, cols, hidden, ACTS[act], 0, *_mat(x, rows, cols), *_mat(y, rows, cols),
+                         *_mat(w_gate, hidden, cols), *_mat(w_up, hidden, cols), *_mat(w_down, cols, hidden),
+                         *_mat(gu, rows, 2 * hidden), *(5 * _NO_MAT))
+    _call("muon_ffn_fwd", args, dev)
+    return y, gu
+
+
+def ffn_bwd(d_y, x, w_gate, w_up, w_down, gu, *, act: str = "silu", grad_dtype=torch.bfloat16):
+    """Gradients (d_x, d_w_gate, d_w_up, d_w_down) of ffn_fwd's y; the weights'
+    are contiguous, of grad_dtype (bf16 or fp32): what muon_step reads."""
+    dev = _device(x, d_y, w_gate, w_up, w_down, gu)
+    rows, cols, hidden = _ffn_dims(x, w_gate, w_up, w_down, act)
+    if d_y.shape != x.shape:
+        raise ValueError(f"d_y {tuple(d_y.shape)} for x {tuple(x.shape)}")
+    if grad_dtype not in _TYPES:
+        raise TypeError(f"unsupported grad_dtype {grad_dtype}")
+    d_x = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    grads = [torch.empty(w.shape, dtype=grad_dtype, device=dev) for w in (w_gate, w_up, w_down)]
+    if rows == 0:
+        return (d_x, *(w.zero_() for w in grads))
+    args = FFN_ARGS.pack(rows, cols, hidden, ACTS[act], 0, *_mat(x, rows, cols), *_NO_MAT,
+                         *_mat(w_gate, hidden, cols), *_mat(w_up, hidden, cols), *_mat(w_down, cols, hidden),
+                         *_mat(gu, rows, 2 * hidden), *_mat(d_y, rows, cols), *_mat(d_x, rows, cols),
+                         *_mat(grads[0], hidden, cols), *_mat(grads[1], hidden, cols), *_mat(grads[2], cols, hidden))
+    _call("muon_ffn_bwd", args, dev)
+    return (d_x, *grads)
+
+
+class _GatedFfn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w_gate, w_up, w_down, act):
+        y, gu = ffn_fwd(x, w_gate, w_up, w_down, act=act, save=any(ctx.needs_input_grad))
+        ctx.act = act
+        ctx.save_for_backward(x, w_gate, w_up, w_down, gu)
+        return y
+
+    @staticmethod
+    def backward(ctx, d_y):
+        return (*ffn_bwd(d_y.contiguous(), *ctx.saved_tensors, act=ctx.act), None)
+
+
+def gated_ffn(x, w_gate, w_up, w_down, *, act: str = "silu"):
+    """ffn_fwd for autograd; returns y."""
+    return _GatedFfn.apply(x, w_gate, w_up, w_down, act)

@@ -196,6 +196,60 @@ size_t attn_fwd_bytes(const AttnDev& d) {
 
 size_t attn_bwd_bytes(const AttnDev& d) { return 2 * align_up(attn_lines(d) * 4); }
 
+// ---- gated feed-forward ---------------------------------------------------------
+muon_status ffn_dims(const muon_ffn_args* a) {
+  if (!a) return fail(MUON_E_ARG, "args is NULL");
+  const int64_t most = 1 << 20;    // 2 hidden and a column tile stay within kMaxLd
+  if (a->rows < 0 || a->rows > (1 << 30) || a->cols < 8 || a->hidden < 8 || a->cols % 8 || a->hidden % 8 ||
+      a->cols > most || a->hidden > most ||
+      ((a->rows + 127) / 128) * ((a->cols > a->hidden ? a->cols : 2 * a->hidden) / 64 + 1) > (1 << 30))
+    return fail(MUON_E_SHAPE, "rows %lld, cols %lld, hidden %lld: cols and hidden are multiples of 8 up to 2^20",
+                (long long)a->rows, (long long)a->cols, (long long)a->hidden);
+  if ((a->act != MUON_ACT_SILU && a->act != MUON_ACT_GELU_TANH) || a->reserved != 0)
+    return fail(MUON_E_ARG, "unknown act, or reserved is not 0");
+  return MUON_OK;
+}
+
+// As check_mat, and rows whose 16-byte groups are aligned.
+muon_status ffn_mat(const char* name, const muon_tensor& t, int64_t rows, int64_t cols, int32_t dt) {
+  CHECK(check_mat(name, t, rows, cols, dt));
+  if (!aligned(t.ptr, 16) || t.ld % (t.dtype == MUON_F32 ? 4 : 8))
+    return fail(MUON_E_ALIGN, "%s: rows must be 16-byte aligned", name);
+  return MUON_OK;
+}
+
+muon_status ffn_weights(const muon_ffn_args* a) {
+  CHECK(ffn_mat("w_gate", a->w_gate, a->hidden, a->cols, MUON_BF16));
+  CHECK(ffn_mat("w_up", a->w_up, a->hidden, a->cols, MUON_BF16));
+  return ffn_mat("w_down", a->w_down, a->cols, a->hidden, MUON_BF16);
+}
+
+FfnDev ffn_dev(const muon_ffn_args* a) {
+  FfnDev d{};
+  d.rows = a->rows; d.cols = a->cols; d.hidden = a->hidden; d.act = a->act;
+  d.x = a->x.ptr; d.ld_x = a->x.ld;
+  d.w_gate = a->w_gate.ptr; d.ld_wg = a->w_gate.ld;
+  d.w_up = a->w_up.ptr; d.ld_wu = a->w_up.ld;
+  d.w_down = a->w_down.ptr; d.ld_wd = a->w_down.ld;
+  d.y = a->y.ptr; d.ld_y = a->y.ld;
+  d.gu = a->gu.ptr; d.ld_gu = a->gu.ld;
+  d.d_y = a->d_y.ptr; d.ld_dy = a->d_y.ld;
+  d.d_x = a->d_x.ptr; d.ld_dx = a->d_x.ld;
+  d.d_wg = a->d_w_gate.ptr; d.ld_dwg = a->d_w_gate.ld;
+  d.d_wu = a->d_w_up.ptr; d.ld_dwu = a->d_w_up.ld;
+  d.d_wd = a->d_w_down.ptr; d.ld_dwd = a->d_w_down.ld;
+  d.grad_bf16 = a->d_w_gate.dtype == MUON_BF16;
+  return d;
+}
+
+size_t ffn_hid_bytes(const muon_ffn_args* a) { return align_up(size_t(a->rows) * size_t(a->hidden) * 2); }
+size_t ffn_fwd_bytes(const muon_ffn_args* a) {
+  return ffn_hid_bytes(a) + align_up(ffn_fwd_part_bytes(a->rows, a->cols, a->hidden));
+}
+size_t ffn_bwd_bytes(const muon_ffn_args* a) {
+  return 3 * ffn_hid_bytes(a) + align_up(ffn_bwd_part_bytes(a->rows, a->cols, a->hidden));
+}
+
 }  // namespace
 
 extern "C" {
@@ -321,6 +375,53 @@ muon_status muon_attn_bwd(const muon_attn_args* a, void* ws, size_t ws_bytes, vo
   d.part_lse = static_cast<float*>(ws);
   d.delta = reinterpret_cast<float*>(static_cast<char*>(ws) + align_up(attn_lines(d) * 4));
   return launched("muon_attn_bwd", launch_attn_bwd(static_cast<hipStream_t>(hip_stream), d));
+}
+
+muon_status muon_ffn_fwd_workspace(const muon_ffn_args* a, size_t* bytes) {
+  if (!bytes) return fail(MUON_E_ARG, "bytes is NULL");
+  CHECK(ffn_dims(a));
+  *bytes = ffn_fwd_bytes(a);
+  return MUON_OK;
+}
+
+muon_status muon_ffn_fwd(const muon_ffn_args* a, void* ws, size_t ws_bytes, void* hip_stream) {
+  CHECK(ffn_dims(a));
+  CHECK(ffn_weights(a));
+  if (a->rows == 0) return MUON_OK;
+  CHECK(ffn_mat("x", a->x, a->rows, a->cols, MUON_BF16));
+  CHECK(ffn_mat("y", a->y, a->rows, a->cols, MUON_BF16));
+  if (a->gu.ptr) CHECK(ffn_mat("gu", a->gu, a->rows, 2 * a->hidden, MUON_BF16));
+  CHECK(check_workspace(ws, ws_bytes, ffn_fwd_bytes(a)));
+  FfnDev d = ffn_dev(a);
+  d.hid = ws;
+  d.part = reinterpret_cast<float*>(static_cast<char*>(ws) + ffn_hid_bytes(a));
+  return launched("muon_ffn_fwd", launch_ffn_fwd(static_cast<hipStream_t>(hip_stream), d));
+}
+
+muon_status muon_ffn_bwd_workspace(const muon_ffn_args* a, size_t* bytes) {
+  if (!bytes) return fail(MUON_E_ARG, "bytes is NULL");
+  CHECK(ffn_dims(a));
+  *bytes = ffn_bwd_bytes(a);
+  return MUON_OK;
+}
+
+muon_status muon_ffn_bwd(const muon_ffn_args* a, void* ws, size_t ws_bytes, void* hip_stream) {
+  CHECK(ffn_dims(a));
+  CHECK(ffn_weights(a));
+  if (a->rows == 0) return fail(MUON_E_SHAPE, "no rows: the weights' gradients have none to be summed over");
+  CHECK(ffn_mat("x", a->x, a->rows, a->cols, MUON_BF16));
+  CHECK(ffn_mat("gu", a->gu, a->rows, 2 * a->hidden, MUON_BF16));
+  CHECK(ffn_mat("d_y", a->d_y, a->rows, a->cols, MUON_BF16));
+  CHECK(ffn_mat("d_x", a->d_x, a->rows, a->cols, MUON_BF16));
+  CHECK(ffn_mat("d_w_gate", a->d_w_gate, a->hidden, a->cols, -1));
+  CHECK(ffn_mat("d_w_up", a->d_w_up, a->hidden, a->cols, a->d_w_gate.dtype));
+  CHECK(ffn_mat("d_w_down", a->d_w_down, a->cols, a->hidden, a->d_w_gate.dtype));
+  CHECK(check_workspace(ws, ws_bytes, ffn_bwd_bytes(a)));
+  FfnDev d = ffn_dev(a);
+  d.hid = ws;
+  d.dgu = static_cast<char*>(ws) + ffn_hid_bytes(a);
+  d.part = reinterpret_cast<float*>(static_cast<char*>(ws) + 3 * ffn_hid_bytes(a));
+  return launched("muon_ffn_bwd", launch_ffn_bwd(static_cast<hipStream_t>(hip_stream), d));
 }
 
 }  // extern "C"

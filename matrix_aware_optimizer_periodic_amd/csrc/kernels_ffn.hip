@@ -1,0 +1,443 @@
+// Gated feed-forward block on bf16 matrix cores, forward and backward.
+//
+//   g = x Wg^T, u = x Wu^T, h = act(g) u, y = h Wd^T
+//   dh = dy Wd, dg = dh u act'(g), du = dh act(g)
+//   dx = dg Wg + du Wu, dWg = dg^T x, dWu = du^T x, dWd = dy^T h
+//
+// Five products of one kernel template.  Every product is
+// C[m][n] = sum_k A(m, k) B(n, k); an operand lies in memory either along k
+// ("rows": x, h, dy, dg | du, and the weights of the forward pass) or along
+// m / n ("cols": the weights in dh and dx, both operands of the weights'
+// gradients).  Row operands are staged as rows of 64 k values and read as
+// they are, column operands as 64 rows of the tile's width and read through
+// the transposing LDS read, so that nothing is transposed in memory.
+//
+// Fusions: one product forms g and u side by side (the B tile takes 16 rows
+// of Wg and 16 of Wu in turn, so a lane holds both for the same columns) and
+// writes h; the dh product's epilogue reads g and u and writes dg, du and h;
+// dx is one product over 2 f; the three weights' gradients are one launch.
+//
+// Bound by the matrix cores from some hundreds of rows on, by reading the
+// weights below.  Roundings to bf16: g and u as stored, h and dg, du as the
+// next product's operands, and the results.
+#include <type_traits>
+
+#include "block_mfma.h"
+
+namespace muon {
+namespace {
+
+constexpr int kStageK = 64;   // k values per LDS stage, two MFMA groups of 32
+
+// ---- activation -------------------------------------------------------------
+// SiLU g / (1 + e^-g); GELU in its tanh form, 0.5 g (1 + tanh z) = g / (1 + e^-2z)
+// with z = sqrt(2/pi) (g + 0.044715 g^3).  Both are g e for a logistic e of
+// some w(g), so the derivative is e + g e (1 - e) w'(g).
+template <int ACT>
+__device__ __forceinline__ void act_of(float g, float& a, float& da) {
+  float w = g, dw = 1.f;
+  if constexpr (ACT == 1) {
+    const float c = 1.5957691216057308f;     // 2 sqrt(2 / pi)
+    w = c * fmaf(0.044715f * g, g * g, g);
+    dw = c * fmaf(3.f * 0.044715f * g, g, 1.f);
+  }
+  const float e = 1.0f / (1.0f + __expf(-w));
+  a = g * e;
+  // 1 - e as the logistic of -w keeps its digits where e is near 1
+  da = fmaf(a * dw, 1.0f / (1.0f + __expf(w)), e);
+}
+
+// ---- products ---------------------------------------------------------------
+struct Prod {
+  const void* a;
+  const void* b;
+  const void* b2;       // EPI_GATE: Wu; two segments: the second segment's B
+  void* c;
+  void* c2;             // EPI_DGATE: h
+  const void* gu;       // EPI_DGATE
+  int64_t lda, ldb, ldb2, ldc, ldc2, ldgu;
+  int32_t m, n, k;      // k of one segment
+  int32_t mt, nt;       // tiles
+};
+struct ProdArgs {
+  Prod p[3];
+  int32_t count;
+  int32_t segments;     // 1, or 2: the sum goes on over a second k range (A's
+                        // columns k .. 2 k - 1, B in b2)
+  int32_t hidden;
+  int32_t tiles;
+};
+
+enum { EPI_BF16 = 0, EPI_F32 = 1, EPI_GATE = 2, EPI_DGATE = 3 };
+
+// One operand's side of a stage.  COLS: rows of the stage are k.
+template <int BT, bool COLS>
+struct Side {
+  static constexpr int DMA = BT * kStageK * 2 / 1024 / 4;    // per wave
+  static constexpr int BYTES = BT * kStageK * 2;
+  static constexpr int CH = BT / 8;                          // COLS: chunks per row
+  unsigned v0, v1, step;
+  const char* base;
+  int64_t kbytes;            // bytes per stage along k
+  int64_t ldbytes;
+  unsigned limit;            // rows: bytes of the rows that are there
+  int chunk;
+
+  // first: first row (column) of the tile; there: how many there are; rstep:
+  // rows between the blocks of 32 (16 where two matrices alternate).
+  __device__ __forceinline__ void init(const void* p, int64_t ld, int64_t first, int there, int wave, int lane,
+                                       bool alternate) {
+    ldbytes = ld * 2;
+    if constexpr (!COLS) {
+      base = static_cast<const char*>(p) + first * ldbytes;
+      const int row = (alternate ? 8 * (wave & 1) : 8 * wave) + (lane >> 3);   // + i * step rows
+      const int sw = (4 * (wave & 1) + (lane >> 4)) & 7;                       // (LDS row / 2) % 8
+      chunk = (lane & 7) ^ sw;
+      v0 = unsigned(row * ldbytes + chunk * 16);
+      step = unsigned((alternate ? 16 : 32) * ldbytes);
+      limit = unsigned(min(there, alternate ? BT / 2 : BT) * ldbytes);
+      kbytes = kStageK * 2;
+      v1 = 0;
+    } else {
+      base = static_cast<const char*>(p) + first * 2;
+      constexpr int RPB = 64 / CH;                       // rows per 1 KB block
+      const int row = RPB * wave + lane / CH;
+      const int sw = ((row & 3) << 2) ^ (RPB * 4 == 8 ? 0 : ((row >> 3) & 1) << 1);
+      const int c0 = (lane % CH) ^ sw, c1 = c0 ^ 2;
+      v0 = c0 * 8 < there ? unsigned(row * ldbytes + c0 * 16) : kBufNone;
+      v1 = RPB * 4 == 8 ? (c1 * 8 < there ? unsigned(row * ldbytes + c1 * 16) : kBufNone) : v0;
+      step = unsigned(4 * RPB * ldbytes);
+      kbytes = kStageK * ldbytes;
+      limit = 0;
+      chunk = 0;
+    }
+  }
+  // DMA i of the stage that starts at k0 (of a sum that ends at k).
+  __device__ __forceinline__ void issue(int i, const char* at, int left, unsigned lds, int wave) const {
+    u32x4_t r = buffer_at(at);
+    unsigned v;
+    if constexpr (!COLS) {
+      r[2] = limit;
+      v = v0 + unsigned(i) * step;
+      if (left < kStageK && chunk * 8 >= left) v = kBufNone;
+    } else {
+      r[2] = unsigned(min(int64_t(min(left, kStageK)) * ldbytes, int64_t(kBufNone)));
+      v = ((i & 1) ? v1 : v0) + unsigned(i) * step;
+    }
+    dma16(r, lds + unsigned(wave + 4 * i) * 1024u, v);
+  }
+};
+
+// Fragment reads (16 rows or columns, 32 k) of one operand.
+template <int BT, bool COLS>
+struct Frag {
+  unsigned off[COLS ? BT / 32 : 2];
+  __device__ __forceinline__ void init(int wpos, int lane) {
+    const int r = lane & 15, q = lane >> 4;
+    if constexpr (!COLS) {
+      const unsigned row = unsigned(wpos * (BT / 2) + r) * 128u;
+      const int sw = (r >> 1) & 7;
+      off[0] = row + unsigned((q ^ sw) << 4);
+      off[1] = row + unsigned(((4 + q) ^ sw) << 4);
+    } else {
+      const int row = 8 * q + (r >> 2);
+      const int sw = ((row & 3) << 2) ^ (((row >> 3) & 1) << 1);
+#pragma unroll
+      for (int f = 0; f < BT / 32; ++f) {
+        const int col = wpos * (BT / 2) + f * 16 + 4 * (lane & 3);
+        off[f] = unsigned(row * (2 * BT) + (((col >> 3) ^ sw) << 4) + ((col & 7) << 1));
+      }
+    }
+  }
+  __device__ __forceinline__ void read(u32x4_t& o, const unsigned char* s, int group, int f) const {
+    if constexpr (!COLS) {
+      o = lds_read16(s, off[group] + unsigned(f * 2048));
+    } else {
+      const u32x2_t x = lds_read_tr(s, off[f] + unsigned(group * 32 * 2 * BT));
+      const u32x2_t y = lds_read_tr(s, off[f] + unsigned((group * 32 + 4) * 2 * BT));
+      o = u32x4_t{x[0], x[1], y[0], y[1]};
+    }
+  }
+};
+
+// One BT x BT tile per workgroup of four waves, each (BT / 2) x (BT / 2).
+// Software pipeline: the fragments of one 32-deep group are in registers
+// while its MFMAs run; each fragment is refilled with the next group's as its
+// last MFMA has been issued, and the DMA of the stage after next goes out
+// between MFMAs.  A stage's buffer is refilled once its second group is in
+// registers everywhere, that is after the barrier inside that group's MFMAs,
+// which also makes the next stage visible.
+template <int BT, bool ACOLS, bool BCOLS, int EPI, int ACT>
+__global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void ffn_gemm_kernel(ProdArgs g) {
+  constexpr int F = BT / 32;                       // fragments per wave and side
+  constexpr int STAGE = 2 * BT * kStageK * 2;
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[2 * STAGE];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+
+  int item = int(xcd_item(blockIdx.x, unsigned(g.tiles)));
+  int which = 0;
+  while (which + 1 < g.count && item >= g.p[which].mt * g.p[which].nt) {
+    item -= g.p[which].mt * g.p[which].nt;
+    ++which;
+  }
+  const Prod& p = g.p[which];
+  // Bands of 8 tile rows, walked column by column, so that tiles near each
+  // other share operands in their XCD's L2.
+  const int band = item / (8 * p.nt), inb = item - band * 8 * p.nt;
+  const int bh = min(8, p.mt - band * 8);
+  const int tm = band * 8 + inb % bh, tn = inb / bh;
+  constexpr int NSTEP = EPI == EPI_GATE ? BT / 2 : BT;   // output columns of a tile
+  const int64_t m0 = int64_t(tm) * BT, n0 = int64_t(tn) * NSTEP;
+
+  Side<BT, ACOLS> sa;
+  Side<BT, BCOLS> sb;
+  sa.init(p.a, p.lda, m0, int(min(int64_t(BT), p.m - m0)), wave, lane, false);
+  // EPI_GATE: waves 0 and 1 bring rows of Wg, 2 and 3 those of Wu, which land
+  // 16 rows of each in turn.
+  sb.init(EPI == EPI_GATE && wave >= 2 ? p.b2 : p.b, EPI == EPI_GATE && wave >= 2 ? p.ldb2 : p.ldb, n0,
+          int(min(int64_t(NSTEP), p.n - n0)), wave, lane, EPI == EPI_GATE);
+  const char* b2 = static_cast<const char*>(p.b2) + (BCOLS ? n0 * 2 : n0 * p.ldb2 * 2);
+  Frag<BT, ACOLS> fa;
+  Frag<BT, BCOLS> fb;
+  fa.init(wm, lane);
+  fb.init(wn, lane);
+
+  const int per = (p.k + kStageK - 1) / kStageK, stages = per * g.segments;
+  const unsigned lds = lds_offset(smem);
+  auto issue_one = [&](int s, int i) {
+    const int seg = EPI == EPI_BF16 && BCOLS && s >= per ? 1 : 0;
+    const int ks = s - seg * per, left = p.k - ks * kStageK;
+    const unsigned at = lds + unsigned(s & 1) * STAGE;
+    if (i < sa.DMA) {
+      sa.issue(i, sa.base + ks * sa.kbytes + (ACOLS ? 0 : int64_t(seg) * p.k * 2), left, at, wave);
+    } else {
+      sb.issue(i - sa.DMA, (seg ? b2 : sb.base) + ks * sb.kbytes, left, at + Side<BT, ACOLS>::BYTES, wave);
+    }
+  };
+  constexpr int DMA = Side<BT, ACOLS>::DMA + Side<BT, BCOLS>::DMA;
+  auto issue = [&](int s) {
+#pragma unroll
+    for (int i = 0; i < DMA; ++i) issue_one(s, i);
+  };
+
+  f32x4_t acc[F][F];
+#pragma unroll
+  for (int x = 0; x < F; ++x)
+#pragma unroll
+    for (int y = 0; y < F; ++y) acc[x][y] = (f32x4_t)(0.f);
+  u32x4_t a[F], b[F];
+
+  issue(0);
+  wait_vm<0>();
+  barrier();
+  if (stages > 1) issue(1);
+#pragma unroll
+  for (int f = 0; f < F; ++f) fa.read(a[f], smem, 0, f);
+#pragma unroll
+  for (int f = 0; f < F; ++f) fb.read(b[f], smem + Side<BT, ACOLS>::BYTES, 0, f);
+
+  constexpr int NXY = F * F, HB = F / 2, PRE = 2;
+  auto group = [&](int s, auto oddv) {
+    constexpr bool ODD = decltype(oddv)::value;
+    auto mma = [&](int i) {
+      const int x = (i % (F * HB)) / HB, y = (i / (F * HB)) * HB + i % HB;
+      // operands swapped: a lane then holds four consecutive n of one m
+      acc[x][y] = mfma16(b[y], a[x], acc[x][y]);
+    };
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < PRE; ++i) mma(i);
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (ODD) {
+      wait_vm<0>();
+      barrier();
+    }
+    const unsigned char* sA = smem + ((ODD ? s + 1 : s) & 1) * STAGE;
+    const unsigned char* sB = sA + Side<BT, ACOLS>::BYTES;
+    constexpr int NG = ODD ? 0 : 1;
+    const bool more = ODD && s + 2 < stages;
+    int nd = 0;
+#pragma unroll
+    for (int i = PRE; i < NXY; ++i) {
+      mma(i);
+      const int x = (i % (F * HB)) / HB, y = (i / (F * HB)) * HB + i % HB;
+      if (ODD && nd < DMA && i % 2 == 0) {
+        if (more) issue_one(s + 2, nd);
+        ++nd;
+      }
+      if (x == F - 1) fb.read(b[y], sB, NG, y);
+      if (y == F - 1) fa.read(a[x], sA, NG, x);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (ODD) {
+#pragma unroll
+      for (int i = (NXY - PRE + 1) / 2; i < DMA; ++i)
+        if (more) issue_one(s + 2, i);
+    }
+  };
+  for (int s = 0; s < stages; ++s) {
+    group(s, std::false_type{});
+    group(s, std::true_type{});
+  }
+
+  // Epilogue, 16 rows at a time through a part of LDS of the wave's own (the
+  // stages' fragments are all in registers since the last barrier): a lane
+  // has four columns of one row per block, and takes eight consecutive
+  // columns, so that rows are read and written 16 bytes at a time.
+  constexpr int W = BT / 2, LDR = W + 4;           // the wave's columns, LDS row in floats
+  constexpr int WOUT = EPI == EPI_GATE ? W / 2 : W;   // its output columns
+  static_assert(4 * 16 * LDR * 4 <= 2 * STAGE, "epilogue rows fit");
+  float* er = reinterpret_cast<float*>(smem) + wave * 16 * LDR;
+  const int64_t ncol = n0 + wn * WOUT;
+#pragma unroll
+  for (int x = 0; x < F; ++x) {
+#pragma unroll
+    for (int y = 0; y < F; ++y) {
+      const int col = EPI == EPI_GATE ? (y >> 1) * 16 + (y & 1) * WOUT : y * 16;
+      *(MUON_LOCAL f32x4_t*)(MUON_LOCAL float*)(er + (lane & 15) * LDR + col + 4 * (lane >> 4)) = acc[x][y];
+    }
+    __builtin_amdgcn_wave_barrier();
+    const int64_t mrow = m0 + wm * W + x * 16;
+#pragma unroll 1
+    for (int j = lane; j < 16 * WOUT / 8; j += 64) {
+      const int row = j / (WOUT / 8), col = j % (WOUT / 8) * 8;
+      const int64_t m = mrow + row, n = ncol + col;
+      float v[8];
+      const MUON_LOCAL float* q = (const MUON_LOCAL float*)(er + row * LDR + col);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = q[k];
+      if (m >= p.m || n >= p.n) continue;
+      if constexpr (EPI == EPI_GATE) {
+        float u[8], h[8], d;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) u[k] = q[WOUT + k];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          act_of<ACT>(v[k], h[k], d);
+          h[k] *= u[k];
+        }
+        if (p.c2) {
+          store_vals<uint16_t, 8>(p.c2, m * p.ldc2 + n, v);
+          store_vals<uint16_t, 8>(p.c2, m * p.ldc2 + p.n + n, u);
+        }
+        store_vals<uint16_t, 8>(p.c, m * p.ldc + n, h);
+      } else if constexpr (EPI == EPI_DGATE) {
+        float gv[8], uv[8];
+        load_vals<uint16_t, 8>(p.gu, m * p.ldgu + n, gv);
+        load_vals<uint16_t, 8>(p.gu, m * p.ldgu + p.n + n, uv);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          float av, da;
+          act_of<ACT>(gv[k], av, da);
+          gv[k] = av * uv[k];
+          uv[k] *= v[k] * da;
+          v[k] *= av;
+        }
+        store_vals<uint16_t, 8>(p.c, m * p.ldc + n, uv);
+        store_vals<uint16_t, 8>(p.c, m * p.ldc + p.n + n, v);
+        store_vals<uint16_t, 8>(p.c2, m * p.ldc2 + n, gv);
+      } else if constexpr (EPI == EPI_F32) {
+        store_vals<float, 8>(p.c, m * p.ldc + n, v);
+      } else {
+        store_vals<uint16_t, 8>(p.c, m * p.ldc + n, v);
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+template <int BT, bool ACOLS, bool BCOLS, int EPI, int ACT = 0>
+hipError_t launch_prod(hipStream_t s, ProdArgs g) {
+  constexpr int NSTEP = EPI == EPI_GATE ? BT / 2 : BT;
+  g.tiles = 0;
+  for (int i = 0; i < g.count; ++i) {
+    g.p[i].mt = (g.p[i].m + BT - 1) / BT;
+    g.p[i].nt = (g.p[i].n + NSTEP - 1) / NSTEP;
+    g.tiles += g.p[i].mt * g.p[i].nt;
+  }
+  hipLaunchKernelGGL((ffn_gemm_kernel<BT, ACOLS, BCOLS, EPI, ACT>), dim3(unsigned(g.tiles)), dim3(256), 0, s, g);
+  return hipGetLastError();
+}
+
+// 256-tiles reuse a staged value twice as often as 128-tiles; they are taken
+// where they still give most of the 256 CUs a tile.
+bool big_tiles(const ProdArgs& g, int nstep) {
+  int64_t tiles = 0;
+  for (int i = 0; i < g.count; ++i) tiles += int64_t((g.p[i].m + 255) / 256) * ((g.p[i].n + nstep - 1) / nstep);
+  return tiles >= 200;
+}
+
+template <bool ACOLS, bool BCOLS, int EPI, int ACT = 0>
+hipError_t run_prod(hipStream_t s, const ProdArgs& g) {
+  return big_tiles(g, EPI == EPI_GATE ? 128 : 256) ? launch_prod<256, ACOLS, BCOLS, EPI, ACT>(s, g)
+                                                   : launch_prod<128, ACOLS, BCOLS, EPI, ACT>(s, g);
+}
+
+}  // namespace
+
+size_t ffn_fwd_part_bytes(int64_t, int64_t, int64_t) { return 0; }
+size_t ffn_bwd_part_bytes(int64_t, int64_t, int64_t) { return 0; }
+
+hipError_t launch_ffn_fwd(hipStream_t s, const FfnDev& f) {
+  const int32_t t = int32_t(f.rows), d = int32_t(f.cols), h = int32_t(f.hidden);
+  ProdArgs g{};
+  g.count = 1;
+  g.segments = 1;
+  Prod& p = g.p[0];
+  p.a = f.x; p.lda = f.ld_x;
+  p.b = f.w_gate; p.ldb = f.ld_wg; p.b2 = f.w_up; p.ldb2 = f.ld_wu;
+  p.c = f.hid; p.ldc = h; p.c2 = f.gu; p.ldc2 = f.ld_gu;
+  p.m = t; p.n = h; p.k = d;
+  hipError_t e = f.act ? run_prod<false, false, EPI_GATE, 1>(s, g) : run_prod<false, false, EPI_GATE, 0>(s, g);
+  if (e != hipSuccess) return e;
+  p = Prod{};
+  p.a = f.hid; p.lda = h;
+  p.b = f.w_down; p.ldb = f.ld_wd;
+  p.c = f.y; p.ldc = f.ld_y;
+  p.m = t; p.n = d; p.k = h;
+  return run_prod<false, false, EPI_BF16>(s, g);
+}
+
+hipError_t launch_ffn_bwd(hipStream_t s, const FfnDev& f) {
+  const int32_t t = int32_t(f.rows), d = int32_t(f.cols), h = int32_t(f.hidden);
+  ProdArgs g{};
+  g.count = 1;
+  g.segments = 1;
+  Prod& p = g.p[0];
+  p.a = f.d_y; p.lda = f.ld_dy;
+  p.b = f.w_down; p.ldb = f.ld_wd;
+  p.c = f.dgu; p.ldc = 2 * int64_t(h); p.c2 = f.hid; p.ldc2 = h;
+  p.gu = f.gu; p.ldgu = f.ld_gu;
+  p.m = t; p.n = h; p.k = d;
+  hipError_t e = f.act ? run_prod<false, true, EPI_DGATE, 1>(s, g) : run_prod<false, true, EPI_DGATE, 0>(s, g);
+  if (e != hipSuccess) return e;
+  // dx, over the k range of dg and then that of du
+  p = Prod{};
+  g.segments = 2;
+  p.a = f.dgu; p.lda = 2 * int64_t(h);
+  p.b = f.w_gate; p.ldb = f.ld_wg; p.b2 = f.w_up; p.ldb2 = f.ld_wu;
+  p.c = f.d_x; p.ldc = f.ld_dx;
+  p.m = t; p.n = d; p.k = h;
+  e = run_prod<false, true, EPI_BF16>(s, g);
+  if (e != hipSuccess) return e;
+  g = ProdArgs{};
+  g.count = 3;
+  g.segments = 1;
+  for (int i = 0; i < 2; ++i) {
+    Prod& w = g.p[i];
+    w.a = static_cast<const uint16_t*>(f.dgu) + i * int64_t(h); w.lda = 2 * int64_t(h);
+    w.b = f.x; w.ldb = f.ld_x;
+    w.c = i ? f.d_wu : f.d_wg; w.ldc = i ? f.ld_dwu : f.ld_dwg;
+    w.m = h; w.n = d; w.k = t;
+  }
+  Prod& w = g.p[2];
+  w.a = f.d_y; w.lda = f.ld_dy;
+  w.b = f.hid; w.ldb = h;
+  w.c = f.d_wd; w.ldc = f.ld_dwd;
+  w.m = d; w.n = h; w.k = t;
+  return f.grad_bf16 ? run_prod<true, true, EPI_BF16>(s, g) : run_prod<true, true, EPI_F32>(s, g);
+}
+
+}  // namespace muon

@@ -88,3 +88,9 @@ def attention(q, k, v, causal=False, offset=0, q_lens=None, k_lens=None, scale=N
             o[i, :mi, j] = p @ v[i, :ni, kj]
             lse[i, j, :mi] = torch.where(some, torch.logsumexp(s, dim=1), float("-inf"))
     return o, lse
+
+
+def act(g, kind):
+    if kind == "silu":
+        return torch.nn.functional.silu(g)
+    return torch.nn.functional.gelu(g, approximate="tanh")
