@@ -8,8 +8,8 @@
 // C[m][n] = sum_k A(m, k) B(n, k); an operand lies in memory either along k
 // ("rows": x, h, dy, dg | du, and the weights of the forward pass) or along
 // m / n ("cols": the weights in dh and dx, both operands of the weights'
-// gradients).  Row operands are staged as rows of 64 k values and read as
-// they are, column operands as 64 rows of the tile's width and read through
+// gradients).  Row operands are staged as rows of 32 k values and read as
+// they are, column operands as 32 rows of the tile's width and read through
 // the transposing LDS read, so that nothing is transposed in memory.
 //
 // Fusions: one product forms g and u side by side (the B tile takes 16 rows
@@ -27,7 +27,7 @@
 namespace muon {
 namespace {
 
-constexpr int kStageK = 64;   // k values per LDS stage, two MFMA groups of 32
+constexpr int kStageK = 32;   // k values per LDS stage: one MFMA deep
 
 // ---- activation -------------------------------------------------------------
 // SiLU g / (1 + e^-g); GELU in its tanh form, 0.5 g (1 + tanh z) = g / (1 + e^-2z)
@@ -70,12 +70,13 @@ struct ProdArgs {
 
 enum { EPI_BF16 = 0, EPI_F32 = 1, EPI_GATE = 2, EPI_DGATE = 3 };
 
-// One operand's side of a stage.  COLS: rows of the stage are k.
+// One operand's side of a stage: 32 k of BT rows (64 bytes each in LDS), or
+// COLS, BT columns of 32 rows of k (2 BT bytes each).
 template <int BT, bool COLS>
 struct Side {
-  static constexpr int DMA = BT * kStageK * 2 / 1024 / 4;    // per wave
   static constexpr int BYTES = BT * kStageK * 2;
-  static constexpr int CH = BT / 8;                          // COLS: chunks per row
+  static constexpr int DMA = BYTES / 1024 / 4;               // per wave and stage
+  static constexpr int CH = BT / 8;                          // COLS: 16-byte chunks per row
   unsigned v0, v1, step;
   const char* base;
   int64_t kbytes;            // bytes per stage along k
@@ -83,18 +84,18 @@ struct Side {
   unsigned limit;            // rows: bytes of the rows that are there
   int chunk;
 
-  // first: first row (column) of the tile; there: how many there are; rstep:
-  // rows between the blocks of 32 (16 where two matrices alternate).
+  // first: first row (column) of the tile; there: how many there are;
+  // alternate: every other block of 16 LDS rows is another matrix's (waves 0
+  // and 2 bring one, 1 and 3 the other).
   __device__ __forceinline__ void init(const void* p, int64_t ld, int64_t first, int there, int wave, int lane,
                                        bool alternate) {
     ldbytes = ld * 2;
     if constexpr (!COLS) {
       base = static_cast<const char*>(p) + first * ldbytes;
-      const int row = (alternate ? 8 * (wave & 1) : 8 * wave) + (lane >> 3);   // + i * step rows
-      const int sw = (4 * (wave & 1) + (lane >> 4)) & 7;                       // (LDS row / 2) % 8
-      chunk = (lane & 7) ^ sw;
+      const int row = (alternate ? 16 * (wave >> 1) : 16 * wave) + (lane >> 2);   // + i * step rows
+      chunk = (lane & 3) ^ ((lane >> 3) & 3);                                     // swizzle (row / 2) % 4
       v0 = unsigned(row * ldbytes + chunk * 16);
-      step = unsigned((alternate ? 16 : 32) * ldbytes);
+      step = unsigned((alternate ? 32 : 64) * ldbytes);
       limit = unsigned(min(there, alternate ? BT / 2 : BT) * ldbytes);
       kbytes = kStageK * 2;
       v1 = 0;
@@ -112,7 +113,7 @@ struct Side {
       chunk = 0;
     }
   }
-  // DMA i of the stage that starts at k0 (of a sum that ends at k).
+  // DMA i of a stage that starts at `at` and has `left` k to go.
   __device__ __forceinline__ void issue(int i, const char* at, int left, unsigned lds, int wave) const {
     u32x4_t r = buffer_at(at);
     unsigned v;
@@ -131,14 +132,11 @@ struct Side {
 // Fragment reads (16 rows or columns, 32 k) of one operand.
 template <int BT, bool COLS>
 struct Frag {
-  unsigned off[COLS ? BT / 32 : 2];
+  unsigned off[COLS ? BT / 32 : 1];
   __device__ __forceinline__ void init(int wpos, int lane) {
     const int r = lane & 15, q = lane >> 4;
     if constexpr (!COLS) {
-      const unsigned row = unsigned(wpos * (BT / 2) + r) * 128u;
-      const int sw = (r >> 1) & 7;
-      off[0] = row + unsigned((q ^ sw) << 4);
-      off[1] = row + unsigned(((4 + q) ^ sw) << 4);
+      off[0] = unsigned((wpos * (BT / 2) + r) * 64 + ((q ^ ((r >> 1) & 3)) << 4));
     } else {
       const int row = 8 * q + (r >> 2);
       const int sw = ((row & 3) << 2) ^ (((row >> 3) & 1) << 1);
@@ -149,29 +147,30 @@ struct Frag {
       }
     }
   }
-  __device__ __forceinline__ void read(u32x4_t& o, const unsigned char* s, int group, int f) const {
+  __device__ __forceinline__ void read(u32x4_t& o, const unsigned char* s, int f) const {
     if constexpr (!COLS) {
-      o = lds_read16(s, off[group] + unsigned(f * 2048));
+      o = lds_read16(s, off[0] + unsigned(f * 1024));
     } else {
-      const u32x2_t x = lds_read_tr(s, off[f] + unsigned(group * 32 * 2 * BT));
-      const u32x2_t y = lds_read_tr(s, off[f] + unsigned((group * 32 + 4) * 2 * BT));
+      const u32x2_t x = lds_read_tr(s, off[f]);
+      const u32x2_t y = lds_read_tr(s, off[f] + unsigned(4 * 2 * BT));
       o = u32x4_t{x[0], x[1], y[0], y[1]};
     }
   }
 };
 
 // One BT x BT tile per workgroup of four waves, each (BT / 2) x (BT / 2).
-// Software pipeline: the fragments of one 32-deep group are in registers
-// while its MFMAs run; each fragment is refilled with the next group's as its
-// last MFMA has been issued, and the DMA of the stage after next goes out
-// between MFMAs.  A stage's buffer is refilled once its second group is in
-// registers everywhere, that is after the barrier inside that group's MFMAs,
-// which also makes the next stage visible.
+// Software pipeline over a ring of stages: the fragments of one stage are in
+// registers while its MFMAs run; each fragment is refilled with the next
+// stage's once its last MFMA has been issued, and the DMA of the stage
+// NSTAGE - 1 ahead goes out between MFMAs.  The barrier, behind the first two
+// MFMAs of a stage, makes the next stage visible and says that the previous
+// one's buffer is free (its fragments are in registers everywhere).
 template <int BT, bool ACOLS, bool BCOLS, int EPI, int ACT>
 __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void ffn_gemm_kernel(ProdArgs g) {
   constexpr int F = BT / 32;                       // fragments per wave and side
   constexpr int STAGE = 2 * BT * kStageK * 2;
-  __shared__ __attribute__((aligned(1024))) unsigned char smem[2 * STAGE];
+  constexpr int NSTAGE = BT == 256 ? 4 : 5;        // 128 KB, or 80 KB for two workgroups per CU
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[NSTAGE * STAGE];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1;
@@ -194,9 +193,9 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void ffn_gemm_kernel(ProdAr
   Side<BT, ACOLS> sa;
   Side<BT, BCOLS> sb;
   sa.init(p.a, p.lda, m0, int(min(int64_t(BT), p.m - m0)), wave, lane, false);
-  // EPI_GATE: waves 0 and 1 bring rows of Wg, 2 and 3 those of Wu, which land
+  // EPI_GATE: waves 0 and 2 bring rows of Wg, 1 and 3 those of Wu, which land
   // 16 rows of each in turn.
-  sb.init(EPI == EPI_GATE && wave >= 2 ? p.b2 : p.b, EPI == EPI_GATE && wave >= 2 ? p.ldb2 : p.ldb, n0,
+  sb.init(EPI == EPI_GATE && (wave & 1) ? p.b2 : p.b, EPI == EPI_GATE && (wave & 1) ? p.ldb2 : p.ldb, n0,
           int(min(int64_t(NSTEP), p.n - n0)), wave, lane, EPI == EPI_GATE);
   const char* b2 = static_cast<const char*>(p.b2) + (BCOLS ? n0 * 2 : n0 * p.ldb2 * 2);
   Frag<BT, ACOLS> fa;
@@ -206,10 +205,13 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void ffn_gemm_kernel(ProdAr
 
   const int per = (p.k + kStageK - 1) / kStageK, stages = per * g.segments;
   const unsigned lds = lds_offset(smem);
+  // Stages past the end are issued as a reload of the last one, so that every
+  // stage waits for the same number of DMAs; nothing reads them.
   auto issue_one = [&](int s, int i) {
-    const int seg = EPI == EPI_BF16 && BCOLS && s >= per ? 1 : 0;
-    const int ks = s - seg * per, left = p.k - ks * kStageK;
-    const unsigned at = lds + unsigned(s & 1) * STAGE;
+    const int sc = min(s, stages - 1);
+    const int seg = EPI == EPI_BF16 && BCOLS && sc >= per ? 1 : 0;
+    const int ks = sc - seg * per, left = p.k - ks * kStageK;
+    const unsigned at = lds + unsigned(s % NSTAGE) * STAGE;
     if (i < sa.DMA) {
       sa.issue(i, sa.base + ks * sa.kbytes + (ACOLS ? 0 : int64_t(seg) * p.k * 2), left, at, wave);
     } else {
@@ -217,10 +219,6 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void ffn_gemm_kernel(ProdAr
     }
   };
   constexpr int DMA = Side<BT, ACOLS>::DMA + Side<BT, BCOLS>::DMA;
-  auto issue = [&](int s) {
-#pragma unroll
-    for (int i = 0; i < DMA; ++i) issue_one(s, i);
-  };
 
   f32x4_t acc[F][F];
 #pragma unroll
@@ -229,18 +227,18 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void ffn_gemm_kernel(ProdAr
     for (int y = 0; y < F; ++y) acc[x][y] = (f32x4_t)(0.f);
   u32x4_t a[F], b[F];
 
-  issue(0);
-  wait_vm<0>();
+  for (int s = 0; s < NSTAGE - 1; ++s)
+#pragma unroll
+    for (int i = 0; i < DMA; ++i) issue_one(s, i);
+  wait_vm<(NSTAGE - 2) * DMA>();
   barrier();
-  if (stages > 1) issue(1);
 #pragma unroll
-  for (int f = 0; f < F; ++f) fa.read(a[f], smem, 0, f);
+  for (int f = 0; f < F; ++f) fa.read(a[f], smem, f);
 #pragma unroll
-  for (int f = 0; f < F; ++f) fb.read(b[f], smem + Side<BT, ACOLS>::BYTES, 0, f);
+  for (int f = 0; f < F; ++f) fb.read(b[f], smem + Side<BT, ACOLS>::BYTES, f);
 
   constexpr int NXY = F * F, HB = F / 2, PRE = 2;
-  auto group = [&](int s, auto oddv) {
-    constexpr bool ODD = decltype(oddv)::value;
+  for (int s = 0; s < stages; ++s) {
     auto mma = [&](int i) {
       const int x = (i % (F * HB)) / HB, y = (i / (F * HB)) * HB + i % HB;
       // operands swapped: a lane then holds four consecutive n of one m
@@ -250,45 +248,32 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void ffn_gemm_kernel(ProdAr
 #pragma unroll
     for (int i = 0; i < PRE; ++i) mma(i);
     __builtin_amdgcn_sched_barrier(0);
-    if constexpr (ODD) {
-      wait_vm<0>();
-      barrier();
-    }
-    const unsigned char* sA = smem + ((ODD ? s + 1 : s) & 1) * STAGE;
+    wait_vm<(NSTAGE - 3) * DMA>();
+    barrier();
+    const unsigned char* sA = smem + ((s + 1) % NSTAGE) * STAGE;
     const unsigned char* sB = sA + Side<BT, ACOLS>::BYTES;
-    constexpr int NG = ODD ? 0 : 1;
-    const bool more = ODD && s + 2 < stages;
     int nd = 0;
 #pragma unroll
     for (int i = PRE; i < NXY; ++i) {
       mma(i);
       const int x = (i % (F * HB)) / HB, y = (i / (F * HB)) * HB + i % HB;
-      if (ODD && nd < DMA && i % 2 == 0) {
-        if (more) issue_one(s + 2, nd);
-        ++nd;
-      }
-      if (x == F - 1) fb.read(b[y], sB, NG, y);
-      if (y == F - 1) fa.read(a[x], sA, NG, x);
+      if (nd < DMA && i % 2 == 0) issue_one(s + NSTAGE - 1, nd++);
+      if (x == F - 1) fb.read(b[y], sB, y);
+      if (y == F - 1) fa.read(a[x], sA, x);
       __builtin_amdgcn_sched_barrier(0);
     }
-    if constexpr (ODD) {
-#pragma unroll
-      for (int i = (NXY - PRE + 1) / 2; i < DMA; ++i)
-        if (more) issue_one(s + 2, i);
-    }
-  };
-  for (int s = 0; s < stages; ++s) {
-    group(s, std::false_type{});
-    group(s, std::true_type{});
+    static_assert(DMA <= (NXY - PRE) / 2, "a slot for every DMA");
   }
+  // The reloads of the last stage may still be on their way into LDS.
+  wait_vm<0>();
+  barrier();
 
-  // Epilogue, 16 rows at a time through a part of LDS of the wave's own (the
-  // stages' fragments are all in registers since the last barrier): a lane
+  // Epilogue, 16 rows at a time through a part of LDS of the wave's own: a lane
   // has four columns of one row per block, and takes eight consecutive
   // columns, so that rows are read and written 16 bytes at a time.
   constexpr int W = BT / 2, LDR = W + 4;           // the wave's columns, LDS row in floats
   constexpr int WOUT = EPI == EPI_GATE ? W / 2 : W;   // its output columns
-  static_assert(4 * 16 * LDR * 4 <= 2 * STAGE, "epilogue rows fit");
+  static_assert(4 * 16 * LDR * 4 <= NSTAGE * STAGE, "epilogue rows fit");
   float* er = reinterpret_cast<float*>(smem) + wave * 16 * LDR;
   const int64_t ncol = n0 + wn * WOUT;
 #pragma unroll
