@@ -64,8 +64,11 @@ struct ProdArgs {
   int32_t count;
   int32_t segments;     // 1, or 2: the sum goes on over a second k range (A's
                         // columns k .. 2 k - 1, B in b2)
-  int32_t hidden;
-  int32_t tiles;
+  // The first `full` tiles are one workgroup each; the others' sums are cut
+  // into `splits` ranges of split_stages stages, a workgroup each, whose fp32
+  // results go to part and are added by a second kernel.
+  int32_t full, splits, split_stages;
+  float* part;
 };
 
 enum { EPI_BF16 = 0, EPI_F32 = 1, EPI_GATE = 2, EPI_DGATE = 3 };
@@ -158,6 +161,88 @@ struct Frag {
   }
 };
 
+// Tile `item` of the list: its product and place.  Bands of 8 tile rows,
+// walked column by column, so that tiles near each other share operands in
+// their XCD's L2.
+struct Tile { int which, tm, tn; };
+__device__ __forceinline__ Tile tile_of(const ProdArgs& g, int item) {
+  int which = 0;
+  while (which + 1 < g.count && item >= g.p[which].mt * g.p[which].nt) {
+    item -= g.p[which].mt * g.p[which].nt;
+    ++which;
+  }
+  const Prod& p = g.p[which];
+  const int band = item / (8 * p.nt), inb = item - band * 8 * p.nt;
+  const int bh = min(8, p.mt - band * 8);
+  return Tile{which, band * 8 + inb % bh, inb / bh};
+}
+
+// Output columns of a tile.
+template <int BT, int EPI>
+constexpr int tile_cols() { return EPI == EPI_GATE ? BT / 2 : BT; }
+
+// 16 rows of a wave's part of a tile, from its accumulators (a lane has four
+// columns of one row per block) through a part of LDS of the wave's own: a
+// lane then takes eight consecutive columns, so that rows are read and
+// written 16 bytes at a time.
+template <int BT, int EPI, int ACT>
+__device__ __forceinline__ void emit_rows(const Prod& p, const f32x4_t (&acc)[BT / 32], float* er, int64_t mrow,
+                                          int64_t ncol, int lane) {
+  constexpr int F = BT / 32, W = BT / 2, LDR = W + 4;
+  constexpr int WOUT = tile_cols<BT, EPI>() / 2;
+#pragma unroll
+  for (int y = 0; y < F; ++y) {
+    const int col = EPI == EPI_GATE ? (y >> 1) * 16 + (y & 1) * WOUT : y * 16;
+    *(MUON_LOCAL f32x4_t*)(MUON_LOCAL float*)(er + (lane & 15) * LDR + col + 4 * (lane >> 4)) = acc[y];
+  }
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+  for (int j = lane; j < 16 * WOUT / 8; j += 64) {
+    const int row = j / (WOUT / 8), col = j % (WOUT / 8) * 8;
+    const int64_t m = mrow + row, n = ncol + col;
+    float v[8];
+    const MUON_LOCAL float* q = (const MUON_LOCAL float*)(er + row * LDR + col);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = q[k];
+    if (m >= p.m || n >= p.n) continue;
+    if constexpr (EPI == EPI_GATE) {
+      float u[8], h[8], d;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) u[k] = q[WOUT + k];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        act_of<ACT>(v[k], h[k], d);
+        h[k] *= u[k];
+      }
+      if (p.c2) {
+        store_vals<uint16_t, 8>(p.c2, m * p.ldc2 + n, v);
+        store_vals<uint16_t, 8>(p.c2, m * p.ldc2 + p.n + n, u);
+      }
+      store_vals<uint16_t, 8>(p.c, m * p.ldc + n, h);
+    } else if constexpr (EPI == EPI_DGATE) {
+      float gv[8], uv[8];
+      load_vals<uint16_t, 8>(p.gu, m * p.ldgu + n, gv);
+      load_vals<uint16_t, 8>(p.gu, m * p.ldgu + p.n + n, uv);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        float av, da;
+        act_of<ACT>(gv[k], av, da);
+        gv[k] = av * uv[k];
+        uv[k] *= v[k] * da;
+        v[k] *= av;
+      }
+      store_vals<uint16_t, 8>(p.c, m * p.ldc + n, uv);
+      store_vals<uint16_t, 8>(p.c, m * p.ldc + p.n + n, v);
+      store_vals<uint16_t, 8>(p.c2, m * p.ldc2 + n, gv);
+    } else if constexpr (EPI == EPI_F32) {
+      store_vals<float, 8>(p.c, m * p.ldc + n, v);
+    } else {
+      store_vals<uint16_t, 8>(p.c, m * p.ldc + n, v);
+    }
+  }
+  __builtin_amdgcn_wave_barrier();
+}
+
 // One BT x BT tile per workgroup of four waves, each (BT / 2) x (BT / 2).
 // Software pipeline over a ring of stages: the fragments of one stage are in
 // registers while its MFMAs run; each fragment is refilled with the next
@@ -175,20 +260,19 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void ffn_gemm_kernel(ProdAr
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1;
 
-  int item = int(xcd_item(blockIdx.x, unsigned(g.tiles)));
-  int which = 0;
-  while (which + 1 < g.count && item >= g.p[which].mt * g.p[which].nt) {
-    item -= g.p[which].mt * g.p[which].nt;
-    ++which;
+  // Whole tiles first, then the ranges of the split ones.
+  const int id = int(blockIdx.x);
+  int item, range = -1;
+  if (id < g.full) {
+    item = int(xcd_item(unsigned(id), unsigned(g.full)));
+  } else {
+    range = int(xcd_item(unsigned(id - g.full), gridDim.x - unsigned(g.full)));
+    item = g.full + range / g.splits;
   }
-  const Prod& p = g.p[which];
-  // Bands of 8 tile rows, walked column by column, so that tiles near each
-  // other share operands in their XCD's L2.
-  const int band = item / (8 * p.nt), inb = item - band * 8 * p.nt;
-  const int bh = min(8, p.mt - band * 8);
-  const int tm = band * 8 + inb % bh, tn = inb / bh;
-  constexpr int NSTEP = EPI == EPI_GATE ? BT / 2 : BT;   // output columns of a tile
-  const int64_t m0 = int64_t(tm) * BT, n0 = int64_t(tn) * NSTEP;
+  const Tile tile = tile_of(g, item);
+  const Prod& p = g.p[tile.which];
+  constexpr int NSTEP = tile_cols<BT, EPI>();
+  const int64_t m0 = int64_t(tile.tm) * BT, n0 = int64_t(tile.tn) * NSTEP;
 
   Side<BT, ACOLS> sa;
   Side<BT, BCOLS> sb;
@@ -203,12 +287,14 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void ffn_gemm_kernel(ProdAr
   fa.init(wm, lane);
   fb.init(wn, lane);
 
-  const int per = (p.k + kStageK - 1) / kStageK, stages = per * g.segments;
+  const int per = (p.k + kStageK - 1) / kStageK, all = per * g.segments;
+  const int first = range < 0 ? 0 : range % g.splits * g.split_stages;
+  const int stages = range < 0 ? all : max(0, min(all - first, g.split_stages));
   const unsigned lds = lds_offset(smem);
   // Stages past the end are issued as a reload of the last one, so that every
   // stage waits for the same number of DMAs; nothing reads them.
   auto issue_one = [&](int s, int i) {
-    const int sc = min(s, stages - 1);
+    const int sc = first + min(s, stages - 1);
     const int seg = EPI == EPI_BF16 && BCOLS && sc >= per ? 1 : 0;
     const int ks = sc - seg * per, left = p.k - ks * kStageK;
     const unsigned at = lds + unsigned(s % NSTAGE) * STAGE;
@@ -268,108 +354,157 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void ffn_gemm_kernel(ProdAr
   wait_vm<0>();
   barrier();
 
-  // Epilogue, 16 rows at a time through a part of LDS of the wave's own: a lane
-  // has four columns of one row per block, and takes eight consecutive
-  // columns, so that rows are read and written 16 bytes at a time.
-  constexpr int W = BT / 2, LDR = W + 4;           // the wave's columns, LDS row in floats
-  constexpr int WOUT = EPI == EPI_GATE ? W / 2 : W;   // its output columns
-  static_assert(4 * 16 * LDR * 4 <= NSTAGE * STAGE, "epilogue rows fit");
-  float* er = reinterpret_cast<float*>(smem) + wave * 16 * LDR;
-  const int64_t ncol = n0 + wn * WOUT;
+  if (range >= 0) {
+    float* o = g.part + (int64_t(range) * 4 + wave) * (F * F * 256) + lane * 4;
 #pragma unroll
-  for (int x = 0; x < F; ++x) {
+    for (int x = 0; x < F; ++x)
 #pragma unroll
-    for (int y = 0; y < F; ++y) {
-      const int col = EPI == EPI_GATE ? (y >> 1) * 16 + (y & 1) * WOUT : y * 16;
-      *(MUON_LOCAL f32x4_t*)(MUON_LOCAL float*)(er + (lane & 15) * LDR + col + 4 * (lane >> 4)) = acc[x][y];
-    }
-    __builtin_amdgcn_wave_barrier();
-    const int64_t mrow = m0 + wm * W + x * 16;
-#pragma unroll 1
-    for (int j = lane; j < 16 * WOUT / 8; j += 64) {
-      const int row = j / (WOUT / 8), col = j % (WOUT / 8) * 8;
-      const int64_t m = mrow + row, n = ncol + col;
-      float v[8];
-      const MUON_LOCAL float* q = (const MUON_LOCAL float*)(er + row * LDR + col);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = q[k];
-      if (m >= p.m || n >= p.n) continue;
-      if constexpr (EPI == EPI_GATE) {
-        float u[8], h[8], d;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) u[k] = q[WOUT + k];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          act_of<ACT>(v[k], h[k], d);
-          h[k] *= u[k];
-        }
-        if (p.c2) {
-          store_vals<uint16_t, 8>(p.c2, m * p.ldc2 + n, v);
-          store_vals<uint16_t, 8>(p.c2, m * p.ldc2 + p.n + n, u);
-        }
-        store_vals<uint16_t, 8>(p.c, m * p.ldc + n, h);
-      } else if constexpr (EPI == EPI_DGATE) {
-        float gv[8], uv[8];
-        load_vals<uint16_t, 8>(p.gu, m * p.ldgu + n, gv);
-        load_vals<uint16_t, 8>(p.gu, m * p.ldgu + p.n + n, uv);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          float av, da;
-          act_of<ACT>(gv[k], av, da);
-          gv[k] = av * uv[k];
-          uv[k] *= v[k] * da;
-          v[k] *= av;
-        }
-        store_vals<uint16_t, 8>(p.c, m * p.ldc + n, uv);
-        store_vals<uint16_t, 8>(p.c, m * p.ldc + p.n + n, v);
-        store_vals<uint16_t, 8>(p.c2, m * p.ldc2 + n, gv);
-      } else if constexpr (EPI == EPI_F32) {
-        store_vals<float, 8>(p.c, m * p.ldc + n, v);
-      } else {
-        store_vals<uint16_t, 8>(p.c, m * p.ldc + n, v);
-      }
-    }
-    __builtin_amdgcn_wave_barrier();
+      for (int y = 0; y < F; ++y) *as_global(reinterpret_cast<f32x4_t*>(o + (x * F + y) * 256)) = acc[x][y];
+    return;
   }
+  static_assert(4 * 16 * (BT / 2 + 4) * 4 <= NSTAGE * STAGE, "epilogue rows fit");
+  float* er = reinterpret_cast<float*>(smem) + wave * 16 * (BT / 2 + 4);
+#pragma unroll
+  for (int x = 0; x < F; ++x)
+    emit_rows<BT, EPI, ACT>(p, acc[x], er, m0 + wm * (BT / 2) + x * 16, n0 + wn * (NSTEP / 2), lane);
 }
 
-template <int BT, bool ACOLS, bool BCOLS, int EPI, int ACT = 0>
-hipError_t launch_prod(hipStream_t s, ProdArgs g) {
-  constexpr int NSTEP = EPI == EPI_GATE ? BT / 2 : BT;
-  g.tiles = 0;
+// Adds the ranges of one split tile, 16 rows of each wave's part per
+// workgroup, and finishes them as the product's own epilogue would.
+template <int BT, int EPI, int ACT>
+__global__ __launch_bounds__(256) void ffn_join_kernel(ProdArgs g) {
+  constexpr int F = BT / 32;
+  __shared__ float rows[4 * 16 * (BT / 2 + 4)];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tile = blockIdx.x / F, x = blockIdx.x % F;
+  const Tile t = tile_of(g, g.full + tile);
+  const Prod& p = g.p[t.which];
+  f32x4_t acc[F];
+#pragma unroll
+  for (int y = 0; y < F; ++y) acc[y] = (f32x4_t)(0.f);
+#pragma unroll 4
+  for (int i = 0; i < g.splits; ++i) {
+    const float* o = g.part + (int64_t(tile * g.splits + i) * 4 + wave) * (F * F * 256) + lane * 4;
+#pragma unroll
+    for (int y = 0; y < F; ++y) acc[y] += *as_global(reinterpret_cast<const f32x4_t*>(o + (x * F + y) * 256));
+  }
+  emit_rows<BT, EPI, ACT>(p, acc, rows + wave * 16 * (BT / 2 + 4),
+                          int64_t(t.tm) * BT + (wave >> 1) * (BT / 2) + x * 16,
+                          int64_t(t.tn) * tile_cols<BT, EPI>() + (wave & 1) * (tile_cols<BT, EPI>() / 2), lane);
+}
+
+
+// How a list of products is run.  A workgroup of a 256-tile takes a CU, of
+// 128-tiles two fit.  Tiles beyond the last whole round over the CUs would
+// leave most of them idle; their sums over k are divided so that they fill
+// one more, shorter round.
+struct Plan {
+  int bt, tiles, full, splits, split_stages;
+  double time;              // in stages of a 256-tile
+};
+Plan plan_with(const ProdArgs& g, int bt, bool gate) {
+  Plan q{};
+  q.bt = bt;
+  const int nstep = gate ? bt / 2 : bt, slots = bt == 256 ? 256 : 512;
+  int stages = 0;
+  for (int i = 0; i < g.count; ++i) {
+    q.tiles += ((g.p[i].m + bt - 1) / bt) * ((g.p[i].n + nstep - 1) / nstep);
+    const int st = (g.p[i].k + kStageK - 1) / kStageK * g.segments;
+    stages = st > stages ? st : stages;
+  }
+  const int rem = q.tiles % slots;
+  q.full = q.tiles;
+  q.splits = 1;
+  q.split_stages = stages;
+  double rounds = (q.tiles + slots - 1) / slots;
+  if (rem > 0) {
+    // ranges of 8 stages at least: a range costs its pipeline's start, the
+    // writing of its tile in fp32 and the reading back
+    int n = slots / rem;
+    if (n > stages / 8) n = stages / 8;
+    if (n > 1) {
+      q.split_stages = (stages + n - 1) / n;
+      q.splits = (stages + q.split_stages - 1) / q.split_stages;
+      q.full = q.tiles - rem;
+      rounds = q.full / slots + (double(q.split_stages) + 16.0) / stages;
+    }
+  }
+  // Two 128-tiles of a CU do half the work of a 256-tile in about 0.65 of its
+  // time (measured on long sums).
+  q.time = rounds * (stages + 12) * (bt == 256 ? 1.0 : 0.65);
+  return q;
+}
+Plan plan_of(const ProdArgs& g, bool gate) {
+  const Plan big = plan_with(g, 256, gate), small = plan_with(g, 128, gate);
+  return big.time <= small.time ? big : small;
+}
+size_t part_bytes(const Plan& q) {
+  return q.full == q.tiles ? 0 : size_t(q.tiles - q.full) * q.splits * q.bt * q.bt * 4;
+}
+
+template <int BT, bool ACOLS, bool BCOLS, int EPI, int ACT>
+hipError_t launch_prod(hipStream_t s, ProdArgs g, const Plan& q) {
+  constexpr int NSTEP = tile_cols<BT, EPI>();
   for (int i = 0; i < g.count; ++i) {
     g.p[i].mt = (g.p[i].m + BT - 1) / BT;
     g.p[i].nt = (g.p[i].n + NSTEP - 1) / NSTEP;
-    g.tiles += g.p[i].mt * g.p[i].nt;
   }
-  hipLaunchKernelGGL((ffn_gemm_kernel<BT, ACOLS, BCOLS, EPI, ACT>), dim3(unsigned(g.tiles)), dim3(256), 0, s, g);
+  g.full = q.full;
+  g.splits = q.splits;
+  g.split_stages = q.split_stages;
+  const int rem = q.tiles - q.full;
+  hipLaunchKernelGGL((ffn_gemm_kernel<BT, ACOLS, BCOLS, EPI, ACT>), dim3(unsigned(q.full + rem * q.splits)), dim3(256),
+                     0, s, g);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || rem == 0) return e;
+  hipLaunchKernelGGL((ffn_join_kernel<BT, EPI, ACT>), dim3(unsigned(rem * (BT / 32))), dim3(256), 0, s, g);
   return hipGetLastError();
-}
-
-// 256-tiles reuse a staged value twice as often as 128-tiles; they are taken
-// where they still give most of the 256 CUs a tile.
-bool big_tiles(const ProdArgs& g, int nstep) {
-  int64_t tiles = 0;
-  for (int i = 0; i < g.count; ++i) tiles += int64_t((g.p[i].m + 255) / 256) * ((g.p[i].n + nstep - 1) / nstep);
-  return tiles >= 200;
 }
 
 template <bool ACOLS, bool BCOLS, int EPI, int ACT = 0>
 hipError_t run_prod(hipStream_t s, const ProdArgs& g) {
-  return big_tiles(g, EPI == EPI_GATE ? 128 : 256) ? launch_prod<256, ACOLS, BCOLS, EPI, ACT>(s, g)
-                                                   : launch_prod<128, ACOLS, BCOLS, EPI, ACT>(s, g);
+  const Plan q = plan_of(g, EPI == EPI_GATE);
+  return q.bt == 256 ? launch_prod<256, ACOLS, BCOLS, EPI, ACT>(s, g, q)
+                     : launch_prod<128, ACOLS, BCOLS, EPI, ACT>(s, g, q);
+}
+
+// Sizes of the products, for the workspace.
+ProdArgs sizes(int64_t m, int64_t n, int64_t k, int segments) {
+  ProdArgs g{};
+  g.count = 1;
+  g.segments = segments;
+  g.p[0].m = int32_t(m); g.p[0].n = int32_t(n); g.p[0].k = int32_t(k);
+  return g;
+}
+ProdArgs weight_sizes(int64_t t, int64_t d, int64_t h) {
+  ProdArgs g = sizes(h, d, t, 1);
+  g.count = 3;
+  g.p[1] = g.p[2] = g.p[0];
+  g.p[2].m = int32_t(d); g.p[2].n = int32_t(h);
+  return g;
 }
 
 }  // namespace
 
-size_t ffn_fwd_part_bytes(int64_t, int64_t, int64_t) { return 0; }
-size_t ffn_bwd_part_bytes(int64_t, int64_t, int64_t) { return 0; }
+size_t ffn_fwd_part_bytes(int64_t t, int64_t d, int64_t h) {
+  if (t == 0) return 0;
+  const size_t a = part_bytes(plan_of(sizes(t, h, d, 1), true)), b = part_bytes(plan_of(sizes(t, d, h, 1), false));
+  return a > b ? a : b;
+}
+size_t ffn_bwd_part_bytes(int64_t t, int64_t d, int64_t h) {
+  if (t == 0) return 0;
+  const size_t a = part_bytes(plan_of(sizes(t, h, d, 1), false)), b = part_bytes(plan_of(sizes(t, d, h, 2), false));
+  const size_t c = part_bytes(plan_of(weight_sizes(t, d, h), false));
+  return a > b ? (a > c ? a : c) : (b > c ? b : c);
+}
 
 hipError_t launch_ffn_fwd(hipStream_t s, const FfnDev& f) {
   const int32_t t = int32_t(f.rows), d = int32_t(f.cols), h = int32_t(f.hidden);
   ProdArgs g{};
   g.count = 1;
   g.segments = 1;
+  g.part = f.part;
   Prod& p = g.p[0];
   p.a = f.x; p.lda = f.ld_x;
   p.b = f.w_gate; p.ldb = f.ld_wg; p.b2 = f.w_up; p.ldb2 = f.ld_wu;
@@ -390,6 +525,7 @@ hipError_t launch_ffn_bwd(hipStream_t s, const FfnDev& f) {
   ProdArgs g{};
   g.count = 1;
   g.segments = 1;
+  g.part = f.part;
   Prod& p = g.p[0];
   p.a = f.d_y; p.lda = f.ld_dy;
   p.b = f.w_down; p.ldb = f.ld_wd;
@@ -410,6 +546,7 @@ hipError_t launch_ffn_bwd(hipStream_t s, const FfnDev& f) {
   g = ProdArgs{};
   g.count = 3;
   g.segments = 1;
+  g.part = f.part;
   for (int i = 0; i < 2; ++i) {
     Prod& w = g.p[i];
     w.a = static_cast<const uint16_t*>(f.dgu) + i * int64_t(h); w.lda = 2 * int64_t(h);
