@@ -45,7 +45,6 @@ struct Geo {
   static constexpr int PITCH = DB <= 2 ? 8 : 16;
   static constexpr int ROWB = PITCH * 16;           // bytes of a row
   static constexpr int TILEB = kTile * ROWB;
-  static constexpr int DMA = TILEB / 1024 / 4;      // per wave and tile
   static __device__ __forceinline__ int swz(int row) {
     return PITCH == 16 ? ((row & 3) << 2) | ((row >> 2) & 3) : (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
   }
@@ -53,27 +52,26 @@ struct Geo {
 
 // Moves one tile of kTile rows, `stride` values apart, into LDS.  What is past
 // `there` rows or past dim values reads as zero.
-template <int DB>
+template <int DB, int WAVES = 4>
 struct TileMove {
-  unsigned voff[Geo<DB>::DMA];
+  static constexpr int P = Geo<DB>::PITCH;
+  static constexpr int STEP = WAVES * (64 / P);       // rows between a wave's DMAs
+  static constexpr int N = kTile / STEP;
+  static_assert(STEP % 16 == 0, "a lane's swizzle is the same in all of its rows");
+  unsigned voff;
   int row0;
-  int chunk;
-  bool dim_ok;
+  int64_t step;
   __device__ __forceinline__ TileMove(int64_t stride, int dim, int wave, int lane) {
-    constexpr int P = Geo<DB>::PITCH;
     row0 = wave * (64 / P) + lane / P;
-    chunk = (lane % P) ^ Geo<DB>::swz(row0);
-    dim_ok = chunk * 8 < dim;
-#pragma unroll
-    for (int i = 0; i < Geo<DB>::DMA; ++i)
-      voff[i] = dim_ok ? unsigned(int64_t(row0 + i * (256 / P)) * stride * 2 + chunk * 16) : kBufNone;
+    const int chunk = (lane % P) ^ Geo<DB>::swz(row0);
+    voff = chunk * 8 < dim ? unsigned(int64_t(row0) * stride * 2 + chunk * 16) : kBufNone;
+    step = STEP * stride;
   }
   __device__ __forceinline__ void issue(const uint16_t* tile, int there, unsigned lds, int wave) const {
-    const u32x4_t r = buffer_at(tile);
 #pragma unroll
-    for (int i = 0; i < Geo<DB>::DMA; ++i)
-      dma16(r, lds + unsigned(wave + 4 * i) * 1024u,
-            row0 + i * (256 / Geo<DB>::PITCH) < there ? voff[i] : kBufNone);
+    for (int i = 0; i < N; ++i)
+      dma16(buffer_at(tile + i * step), lds + unsigned(wave + WAVES * i) * 1024u,
+            row0 + i * STEP < there ? voff : kBufNone);
   }
 };
 
@@ -89,33 +87,28 @@ __device__ __forceinline__ void load_rows(u32x4_t (&f)[2 * DB], const uint16_t* 
   }
 }
 
-// Byte offsets of this lane's reads within a tile: row reads (32 rows of one
-// chunk) and transposed reads (A operand: dims down, k across).
+// This lane's reads within a tile: row reads (32 rows of one chunk) and
+// transposed reads (A operand: dims down, k across).  The chunk's number is
+// xored into the low bits of an offset, so one offset serves all of them.
 template <int DB>
 struct TileRead {
-  unsigned row[2 * DB];       // + 32 rows per block
-  unsigned tr[DB][2];         // + 16 rows per k step
-  __device__ __forceinline__ TileRead(int lane) {
-    using G = Geo<DB>;
-    const int l = lane & 31, half = lane >> 5;
-#pragma unroll
-    for (int ks = 0; ks < 2 * DB; ++ks) row[ks] = unsigned(l * G::ROWB + (((2 * ks + half) ^ G::swz(l)) << 4));
-    const int s = lane & 15;
-#pragma unroll
-    for (int db = 0; db < DB; ++db)
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int r = 4 * half + 8 * u + (s >> 2);
-        const int c = 4 * db + 2 * ((lane >> 4) & 1) + ((s & 3) >> 1);
-        tr[db][u] = unsigned(r * G::ROWB + ((c ^ G::swz(r)) << 4) + (s & 1) * 8);
-      }
+  using G = Geo<DB>;
+  unsigned row, tr;
+  __device__ __forceinline__ explicit TileRead(int lane) {
+    const int l = lane & 31, half = lane >> 5, s = lane & 15;
+    row = unsigned(l * G::ROWB + ((half ^ G::swz(l)) << 4));
+    const int r = 4 * half + (s >> 2), c = 2 * ((lane >> 4) & 1) + ((s & 3) >> 1);
+    tr = unsigned(r * G::ROWB + ((c ^ G::swz(r)) << 4) + (s & 1) * 8);
   }
+  // 16 dims from 16 ks of the rows of block `block` of 32
   __device__ __forceinline__ u32x4_t rows(const unsigned char* t, int ks, int block) const {
-    return lds_read16(t, row[ks] + unsigned(block * 32 * Geo<DB>::ROWB));
+    return lds_read16(t + block * 32 * G::ROWB, row ^ unsigned(32 * ks));
   }
+  // dims 32 db .. + 31, k step `step` of 16 rows: rows 4 half .. and 8 + 4 half ..
   __device__ __forceinline__ u32x4_t cols(const unsigned char* t, int db, int step) const {
-    const u32x2_t a = lds_read_tr(t, tr[db][0] + unsigned(step * 16 * Geo<DB>::ROWB));
-    const u32x2_t b = lds_read_tr(t, tr[db][1] + unsigned(step * 16 * Geo<DB>::ROWB));
+    const unsigned char* at = t + step * 16 * G::ROWB;
+    const u32x2_t a = lds_read_tr(at, tr ^ unsigned(64 * db));
+    const u32x2_t b = lds_read_tr(at + 8 * G::ROWB, tr ^ unsigned(64 * db) ^ 32u);
     return u32x4_t{a[0], a[1], b[0], b[1]};
   }
 };
@@ -449,13 +442,17 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnDev a, unsigned ite
 }
 
 // ---------------------------------------------------------------------------
-// dk and dv: 32 keys per wave, whose k and v rows stay in registers as the
+// dk and dv: 32 KB keys per wave, whose k and v rows stay in registers as the
 // first products' operands.  Over the heads of the group and tiles of 64
 // queries, 32 at a time: s = q k^T, dp = do v^T (a lane has one key), then
-// dv^T += do^T p, dk^T += q^T ds.
-template <int DB>
-__global__ __launch_bounds__(256, 2) void attn_dkv_kernel(AttnDev a, unsigned items, unsigned blocks) {
+// dv^T += do^T p, dk^T += q^T ds.  Every q and do fragment from LDS serves KB
+// products; for heads of more than 64 dims KB = 2 and one wave per SIMD, since
+// at KB = 1 the fragment reads alone would take the LDS all of the time that
+// the products take.
+template <int DB, int KB>
+__global__ __launch_bounds__(256, KB == 2 ? 1 : 2) void attn_dkv_kernel(AttnDev a, unsigned items, unsigned blocks) {
   using G = Geo<DB>;
+  constexpr int KEYS = 128 * KB;                        // of the workgroup
   constexpr int BUF = 2 * G::TILEB + 2 * kTile * 4;     // q, do, offsets, deltas
   __shared__ __attribute__((aligned(1024))) unsigned char smem[2 * BUF];
   const int lane = threadIdx.x & 63, half = lane >> 5;
@@ -464,100 +461,145 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(AttnDev a, unsigned it
   const unsigned bh = item / blocks;
   const int b = int(bh) / a.kv_heads, kvh = int(bh) % a.kv_heads, group = a.heads / a.kv_heads;
   const int q_here = clamp_len(a.q_lens, b, a.q_len), k_here = clamp_len(a.k_lens, b, a.k_len);
-  const int key0 = int(item % blocks) * kRowsWg;
-  const int wkey = key0 + wave * 32, key = wkey + (lane & 31);
-  // First query that sees the workgroup's (wave's, lane's) first key.
+  const int key0 = int(item % blocks) * KEYS;
+  const int wkey = key0 + wave * 32 * KB, key = wkey + (lane & 31);   // + 32 per block
+  // First query that sees a key.
   const int64_t border = a.causal ? -a.offset : int64_t(-0x7fffffff);
   auto first_query = [&](int k) { return int(max(int64_t(0), min(int64_t(q_here), int64_t(k) + border))); };
   const int tile0 = first_query(key0) / kTile, tile_end = (q_here + kTile - 1) / kTile;
-  const int per_head = key0 < k_here && tile_end > tile0 && first_query(key0) < q_here ? tile_end - tile0 : 0;
+  const int per_head = key0 < k_here && first_query(key0) < q_here ? tile_end - tile0 : 0;
   const int tiles = per_head * group;
-  const int wave_first = first_query(wkey), wave_all = first_query(wkey + 31), mine = first_query(key);
+  const int wave_first = first_query(wkey), wave_all = first_query(wkey + 32 * KB - 1);
+  int mine[KB];
 
-  u32x4_t kf[2 * DB], vf[2 * DB];
-  load_rows<DB>(kf, static_cast<const uint16_t*>(a.k.p) + b * a.k.sb + key * a.k.sl + kvh * a.k.sh, key < k_here,
-                a.dim, half);
-  load_rows<DB>(vf, static_cast<const uint16_t*>(a.v.p) + b * a.v.sb + key * a.v.sl + kvh * a.v.sh, key < k_here,
-                a.dim, half);
+  u32x4_t kf[KB][2 * DB], vf[KB][2 * DB];
+#pragma unroll
+  for (int kb = 0; kb < KB; ++kb) {
+    const int kk = key + 32 * kb;
+    mine[kb] = first_query(kk) - 4 * half;
+    load_rows<DB>(kf[kb], static_cast<const uint16_t*>(a.k.p) + b * a.k.sb + kk * a.k.sl + kvh * a.k.sh, kk < k_here,
+                  a.dim, half);
+    load_rows<DB>(vf[kb], static_cast<const uint16_t*>(a.v.p) + b * a.v.sb + kk * a.v.sl + kvh * a.v.sh, kk < k_here,
+                  a.dim, half);
+  }
   const TileMove<DB> mq(a.q.sl, a.dim, wave, lane), mg(a.d_o.sl, a.dim, wave, lane);
   const TileRead<DB> rd(lane);
   const unsigned lds = lds_offset(smem);
-  auto fetch = [&](int t) {
-    const int head = kvh * group + t / per_head, q0 = (tile0 + t % per_head) * kTile;
+  const uint16_t* qb0 = static_cast<const uint16_t*>(a.q.p) + b * a.q.sb + kvh * group * a.q.sh;
+  const uint16_t* gb0 = static_cast<const uint16_t*>(a.d_o.p) + b * a.d_o.sb + kvh * group * a.d_o.sh;
+  const int64_t line0 = (int64_t(b) * a.heads + kvh * group) * a.q_len;
+  auto fetch = [&](int head, int q0, int t) {
     const unsigned at = lds + unsigned(t & 1) * BUF;
-    mq.issue(static_cast<const uint16_t*>(a.q.p) + b * a.q.sb + head * a.q.sh + q0 * a.q.sl, q_here - q0, at, wave);
-    mg.issue(static_cast<const uint16_t*>(a.d_o.p) + b * a.d_o.sb + head * a.d_o.sh + q0 * a.d_o.sl, q_here - q0,
-             at + G::TILEB, wave);
-    const int64_t line = (int64_t(b) * a.heads + head) * a.q_len + q0;
+    mq.issue(qb0 + head * a.q.sh + q0 * a.q.sl, q_here - q0, at, wave);
+    mg.issue(gb0 + head * a.d_o.sh + q0 * a.d_o.sl, q_here - q0, at + G::TILEB, wave);
+    const int64_t line = line0 + int64_t(head) * a.q_len + q0;
     const unsigned off = lane < q_here - q0 ? unsigned(lane) * 4u : kBufNone;
     if (wave == 0) dma4(buffer_at(a.part_lse + line), at + 2 * G::TILEB, off);
     if (wave == 1) dma4(buffer_at(a.delta + line), at + 2 * G::TILEB + kTile * 4, off);
   };
-  f32x16_t dk[DB], dv[DB];
+  f32x16_t dk[KB][DB], dv[KB][DB];
 #pragma unroll
-  for (int db = 0; db < DB; ++db) dk[db] = dv[db] = (f32x16_t)(0.f);
+  for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+    for (int db = 0; db < DB; ++db) dk[kb][db] = dv[kb][db] = (f32x16_t)(0.f);
   const float c = a.scale * kLog2e;
 
-  if (tiles > 0) fetch(0);
+  int head = 0, q0 = tile0 * kTile;      // of the tile worked on
+  if (tiles > 0) fetch(0, q0, 0);
   for (int t = 0; t < tiles; ++t) {
     wait_vm<0>();
     barrier();
-    if (t + 1 < tiles) fetch(t + 1);
-    const int q0 = (tile0 + t % per_head) * kTile;
+    int next_head = head, next_q0 = q0 + kTile;
+    if (next_q0 >= q_here) { next_q0 = tile0 * kTile; ++next_head; }
+    if (t + 1 < tiles) fetch(next_head, next_q0, t + 1);
     const unsigned char* qt = smem + (t & 1) * BUF;
     const unsigned char* gt = qt + G::TILEB;
     const float* lt = reinterpret_cast<const float*>(gt + G::TILEB);
-#pragma unroll
+#pragma unroll 1
     for (int qb = 0; qb < 2; ++qb) {
-      if (q0 + 32 * qb + 32 <= wave_first || q0 + 32 * qb >= q_here || wkey >= k_here) continue;
-      f32x16_t s = (f32x16_t)(0.f);
+      const int qq = q0 + 32 * qb;
+      if (qq + 32 <= wave_first || qq >= q_here || wkey >= k_here) continue;
+      const unsigned char* qh = qt + qb * 32 * G::ROWB;
+      const unsigned char* gh = gt + qb * 32 * G::ROWB;
+      f32x16_t s[KB], dp[KB];
 #pragma unroll
-      for (int ks = 0; ks < G::KS; ++ks) s = mfma32(rd.rows(qt, ks, qb), kf[ks], s);
-      if (q0 + 32 * qb < wave_all) {
-        const int n = mine - q0 - 32 * qb - 4 * half;
+      for (int kb = 0; kb < KB; ++kb) s[kb] = dp[kb] = (f32x16_t)(0.f);
 #pragma unroll
-        for (int v = 0; v < 16; ++v)
-          if (8 * (v >> 2) + (v & 3) < n) s[v] = -INFINITY;
+      for (int ks = 0; ks < G::KS; ++ks) {
+        const u32x4_t f = rd.rows(qh, ks, 0);
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) s[kb] = mfma32(f, kf[kb][ks], s[kb]);
+      }
+      if (qq < wave_all) {
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+          for (int v = 0; v < 16; ++v)
+            if (8 * (v >> 2) + (v & 3) < mine[kb] - qq) s[kb][v] = -INFINITY;
+      }
+#pragma unroll
+      for (int ks = 0; ks < G::KS; ++ks) {
+        const u32x4_t f = rd.rows(gh, ks, 0);
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) dp[kb] = mfma32(f, vf[kb][ks], dp[kb]);
       }
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const f32x4_t l = *(const MUON_LOCAL f32x4_t*)(const MUON_LOCAL float*)(lt + 32 * qb + 8 * g + 4 * half);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) s[4 * g + k] = exp2_fast(fmaf(s[4 * g + k], c, -l[k]));
-      }
-      f32x16_t dp = (f32x16_t)(0.f);
+        for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-      for (int ks = 0; ks < G::KS; ++ks) dp = mfma32(rd.rows(gt, ks, qb), vf[ks], dp);
+          for (int k = 0; k < 4; ++k) s[kb][4 * g + k] = exp2_fast(fmaf(s[kb][4 * g + k], c, -l[k]));
+      }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const u32x4_t p = pack8(s, 8 * j);
+        u32x4_t p[KB];
 #pragma unroll
-        for (int db = 0; db < DB; ++db) dv[db] = mfma32(rd.cols(gt, db, 2 * qb + j), p, dv[db]);
+        for (int kb = 0; kb < KB; ++kb) p[kb] = pack8(s[kb], 8 * j);
+#pragma unroll
+        for (int db = 0; db < DB; ++db) {
+          const u32x4_t f = rd.cols(gh, db, j);
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb) dv[kb][db] = mfma32(f, p[kb], dv[kb][db]);
+        }
       }
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const f32x4_t l = *(const MUON_LOCAL f32x4_t*)(const MUON_LOCAL float*)(lt + kTile + 32 * qb + 8 * g + 4 * half);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) s[4 * g + k] *= dp[4 * g + k] - l[k];
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s[kb][4 * g + k] *= dp[kb][4 * g + k] - l[k];
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const u32x4_t ds = pack8(s, 8 * j);
+        u32x4_t ds[KB];
 #pragma unroll
-        for (int db = 0; db < DB; ++db) dk[db] = mfma32(rd.cols(qt, db, 2 * qb + j), ds, dk[db]);
+        for (int kb = 0; kb < KB; ++kb) ds[kb] = pack8(s[kb], 8 * j);
+#pragma unroll
+        for (int db = 0; db < DB; ++db) {
+          const u32x4_t f = rd.cols(qh, db, j);
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb) dk[kb][db] = mfma32(f, ds[kb], dk[kb][db]);
+        }
       }
     }
+    head = next_head;
+    q0 = next_q0;
   }
-  if (key >= a.k_len) return;
-  const bool there = key < k_here;   // a key past the length has no gradient
-  if (!there) {
 #pragma unroll
-    for (int db = 0; db < DB; ++db) dk[db] = dv[db] = (f32x16_t)(0.f);
+  for (int kb = 0; kb < KB; ++kb) {
+    const int kk = key + 32 * kb;
+    if (kk >= a.k_len) continue;
+    if (kk >= k_here) {      // a key past the length has no gradient
+#pragma unroll
+      for (int db = 0; db < DB; ++db) dk[kb][db] = dv[kb][db] = (f32x16_t)(0.f);
+    }
+    store_rows<DB>(dk[kb], a.scale, static_cast<uint16_t*>(a.d_k.p) + b * a.d_k.sb + kk * a.d_k.sl + kvh * a.d_k.sh,
+                   a.dim, half);
+    store_rows<DB>(dv[kb], 1.f, static_cast<uint16_t*>(a.d_v.p) + b * a.d_v.sb + kk * a.d_v.sl + kvh * a.d_v.sh, a.dim,
+                   half);
   }
-  store_rows<DB>(dk, a.scale, static_cast<uint16_t*>(a.d_k.p) + b * a.d_k.sb + key * a.d_k.sl + kvh * a.d_k.sh, a.dim,
-                 half);
-  store_rows<DB>(dv, 1.f, static_cast<uint16_t*>(a.d_v.p) + b * a.d_v.sb + key * a.d_v.sl + kvh * a.d_v.sh, a.dim,
-                 half);
 }
 
 unsigned row_blocks(const AttnDev& a) {
@@ -615,8 +657,10 @@ hipError_t launch_attn_bwd(hipStream_t s, const AttnDev& a) {
     if (e != hipSuccess) return e;
   }
   if (a.k_len > 0) {
-    const unsigned blocks = unsigned((a.k_len + kRowsWg - 1) / kRowsWg), items = blocks * bh;
-    auto* k = BY_DIM(attn_dkv_kernel, );
+    const int keys = a.dim <= 64 ? 128 : 256;
+    const unsigned blocks = unsigned((a.k_len + keys - 1) / keys), items = blocks * bh;
+    auto* k = a.dim <= 32 ? attn_dkv_kernel<1, 1> : a.dim <= 64 ? attn_dkv_kernel<2, 1>
+              : a.dim <= 96 ? attn_dkv_kernel<3, 2> : attn_dkv_kernel<4, 2>;
     hipLaunchKernelGGL(k, dim3(items), dim3(256), 0, s, a, items, blocks);
     return hipGetLastError();
   }
