@@ -59,11 +59,14 @@ struct AttnDev {
   float* part_lse;       // split forward: [split][batch][heads][q_len]
   int32_t splits;        // key ranges worked on apart (1: no join)
   int32_t split_keys;    // keys per range, a multiple of the key tile
+  int32_t parts;         // backward: workgroups that share a key block (1: no join)
+  float* part_kv;        // [part][batch][kv_heads][k_len][2][dim] fp32 sums of dk / scale, dv
 };
 
 hipError_t launch_attn_fwd(hipStream_t s, const AttnDev& a);
 hipError_t launch_attn_bwd(hipStream_t s, const AttnDev& a);
 int attn_splits(const AttnDev& a, int* split_keys);
+int attn_parts(const AttnDev& a);
 
 // ---- gated feed-forward -----------------------------------------------------
 struct FfnDev {

@@ -184,6 +184,7 @@ AttnDev attn_dev(const muon_attn_args* a) {
   int keys = 0;
   d.splits = attn_splits(d, &keys);
   d.split_keys = keys;
+  d.parts = attn_parts(d);
   return d;
 }
 
@@ -194,7 +195,10 @@ size_t attn_fwd_bytes(const AttnDev& d) {
   return align_up(attn_lines(d) * d.splits * d.dim * 4) + align_up(attn_lines(d) * d.splits * 4);
 }
 
-size_t attn_bwd_bytes(const AttnDev& d) { return 2 * align_up(attn_lines(d) * 4); }
+size_t attn_bwd_bytes(const AttnDev& d) {
+  const size_t sums = size_t(d.batch) * d.kv_heads * d.k_len * 2 * d.dim * 4;
+  return 2 * align_up(attn_lines(d) * 4) + (d.parts > 1 ? d.parts * sums : 0);
+}
 
 // ---- gated feed-forward ---------------------------------------------------------
 muon_status ffn_dims(const muon_ffn_args* a) {
@@ -374,6 +378,7 @@ muon_status muon_attn_bwd(const muon_attn_args* a, void* ws, size_t ws_bytes, vo
   CHECK(check_workspace(ws, ws_bytes, attn_bwd_bytes(d)));
   d.part_lse = static_cast<float*>(ws);
   d.delta = reinterpret_cast<float*>(static_cast<char*>(ws) + align_up(attn_lines(d) * 4));
+  d.part_kv = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * align_up(attn_lines(d) * 4));
   return launched("muon_attn_bwd", launch_attn_bwd(static_cast<hipStream_t>(hip_stream), d));
 }
 

@@ -26,6 +26,9 @@
 // Rows of the forward and dq kernels are the (query, head) pairs that share a
 // key head, the heads of one query next to each other: grouped heads and few
 // queries share the key tiles of one workgroup.
+#include <algorithm>
+#include <cmath>
+
 #include "block_mfma.h"
 
 namespace muon {
@@ -33,9 +36,14 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kTile = 64;        // keys (dq, forward) or queries (dk, dv) per LDS tile
-constexpr int kRowsWg = 128;     // rows per workgroup: four waves of 32
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+// The lane's number, formed where it is called (the compiler cannot keep it).
+__device__ __forceinline__ int fresh_lane() {
+  unsigned all = ~0u;
+  asm volatile("" : "+s"(all));
+  return int(__builtin_amdgcn_mbcnt_hi(all, __builtin_amdgcn_mbcnt_lo(all, 0u)));
+}
 __device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32, 64); }
 
 // Head geometry: DB blocks of 32 dims; LDS rows of PITCH 16-byte chunks.
@@ -155,6 +163,7 @@ __device__ __forceinline__ int seen(const AttnDev& a, int qi, int k_here) {
   return int(max(int64_t(0), min(int64_t(k_here), n)));
 }
 
+template <int ROWS>
 __device__ __forceinline__ Rows rows_of(const AttnDev& a, unsigned item, unsigned blocks, int wave, int lane) {
   Rows r;
   // Later rows see more keys under a causal border: they go first.
@@ -164,7 +173,7 @@ __device__ __forceinline__ Rows rows_of(const AttnDev& a, unsigned item, unsigne
   r.group = a.heads / a.kv_heads;
   r.q_here = clamp_len(a.q_lens, r.b, a.q_len);
   r.k_here = clamp_len(a.k_lens, r.b, a.k_len);
-  r.row0 = int(blk) * kRowsWg;
+  r.row0 = int(blk) * ROWS;
   const int row = r.row0 + wave * 32 + (lane & 31);
   r.qi = row / r.group;
   r.head = r.kvh * r.group + row % r.group;
@@ -181,8 +190,9 @@ __device__ __forceinline__ int wave_max(int v) {
 }
 
 // Keys that the last of the workgroup's rows sees (the most of any).
+template <int ROWS>
 __device__ __forceinline__ int seen_most(const AttnDev& a, const Rows& r) {
-  const int last = min((r.row0 + kRowsWg - 1) / r.group, r.q_here - 1);
+  const int last = min((r.row0 + ROWS - 1) / r.group, r.q_here - 1);
   return last < r.row0 / r.group ? 0 : seen(a, last, r.k_here);
 }
 
@@ -192,17 +202,18 @@ __device__ __forceinline__ int seen_most(const AttnDev& a, const Rows& r) {
 // exponents are taken against follows the running one only when that has
 // grown by more than 2^8 (the result does not depend on it), so that the
 // accumulators are rarely rescaled.
-template <int DB, bool SPLIT>
-__global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnDev a, unsigned items, unsigned blocks) {
+template <int DB, int NW, bool SPLIT>
+__global__ __launch_bounds__(64 * NW, 2) void attn_fwd_kernel(AttnDev a, unsigned items, unsigned blocks) {
   using G = Geo<DB>;
-  __shared__ __attribute__((aligned(1024))) unsigned char smem[4 * G::TILEB];   // two of k, two of v
+  constexpr int ROWS = 32 * NW, NBUF = NW == 8 ? 3 : 2;
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[NBUF * 2 * G::TILEB];   // k, v of each tile
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const unsigned id = xcd_item(blockIdx.x, items);
   const unsigned split = SPLIT ? id % unsigned(a.splits) : 0;
-  const Rows r = rows_of(a, SPLIT ? id / unsigned(a.splits) : id, blocks, wave, lane);
+  const Rows r = rows_of<ROWS>(a, SPLIT ? id / unsigned(a.splits) : id, blocks, wave, lane);
   const int first = SPLIT ? int(split) * a.split_keys : 0;
-  const int end = SPLIT ? min(seen_most(a, r), first + a.split_keys) : seen_most(a, r);
+  const int most = seen_most<ROWS>(a, r), end = SPLIT ? min(most, first + a.split_keys) : most;
   const int tiles = end > first ? (end - first + kTile - 1) / kTile : 0;
 
   u32x4_t q[2 * DB];
@@ -210,11 +221,11 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnDev a, unsigned it
   load_rows<DB>(q, qrow, r.live, a.dim, half);
   const uint16_t* kbase = static_cast<const uint16_t*>(a.k.p) + r.b * a.k.sb + r.kvh * a.k.sh + first * a.k.sl;
   const uint16_t* vbase = static_cast<const uint16_t*>(a.v.p) + r.b * a.v.sb + r.kvh * a.v.sh + first * a.v.sl;
-  const TileMove<DB> mk(a.k.sl, a.dim, wave, lane), mv(a.v.sl, a.dim, wave, lane);
+  const TileMove<DB, NW> mk(a.k.sl, a.dim, wave, lane), mv(a.v.sl, a.dim, wave, lane);
   const TileRead<DB> rd(lane);
   const unsigned lds = lds_offset(smem);
   auto fetch = [&](int t) {
-    const unsigned at = lds + unsigned(t & 1) * 2u * G::TILEB;
+    const unsigned at = lds + unsigned(t % NBUF) * 2u * G::TILEB;
     mk.issue(kbase + int64_t(t) * kTile * a.k.sl, r.k_here - first - t * kTile, at, wave);
     mv.issue(vbase + int64_t(t) * kTile * a.v.sl, r.k_here - first - t * kTile, at + G::TILEB, wave);
   };
@@ -226,14 +237,17 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnDev a, unsigned it
   float top = -INFINITY, top_c = 0.f, sum = 0.f;
   const int wave_see = wave_max(r.see), wave_all = -wave_max(r.ok ? -r.see : -0x7fffffff);
 
-  if (tiles > 0) fetch(0);
+  for (int t = 0; t < NBUF - 1; ++t)
+    if (t < tiles) fetch(t);
   for (int t = 0; t < tiles; ++t) {
-    wait_vm<0>();
+    // tile t is in; the next may be on its way
+    if (NBUF == 3 && t + 1 < tiles) wait_vm<2 * TileMove<DB, NW>::N>();
+    else wait_vm<0>();
     barrier();
-    if (t + 1 < tiles) fetch(t + 1);
+    if (t + NBUF - 1 < tiles) fetch(t + NBUF - 1);
     const int key0 = first + t * kTile;
     if (key0 >= wave_see) continue;
-    const unsigned char* kt = smem + (t & 1) * 2 * G::TILEB;
+    const unsigned char* kt = smem + (t % NBUF) * 2 * G::TILEB;
     const unsigned char* vt = kt + G::TILEB;
     f32x16_t s[2];
 #pragma unroll
@@ -344,14 +358,15 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnDev a) {
 // dq, and per row delta = do . o and the exponent's offset for the dk, dv
 // kernel.  Per tile of 64 keys, 32 at a time: s^T = k q^T, dp^T = v do^T,
 // ds^T = p^T (dp^T - delta), dq^T += k^T ds^T.
-template <int DB>
-__global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnDev a, unsigned items, unsigned blocks) {
+template <int DB, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void attn_dq_kernel(AttnDev a, unsigned items, unsigned blocks) {
   using G = Geo<DB>;
-  __shared__ __attribute__((aligned(1024))) unsigned char smem[4 * G::TILEB];
+  constexpr int ROWS = 32 * NW, NBUF = NW == 8 ? 3 : 2;
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[NBUF * 2 * G::TILEB];
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Rows r = rows_of(a, xcd_item(blockIdx.x, items), blocks, wave, lane);
-  const int end = seen_most(a, r);
+  const Rows r = rows_of<ROWS>(a, xcd_item(blockIdx.x, items), blocks, wave, lane);
+  const int end = seen_most<ROWS>(a, r);
   const int tiles = (end + kTile - 1) / kTile;
 
   u32x4_t q[2 * DB], g[2 * DB];
@@ -389,11 +404,11 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnDev a, unsigned ite
 
   const uint16_t* kbase = static_cast<const uint16_t*>(a.k.p) + r.b * a.k.sb + r.kvh * a.k.sh;
   const uint16_t* vbase = static_cast<const uint16_t*>(a.v.p) + r.b * a.v.sb + r.kvh * a.v.sh;
-  const TileMove<DB> mk(a.k.sl, a.dim, wave, lane), mv(a.v.sl, a.dim, wave, lane);
+  const TileMove<DB, NW> mk(a.k.sl, a.dim, wave, lane), mv(a.v.sl, a.dim, wave, lane);
   const TileRead<DB> rd(lane);
   const unsigned lds = lds_offset(smem);
   auto fetch = [&](int t) {
-    const unsigned at = lds + unsigned(t & 1) * 2u * G::TILEB;
+    const unsigned at = lds + unsigned(t % NBUF) * 2u * G::TILEB;
     mk.issue(kbase + int64_t(t) * kTile * a.k.sl, r.k_here - t * kTile, at, wave);
     mv.issue(vbase + int64_t(t) * kTile * a.v.sl, r.k_here - t * kTile, at + G::TILEB, wave);
   };
@@ -403,14 +418,17 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnDev a, unsigned ite
   const float c = a.scale * kLog2e;
   const int wave_see = wave_max(r.see), wave_all = -wave_max(r.ok ? -r.see : -0x7fffffff);
 
-  if (tiles > 0) fetch(0);
+  for (int t = 0; t < NBUF - 1; ++t)
+    if (t < tiles) fetch(t);
   for (int t = 0; t < tiles; ++t) {
-    wait_vm<0>();
+    // tile t is in; the next may be on its way
+    if (NBUF == 3 && t + 1 < tiles) wait_vm<2 * TileMove<DB, NW>::N>();
+    else wait_vm<0>();
     barrier();
-    if (t + 1 < tiles) fetch(t + 1);
+    if (t + NBUF - 1 < tiles) fetch(t + NBUF - 1);
     const int key0 = t * kTile;
     if (key0 >= wave_see) continue;
-    const unsigned char* kt = smem + (t & 1) * 2 * G::TILEB;
+    const unsigned char* kt = smem + (t % NBUF) * 2 * G::TILEB;
     const unsigned char* vt = kt + G::TILEB;
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
@@ -442,54 +460,59 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnDev a, unsigned ite
 }
 
 // ---------------------------------------------------------------------------
-// dk and dv: 32 KB keys per wave, whose k and v rows stay in registers as the
-// first products' operands.  Over the heads of the group and tiles of 64
-// queries, 32 at a time: s = q k^T, dp = do v^T (a lane has one key), then
-// dv^T += do^T p, dk^T += q^T ds.  Every q and do fragment from LDS serves KB
-// products; for heads of more than 64 dims KB = 2 and one wave per SIMD, since
-// at KB = 1 the fragment reads alone would take the LDS all of the time that
-// the products take.
-template <int DB, int KB>
-__global__ __launch_bounds__(256, KB == 2 ? 1 : 2) void attn_dkv_kernel(AttnDev a, unsigned items, unsigned blocks) {
+// dk and dv of 256 keys, 32 per wave: the wave's k rows stay in registers, the
+// workgroup's v rows in LDS, as the first products' second operand.  Over the
+// heads of the group and tiles of 64 queries, 32 at a time: s = q k^T,
+// dp = do v^T (a lane has one key), then dv^T += do^T p, dk^T += q^T ds.
+// The accumulators (2 x 32 keys x dim) and k take 160 of the 256 registers at
+// 128 dims; with v there too they would spill.  256 keys share a tile, since
+// a CU takes in only some 25 bytes per cycle on the way into LDS.
+//
+// The (head, query tile) pairs of a key block may be divided over several
+// workgroups (a.parts), whose fp32 sums a second kernel adds.
+template <int DB, int AHEAD>
+__global__ __launch_bounds__(512, 2) void attn_dkv_kernel(AttnDev a, unsigned items, unsigned blocks) {
   using G = Geo<DB>;
-  constexpr int KEYS = 128 * KB;                        // of the workgroup
+  constexpr int NW = 8, KEYS = 32 * NW;
   constexpr int BUF = 2 * G::TILEB + 2 * kTile * 4;     // q, do, offsets, deltas
-  __shared__ __attribute__((aligned(1024))) unsigned char smem[2 * BUF];
+  constexpr int VB = KEYS * G::ROWB;
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[VB + 2 * BUF];
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const unsigned item = xcd_item(blockIdx.x, items);
-  const unsigned bh = item / blocks;
+  // Under a causal border the first keys are seen by the most queries: their
+  // workgroups go first, those of all heads in turn.
+  const unsigned bhs = unsigned(a.batch) * unsigned(a.kv_heads), parts = unsigned(a.parts);
+  const unsigned item = a.causal ? blockIdx.x : xcd_item(blockIdx.x, items);
+  const unsigned part = item % parts;
+  const unsigned bh = a.causal ? item / parts % bhs : item / parts / blocks;
+  const unsigned blk = a.causal ? item / parts / bhs : item / parts % blocks;
   const int b = int(bh) / a.kv_heads, kvh = int(bh) % a.kv_heads, group = a.heads / a.kv_heads;
   const int q_here = clamp_len(a.q_lens, b, a.q_len), k_here = clamp_len(a.k_lens, b, a.k_len);
-  const int key0 = int(item % blocks) * KEYS;
-  const int wkey = key0 + wave * 32 * KB, key = wkey + (lane & 31);   // + 32 per block
+  const int key0 = int(blk) * KEYS;
+  const int wkey = key0 + wave * 32, key = wkey + (lane & 31);
   // First query that sees a key.
   const int64_t border = a.causal ? -a.offset : int64_t(-0x7fffffff);
   auto first_query = [&](int k) { return int(max(int64_t(0), min(int64_t(q_here), int64_t(k) + border))); };
   const int tile0 = first_query(key0) / kTile, tile_end = (q_here + kTile - 1) / kTile;
   const int per_head = key0 < k_here && first_query(key0) < q_here ? tile_end - tile0 : 0;
-  const int tiles = per_head * group;
-  const int wave_first = first_query(wkey), wave_all = first_query(wkey + 32 * KB - 1);
-  int mine[KB];
+  const int all = per_head * group, share = (all + a.parts - 1) / a.parts;
+  const int t0 = min(all, int(part) * share), tiles = min(all, t0 + share) - t0;
+  const int wave_first = first_query(wkey), wave_all = first_query(wkey + 31);
 
-  u32x4_t kf[KB][2 * DB], vf[KB][2 * DB];
-#pragma unroll
-  for (int kb = 0; kb < KB; ++kb) {
-    const int kk = key + 32 * kb;
-    mine[kb] = first_query(kk) - 4 * half;
-    load_rows<DB>(kf[kb], static_cast<const uint16_t*>(a.k.p) + b * a.k.sb + kk * a.k.sl + kvh * a.k.sh, kk < k_here,
-                  a.dim, half);
-    load_rows<DB>(vf[kb], static_cast<const uint16_t*>(a.v.p) + b * a.v.sb + kk * a.v.sl + kvh * a.v.sh, kk < k_here,
-                  a.dim, half);
-  }
-  const TileMove<DB> mq(a.q.sl, a.dim, wave, lane), mg(a.d_o.sl, a.dim, wave, lane);
+  const uint16_t* kbase = static_cast<const uint16_t*>(a.k.p) + b * a.k.sb + kvh * a.k.sh;
+  const uint16_t* vbase = static_cast<const uint16_t*>(a.v.p) + b * a.v.sb + kvh * a.v.sh;
+  u32x4_t kf[2 * DB];
   const TileRead<DB> rd(lane);
   const unsigned lds = lds_offset(smem);
   const uint16_t* qb0 = static_cast<const uint16_t*>(a.q.p) + b * a.q.sb + kvh * group * a.q.sh;
   const uint16_t* gb0 = static_cast<const uint16_t*>(a.d_o.p) + b * a.d_o.sb + kvh * group * a.d_o.sh;
   const int64_t line0 = (int64_t(b) * a.heads + kvh * group) * a.q_len;
   auto fetch = [&](int head, int q0, int t) {
-    const unsigned at = lds + unsigned(t & 1) * BUF;
+    const unsigned at = lds + VB + unsigned(t & 1) * BUF;
+    // Formed anew for each tile: kept, its registers would spill, and a
+    // reload's wait would also wait for the DMA in flight.
+    const int lane = fresh_lane();
+    const TileMove<DB, NW> mq(a.q.sl, a.dim, wave, lane), mg(a.d_o.sl, a.dim, wave, lane);
     mq.issue(qb0 + head * a.q.sh + q0 * a.q.sl, q_here - q0, at, wave);
     mg.issue(gb0 + head * a.d_o.sh + q0 * a.d_o.sl, q_here - q0, at + G::TILEB, wave);
     const int64_t line = line0 + int64_t(head) * a.q_len + q0;
@@ -497,131 +520,203 @@ __global__ __launch_bounds__(256, KB == 2 ? 1 : 2) void attn_dkv_kernel(AttnDev 
     if (wave == 0) dma4(buffer_at(a.part_lse + line), at + 2 * G::TILEB, off);
     if (wave == 1) dma4(buffer_at(a.delta + line), at + 2 * G::TILEB + kTile * 4, off);
   };
-  f32x16_t dk[KB][DB], dv[KB][DB];
+  f32x16_t dk[DB], dv[DB];
 #pragma unroll
-  for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-    for (int db = 0; db < DB; ++db) dk[kb][db] = dv[kb][db] = (f32x16_t)(0.f);
+  for (int db = 0; db < DB; ++db) dk[db] = dv[db] = (f32x16_t)(0.f);
   const float c = a.scale * kLog2e;
 
-  int head = 0, q0 = tile0 * kTile;      // of the tile worked on
-  if (tiles > 0) fetch(0, q0, 0);
+  int head = 0, q0 = 0;                 // of the tile worked on
+  if (tiles > 0) {
+    head = t0 / per_head;
+    q0 = (tile0 + t0 % per_head) * kTile;
+    const TileMove<DB, NW> mv(a.v.sl, a.dim, wave, lane);
+#pragma unroll
+    for (int i = 0; i < KEYS / kTile; ++i)
+      mv.issue(vbase + (key0 + i * kTile) * a.v.sl, k_here - key0 - i * kTile, lds + unsigned(i) * G::TILEB, wave);
+    fetch(head, q0, 0);
+    load_rows<DB>(kf, kbase + key * a.k.sl, key < k_here, a.dim, half);
+  }
+  const unsigned char* vh = smem + wave * 32 * G::ROWB;
   for (int t = 0; t < tiles; ++t) {
     wait_vm<0>();
     barrier();
     int next_head = head, next_q0 = q0 + kTile;
     if (next_q0 >= q_here) { next_q0 = tile0 * kTile; ++next_head; }
     if (t + 1 < tiles) fetch(next_head, next_q0, t + 1);
-    const unsigned char* qt = smem + (t & 1) * BUF;
+    const unsigned char* qt = smem + VB + (t & 1) * BUF;
     const unsigned char* gt = qt + G::TILEB;
     const float* lt = reinterpret_cast<const float*>(gt + G::TILEB);
+    if (q0 + kTile > wave_first && wkey < k_here) {
+      // Fragment n of 32 queries: KS row reads of q, KS of do (and of v), 2 DB
+      // transposed reads of do, 2 DB of q; AHEAD of them are on their way.
+      // The order of a slot's products, reads and arithmetic is fixed: left to
+      // itself the compiler waits for each read at once.
+      constexpr int KS = G::KS, DB2 = 2 * DB, NF = 2 * KS + 2 * DB2;
+      u32x4_t f[AHEAD], fv[AHEAD];
+      auto fragment = [&](int qb, int n) {
+        const unsigned char* qh = qt + qb * 32 * G::ROWB;
+        const unsigned char* gh = gt + qb * 32 * G::ROWB;
+        if (n < KS) return rd.rows(qh, n, 0);
+        if (n < 2 * KS) return rd.rows(gh, n - KS, 0);
+        if (n < 2 * KS + DB2) return rd.cols(gh, (n - 2 * KS) % DB, (n - 2 * KS) / DB);
+        return rd.cols(qh, (n - 2 * KS - DB2) % DB, (n - 2 * KS - DB2) / DB);
+      };
+#pragma unroll
+      for (int n = 0; n < AHEAD; ++n) f[n] = fragment(0, n);
 #pragma unroll 1
-    for (int qb = 0; qb < 2; ++qb) {
-      const int qq = q0 + 32 * qb;
-      if (qq + 32 <= wave_first || qq >= q_here || wkey >= k_here) continue;
-      const unsigned char* qh = qt + qb * 32 * G::ROWB;
-      const unsigned char* gh = gt + qb * 32 * G::ROWB;
-      f32x16_t s[KB], dp[KB];
+      for (int qb = 0; qb < 2; ++qb) {
+        const MUON_LOCAL float* lh = (const MUON_LOCAL float*)(lt + 32 * qb + 4 * half);
+        f32x16_t s, dp;
+        u32x4_t p[2];
+        f32x4_t l[2];
+        auto slot_end = [&](int n) {
+          const int m = n + AHEAD;
+          if (m < NF) f[n % AHEAD] = fragment(qb, m);
+          else f[n % AHEAD] = fragment(1, m - NF);      // of the second half (read again there: unused)
+          if (m >= KS && m < 2 * KS) fv[n % AHEAD] = rd.rows(vh, m - KS, 0);
+          __builtin_amdgcn_sched_barrier(0);
+        };
+        // Quarter g of the rows: p = exp2(c s - offset), then ds = p (dp - delta)
+        auto probs = [&](int g) {
 #pragma unroll
-      for (int kb = 0; kb < KB; ++kb) s[kb] = dp[kb] = (f32x16_t)(0.f);
+          for (int k = 0; k < 4; ++k) s[4 * g + k] = exp2_fast(fmaf(s[4 * g + k], c, -l[g & 1][k]));
+          if (g & 1) p[g >> 1] = pack8(s, 8 * (g >> 1));
+          if (g + 2 < 4) l[g & 1] = *(const MUON_LOCAL f32x4_t*)(lh + 8 * (g + 2));
+        };
+        auto grads = [&](int g) {
 #pragma unroll
-      for (int ks = 0; ks < G::KS; ++ks) {
-        const u32x4_t f = rd.rows(qh, ks, 0);
+          for (int k = 0; k < 4; ++k) s[4 * g + k] *= dp[4 * g + k] - l[g & 1][k];
+          if (g & 1) p[g >> 1] = pack8(s, 8 * (g >> 1));
+          if (g + 2 < 4) l[g & 1] = *(const MUON_LOCAL f32x4_t*)(lh + kTile + 8 * (g + 2));
+        };
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) s[kb] = mfma32(f, kf[kb][ks], s[kb]);
-      }
-      if (qq < wave_all) {
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
+        for (int n = 0; n < KS; ++n) {
+          s = mfma32(f[n % AHEAD], kf[n], n ? s : (f32x16_t)(0.f));
+          if (n < 2) l[n] = *(const MUON_LOCAL f32x4_t*)(lh + 8 * n);
+          slot_end(n);
+        }
+        const int qq = q0 + 32 * qb;
+        if (qq < wave_all) {
+          const int l = fresh_lane(), unseen = first_query(wkey + (l & 31)) - 4 * (l >> 5) - qq;
 #pragma unroll
           for (int v = 0; v < 16; ++v)
-            if (8 * (v >> 2) + (v & 3) < mine[kb] - qq) s[kb][v] = -INFINITY;
-      }
-#pragma unroll
-      for (int ks = 0; ks < G::KS; ++ks) {
-        const u32x4_t f = rd.rows(gh, ks, 0);
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb) dp[kb] = mfma32(f, vf[kb][ks], dp[kb]);
-      }
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const f32x4_t l = *(const MUON_LOCAL f32x4_t*)(const MUON_LOCAL float*)(lt + 32 * qb + 8 * g + 4 * half);
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) s[kb][4 * g + k] = exp2_fast(fmaf(s[kb][4 * g + k], c, -l[k]));
-      }
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        u32x4_t p[KB];
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb) p[kb] = pack8(s[kb], 8 * j);
-#pragma unroll
-        for (int db = 0; db < DB; ++db) {
-          const u32x4_t f = rd.cols(gh, db, j);
-#pragma unroll
-          for (int kb = 0; kb < KB; ++kb) dv[kb][db] = mfma32(f, p[kb], dv[kb][db]);
+            if (8 * (v >> 2) + (v & 3) < unseen) s[v] = -INFINITY;
         }
-      }
+        __builtin_amdgcn_sched_barrier(0);
+        // The pieces of arithmetic are spread over the slots of a phase, none
+        // in its first (their inputs are the last results of the one before).
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const f32x4_t l = *(const MUON_LOCAL f32x4_t*)(const MUON_LOCAL float*)(lt + kTile + 32 * qb + 8 * g + 4 * half);
+        for (int n = KS; n < 2 * KS; ++n) {
+          dp = mfma32(f[n % AHEAD], fv[n % AHEAD], n > KS ? dp : (f32x16_t)(0.f));
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
+          for (int g = 0; g < 4; ++g)
+            if (1 + g * (KS - 1) / 4 == n - KS) probs(g);
+          if (n == 2 * KS - 1) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) s[kb][4 * g + k] *= dp[kb][4 * g + k] - l[k];
-      }
+            for (int g = 0; g < 2; ++g) l[g] = *(const MUON_LOCAL f32x4_t*)(lh + kTile + 8 * g);
+          }
+          slot_end(n);
+        }
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        u32x4_t ds[KB];
+        for (int n = 2 * KS; n < 2 * KS + DB2; ++n) {
+          const int m = n - 2 * KS;
+          dv[m % DB] = mfma32(f[n % AHEAD], p[m / DB], dv[m % DB]);
+          // p's first half is overwritten once it has been used, the second
+          // in the last slot
+          if (m == DB) { grads(0); grads(1); }
+          if (m == DB2 - 1) { grads(2); grads(3); }
+          slot_end(n);
+        }
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) ds[kb] = pack8(s[kb], 8 * j);
-#pragma unroll
-        for (int db = 0; db < DB; ++db) {
-          const u32x4_t f = rd.cols(qh, db, j);
-#pragma unroll
-          for (int kb = 0; kb < KB; ++kb) dk[kb][db] = mfma32(f, ds[kb], dk[kb][db]);
+        for (int n = 2 * KS + DB2; n < NF; ++n) {
+          const int m = n - 2 * KS - DB2;
+          dk[m % DB] = mfma32(f[n % AHEAD], p[m / DB], dk[m % DB]);
+          slot_end(n);
         }
       }
     }
     head = next_head;
     q0 = next_q0;
   }
+  if (key >= a.k_len) return;
+  if (key >= k_here) {      // a key past the length has no gradient
 #pragma unroll
-  for (int kb = 0; kb < KB; ++kb) {
-    const int kk = key + 32 * kb;
-    if (kk >= a.k_len) continue;
-    if (kk >= k_here) {      // a key past the length has no gradient
-#pragma unroll
-      for (int db = 0; db < DB; ++db) dk[kb][db] = dv[kb][db] = (f32x16_t)(0.f);
-    }
-    store_rows<DB>(dk[kb], a.scale, static_cast<uint16_t*>(a.d_k.p) + b * a.d_k.sb + kk * a.d_k.sl + kvh * a.d_k.sh,
-                   a.dim, half);
-    store_rows<DB>(dv[kb], 1.f, static_cast<uint16_t*>(a.d_v.p) + b * a.d_v.sb + kk * a.d_v.sl + kvh * a.d_v.sh, a.dim,
-                   half);
+    for (int db = 0; db < DB; ++db) dk[db] = dv[db] = (f32x16_t)(0.f);
   }
+  if (parts > 1) {
+    float* o = a.part_kv + (((int64_t(part) * a.batch + b) * a.kv_heads + kvh) * a.k_len + key) * 2 * a.dim;
+#pragma unroll
+    for (int db = 0; db < DB; ++db)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int d = 32 * db + 8 * g + 4 * half;
+        if (d >= a.dim) continue;
+        *as_global(reinterpret_cast<f32x4_t*>(o + d)) =
+            f32x4_t{dk[db][4 * g], dk[db][4 * g + 1], dk[db][4 * g + 2], dk[db][4 * g + 3]};
+        *as_global(reinterpret_cast<f32x4_t*>(o + a.dim + d)) =
+            f32x4_t{dv[db][4 * g], dv[db][4 * g + 1], dv[db][4 * g + 2], dv[db][4 * g + 3]};
+      }
+    return;
+  }
+  store_rows<DB>(dk, a.scale, static_cast<uint16_t*>(a.d_k.p) + b * a.d_k.sb + key * a.d_k.sl + kvh * a.d_k.sh, a.dim,
+                 half);
+  store_rows<DB>(dv, 1.f, static_cast<uint16_t*>(a.d_v.p) + b * a.d_v.sb + key * a.d_v.sl + kvh * a.d_v.sh, a.dim,
+                 half);
 }
 
+// Adds the parts of dk and dv, eight values per thread.
+__global__ __launch_bounds__(256) void attn_dkv_join_kernel(AttnDev a, int64_t n, int64_t stride) {
+  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= n) return;
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int p = 0; p < a.parts; ++p) {
+    float t[8];
+    load_vals<float, 8>(a.part_kv, p * stride + i * 8, t);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] += t[k];
+  }
+  const int cpr = a.dim / 8;
+  const int c = int(i % (2 * cpr));
+  const int64_t line = i / (2 * cpr);
+  const int key = int(line % a.k_len);
+  const int64_t bh = line / a.k_len, b = bh / a.kv_heads, h = bh % a.kv_heads;
+  const bool is_v = c >= cpr;
+  const HeadsDev& o = is_v ? a.d_v : a.d_k;
+  if (!is_v) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] *= a.scale;
+  }
+  store_vals<uint16_t, 8>(o.p, b * o.sb + key * o.sl + h * o.sh + (is_v ? c - cpr : c) * 8, v);
+}
+
+int64_t rows_in(const AttnDev& a) { return int64_t(a.q_len) * (a.heads / a.kv_heads); }
+// Workgroups of eight waves (256 rows) bring in a key tile for twice the rows
+// that four waves do; four are taken where 128 rows are all there are.
+int waves_of(const AttnDev& a) { return rows_in(a) > 128 ? 8 : 4; }
 unsigned row_blocks(const AttnDev& a) {
-  const int64_t rows = int64_t(a.q_len) * (a.heads / a.kv_heads);
-  return unsigned((rows + kRowsWg - 1) / kRowsWg);
+  const int64_t rows = 32 * waves_of(a);
+  return unsigned((rows_in(a) + rows - 1) / rows);
 }
+unsigned key_blocks(const AttnDev& a) { return unsigned((a.k_len + 255) / 256); }
 
-#define BY_DIM(K, ...)                                                                            \
-  (a.dim <= 32 ? K<1 __VA_ARGS__> : a.dim <= 64 ? K<2 __VA_ARGS__> : a.dim <= 96 ? K<3 __VA_ARGS__> \
-                                                                                 : K<4 __VA_ARGS__>)
+#define BY_DIM(K, ...)                                                                                       \
+  (a.dim <= 32 ? K<1, __VA_ARGS__> : a.dim <= 64 ? K<2, __VA_ARGS__> : a.dim <= 96 ? K<3, __VA_ARGS__>         \
+                                                                                   : K<4, __VA_ARGS__>)
+#define BY_DIM_ROWS(K, ...) (waves_of(a) == 8 ? BY_DIM(K, 8 __VA_ARGS__) : BY_DIM(K, 4 __VA_ARGS__))
 #define COMMA ,
 
 }  // namespace
 
 int attn_splits(const AttnDev& a, int* split_keys) {
-  // Two workgroups fit on each of 256 CUs.  With fewer than half of that,
-  // the keys are divided, in ranges of at least four tiles.
-  const int64_t items = int64_t(row_blocks(a)) * a.batch * a.kv_heads;
+  // A workgroup of eight waves takes a CU, two of four waves fit.  With fewer
+  // than half of that, the keys are divided, in ranges of at least four tiles.
+  const int64_t items = int64_t(row_blocks(a)) * a.batch * a.kv_heads, slots = waves_of(a) == 8 ? 256 : 512;
   const int tiles = (a.k_len + kTile - 1) / kTile;
   int64_t n = 1;
-  if (items > 0 && items < 256) {
-    n = 512 / items;
+  if (items > 0 && 2 * items < slots) {
+    n = slots / items;
     if (n > tiles / 4) n = tiles / 4;
     if (n < 1) n = 1;
   }
@@ -630,16 +725,37 @@ int attn_splits(const AttnDev& a, int* split_keys) {
   return tiles == 0 ? 1 : (tiles + per - 1) / per;
 }
 
+int attn_parts(const AttnDev& a) {
+  // The time of the dk, dv kernel in tiles of one workgroup per CU: whole
+  // rounds of workgroups, or under a causal border, where their work differs,
+  // the average plus the last one's.  A divided block's part costs about as
+  // much as four tiles more, to write its sums and read them back.
+  const double items = double(key_blocks(a)) * a.batch * a.kv_heads;
+  const double tiles = double((a.q_len + kTile - 1) / kTile) * (a.heads / a.kv_heads);
+  int best = 1;
+  double least = 0;
+  for (int p = 1; p <= 16 && (p == 1 || tiles / p >= 4); ++p) {
+    const double one = tiles / p + (p > 1 ? 4 : 0);
+    const double time = a.causal ? std::max(one, items * p * (0.55 * tiles / p + (p > 1 ? 4 : 0)) / 256 + 0.5 * one)
+                                 : std::ceil(items * p / 256) * one;
+    if (p == 1 || time < 0.97 * least) {
+      best = p;
+      least = time;
+    }
+  }
+  return best;
+}
+
 hipError_t launch_attn_fwd(hipStream_t s, const AttnDev& a) {
-  const unsigned blocks = row_blocks(a);
+  const unsigned blocks = row_blocks(a), threads = 64u * unsigned(waves_of(a));
   const unsigned items = blocks * unsigned(a.batch) * unsigned(a.kv_heads) * unsigned(a.splits);
   if (a.splits == 1) {
-    auto* k = BY_DIM(attn_fwd_kernel, COMMA false);
-    hipLaunchKernelGGL(k, dim3(items), dim3(256), 0, s, a, items, blocks);
+    auto* k = BY_DIM_ROWS(attn_fwd_kernel, COMMA false);
+    hipLaunchKernelGGL(k, dim3(items), dim3(threads), 0, s, a, items, blocks);
     return hipGetLastError();
   }
-  auto* k = BY_DIM(attn_fwd_kernel, COMMA true);
-  hipLaunchKernelGGL(k, dim3(items), dim3(256), 0, s, a, items, blocks);
+  auto* k = BY_DIM_ROWS(attn_fwd_kernel, COMMA true);
+  hipLaunchKernelGGL(k, dim3(items), dim3(threads), 0, s, a, items, blocks);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t lines = int64_t(a.batch) * a.heads * a.q_len;
@@ -651,17 +767,19 @@ hipError_t launch_attn_bwd(hipStream_t s, const AttnDev& a) {
   const unsigned bh = unsigned(a.batch) * unsigned(a.kv_heads);
   if (a.q_len > 0) {
     const unsigned blocks = row_blocks(a), items = blocks * bh;
-    auto* k = BY_DIM(attn_dq_kernel, );
-    hipLaunchKernelGGL(k, dim3(items), dim3(256), 0, s, a, items, blocks);
+    auto* k = BY_DIM_ROWS(attn_dq_kernel, );
+    hipLaunchKernelGGL(k, dim3(items), dim3(64u * unsigned(waves_of(a))), 0, s, a, items, blocks);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (a.k_len > 0) {
-    const int keys = a.dim <= 64 ? 128 : 256;
-    const unsigned blocks = unsigned((a.k_len + keys - 1) / keys), items = blocks * bh;
-    auto* k = a.dim <= 32 ? attn_dkv_kernel<1, 1> : a.dim <= 64 ? attn_dkv_kernel<2, 1>
-              : a.dim <= 96 ? attn_dkv_kernel<3, 2> : attn_dkv_kernel<4, 2>;
-    hipLaunchKernelGGL(k, dim3(items), dim3(256), 0, s, a, items, blocks);
+    const unsigned blocks = key_blocks(a), items = blocks * bh * unsigned(a.parts);
+    auto* k = BY_DIM(attn_dkv_kernel, 2);
+    hipLaunchKernelGGL(k, dim3(items), dim3(512), 0, s, a, items, blocks);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.parts == 1) return e;
+    const int64_t stride = int64_t(a.batch) * a.kv_heads * a.k_len * 2 * a.dim, n = stride / 8;
+    hipLaunchKernelGGL(attn_dkv_join_kernel, dim3(unsigned((n + 255) / 256)), dim3(256), 0, s, a, n, stride);
     return hipGetLastError();
   }
   return hipSuccess;
