@@ -36,6 +36,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kTile = 64;        // keys (dq, forward) or queries (dk, dv) per LDS tile
+constexpr int kRowsWg = 128;     // rows of the forward and dq workgroups: four waves of 32
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 // The lane's number, formed where it is called (the compiler cannot keep it).
@@ -163,7 +164,6 @@ __device__ __forceinline__ int seen(const AttnDev& a, int qi, int k_here) {
   return int(max(int64_t(0), min(int64_t(k_here), n)));
 }
 
-template <int ROWS>
 __device__ __forceinline__ Rows rows_of(const AttnDev& a, unsigned item, unsigned blocks, int wave, int lane) {
   Rows r;
   // Later rows see more keys under a causal border: they go first.
@@ -173,7 +173,7 @@ __device__ __forceinline__ Rows rows_of(const AttnDev& a, unsigned item, unsigne
   r.group = a.heads / a.kv_heads;
   r.q_here = clamp_len(a.q_lens, r.b, a.q_len);
   r.k_here = clamp_len(a.k_lens, r.b, a.k_len);
-  r.row0 = int(blk) * ROWS;
+  r.row0 = int(blk) * kRowsWg;
   const int row = r.row0 + wave * 32 + (lane & 31);
   r.qi = row / r.group;
   r.head = r.kvh * r.group + row % r.group;
@@ -190,9 +190,8 @@ __device__ __forceinline__ int wave_max(int v) {
 }
 
 // Keys that the last of the workgroup's rows sees (the most of any).
-template <int ROWS>
 __device__ __forceinline__ int seen_most(const AttnDev& a, const Rows& r) {
-  const int last = min((r.row0 + ROWS - 1) / r.group, r.q_here - 1);
+  const int last = min((r.row0 + kRowsWg - 1) / r.group, r.q_here - 1);
   return last < r.row0 / r.group ? 0 : seen(a, last, r.k_here);
 }
 
@@ -202,18 +201,25 @@ __device__ __forceinline__ int seen_most(const AttnDev& a, const Rows& r) {
 // exponents are taken against follows the running one only when that has
 // grown by more than 2^8 (the result does not depend on it), so that the
 // accumulators are rarely rescaled.
-template <int DB, int NW, bool SPLIT>
-__global__ __launch_bounds__(64 * NW, 2) void attn_fwd_kernel(AttnDev a, unsigned items, unsigned blocks) {
+//
+// Software pipeline: the products of the next tile's scores run between this
+// tile's exponentials, and the maxima of the next tile between the products
+// with v, so that the matrix cores and the vector units work at once.  The
+// order within a slot (one product, its fragment's successor, a piece of
+// arithmetic) is fixed; left to itself the compiler waits for each read at
+// once.
+template <int DB, bool SPLIT>
+__global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnDev a, unsigned items, unsigned blocks) {
   using G = Geo<DB>;
-  constexpr int ROWS = 32 * NW, NBUF = NW == 8 ? 3 : 2;
-  __shared__ __attribute__((aligned(1024))) unsigned char smem[NBUF * 2 * G::TILEB];   // k, v of each tile
+  constexpr int KS = G::KS, AHEAD = 3;
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[4 * G::TILEB];   // two of k, two of v
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const unsigned id = xcd_item(blockIdx.x, items);
   const unsigned split = SPLIT ? id % unsigned(a.splits) : 0;
-  const Rows r = rows_of<ROWS>(a, SPLIT ? id / unsigned(a.splits) : id, blocks, wave, lane);
+  const Rows r = rows_of(a, SPLIT ? id / unsigned(a.splits) : id, blocks, wave, lane);
   const int first = SPLIT ? int(split) * a.split_keys : 0;
-  const int most = seen_most<ROWS>(a, r), end = SPLIT ? min(most, first + a.split_keys) : most;
+  const int most = seen_most(a, r), end = SPLIT ? min(most, first + a.split_keys) : most;
   const int tiles = end > first ? (end - first + kTile - 1) / kTile : 0;
 
   u32x4_t q[2 * DB];
@@ -221,13 +227,16 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_fwd_kernel(AttnDev a, unsigne
   load_rows<DB>(q, qrow, r.live, a.dim, half);
   const uint16_t* kbase = static_cast<const uint16_t*>(a.k.p) + r.b * a.k.sb + r.kvh * a.k.sh + first * a.k.sl;
   const uint16_t* vbase = static_cast<const uint16_t*>(a.v.p) + r.b * a.v.sb + r.kvh * a.v.sh + first * a.v.sl;
-  const TileMove<DB, NW> mk(a.k.sl, a.dim, wave, lane), mv(a.v.sl, a.dim, wave, lane);
+  const TileMove<DB, 4> mk(a.k.sl, a.dim, wave, lane), mv(a.v.sl, a.dim, wave, lane);
   const TileRead<DB> rd(lane);
   const unsigned lds = lds_offset(smem);
-  auto fetch = [&](int t) {
-    const unsigned at = lds + unsigned(t % NBUF) * 2u * G::TILEB;
-    mk.issue(kbase + int64_t(t) * kTile * a.k.sl, r.k_here - first - t * kTile, at, wave);
-    mv.issue(vbase + int64_t(t) * kTile * a.v.sl, r.k_here - first - t * kTile, at + G::TILEB, wave);
+  const unsigned char* vs = smem + 2 * G::TILEB;
+  auto fetch_k = [&](int t) {
+    mk.issue(kbase + int64_t(t) * kTile * a.k.sl, r.k_here - first - t * kTile, lds + unsigned(t & 1) * G::TILEB, wave);
+  };
+  auto fetch_v = [&](int t) {
+    mv.issue(vbase + int64_t(t) * kTile * a.v.sl, r.k_here - first - t * kTile, lds + unsigned(2 + (t & 1)) * G::TILEB,
+             wave);
   };
 
   f32x16_t o[DB];
@@ -235,27 +244,10 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_fwd_kernel(AttnDev a, unsigne
   for (int db = 0; db < DB; ++db) o[db] = (f32x16_t)(0.f);
   const float c = a.scale * kLog2e;
   float top = -INFINITY, top_c = 0.f, sum = 0.f;
-  const int wave_see = wave_max(r.see), wave_all = -wave_max(r.ok ? -r.see : -0x7fffffff);
-
-  for (int t = 0; t < NBUF - 1; ++t)
-    if (t < tiles) fetch(t);
-  for (int t = 0; t < tiles; ++t) {
-    // tile t is in; the next may be on its way
-    if (NBUF == 3 && t + 1 < tiles) wait_vm<2 * TileMove<DB, NW>::N>();
-    else wait_vm<0>();
-    barrier();
-    if (t + NBUF - 1 < tiles) fetch(t + NBUF - 1);
-    const int key0 = first + t * kTile;
-    if (key0 >= wave_see) continue;
-    const unsigned char* kt = smem + (t % NBUF) * 2 * G::TILEB;
-    const unsigned char* vt = kt + G::TILEB;
-    f32x16_t s[2];
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      s[kb] = (f32x16_t)(0.f);
-#pragma unroll
-      for (int ks = 0; ks < G::KS; ++ks) s[kb] = mfma32(rd.rows(kt, ks, kb), q[ks], s[kb]);
-    }
+  const int wave_all = -wave_max(r.ok ? -r.see : -0x7fffffff);
+  const bool work = wave_max(r.see) > 0;
+  // Keys of a tile that a row does not see.
+  auto mask = [&](f32x16_t (&s)[2], int key0) {
     if (key0 + kTile > wave_all) {
       const int n = r.see - key0 - 4 * half;
 #pragma unroll
@@ -264,11 +256,9 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_fwd_kernel(AttnDev a, unsigne
         for (int v = 0; v < 16; ++v)
           if (32 * kb + 8 * (v >> 2) + (v & 3) >= n) s[kb][v] = -INFINITY;
     }
-    float m = s[0][0];
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) m = fmaxf(m, s[kb][v]);
+  };
+  // Raises the maximum where a tile's is much larger.
+  auto raise = [&](float m) {
     m = fmaxf(m, other_half(m));
     if (__any((m - top) * c > 8.f)) {        // also where top is -inf and m is not
       const float to = fmaxf(top, m);
@@ -281,21 +271,97 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_fwd_kernel(AttnDev a, unsigne
 #pragma unroll
         for (int v = 0; v < 16; ++v) o[db][v] *= f;
     }
-    u32x4_t p[4];
+  };
+
+  f32x16_t s0[2], s1[2];
+  if (tiles > 0) {
+    fetch_k(0);
+    fetch_v(0);
+    if (tiles > 1) fetch_k(1);
+    wait_vm<0>();
+    barrier();
+    if (work) {
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
+      for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        s[kb][v] = exp2_fast(fmaf(s[kb][v], c, -top_c));
-        sum += s[kb][v];
-      }
-      p[2 * kb] = pack8(s[kb], 0);
-      p[2 * kb + 1] = pack8(s[kb], 8);
+        for (int ks = 0; ks < KS; ++ks) s0[kb] = mfma32(rd.rows(smem, ks, kb), q[ks], ks ? s0[kb] : (f32x16_t)(0.f));
+      mask(s0, first);
+      float m = s0[0][0];
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) m = fmaxf(m, s0[kb][v]);
+      raise(m);
     }
+  }
+  // Tile t, whose scores are in s; the next tile's go to sn (past the last
+  // tile from what is in LDS, and unused).
+  auto step = [&](int t, f32x16_t (&s)[2], f32x16_t (&sn)[2]) {
+    if (t > 0) {
+      wait_vm<0>();
+      barrier();
+    }
+    // k of tile t was read in the step before, v of tile t - 1 too
+    if (t + 2 < tiles) fetch_k(t + 2);
+    if (t + 1 < tiles) fetch_v(t + 1);
+    if (!work) return;
+    const unsigned char* kt = smem + ((t + 1) & 1) * G::TILEB;
+    const unsigned char* vt = vs + (t & 1) * G::TILEB;
+    constexpr int N1 = 2 * KS, N2 = 4 * DB;
+    u32x4_t f[AHEAD], p[4];
+    auto fragment = [&](int n) {
+      return n < N1 ? rd.rows(kt, n % KS, n / KS) : rd.cols(vt, (n - N1) % DB, (n - N1) / DB);
+    };
+    auto slot_end = [&](int n) {
+      if (n + AHEAD < N1 + N2) f[n % AHEAD] = fragment(n + AHEAD);
+      __builtin_amdgcn_sched_barrier(0);
+    };
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int n = 0; n < AHEAD; ++n) f[n] = fragment(n);
+    __builtin_amdgcn_sched_barrier(0);
+    // 8 pieces of four values
+    auto probs = [&](int i) {
+      const int kb = i / 4, g = i % 4;
 #pragma unroll
-      for (int db = 0; db < DB; ++db) o[db] = mfma32(rd.cols(vt, db, j), p[j], o[db]);
+      for (int k = 0; k < 4; ++k) {
+        s[kb][4 * g + k] = exp2_fast(fmaf(s[kb][4 * g + k], c, -top_c));
+        sum += s[kb][4 * g + k];
+      }
+      if (g & 1) {
+        p[2 * kb + (g >> 1)] = pack8(s[kb], 8 * (g >> 1));
+        // pins the work here: it would be sunk past the mask's branch
+        asm volatile("" : "+v"(p[2 * kb + (g >> 1)]), "+v"(sum));
+      }
+    };
+#pragma unroll
+    for (int n = 0; n < N1; ++n) {
+      sn[n / KS] = mfma32(f[n % AHEAD], q[n % KS], n % KS ? sn[n / KS] : (f32x16_t)(0.f));
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i * N1 / 8 == n) probs(i);
+      slot_end(n);
+    }
+    mask(sn, first + (t + 1) * kTile);
+    __builtin_amdgcn_sched_barrier(0);
+    float m = -INFINITY;
+#pragma unroll
+    for (int n = N1; n < N1 + N2; ++n) {
+      const int j = (n - N1) / DB, db = (n - N1) % DB;
+      o[db] = mfma32(f[n % AHEAD], p[j], o[db]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i * N2 / 8 == n - N1) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) m = fmaxf(m, sn[i / 4][4 * (i % 4) + k]);
+          asm volatile("" : "+v"(m));
+        }
+      slot_end(n);
+    }
+    if (t + 1 < tiles) raise(m);
+  };
+  for (int t = 0; t < tiles; t += 2) {
+    step(t, s0, s1);
+    if (t + 1 < tiles) step(t + 1, s1, s0);
   }
   sum += other_half(sum);
   const float inv = sum == 0.f ? 0.f : 1.0f / sum;
@@ -358,15 +424,15 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnDev a) {
 // dq, and per row delta = do . o and the exponent's offset for the dk, dv
 // kernel.  Per tile of 64 keys, 32 at a time: s^T = k q^T, dp^T = v do^T,
 // ds^T = p^T (dp^T - delta), dq^T += k^T ds^T.
-template <int DB, int NW>
-__global__ __launch_bounds__(64 * NW, 2) void attn_dq_kernel(AttnDev a, unsigned items, unsigned blocks) {
+template <int DB>
+__global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnDev a, unsigned items, unsigned blocks) {
   using G = Geo<DB>;
-  constexpr int ROWS = 32 * NW, NBUF = NW == 8 ? 3 : 2;
-  __shared__ __attribute__((aligned(1024))) unsigned char smem[NBUF * 2 * G::TILEB];
+  constexpr int AHEAD = 3;
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[4 * G::TILEB];
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Rows r = rows_of<ROWS>(a, xcd_item(blockIdx.x, items), blocks, wave, lane);
-  const int end = seen_most<ROWS>(a, r);
+  const Rows r = rows_of(a, xcd_item(blockIdx.x, items), blocks, wave, lane);
+  const int end = seen_most(a, r);
   const int tiles = (end + kTile - 1) / kTile;
 
   u32x4_t q[2 * DB], g[2 * DB];
@@ -404,11 +470,11 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_dq_kernel(AttnDev a, unsigned
 
   const uint16_t* kbase = static_cast<const uint16_t*>(a.k.p) + r.b * a.k.sb + r.kvh * a.k.sh;
   const uint16_t* vbase = static_cast<const uint16_t*>(a.v.p) + r.b * a.v.sb + r.kvh * a.v.sh;
-  const TileMove<DB, NW> mk(a.k.sl, a.dim, wave, lane), mv(a.v.sl, a.dim, wave, lane);
+  const TileMove<DB, 4> mk(a.k.sl, a.dim, wave, lane), mv(a.v.sl, a.dim, wave, lane);
   const TileRead<DB> rd(lane);
   const unsigned lds = lds_offset(smem);
   auto fetch = [&](int t) {
-    const unsigned at = lds + unsigned(t % NBUF) * 2u * G::TILEB;
+    const unsigned at = lds + unsigned(t & 1) * 2u * G::TILEB;
     mk.issue(kbase + int64_t(t) * kTile * a.k.sl, r.k_here - t * kTile, at, wave);
     mv.issue(vbase + int64_t(t) * kTile * a.v.sl, r.k_here - t * kTile, at + G::TILEB, wave);
   };
@@ -418,39 +484,72 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_dq_kernel(AttnDev a, unsigned
   const float c = a.scale * kLog2e;
   const int wave_see = wave_max(r.see), wave_all = -wave_max(r.ok ? -r.see : -0x7fffffff);
 
-  for (int t = 0; t < NBUF - 1; ++t)
-    if (t < tiles) fetch(t);
+  if (tiles > 0) fetch(0);
   for (int t = 0; t < tiles; ++t) {
-    // tile t is in; the next may be on its way
-    if (NBUF == 3 && t + 1 < tiles) wait_vm<2 * TileMove<DB, NW>::N>();
-    else wait_vm<0>();
+    wait_vm<0>();
     barrier();
-    if (t + NBUF - 1 < tiles) fetch(t + NBUF - 1);
-    const int key0 = t * kTile;
-    if (key0 >= wave_see) continue;
-    const unsigned char* kt = smem + (t % NBUF) * 2 * G::TILEB;
+    if (t + 1 < tiles) fetch(t + 1);
+    if (t * kTile >= wave_see) continue;
+    const unsigned char* kt = smem + (t & 1) * 2 * G::TILEB;
     const unsigned char* vt = kt + G::TILEB;
+    // Slots as in the forward kernel: KS row reads of k, KS of v, 2 DB
+    // transposed reads of k.
+    constexpr int KS = G::KS, N = 2 * KS + 2 * DB;
+    u32x4_t f[AHEAD];
+    auto fragment = [&](int kb, int n) {
+      if (n < KS) return rd.rows(kt + kb * 32 * G::ROWB, n, 0);
+      if (n < 2 * KS) return rd.rows(vt + kb * 32 * G::ROWB, n - KS, 0);
+      return rd.cols(kt + kb * 32 * G::ROWB, (n - 2 * KS) % DB, (n - 2 * KS) / DB);
+    };
 #pragma unroll
+    for (int n = 0; n < AHEAD; ++n) f[n] = fragment(0, n);
+#pragma unroll 1
     for (int kb = 0; kb < 2; ++kb) {
-      f32x16_t s = (f32x16_t)(0.f), dp = (f32x16_t)(0.f);
+      const int key0 = t * kTile + 32 * kb;
+      f32x16_t s, dp;
+      u32x4_t ds[2];
+      auto slot_end = [&](int n) {
+        if (n + AHEAD < N) f[n % AHEAD] = fragment(kb, n + AHEAD);
+        else f[n % AHEAD] = fragment(1, n + AHEAD - N);   // of the second half (read again there: unused)
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      auto grads = [&](int g) {
 #pragma unroll
-      for (int ks = 0; ks < G::KS; ++ks) {
-        s = mfma32(rd.rows(kt, ks, kb), q[ks], s);
-        dp = mfma32(rd.rows(vt, ks, kb), g[ks], dp);
+        for (int k = 0; k < 4; ++k) s[4 * g + k] *= dp[4 * g + k] - delta;
+        if (g & 1) ds[g >> 1] = pack8(s, 8 * (g >> 1));
+      };
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int n = 0; n < KS; ++n) {
+        s = mfma32(f[n % AHEAD], q[n], n ? s : (f32x16_t)(0.f));
+        slot_end(n);
       }
-      if (key0 + 32 * kb + 32 > wave_all) {
-        const int n = r.see - key0 - 32 * kb - 4 * half;
+      if (key0 + 32 > wave_all) {
+        const int n = r.see - key0 - 4 * half;
 #pragma unroll
         for (int v = 0; v < 16; ++v)
           if (8 * (v >> 2) + (v & 3) >= n) s[v] = -INFINITY;
       }
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int v = 0; v < 16; ++v) s[v] = exp2_fast(fmaf(s[v], c, -lse)) * (dp[v] - delta);
+      for (int n = KS; n < 2 * KS; ++n) {
+        dp = mfma32(f[n % AHEAD], g[n - KS], n > KS ? dp : (f32x16_t)(0.f));
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const u32x4_t ds = pack8(s, 8 * j);
+        for (int i = 0; i < 4; ++i)
+          if (1 + i * (KS - 1) / 4 == n - KS) {
 #pragma unroll
-        for (int db = 0; db < DB; ++db) acc[db] = mfma32(rd.cols(kt, db, 2 * kb + j), ds, acc[db]);
+            for (int k = 0; k < 4; ++k) s[4 * i + k] = exp2_fast(fmaf(s[4 * i + k], c, -lse));
+          }
+        slot_end(n);
+      }
+      grads(0);
+      grads(1);
+#pragma unroll
+      for (int n = 2 * KS; n < N; ++n) {
+        const int m = n - 2 * KS;
+        acc[m % DB] = mfma32(f[n % AHEAD], ds[m / DB], acc[m % DB]);
+        if (m == 0) { grads(2); grads(3); }
+        slot_end(n);
       }
     }
   }
@@ -691,32 +790,27 @@ __global__ __launch_bounds__(256) void attn_dkv_join_kernel(AttnDev a, int64_t n
   store_vals<uint16_t, 8>(o.p, b * o.sb + key * o.sl + h * o.sh + (is_v ? c - cpr : c) * 8, v);
 }
 
-int64_t rows_in(const AttnDev& a) { return int64_t(a.q_len) * (a.heads / a.kv_heads); }
-// Workgroups of eight waves (256 rows) bring in a key tile for twice the rows
-// that four waves do; four are taken where 128 rows are all there are.
-int waves_of(const AttnDev& a) { return rows_in(a) > 128 ? 8 : 4; }
 unsigned row_blocks(const AttnDev& a) {
-  const int64_t rows = 32 * waves_of(a);
-  return unsigned((rows_in(a) + rows - 1) / rows);
+  const int64_t rows = int64_t(a.q_len) * (a.heads / a.kv_heads);
+  return unsigned((rows + kRowsWg - 1) / kRowsWg);
 }
 unsigned key_blocks(const AttnDev& a) { return unsigned((a.k_len + 255) / 256); }
 
-#define BY_DIM(K, ...)                                                                                       \
-  (a.dim <= 32 ? K<1, __VA_ARGS__> : a.dim <= 64 ? K<2, __VA_ARGS__> : a.dim <= 96 ? K<3, __VA_ARGS__>         \
-                                                                                   : K<4, __VA_ARGS__>)
-#define BY_DIM_ROWS(K, ...) (waves_of(a) == 8 ? BY_DIM(K, 8 __VA_ARGS__) : BY_DIM(K, 4 __VA_ARGS__))
+#define BY_DIM(K, ...)                                                                             \
+  (a.dim <= 32 ? K<1 __VA_ARGS__> : a.dim <= 64 ? K<2 __VA_ARGS__> : a.dim <= 96 ? K<3 __VA_ARGS__> \
+                                                                                 : K<4 __VA_ARGS__>)
 #define COMMA ,
 
 }  // namespace
 
 int attn_splits(const AttnDev& a, int* split_keys) {
-  // A workgroup of eight waves takes a CU, two of four waves fit.  With fewer
-  // than half of that, the keys are divided, in ranges of at least four tiles.
-  const int64_t items = int64_t(row_blocks(a)) * a.batch * a.kv_heads, slots = waves_of(a) == 8 ? 256 : 512;
+  // Two workgroups fit on each of 256 CUs.  With fewer than half of that,
+  // the keys are divided, in ranges of at least four tiles.
+  const int64_t items = int64_t(row_blocks(a)) * a.batch * a.kv_heads;
   const int tiles = (a.k_len + kTile - 1) / kTile;
   int64_t n = 1;
-  if (items > 0 && 2 * items < slots) {
-    n = slots / items;
+  if (items > 0 && items < 256) {
+    n = 512 / items;
     if (n > tiles / 4) n = tiles / 4;
     if (n < 1) n = 1;
   }
@@ -747,15 +841,15 @@ int attn_parts(const AttnDev& a) {
 }
 
 hipError_t launch_attn_fwd(hipStream_t s, const AttnDev& a) {
-  const unsigned blocks = row_blocks(a), threads = 64u * unsigned(waves_of(a));
+  const unsigned blocks = row_blocks(a);
   const unsigned items = blocks * unsigned(a.batch) * unsigned(a.kv_heads) * unsigned(a.splits);
   if (a.splits == 1) {
-    auto* k = BY_DIM_ROWS(attn_fwd_kernel, COMMA false);
-    hipLaunchKernelGGL(k, dim3(items), dim3(threads), 0, s, a, items, blocks);
+    auto* k = BY_DIM(attn_fwd_kernel, COMMA false);
+    hipLaunchKernelGGL(k, dim3(items), dim3(256), 0, s, a, items, blocks);
     return hipGetLastError();
   }
-  auto* k = BY_DIM_ROWS(attn_fwd_kernel, COMMA true);
-  hipLaunchKernelGGL(k, dim3(items), dim3(threads), 0, s, a, items, blocks);
+  auto* k = BY_DIM(attn_fwd_kernel, COMMA true);
+  hipLaunchKernelGGL(k, dim3(items), dim3(256), 0, s, a, items, blocks);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t lines = int64_t(a.batch) * a.heads * a.q_len;
@@ -767,14 +861,14 @@ hipError_t launch_attn_bwd(hipStream_t s, const AttnDev& a) {
   const unsigned bh = unsigned(a.batch) * unsigned(a.kv_heads);
   if (a.q_len > 0) {
     const unsigned blocks = row_blocks(a), items = blocks * bh;
-    auto* k = BY_DIM_ROWS(attn_dq_kernel, );
-    hipLaunchKernelGGL(k, dim3(items), dim3(64u * unsigned(waves_of(a))), 0, s, a, items, blocks);
+    auto* k = BY_DIM(attn_dq_kernel, );
+    hipLaunchKernelGGL(k, dim3(items), dim3(256), 0, s, a, items, blocks);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (a.k_len > 0) {
     const unsigned blocks = key_blocks(a), items = blocks * bh * unsigned(a.parts);
-    auto* k = BY_DIM(attn_dkv_kernel, 2);
+    auto* k = BY_DIM(attn_dkv_kernel, COMMA 2);
     hipLaunchKernelGGL(k, dim3(items), dim3(512), 0, s, a, items, blocks);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.parts == 1) return e;
