@@ -45,7 +45,12 @@ __device__ __forceinline__ int fresh_lane() {
   asm volatile("" : "+s"(all));
   return int(__builtin_amdgcn_mbcnt_hi(all, __builtin_amdgcn_mbcnt_lo(all, 0u)));
 }
-__device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32, 64); }
+// The value of the lane 32 away.
+__device__ __forceinline__ float other_half(float x) {
+  const unsigned u = __float_as_uint(x);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);   // (low of both, high of both)
+  return __uint_as_float(__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u)) < 32 ? r[1] : r[0]);
+}
 
 // Head geometry: DB blocks of 32 dims; LDS rows of PITCH 16-byte chunks.
 template <int DB>
@@ -310,7 +315,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnDev a, unsigned it
     constexpr int N1 = 2 * KS, N2 = 4 * DB;
     u32x4_t f[AHEAD], p[4];
     auto fragment = [&](int n) {
-      return n < N1 ? rd.rows(kt, n % KS, n / KS) : rd.cols(vt, (n - N1) % DB, (n - N1) / DB);
+      return n < N1 ? rd.rows(kt, n / 2, n & 1) : rd.cols(vt, (n - N1) % DB, (n - N1) / DB);
     };
     auto slot_end = [&](int n) {
       if (n + AHEAD < N1 + N2) f[n % AHEAD] = fragment(n + AHEAD);
@@ -335,7 +340,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnDev a, unsigned it
     };
 #pragma unroll
     for (int n = 0; n < N1; ++n) {
-      sn[n / KS] = mfma32(f[n % AHEAD], q[n % KS], n % KS ? sn[n / KS] : (f32x16_t)(0.f));
+      sn[n & 1] = mfma32(f[n % AHEAD], q[n / 2], n > 1 ? sn[n & 1] : (f32x16_t)(0.f));
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (i * N1 / 8 == n) probs(i);
