@@ -68,19 +68,33 @@ def _check(status: int) -> None:
         raise MuonError(status, _lib().muon_block_last_error().decode())
 
 
+def _stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# The handle of the current stream without the Python object around it (2 us
+# of a call's 15), where this torch has it.
+_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream)
+
+
 def _call(name: str, args: bytes, device, workspace: bool = True) -> None:
-    L = _lib()
-    if device.index != torch.cuda.current_device():
+    L = _READY or _lib()
+    index = device.index
+    if index != torch.cuda.current_device():
         with torch.cuda.device(device):
             return _call(name, args, device, workspace)
-    stream = torch.cuda.current_stream(device).cuda_stream
     if not workspace:
-        _check(getattr(L, name)(args, stream))
-        return
-    need = ctypes.c_size_t(0)
-    _check(getattr(L, name + "_workspace")(args, need))
-    ws = torch.empty(need.value, dtype=torch.uint8, device=device) if need.value else None
-    _check(getattr(L, name)(args, ws.data_ptr() if need.value else None, need.value, stream))
+        status = getattr(L, name)(args, _stream(index))
+    else:
+        need = ctypes.c_size_t(0)
+        _check(getattr(L, name + "_workspace")(args, need))
+        if need.value:
+            ws = torch.empty(need.value, dtype=torch.uint8, device=device)
+            status = getattr(L, name)(args, ws.data_ptr(), need.value, _stream(index))
+        else:
+            status = getattr(L, name)(args, None, 0, _stream(index))
+    if status != MUON_OK:
+        _check(status)
 
 
 def _device(first, *others):
@@ -92,6 +106,11 @@ def _device(first, *others):
         if t is not None and t.device != d:
             raise ValueError(f"tensors on {d} and {t.device}")
     return d
+
+
+def _out(t):
+    """A contiguous tensor of t's shape, type and device."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 def _mat(t, rows: int, cols: int):
@@ -159,8 +178,8 @@ def norm_fwd(resid, h=None, gate=None, post_weight=None, pre_weight=None, scale=
     if h is not None and h.shape != resid.shape:
         raise ValueError(f"h {tuple(h.shape)} and resid {tuple(resid.shape)}")
     want_y = k_pre != 0 or pre_weight is not None or scale is not None or shift is not None
-    out = resid if h is None else torch.empty(resid.shape, dtype=resid.dtype, device=dev)
-    y = torch.empty(resid.shape, dtype=(resid if h is None else h).dtype, device=dev) if want_y else None
+    out = resid if h is None else _out(resid)
+    y = _out(resid if h is None else h) if want_y else None
     stats = torch.empty((rows, 4), dtype=torch.float32, device=dev)
     if rows == 0 or cols == 0:
         return out, y, stats
@@ -189,9 +208,9 @@ def norm_bwd(d_resid_out, d_y, resid_out, h, stats, gate=None, post_weight=None,
         raise ValueError("stats is norm_fwd's third result")
     if d_y is None and (k_pre != 0 or pre_weight is not None or scale is not None or shift is not None):
         d_y = torch.zeros(x.shape, dtype=(x if h is None else h).dtype, device=dev)
-    d_h = None if h is None else torch.empty(h.shape, dtype=h.dtype, device=dev)
-    d_resid = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    vectors = [None if t is None else torch.empty(t.shape, dtype=t.dtype, device=dev)
+    d_h = None if h is None else _out(h)
+    d_resid = _out(x)
+    vectors = [None if t is None else _out(t)
                for t in (gate, scale, shift, post_weight, pre_weight)]
     if rows == 0 or cols == 0:
         for t in vectors:
@@ -283,7 +302,7 @@ def attn_fwd(q, k, v, *, causal: bool = False, offset: int = 0, q_lens=None, k_l
     lse = -inf."""
     dev = _device(q, k, v, q_lens, k_lens)
     b, m, n, h, g, d, scale = _attn_dims(q, k, v, q_lens, k_lens, scale)
-    o = torch.empty((b, m, h, d), dtype=torch.bfloat16, device=dev)
+    o = _out(q)                              # q's type is checked by _heads
     lse = torch.empty((b, h, m), dtype=torch.float32, device=dev)
     args = ATTN_ARGS.pack(b, m, n, h, g, d, int(causal), offset, scale, 0, _ptr(q_lens), _ptr(k_lens),
                           *_heads(q, "q"), *_heads(k, "k"), *_heads(v, "v"), *_heads(o, "o"), lse.data_ptr(),
@@ -302,7 +321,7 @@ def attn_bwd(d_o, q, k, v, o, lse, *, causal: bool = False, offset: int = 0, q_l
         raise ValueError(f"d_o {tuple(d_o.shape)}, o {tuple(o.shape)}, lse {tuple(lse.shape)} for q {tuple(q.shape)}")
     if lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse is attn_fwd's second result")
-    d_q, d_k, d_v = (torch.empty(t.shape, dtype=torch.bfloat16, device=dev) for t in (q, k, v))
+    d_q, d_k, d_v = _out(q), _out(k), _out(v)
     args = ATTN_ARGS.pack(b, m, n, h, g, d, int(causal), offset, scale, 0, _ptr(q_lens), _ptr(k_lens),
                           *_heads(q, "q"), *_heads(k, "k"), *_heads(v, "v"), *_heads(o, "o"), lse.data_ptr(),
                           *_heads(d_o, "d_o"), *_heads(d_q, "d_q"), *_heads(d_k, "d_k"), *_heads(d_v, "d_v"))
@@ -356,7 +375,7 @@ def ffn_fwd(x, w_gate, w_up, w_down, *, act: str = "silu", save: bool = True):
     save is false."""
     dev = _device(x, w_gate, w_up, w_down)
     rows, cols, hidden = _ffn_dims(x, w_gate, w_up, w_down, act)
-    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    y = _out(x)
     gu = torch.empty((rows, 2 * hidden), dtype=x.dtype, device=dev) if save else None
     if rows == 0:
         return y, gu
@@ -376,7 +395,7 @@ def ffn_bwd(d_y, x, w_gate, w_up, w_down, gu, *, act: str = "silu", grad_dtype=t
         raise ValueError(f"d_y {tuple(d_y.shape)} for x {tuple(x.shape)}")
     if grad_dtype not in _TYPES:
         raise TypeError(f"unsupported grad_dtype {grad_dtype}")
-    d_x = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    d_x = _out(x)
     grads = [torch.empty(w.shape, dtype=grad_dtype, device=dev) for w in (w_gate, w_up, w_down)]
     if rows == 0:
         return (d_x, *(w.zero_() for w in grads))

@@ -392,37 +392,47 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnDev a, unsigned it
   }
 }
 
-// Joins the key ranges of one row: weights exp(lse_i - lse) add up to 1.
-// Sixteen lanes per row, eight dims each.
+// Joins the key ranges of one row: weights exp(lse_i - lse) add up to 1.  A
+// wave per row: its lanes take the ranges' weights at once, then groups of 16
+// lanes, eight dims each, every fourth range.
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnDev a) {
   const int64_t lines = int64_t(a.batch) * a.heads * a.q_len;
-  const int64_t line = int64_t(blockIdx.x) * 16 + (threadIdx.x >> 4);
+  const int64_t line = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
   if (line >= lines) return;
-  const int d = (threadIdx.x & 15) * 8;
+  const int lane = threadIdx.x & 63, d = (lane & 15) * 8;
   float top = -INFINITY;
-  for (int i = 0; i < a.splits; ++i) top = fmaxf(top, *as_global(a.part_lse + i * lines + line));
+  for (int i = lane; i < a.splits; i += 64) top = fmaxf(top, *as_global(a.part_lse + i * lines + line));
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
   float sum = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (top != -INFINITY) {
-    for (int i = 0; i < a.splits; ++i) {
+#pragma unroll 4
+    for (int i = lane >> 4; i < a.splits; i += 4) {
       const float w = exp2_fast((*as_global(a.part_lse + i * lines + line) - top) * kLog2e);
       sum += w;
-      if (d < a.dim && w != 0.f) {
+      if (d < a.dim) {
         float t[8];
         load_vals<float, 8>(a.part_o, (i * lines + line) * a.dim + d, t);
 #pragma unroll
         for (int k = 0; k < 8; ++k) o[k] = fmaf(w, t[k], o[k]);
       }
     }
+#pragma unroll
+    for (int x = 16; x <= 32; x <<= 1) {
+      sum += __shfl_xor(sum, x, 64);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[k] += __shfl_xor(o[k], x, 64);
+    }
   }
   const int qi = int(line % a.q_len);
   const int64_t bh = line / a.q_len;
-  if (d < a.dim) {
+  if (lane < 16 && d < a.dim) {
     const float inv = sum == 0.f ? 0.f : 1.0f / sum;
 #pragma unroll
     for (int k = 0; k < 8; ++k) o[k] *= inv;
     store_vals<uint16_t, 8>(a.o.p, (bh / a.heads) * a.o.sb + qi * a.o.sl + (bh % a.heads) * a.o.sh + d, o);
   }
-  if (d == 0) *as_global(a.lse + line) = sum == 0.f ? -INFINITY : top + __builtin_amdgcn_logf(sum) * kLn2;
+  if (lane == 0) *as_global(a.lse + line) = sum == 0.f ? -INFINITY : top + __builtin_amdgcn_logf(sum) * kLn2;
 }
 
 // ---------------------------------------------------------------------------
@@ -858,7 +868,7 @@ hipError_t launch_attn_fwd(hipStream_t s, const AttnDev& a) {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t lines = int64_t(a.batch) * a.heads * a.q_len;
-  hipLaunchKernelGGL(attn_join_kernel, dim3(unsigned((lines + 15) / 16)), dim3(256), 0, s, a);
+  hipLaunchKernelGGL(attn_join_kernel, dim3(unsigned((lines + 3) / 4)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

@@ -181,63 +181,92 @@ __device__ __forceinline__ Tile tile_of(const ProdArgs& g, int item) {
 template <int BT, int EPI>
 constexpr int tile_cols() { return EPI == EPI_GATE ? BT / 2 : BT; }
 
-// 16 rows of a wave's part of a tile, from its accumulators (a lane has four
-// columns of one row per block) through a part of LDS of the wave's own: a
-// lane then takes eight consecutive columns, so that rows are read and
-// written 16 bytes at a time.
-template <int BT, int EPI, int ACT>
-__device__ __forceinline__ void emit_rows(const Prod& p, const f32x4_t (&acc)[BT / 32], float* er, int64_t mrow,
+// 16 XB rows of a wave's part of a tile, from its accumulators (a lane has
+// four columns of one row per block) through a part of LDS of the wave's own:
+// a lane then takes eight consecutive columns, so that rows are read and
+// written 16 bytes at a time.  EPI_DGATE reads g and u for four such pieces
+// at once, the first four before the accumulators go to LDS: read one by one,
+// their latency took 60 us of the 967 of the dh product of 4096 x 20480 x 5120.
+template <int BT, int EPI, int ACT, int XB>
+__device__ __forceinline__ void emit_rows(const Prod& p, const f32x4_t (*acc)[BT / 32], float* er, int64_t mrow,
                                           int64_t ncol, int lane) {
   constexpr int F = BT / 32, W = BT / 2, LDR = W + 4;
   constexpr int WOUT = tile_cols<BT, EPI>() / 2;
+  constexpr int CPR = WOUT / 8, NIT = 16 * XB * CPR / 64, GRP = NIT < 4 ? NIT : 4;
+  static_assert(NIT * 64 == 16 * XB * CPR && NIT % GRP == 0, "whole pieces per lane");
+  const int64_t m_at = mrow + lane / CPR, n = ncol + lane % CPR * 8;   // + 64 / CPR rows per piece
+  const bool n_ok = n < p.n;
+  u32x4_t raw[GRP][2];
+  auto load_gu = [&](int it) {
+    if constexpr (EPI == EPI_DGATE) {
 #pragma unroll
-  for (int y = 0; y < F; ++y) {
-    const int col = EPI == EPI_GATE ? (y >> 1) * 16 + (y & 1) * WOUT : y * 16;
-    *(MUON_LOCAL f32x4_t*)(MUON_LOCAL float*)(er + (lane & 15) * LDR + col + 4 * (lane >> 4)) = acc[y];
-  }
+      for (int j = 0; j < GRP; ++j) {
+        const int64_t m = m_at + (it + j) * (64 / CPR);
+        raw[j][0] = raw[j][1] = u32x4_t{0, 0, 0, 0};
+        if (n_ok && m < p.m) {
+          const uint16_t* gu = static_cast<const uint16_t*>(p.gu) + m * p.ldgu + n;
+          raw[j][0] = *as_global(reinterpret_cast<const u32x4_t*>(gu));
+          raw[j][1] = *as_global(reinterpret_cast<const u32x4_t*>(gu + p.n));
+        }
+      }
+    }
+  };
+  load_gu(0);
+#pragma unroll
+  for (int x = 0; x < XB; ++x)
+#pragma unroll
+    for (int y = 0; y < F; ++y) {
+      const int col = EPI == EPI_GATE ? (y >> 1) * 16 + (y & 1) * WOUT : y * 16;
+      *(MUON_LOCAL f32x4_t*)(MUON_LOCAL float*)(er + (16 * x + (lane & 15)) * LDR + col + 4 * (lane >> 4)) = acc[x][y];
+    }
   __builtin_amdgcn_wave_barrier();
 #pragma unroll 1
-  for (int j = lane; j < 16 * WOUT / 8; j += 64) {
-    const int row = j / (WOUT / 8), col = j % (WOUT / 8) * 8;
-    const int64_t m = mrow + row, n = ncol + col;
-    float v[8];
-    const MUON_LOCAL float* q = (const MUON_LOCAL float*)(er + row * LDR + col);
+  for (int it = 0; it < NIT; it += GRP) {
+    if (it > 0) load_gu(it);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = q[k];
-    if (m >= p.m || n >= p.n) continue;
-    if constexpr (EPI == EPI_GATE) {
-      float u[8], h[8], d;
+    for (int j = 0; j < GRP; ++j) {
+      const int row = lane / CPR + (it + j) * (64 / CPR);
+      const int64_t m = mrow + row;
+      float v[8];
+      const MUON_LOCAL float* q = (const MUON_LOCAL float*)(er + row * LDR + lane % CPR * 8);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) u[k] = q[WOUT + k];
+      for (int k = 0; k < 8; ++k) v[k] = q[k];
+      if (!n_ok || m >= p.m) continue;
+      if constexpr (EPI == EPI_GATE) {
+        float u[8], h[8], d;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        act_of<ACT>(v[k], h[k], d);
-        h[k] *= u[k];
+        for (int k = 0; k < 8; ++k) u[k] = q[WOUT + k];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          act_of<ACT>(v[k], h[k], d);
+          h[k] *= u[k];
+        }
+        if (p.c2) {
+          store_vals<uint16_t, 8>(p.c2, m * p.ldc2 + n, v);
+          store_vals<uint16_t, 8>(p.c2, m * p.ldc2 + p.n + n, u);
+        }
+        store_vals<uint16_t, 8>(p.c, m * p.ldc + n, h);
+      } else if constexpr (EPI == EPI_DGATE) {
+        float h[8], dg[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const unsigned gb = raw[j][0][k / 2], ub = raw[j][1][k / 2];
+          const float gv = k & 1 ? __uint_as_float(gb & 0xffff0000u) : bf16_to_f32(gb & 0xffffu);
+          const float uv = k & 1 ? __uint_as_float(ub & 0xffff0000u) : bf16_to_f32(ub & 0xffffu);
+          float av, da;
+          act_of<ACT>(gv, av, da);
+          h[k] = av * uv;
+          dg[k] = v[k] * uv * da;
+          v[k] *= av;
+        }
+        store_vals<uint16_t, 8>(p.c, m * p.ldc + n, dg);
+        store_vals<uint16_t, 8>(p.c, m * p.ldc + p.n + n, v);
+        store_vals<uint16_t, 8>(p.c2, m * p.ldc2 + n, h);
+      } else if constexpr (EPI == EPI_F32) {
+        store_vals<float, 8>(p.c, m * p.ldc + n, v);
+      } else {
+        store_vals<uint16_t, 8>(p.c, m * p.ldc + n, v);
       }
-      if (p.c2) {
-        store_vals<uint16_t, 8>(p.c2, m * p.ldc2 + n, v);
-        store_vals<uint16_t, 8>(p.c2, m * p.ldc2 + p.n + n, u);
-      }
-      store_vals<uint16_t, 8>(p.c, m * p.ldc + n, h);
-    } else if constexpr (EPI == EPI_DGATE) {
-      float gv[8], uv[8];
-      load_vals<uint16_t, 8>(p.gu, m * p.ldgu + n, gv);
-      load_vals<uint16_t, 8>(p.gu, m * p.ldgu + p.n + n, uv);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        float av, da;
-        act_of<ACT>(gv[k], av, da);
-        gv[k] = av * uv[k];
-        uv[k] *= v[k] * da;
-        v[k] *= av;
-      }
-      store_vals<uint16_t, 8>(p.c, m * p.ldc + n, uv);
-      store_vals<uint16_t, 8>(p.c, m * p.ldc + p.n + n, v);
-      store_vals<uint16_t, 8>(p.c2, m * p.ldc2 + n, gv);
-    } else if constexpr (EPI == EPI_F32) {
-      store_vals<float, 8>(p.c, m * p.ldc + n, v);
-    } else {
-      store_vals<uint16_t, 8>(p.c, m * p.ldc + n, v);
     }
   }
   __builtin_amdgcn_wave_barrier();
@@ -356,17 +385,20 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void ffn_gemm_kernel(ProdAr
 
   if (range >= 0) {
     float* o = g.part + (int64_t(range) * 4 + wave) * (F * F * 256) + lane * 4;
+    // blocks of 16 rows that the matrix has
 #pragma unroll
     for (int x = 0; x < F; ++x)
+      if (m0 + wm * (BT / 2) + x * 16 < p.m)
 #pragma unroll
-      for (int y = 0; y < F; ++y) *as_global(reinterpret_cast<f32x4_t*>(o + (x * F + y) * 256)) = acc[x][y];
+        for (int y = 0; y < F; ++y) *as_global(reinterpret_cast<f32x4_t*>(o + (x * F + y) * 256)) = acc[x][y];
     return;
   }
-  static_assert(4 * 16 * (BT / 2 + 4) * 4 <= NSTAGE * STAGE, "epilogue rows fit");
-  float* er = reinterpret_cast<float*>(smem) + wave * 16 * (BT / 2 + 4);
+  constexpr int XB = 2;
+  static_assert(4 * 16 * XB * (BT / 2 + 4) * 4 <= NSTAGE * STAGE, "epilogue rows fit");
+  float* er = reinterpret_cast<float*>(smem) + wave * 16 * XB * (BT / 2 + 4);
 #pragma unroll
-  for (int x = 0; x < F; ++x)
-    emit_rows<BT, EPI, ACT>(p, acc[x], er, m0 + wm * (BT / 2) + x * 16, n0 + wn * (NSTEP / 2), lane);
+  for (int x = 0; x < F; x += XB)
+    emit_rows<BT, EPI, ACT, XB>(p, &acc[x], er, m0 + wm * (BT / 2) + x * 16, n0 + wn * (NSTEP / 2), lane);
 }
 
 // Adds the ranges of one split tile, 16 rows of each wave's part per
@@ -380,16 +412,17 @@ __global__ __launch_bounds__(256) void ffn_join_kernel(ProdArgs g) {
   const int tile = blockIdx.x / F, x = blockIdx.x % F;
   const Tile t = tile_of(g, g.full + tile);
   const Prod& p = g.p[t.which];
-  f32x4_t acc[F];
+  if (int64_t(t.tm) * BT + (wave >> 1) * (BT / 2) + x * 16 >= p.m) return;   // a whole wave, no barrier follows
+  f32x4_t acc[1][F];
 #pragma unroll
-  for (int y = 0; y < F; ++y) acc[y] = (f32x4_t)(0.f);
+  for (int y = 0; y < F; ++y) acc[0][y] = (f32x4_t)(0.f);
 #pragma unroll 4
   for (int i = 0; i < g.splits; ++i) {
     const float* o = g.part + (int64_t(tile * g.splits + i) * 4 + wave) * (F * F * 256) + lane * 4;
 #pragma unroll
-    for (int y = 0; y < F; ++y) acc[y] += *as_global(reinterpret_cast<const f32x4_t*>(o + (x * F + y) * 256));
+    for (int y = 0; y < F; ++y) acc[0][y] += *as_global(reinterpret_cast<const f32x4_t*>(o + (x * F + y) * 256));
   }
-  emit_rows<BT, EPI, ACT>(p, acc, rows + wave * 16 * (BT / 2 + 4),
+  emit_rows<BT, EPI, ACT, 1>(p, acc, rows + wave * 16 * (BT / 2 + 4),
                           int64_t(t.tm) * BT + (wave >> 1) * (BT / 2) + x * 16,
                           int64_t(t.tn) * tile_cols<BT, EPI>() + (wave & 1) * (tile_cols<BT, EPI>() / 2), lane);
 }
@@ -397,47 +430,51 @@ __global__ __launch_bounds__(256) void ffn_join_kernel(ProdArgs g) {
 
 // How a list of products is run.  A workgroup of a 256-tile takes a CU, of
 // 128-tiles two fit.  Tiles beyond the last whole round over the CUs would
-// leave most of them idle; their sums over k are divided so that they fill
-// one more, shorter round.
+// leave most of them idle; where that is worth a second kernel, their sums
+// over k are divided so that they fill one more, shorter round.
+//
+// The choice goes by the time of each way, from what was measured on this
+// card: a stage takes 0.78 us in 256-tiles and 0.6 us in two 128-tiles of a CU
+// (which do half the work), a tile's start and epilogue 11 and 7 us, and a
+// join 4 us and its partial sums' writing and reading at 4.5 TB/s.
 struct Plan {
   int bt, tiles, full, splits, split_stages;
-  double time;              // in stages of a 256-tile
+  double us;
 };
 Plan plan_with(const ProdArgs& g, int bt, bool gate) {
   Plan q{};
   q.bt = bt;
   const int nstep = gate ? bt / 2 : bt, slots = bt == 256 ? 256 : 512;
-  int stages = 0;
+  const double stage_us = bt == 256 ? 0.78 : 0.6, tile_us = bt == 256 ? 11 : 7;
+  int stages = 0, rows = 0;
   for (int i = 0; i < g.count; ++i) {
     q.tiles += ((g.p[i].m + bt - 1) / bt) * ((g.p[i].n + nstep - 1) / nstep);
     const int st = (g.p[i].k + kStageK - 1) / kStageK * g.segments;
     stages = st > stages ? st : stages;
+    rows = g.p[i].m > rows ? g.p[i].m : rows;
   }
-  const int rem = q.tiles % slots;
+  const int rem = q.tiles % slots, whole = q.tiles / slots;
+  const double tile = stages * stage_us + tile_us;
   q.full = q.tiles;
   q.splits = 1;
   q.split_stages = stages;
-  double rounds = (q.tiles + slots - 1) / slots;
-  if (rem > 0) {
-    // ranges of 8 stages at least: a range costs its pipeline's start, the
-    // writing of its tile in fp32 and the reading back
-    int n = slots / rem;
-    if (n > stages / 8) n = stages / 8;
-    if (n > 1) {
-      q.split_stages = (stages + n - 1) / n;
-      q.splits = (stages + q.split_stages - 1) / q.split_stages;
+  q.us = (whole + (rem > 0)) * tile;
+  const double part_mb = double(bt) * (rows < bt ? (rows + 15) / 16 * 16 : bt) * 4e-6;
+  for (int n = 2; rem > 0 && n <= slots / rem && n <= stages / 4; ++n) {
+    const int per = (stages + n - 1) / n, got = (stages + per - 1) / per;
+    const double us = whole * tile + per * stage_us + tile_us + 4 + 2 * rem * got * part_mb / 4.5;
+    if (us < q.us) {
+      q.us = us;
+      q.splits = got;
+      q.split_stages = per;
       q.full = q.tiles - rem;
-      rounds = q.full / slots + (double(q.split_stages) + 16.0) / stages;
     }
   }
-  // Two 128-tiles of a CU do half the work of a 256-tile in about 0.65 of its
-  // time (measured on long sums).
-  q.time = rounds * (stages + 12) * (bt == 256 ? 1.0 : 0.65);
   return q;
 }
 Plan plan_of(const ProdArgs& g, bool gate) {
   const Plan big = plan_with(g, 256, gate), small = plan_with(g, 128, gate);
-  return big.time <= small.time ? big : small;
+  return big.us <= small.us ? big : small;
 }
 size_t part_bytes(const Plan& q) {
   return q.full == q.tiles ? 0 : size_t(q.tiles - q.full) * q.splits * q.bt * q.bt * 4;
