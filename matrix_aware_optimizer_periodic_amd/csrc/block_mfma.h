@@ -35,9 +35,10 @@ __device__ __forceinline__ u32x4_t buffer_at(const void* p) {
 // wait_vm() and barriers.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"   // m0 is reserved; naming it is what is meant
-__device__ __forceinline__ void dma16(u32x4_t rsrc, unsigned lds_addr, unsigned voff) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :: "s"(lds_addr), "v"(voff), "s"(rsrc) : "m0", "memory");
+// soff is added to every lane's offset; kBufNone stays out of range with it.
+__device__ __forceinline__ void dma16(u32x4_t rsrc, unsigned lds_addr, unsigned voff, unsigned soff = 0) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :: "s"(lds_addr), "v"(voff), "s"(rsrc), "s"(__builtin_amdgcn_readfirstlane(int(soff))) : "m0", "memory");
 }
 __device__ __forceinline__ void dma4(u32x4_t rsrc, unsigned lds_addr, unsigned voff) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"

@@ -28,6 +28,7 @@
 // queries share the key tiles of one workgroup.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "block_mfma.h"
 
@@ -74,18 +75,24 @@ struct TileMove {
   static_assert(STEP % 16 == 0, "a lane's swizzle is the same in all of its rows");
   unsigned voff;
   int row0;
-  int64_t step;
+  unsigned step;                                      // bytes
   __device__ __forceinline__ TileMove(int64_t stride, int dim, int wave, int lane) {
     row0 = wave * (64 / P) + lane / P;
     const int chunk = (lane % P) ^ Geo<DB>::swz(row0);
     voff = chunk * 8 < dim ? unsigned(int64_t(row0) * stride * 2 + chunk * 16) : kBufNone;
-    step = STEP * stride;
+    step = unsigned(STEP * stride * 2);
   }
   __device__ __forceinline__ void issue(const uint16_t* tile, int there, unsigned lds, int wave) const {
+    const u32x4_t r = buffer_at(tile);
+    if (there >= kTile) {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      dma16(buffer_at(tile + i * step), lds + unsigned(wave + WAVES * i) * 1024u,
-            row0 + i * STEP < there ? voff : kBufNone);
+      for (int i = 0; i < N; ++i) dma16(r, lds + unsigned(wave + WAVES * i) * 1024u, voff, unsigned(i) * step);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        dma16(r, lds + unsigned(wave + WAVES * i) * 1024u, row0 + i * STEP < there ? voff : kBufNone,
+              unsigned(i) * step);
+    }
   }
 };
 
@@ -99,6 +106,14 @@ __device__ __forceinline__ void load_rows(u32x4_t (&f)[2 * DB], const uint16_t* 
     f[ks] = u32x4_t{0, 0, 0, 0};
     if (ok && d < dim) f[ks] = *as_global(reinterpret_cast<const u32x4_t*>(row + d));
   }
+}
+
+// Makes the compiler wait for loaded fragments here.  Left to their first use
+// in a loop it would wait there in every round, and so for the DMA in flight.
+template <int N>
+__device__ __forceinline__ void arrived(u32x4_t (&f)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+v"(f[i]));
 }
 
 // This lane's reads within a tile: row reads (32 rows of one chunk) and
@@ -127,6 +142,42 @@ struct TileRead {
   }
 };
 
+// The same with every offset in a register of its own, for kernels that have
+// room for them: no arithmetic per read (a quarter of the forward kernel's
+// vector instructions were these xors).  `at` is a constant.
+template <int DB>
+struct TileOffsets {
+  using G = Geo<DB>;
+  unsigned row[2 * DB], tr[DB][2];
+  __device__ __forceinline__ explicit TileOffsets(int lane, const unsigned char* smem) {
+    const TileRead<DB> r(lane);
+    const unsigned lds = lds_offset(smem);
+#pragma unroll
+    for (int ks = 0; ks < 2 * DB; ++ks) {
+      row[ks] = lds + (r.row ^ unsigned(32 * ks));
+      asm volatile("" : "+v"(row[ks]));
+    }
+#pragma unroll
+    for (int db = 0; db < DB; ++db)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        tr[db][u] = lds + (r.tr ^ unsigned(64 * db) ^ unsigned(32 * u));
+        asm volatile("" : "+v"(tr[db][u]));
+      }
+  }
+  __device__ __forceinline__ u32x4_t rows(unsigned at, int ks, int block) const {
+    return *(const MUON_LOCAL u32x4_t*)(uintptr_t)(row[ks] + at + unsigned(block * 32 * G::ROWB));
+  }
+  __device__ __forceinline__ u32x4_t cols(unsigned at, int db, int step) const {
+    const unsigned o = at + unsigned(step * 16 * G::ROWB);
+    const u32x2_t a = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                      (MUON_LOCAL s16x4_t*)(uintptr_t)(tr[db][0] + o)));
+    const u32x2_t b = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                      (MUON_LOCAL s16x4_t*)(uintptr_t)(tr[db][1] + o + 8u * G::ROWB)));
+    return u32x4_t{a[0], a[1], b[0], b[1]};
+  }
+};
+
 // Eight results of a product as the next product's operand.
 __device__ __forceinline__ u32x4_t pack8(const f32x16_t& s, int from) {
   return u32x4_t{pack_bf16x2(s[from], s[from + 1]), pack_bf16x2(s[from + 2], s[from + 3]),
@@ -150,7 +201,7 @@ __device__ __forceinline__ void store_rows(const f32x16_t (&acc)[DB], float mul,
 }
 
 __device__ __forceinline__ int clamp_len(const int32_t* lens, int b, int most) {
-  return lens ? min(max(lens[b], 0), most) : most;
+  return __builtin_amdgcn_readfirstlane(lens ? min(max(lens[b], 0), most) : most);
 }
 
 // Which rows a workgroup of the forward or dq kernel has, and what they see.
@@ -233,9 +284,8 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnDev a, unsigned it
   const uint16_t* kbase = static_cast<const uint16_t*>(a.k.p) + r.b * a.k.sb + r.kvh * a.k.sh + first * a.k.sl;
   const uint16_t* vbase = static_cast<const uint16_t*>(a.v.p) + r.b * a.v.sb + r.kvh * a.v.sh + first * a.v.sl;
   const TileMove<DB, 4> mk(a.k.sl, a.dim, wave, lane), mv(a.v.sl, a.dim, wave, lane);
-  const TileRead<DB> rd(lane);
+  const TileOffsets<DB> rd(lane, smem);
   const unsigned lds = lds_offset(smem);
-  const unsigned char* vs = smem + 2 * G::TILEB;
   auto fetch_k = [&](int t) {
     mk.issue(kbase + int64_t(t) * kTile * a.k.sl, r.k_here - first - t * kTile, lds + unsigned(t & 1) * G::TILEB, wave);
   };
@@ -283,13 +333,16 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnDev a, unsigned it
     fetch_k(0);
     fetch_v(0);
     if (tiles > 1) fetch_k(1);
-    wait_vm<0>();
-    barrier();
+  }
+  wait_vm<0>();
+  barrier();
+  arrived(q);
+  if (tiles > 0) {
     if (work) {
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) s0[kb] = mfma32(rd.rows(smem, ks, kb), q[ks], ks ? s0[kb] : (f32x16_t)(0.f));
+        for (int ks = 0; ks < KS; ++ks) s0[kb] = mfma32(rd.rows(0, ks, kb), q[ks], ks ? s0[kb] : (f32x16_t)(0.f));
       mask(s0, first);
       float m = s0[0][0];
 #pragma unroll
@@ -301,7 +354,8 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnDev a, unsigned it
   }
   // Tile t, whose scores are in s; the next tile's go to sn (past the last
   // tile from what is in LDS, and unused).
-  auto step = [&](int t, f32x16_t (&s)[2], f32x16_t (&sn)[2]) {
+  auto step = [&](int t, auto odd, f32x16_t (&s)[2], f32x16_t (&sn)[2]) {
+    constexpr int ODD = decltype(odd)::value;
     if (t > 0) {
       wait_vm<0>();
       barrier();
@@ -310,8 +364,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnDev a, unsigned it
     if (t + 2 < tiles) fetch_k(t + 2);
     if (t + 1 < tiles) fetch_v(t + 1);
     if (!work) return;
-    const unsigned char* kt = smem + ((t + 1) & 1) * G::TILEB;
-    const unsigned char* vt = vs + (t & 1) * G::TILEB;
+    constexpr unsigned kt = (ODD ^ 1) * G::TILEB, vt = (2 + ODD) * G::TILEB;
     constexpr int N1 = 2 * KS, N2 = 4 * DB;
     u32x4_t f[AHEAD], p[4];
     auto fragment = [&](int n) {
@@ -365,8 +418,8 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnDev a, unsigned it
     if (t + 1 < tiles) raise(m);
   };
   for (int t = 0; t < tiles; t += 2) {
-    step(t, s0, s1);
-    if (t + 1 < tiles) step(t + 1, s1, s0);
+    step(t, std::integral_constant<int, 0>{}, s0, s1);
+    if (t + 1 < tiles) step(t + 1, std::integral_constant<int, 1>{}, s1, s0);
   }
   sum += other_half(sum);
   const float inv = sum == 0.f ? 0.f : 1.0f / sum;
@@ -500,6 +553,8 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnDev a, unsigned ite
   const int wave_see = wave_max(r.see), wave_all = -wave_max(r.ok ? -r.see : -0x7fffffff);
 
   if (tiles > 0) fetch(0);
+  arrived(q);
+  arrived(g);
   for (int t = 0; t < tiles; ++t) {
     wait_vm<0>();
     barrier();
@@ -507,65 +562,66 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnDev a, unsigned ite
     if (t * kTile >= wave_see) continue;
     const unsigned char* kt = smem + (t & 1) * 2 * G::TILEB;
     const unsigned char* vt = kt + G::TILEB;
-    // Slots as in the forward kernel: KS row reads of k, KS of v, 2 DB
-    // transposed reads of k.
-    constexpr int KS = G::KS, N = 2 * KS + 2 * DB;
-    u32x4_t f[AHEAD];
-    auto fragment = [&](int kb, int n) {
-      if (n < KS) return rd.rows(kt + kb * 32 * G::ROWB, n, 0);
-      if (n < 2 * KS) return rd.rows(vt + kb * 32 * G::ROWB, n - KS, 0);
-      return rd.cols(kt + kb * 32 * G::ROWB, (n - 2 * KS) % DB, (n - 2 * KS) / DB);
+    // Slots as in the forward kernel: 2 KS row reads of k, 2 KS of v (the two
+    // halves of the tile in turn), 4 DB transposed reads of k.
+    constexpr int KS = G::KS, N = 4 * KS + 4 * DB;
+    u32x4_t f[AHEAD], ds[4];
+    f32x16_t s[2], dp[2];
+    auto fragment = [&](int n) {
+      if (n < 2 * KS) return rd.rows(kt, n / 2, n & 1);
+      if (n < 4 * KS) return rd.rows(vt, (n - 2 * KS) / 2, n & 1);
+      return rd.cols(kt, (n - 4 * KS) % DB, (n - 4 * KS) / DB);
+    };
+    auto slot_end = [&](int n) {
+      if (n + AHEAD < N) f[n % AHEAD] = fragment(n + AHEAD);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto grads = [&](int i) {
+      const int kb = i / 4, g = i % 4;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[kb][4 * g + k] *= dp[kb][4 * g + k] - delta;
+      if (g & 1) ds[2 * kb + (g >> 1)] = pack8(s[kb], 8 * (g >> 1));
     };
 #pragma unroll
-    for (int n = 0; n < AHEAD; ++n) f[n] = fragment(0, n);
-#pragma unroll 1
-    for (int kb = 0; kb < 2; ++kb) {
-      const int key0 = t * kTile + 32 * kb;
-      f32x16_t s, dp;
-      u32x4_t ds[2];
-      auto slot_end = [&](int n) {
-        if (n + AHEAD < N) f[n % AHEAD] = fragment(kb, n + AHEAD);
-        else f[n % AHEAD] = fragment(1, n + AHEAD - N);   // of the second half (read again there: unused)
-        __builtin_amdgcn_sched_barrier(0);
-      };
-      auto grads = [&](int g) {
+    for (int n = 0; n < AHEAD; ++n) f[n] = fragment(n);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) s[4 * g + k] *= dp[4 * g + k] - delta;
-        if (g & 1) ds[g >> 1] = pack8(s, 8 * (g >> 1));
-      };
-      __builtin_amdgcn_sched_barrier(0);
+    for (int n = 0; n < 2 * KS; ++n) {
+      s[n & 1] = mfma32(f[n % AHEAD], q[n / 2], n > 1 ? s[n & 1] : (f32x16_t)(0.f));
+      slot_end(n);
+    }
+    if ((t + 1) * kTile > wave_all) {
+      const int n = r.see - t * kTile - 4 * half;
 #pragma unroll
-      for (int n = 0; n < KS; ++n) {
-        s = mfma32(f[n % AHEAD], q[n], n ? s : (f32x16_t)(0.f));
-        slot_end(n);
-      }
-      if (key0 + 32 > wave_all) {
-        const int n = r.see - key0 - 4 * half;
+      for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
         for (int v = 0; v < 16; ++v)
-          if (8 * (v >> 2) + (v & 3) >= n) s[v] = -INFINITY;
-      }
-      __builtin_amdgcn_sched_barrier(0);
+          if (32 * kb + 8 * (v >> 2) + (v & 3) >= n) s[kb][v] = -INFINITY;
+    }
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int n = KS; n < 2 * KS; ++n) {
-        dp = mfma32(f[n % AHEAD], g[n - KS], n > KS ? dp : (f32x16_t)(0.f));
+    for (int n = 2 * KS; n < 4 * KS; ++n) {
+      const int m = n - 2 * KS;
+      dp[n & 1] = mfma32(f[n % AHEAD], g[m / 2], m > 1 ? dp[n & 1] : (f32x16_t)(0.f));
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (1 + i * (KS - 1) / 4 == n - KS) {
+      for (int i = 0; i < 8; ++i)
+        if (1 + i * (2 * KS - 1) / 8 == m) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) s[4 * i + k] = exp2_fast(fmaf(s[4 * i + k], c, -lse));
-          }
-        slot_end(n);
-      }
-      grads(0);
-      grads(1);
+          for (int k = 0; k < 4; ++k) s[i / 4][4 * (i % 4) + k] = exp2_fast(fmaf(s[i / 4][4 * (i % 4) + k], c, -lse));
+        }
+      slot_end(n);
+    }
+    grads(0);
+    grads(1);
 #pragma unroll
-      for (int n = 2 * KS; n < N; ++n) {
-        const int m = n - 2 * KS;
-        acc[m % DB] = mfma32(f[n % AHEAD], ds[m / DB], acc[m % DB]);
-        if (m == 0) { grads(2); grads(3); }
-        slot_end(n);
-      }
+    for (int n = 4 * KS; n < N; ++n) {
+      const int m = n - 4 * KS;
+      acc[m % DB] = mfma32(f[n % AHEAD], ds[m / DB], acc[m % DB]);
+      // ahead of the products that take them
+#pragma unroll
+      for (int i = 2; i < 8; ++i)
+        if ((i - 2) / 2 * DB + (i & 1 ? DB - 1 : 0) == m) grads(i);
+      slot_end(n);
     }
   }
   if (r.ok)
@@ -615,7 +671,7 @@ __global__ __launch_bounds__(512, 2) void attn_dkv_kernel(AttnDev a, unsigned it
 
   const uint16_t* kbase = static_cast<const uint16_t*>(a.k.p) + b * a.k.sb + kvh * a.k.sh;
   const uint16_t* vbase = static_cast<const uint16_t*>(a.v.p) + b * a.v.sb + kvh * a.v.sh;
-  u32x4_t kf[2 * DB];
+  u32x4_t kf[2 * DB] = {};
   const TileRead<DB> rd(lane);
   const unsigned lds = lds_offset(smem);
   const uint16_t* qb0 = static_cast<const uint16_t*>(a.q.p) + b * a.q.sb + kvh * group * a.q.sh;
@@ -650,6 +706,7 @@ __global__ __launch_bounds__(512, 2) void attn_dkv_kernel(AttnDev a, unsigned it
     fetch(head, q0, 0);
     load_rows<DB>(kf, kbase + key * a.k.sl, key < k_here, a.dim, half);
   }
+  arrived(kf);
   const unsigned char* vh = smem + wave * 32 * G::ROWB;
   for (int t = 0; t < tiles; ++t) {
     wait_vm<0>();
