@@ -46,6 +46,19 @@ struct HeadsDev {
   int64_t sb, sl, sh;    // strides in values
 };
 
+// Division of numbers below 2^31 by a fixed divisor: the high word of a
+// product, an addition and a shift (the round-up method of Granlund and
+// Montgomery, "Division by Invariant Integers using Multiplication").
+struct FastDiv {
+  uint32_t mul, shift, by;
+};
+inline FastDiv fast_div(uint32_t d) {
+  if (d == 0) d = 1;       // nothing is divided where there is nothing
+  uint32_t l = 0;
+  while ((uint64_t(1) << l) < d) ++l;
+  return FastDiv{uint32_t(((uint64_t(1) << 32) * ((uint64_t(1) << l) - d)) / d + 1), l, d};
+}
+
 struct AttnDev {
   int32_t batch, q_len, k_len, heads, kv_heads, dim, causal;
   int64_t offset;
@@ -60,13 +73,14 @@ struct AttnDev {
   int32_t splits;        // key ranges worked on apart (1: no join)
   int32_t split_keys;    // keys per range, a multiple of the key tile
   int32_t parts;         // backward: workgroups that share a key block (1: no join)
+  FastDiv row_blocks, key_blocks, by_kv_heads, by_group, by_splits, by_parts, by_bh;
   float* part_kv;        // [part][batch][kv_heads][k_len][2][dim] fp32 sums of dk / scale, dv
 };
 
 hipError_t launch_attn_fwd(hipStream_t s, const AttnDev& a);
 hipError_t launch_attn_bwd(hipStream_t s, const AttnDev& a);
-int attn_splits(const AttnDev& a, int* split_keys);
-int attn_parts(const AttnDev& a);
+// Fills in splits, split_keys, parts and the divisors.
+void attn_plan(AttnDev& a);
 
 // ---- gated feed-forward -----------------------------------------------------
 struct FfnDev {

@@ -181,10 +181,7 @@ AttnDev attn_dev(const muon_attn_args* a) {
   d.q = heads_dev(a->q); d.k = heads_dev(a->k); d.v = heads_dev(a->v); d.o = heads_dev(a->o);
   d.lse = a->lse;
   d.d_o = heads_dev(a->d_o); d.d_q = heads_dev(a->d_q); d.d_k = heads_dev(a->d_k); d.d_v = heads_dev(a->d_v);
-  int keys = 0;
-  d.splits = attn_splits(d, &keys);
-  d.split_keys = keys;
-  d.parts = attn_parts(d);
+  attn_plan(d);
   return d;
 }
 

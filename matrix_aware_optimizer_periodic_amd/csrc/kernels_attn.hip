@@ -97,16 +97,24 @@ struct TileMove {
 };
 
 // Fragments straight from global memory: one row per lane, 8 values from
-// 16 ks + 8 half.
+// 16 ks + 8 half.  One branch for all loads where the head fills its blocks.
 template <int DB>
 __device__ __forceinline__ void load_rows(u32x4_t (&f)[2 * DB], const uint16_t* row, bool ok, int dim, int half) {
 #pragma unroll
-  for (int ks = 0; ks < 2 * DB; ++ks) {
-    const int d = ks * 16 + half * 8;
-    f[ks] = u32x4_t{0, 0, 0, 0};
-    if (ok && d < dim) f[ks] = *as_global(reinterpret_cast<const u32x4_t*>(row + d));
+  for (int ks = 0; ks < 2 * DB; ++ks) f[ks] = u32x4_t{0, 0, 0, 0};
+  if (!ok) return;
+  const auto* g = as_global(reinterpret_cast<const u32x4_t*>(row + half * 8));
+  if (dim == 32 * DB) {
+#pragma unroll
+    for (int ks = 0; ks < 2 * DB; ++ks) f[ks] = g[2 * ks];
+  } else {
+#pragma unroll
+    for (int ks = 0; ks < 2 * DB; ++ks)
+      if (ks * 16 + half * 8 < dim) f[ks] = g[2 * ks];
   }
 }
+
+__device__ __forceinline__ unsigned div_by(unsigned n, const FastDiv& d) { return (__umulhi(n, d.mul) + n) >> d.shift; }
 
 // Makes the compiler wait for loaded fragments here.  Left to their first use
 // in a loop it would wait there in every round, and so for the DMA in flight.
@@ -206,7 +214,7 @@ __device__ __forceinline__ int clamp_len(const int32_t* lens, int b, int most) {
 
 // Which rows a workgroup of the forward or dq kernel has, and what they see.
 struct Rows {
-  int b, kvh, group, q_here, k_here;
+  int b, kvh, q_here, k_here;
   int row0;                  // first row of the workgroup
   int qi, head;              // this lane's query and head
   bool ok;                   // the lane's row is inside the tensor
@@ -220,19 +228,19 @@ __device__ __forceinline__ int seen(const AttnDev& a, int qi, int k_here) {
   return int(max(int64_t(0), min(int64_t(k_here), n)));
 }
 
-__device__ __forceinline__ Rows rows_of(const AttnDev& a, unsigned item, unsigned blocks, int wave, int lane) {
+__device__ __forceinline__ Rows rows_of(const AttnDev& a, unsigned item, int wave, int lane) {
   Rows r;
   // Later rows see more keys under a causal border: they go first.
-  const unsigned blk = blocks - 1 - item % blocks, bh = item / blocks;
-  r.b = int(bh) / a.kv_heads;
-  r.kvh = int(bh) % a.kv_heads;
-  r.group = a.heads / a.kv_heads;
+  const unsigned bh = div_by(item, a.row_blocks), blk = a.row_blocks.by - 1 - (item - bh * a.row_blocks.by);
+  r.b = int(div_by(bh, a.by_kv_heads));
+  r.kvh = int(bh) - r.b * a.kv_heads;
   r.q_here = clamp_len(a.q_lens, r.b, a.q_len);
   r.k_here = clamp_len(a.k_lens, r.b, a.k_len);
   r.row0 = int(blk) * kRowsWg;
   const int row = r.row0 + wave * 32 + (lane & 31);
-  r.qi = row / r.group;
-  r.head = r.kvh * r.group + row % r.group;
+  const int group = int(a.by_group.by);
+  r.qi = int(div_by(unsigned(row), a.by_group));
+  r.head = r.kvh * group + row - r.qi * group;
   r.ok = r.qi < a.q_len;
   r.live = r.qi < r.q_here;
   r.see = r.live ? seen(a, r.qi, r.k_here) : 0;
@@ -247,8 +255,8 @@ __device__ __forceinline__ int wave_max(int v) {
 
 // Keys that the last of the workgroup's rows sees (the most of any).
 __device__ __forceinline__ int seen_most(const AttnDev& a, const Rows& r) {
-  const int last = min((r.row0 + kRowsWg - 1) / r.group, r.q_here - 1);
-  return last < r.row0 / r.group ? 0 : seen(a, last, r.k_here);
+  const int last = min(int(div_by(unsigned(r.row0 + kRowsWg - 1), a.by_group)), r.q_here - 1);
+  return last < int(div_by(unsigned(r.row0), a.by_group)) ? 0 : seen(a, last, r.k_here);
 }
 
 // ---------------------------------------------------------------------------
@@ -265,26 +273,22 @@ __device__ __forceinline__ int seen_most(const AttnDev& a, const Rows& r) {
 // arithmetic) is fixed; left to itself the compiler waits for each read at
 // once.
 template <int DB, bool SPLIT>
-__global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnDev a, unsigned items, unsigned blocks) {
+__global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnDev a, unsigned items) {
   using G = Geo<DB>;
   constexpr int KS = G::KS, AHEAD = 3;
   __shared__ __attribute__((aligned(1024))) unsigned char smem[4 * G::TILEB];   // two of k, two of v
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const unsigned id = xcd_item(blockIdx.x, items);
-  const unsigned split = SPLIT ? id % unsigned(a.splits) : 0;
-  const Rows r = rows_of(a, SPLIT ? id / unsigned(a.splits) : id, blocks, wave, lane);
+  const unsigned item = SPLIT ? div_by(id, a.by_splits) : id, split = id - item * unsigned(a.splits);
+  const Rows r = rows_of(a, item, wave, lane);
   const int first = SPLIT ? int(split) * a.split_keys : 0;
   const int most = seen_most(a, r), end = SPLIT ? min(most, first + a.split_keys) : most;
   const int tiles = end > first ? (end - first + kTile - 1) / kTile : 0;
 
-  u32x4_t q[2 * DB];
-  const uint16_t* qrow = static_cast<const uint16_t*>(a.q.p) + r.b * a.q.sb + r.qi * a.q.sl + r.head * a.q.sh;
-  load_rows<DB>(q, qrow, r.live, a.dim, half);
   const uint16_t* kbase = static_cast<const uint16_t*>(a.k.p) + r.b * a.k.sb + r.kvh * a.k.sh + first * a.k.sl;
   const uint16_t* vbase = static_cast<const uint16_t*>(a.v.p) + r.b * a.v.sb + r.kvh * a.v.sh + first * a.v.sl;
   const TileMove<DB, 4> mk(a.k.sl, a.dim, wave, lane), mv(a.v.sl, a.dim, wave, lane);
-  const TileOffsets<DB> rd(lane, smem);
   const unsigned lds = lds_offset(smem);
   auto fetch_k = [&](int t) {
     mk.issue(kbase + int64_t(t) * kTile * a.k.sl, r.k_here - first - t * kTile, lds + unsigned(t & 1) * G::TILEB, wave);
@@ -294,6 +298,15 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnDev a, unsigned it
              wave);
   };
 
+  if (tiles > 0) {
+    fetch_k(0);
+    fetch_v(0);
+    if (tiles > 1) fetch_k(1);
+  }
+  u32x4_t q[2 * DB];
+  const uint16_t* qrow = static_cast<const uint16_t*>(a.q.p) + r.b * a.q.sb + r.qi * a.q.sl + r.head * a.q.sh;
+  load_rows<DB>(q, qrow, r.live, a.dim, half);
+  const TileOffsets<DB> rd(lane, smem);
   f32x16_t o[DB];
 #pragma unroll
   for (int db = 0; db < DB; ++db) o[db] = (f32x16_t)(0.f);
@@ -329,11 +342,6 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnDev a, unsigned it
   };
 
   f32x16_t s0[2], s1[2];
-  if (tiles > 0) {
-    fetch_k(0);
-    fetch_v(0);
-    if (tiles > 1) fetch_k(1);
-  }
   wait_vm<0>();
   barrier();
   arrived(q);
@@ -493,13 +501,13 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnDev a) {
 // kernel.  Per tile of 64 keys, 32 at a time: s^T = k q^T, dp^T = v do^T,
 // ds^T = p^T (dp^T - delta), dq^T += k^T ds^T.
 template <int DB>
-__global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnDev a, unsigned items, unsigned blocks) {
+__global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnDev a, unsigned items) {
   using G = Geo<DB>;
   constexpr int AHEAD = 3;
   __shared__ __attribute__((aligned(1024))) unsigned char smem[4 * G::TILEB];
   const int lane = threadIdx.x & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Rows r = rows_of(a, xcd_item(blockIdx.x, items), blocks, wave, lane);
+  const Rows r = rows_of(a, xcd_item(blockIdx.x, items), wave, lane);
   const int end = seen_most(a, r);
   const int tiles = (end + kTile - 1) / kTile;
 
@@ -641,7 +649,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnDev a, unsigned ite
 // The (head, query tile) pairs of a key block may be divided over several
 // workgroups (a.parts), whose fp32 sums a second kernel adds.
 template <int DB, int AHEAD>
-__global__ __launch_bounds__(512, 2) void attn_dkv_kernel(AttnDev a, unsigned items, unsigned blocks) {
+__global__ __launch_bounds__(512, 2) void attn_dkv_kernel(AttnDev a, unsigned items) {
   using G = Geo<DB>;
   constexpr int NW = 8, KEYS = 32 * NW;
   constexpr int BUF = 2 * G::TILEB + 2 * kTile * 4;     // q, do, offsets, deltas
@@ -651,12 +659,13 @@ __global__ __launch_bounds__(512, 2) void attn_dkv_kernel(AttnDev a, unsigned it
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // Under a causal border the first keys are seen by the most queries: their
   // workgroups go first, those of all heads in turn.
-  const unsigned bhs = unsigned(a.batch) * unsigned(a.kv_heads), parts = unsigned(a.parts);
-  const unsigned item = a.causal ? blockIdx.x : xcd_item(blockIdx.x, items);
-  const unsigned part = item % parts;
-  const unsigned bh = a.causal ? item / parts % bhs : item / parts / blocks;
-  const unsigned blk = a.causal ? item / parts / bhs : item / parts % blocks;
-  const int b = int(bh) / a.kv_heads, kvh = int(bh) % a.kv_heads, group = a.heads / a.kv_heads;
+  const unsigned parts = unsigned(a.parts);
+  const unsigned id = a.causal ? blockIdx.x : xcd_item(blockIdx.x, items);
+  const unsigned item = div_by(id, a.by_parts), part = id - item * parts;
+  const unsigned up = div_by(item, a.causal ? a.by_bh : a.key_blocks);
+  const unsigned rest = item - up * (a.causal ? a.by_bh.by : a.key_blocks.by);
+  const unsigned bh = a.causal ? rest : up, blk = a.causal ? up : rest;
+  const int b = int(div_by(bh, a.by_kv_heads)), kvh = int(bh) - b * a.kv_heads, group = int(a.by_group.by);
   const int q_here = clamp_len(a.q_lens, b, a.q_len), k_here = clamp_len(a.k_lens, b, a.k_len);
   const int key0 = int(blk) * KEYS;
   const int wkey = key0 + wave * 32, key = wkey + (lane & 31);
@@ -873,8 +882,6 @@ unsigned key_blocks(const AttnDev& a) { return unsigned((a.k_len + 255) / 256); 
                                                                                  : K<4 __VA_ARGS__>)
 #define COMMA ,
 
-}  // namespace
-
 int attn_splits(const AttnDev& a, int* split_keys) {
   // Two workgroups fit on each of 256 CUs.  With fewer than half of that,
   // the keys are divided, in ranges of at least four tiles.
@@ -912,16 +919,32 @@ int attn_parts(const AttnDev& a) {
   return best;
 }
 
+}  // namespace
+
+void attn_plan(AttnDev& a) {
+  int keys = 0;
+  a.splits = attn_splits(a, &keys);
+  a.split_keys = keys;
+  a.parts = attn_parts(a);
+  a.row_blocks = fast_div(row_blocks(a));
+  a.key_blocks = fast_div(key_blocks(a));
+  a.by_kv_heads = fast_div(unsigned(a.kv_heads));
+  a.by_group = fast_div(unsigned(a.heads / a.kv_heads));
+  a.by_splits = fast_div(unsigned(a.splits));
+  a.by_parts = fast_div(unsigned(a.parts));
+  a.by_bh = fast_div(unsigned(a.batch) * unsigned(a.kv_heads));
+}
+
 hipError_t launch_attn_fwd(hipStream_t s, const AttnDev& a) {
   const unsigned blocks = row_blocks(a);
   const unsigned items = blocks * unsigned(a.batch) * unsigned(a.kv_heads) * unsigned(a.splits);
   if (a.splits == 1) {
     auto* k = BY_DIM(attn_fwd_kernel, COMMA false);
-    hipLaunchKernelGGL(k, dim3(items), dim3(256), 0, s, a, items, blocks);
+    hipLaunchKernelGGL(k, dim3(items), dim3(256), 0, s, a, items);
     return hipGetLastError();
   }
   auto* k = BY_DIM(attn_fwd_kernel, COMMA true);
-  hipLaunchKernelGGL(k, dim3(items), dim3(256), 0, s, a, items, blocks);
+  hipLaunchKernelGGL(k, dim3(items), dim3(256), 0, s, a, items);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t lines = int64_t(a.batch) * a.heads * a.q_len;
@@ -934,14 +957,14 @@ hipError_t launch_attn_bwd(hipStream_t s, const AttnDev& a) {
   if (a.q_len > 0) {
     const unsigned blocks = row_blocks(a), items = blocks * bh;
     auto* k = BY_DIM(attn_dq_kernel, );
-    hipLaunchKernelGGL(k, dim3(items), dim3(256), 0, s, a, items, blocks);
+    hipLaunchKernelGGL(k, dim3(items), dim3(256), 0, s, a, items);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (a.k_len > 0) {
     const unsigned blocks = key_blocks(a), items = blocks * bh * unsigned(a.parts);
     auto* k = BY_DIM(attn_dkv_kernel, COMMA 2);
-    hipLaunchKernelGGL(k, dim3(items), dim3(512), 0, s, a, items, blocks);
+    hipLaunchKernelGGL(k, dim3(items), dim3(512), 0, s, a, items);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.parts == 1) return e;
     const int64_t stride = int64_t(a.batch) * a.kv_heads * a.k_len * 2 * a.dim, n = stride / 8;
