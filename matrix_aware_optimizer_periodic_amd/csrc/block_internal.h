@@ -38,7 +38,7 @@ constexpr int kNormMaxCols = 16384;
 hipError_t launch_norm_fwd(hipStream_t s, const NormDev& a, bool vec);
 hipError_t launch_norm_bwd(hipStream_t s, const NormDev& a, bool vec, bool sums);
 // Shares of a sample's rows that the backward pass sums apart.
-int norm_splits(int64_t groups, int64_t group_rows);
+int norm_splits(int64_t groups, int64_t group_rows, int cols);
 
 // ---- attention ------------------------------------------------------------
 struct HeadsDev {

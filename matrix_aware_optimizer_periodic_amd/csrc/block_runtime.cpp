@@ -136,7 +136,7 @@ bool norm_sums(const muon_norm_args* a) {
 size_t norm_bwd_bytes(const muon_norm_args* a) {
   if (!norm_sums(a) || a->rows == 0) return 0;
   const int64_t g = a->rows / a->group_rows;
-  const size_t part = align_up(size_t(g) * norm_splits(g, a->group_rows) * kNormSums * size_t(a->cols) * 4);
+  const size_t part = align_up(size_t(g) * norm_splits(g, a->group_rows, int(a->cols)) * kNormSums * size_t(a->cols) * 4);
   const bool weights = g > 1 && (a->d_post_weight.ptr || a->d_pre_weight.ptr);
   return part + (weights ? align_up(size_t(g) * 2 * size_t(a->cols) * 4) : 0);
 }
@@ -311,7 +311,7 @@ muon_status muon_norm_bwd(const muon_norm_args* a, void* ws, size_t ws_bytes, vo
   CHECK(check_workspace(ws, ws_bytes, need));
   NormDev dev = norm_dev(a);
   dev.resid_out.dt = rt;
-  dev.splits = norm_splits(g, a->group_rows);
+  dev.splits = norm_splits(g, a->group_rows, int(a->cols));
   dev.split_rows = int32_t((a->group_rows + dev.splits - 1) / dev.splits);
   if (sums) {
     dev.part = static_cast<float*>(ws);

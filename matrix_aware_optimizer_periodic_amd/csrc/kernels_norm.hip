@@ -24,6 +24,8 @@
 // A workgroup keeps the three sums of its share of one sample's rows in
 // registers and writes them once; a second kernel adds the shares in order
 // (no atomics).
+#include <type_traits>
+
 #include "block_device.h"
 
 namespace muon {
@@ -151,10 +153,51 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_fwd_kernel(NormDev a) 
   }
 }
 
+// VEC values of a row as they were loaded, for rows read ahead.
+template <typename T, int VEC>
+struct Raw {
+  using V = std::conditional_t<sizeof(T) == 4, f32x4_t, u32x4_t>;
+  V a[sizeof(T) == 4 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* p, int64_t e) {
+    const auto* q = as_global(reinterpret_cast<const V*>(static_cast<const T*>(p) + e));
+    a[0] = q[0];
+    if constexpr (sizeof(T) == 4) a[1] = q[1];
+  }
+  __device__ __forceinline__ void get(float (&v)[VEC]) const {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (sizeof(T) == 4) {
+        v[k] = a[0][k];
+        v[4 + k] = a[1][k];
+      } else {
+        v[2 * k] = bf16_to_f32(a[0][k] & 0xffffu);
+        v[2 * k + 1] = __uint_as_float(a[0][k] & 0xffff0000u);
+      }
+    }
+  }
+  __device__ __forceinline__ void clear() {
+    a[0] = V{};
+    if constexpr (sizeof(T) == 4) a[1] = V{};
+  }
+};
+template <typename T>
+struct Raw<T, 1> {
+  float a;
+  __device__ __forceinline__ void load(const void* p, int64_t e) {
+    float v[1];
+    load_vals<T, 1>(p, e, v);
+    a = v[0];
+  }
+  __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = a; }
+  __device__ __forceinline__ void clear() { a = 0.f; }
+};
+
 // One share of one sample's rows per wave (WAVE: four shares per workgroup)
-// or per workgroup; share = group * splits + split.
-template <typename TR, typename TH, int VEC, int NC, bool WAVE>
-__global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_bwd_kernel(NormDev a, int64_t shares) {
+// or per workgroup; share = group * splits + split.  AHEAD: the next row is
+// read while this one is worked on; that takes registers which a workgroup of
+// more than 640 threads does not have.
+template <typename TR, typename TH, int VEC, int NC, bool WAVE, bool AHEAD>
+__global__ __launch_bounds__(WAVE ? 256 : AHEAD ? 640 : 1024) void norm_bwd_kernel(NormDev a, int64_t shares) {
   __shared__ float red[2][2][kMaxWaves];
   const int tid = WAVE ? threadIdx.x & 63 : threadIdx.x;
   const int nt = WAVE ? 64 : blockDim.x;
@@ -165,7 +208,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_bwd_kernel(NormDev a, 
   const int64_t first = grp * a.group_rows + (share - grp * a.splits) * int64_t(a.split_rows);
   const int64_t end = min(first + a.split_rows, (grp + 1) * a.group_rows);
   const float inv = 1.0f / float(a.cols);
-  const bool have_h = a.h.p != nullptr;
+  const bool have_h = a.h.p != nullptr, have_y = a.d_y.p != nullptr, have_r = a.d_resid_out.p != nullptr;
   const float kpre = a.pre_kind == 2 ? inv : 0.f, kpost = a.post_kind == 2 ? inv : 0.f;
   const float npre = a.pre_kind ? inv : 0.f, npost = a.post_kind ? inv : 0.f;
   // what multiplies dy and dr in this share's columns, and its sums
@@ -194,24 +237,39 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_bwd_kernel(NormDev a, 
       for (int k = 0; k < VEC; ++k) wr[c][k] *= t[k];
     }
   }
-  for (int64_t row = first; row < end; ++row) {
-    const f32x4_t st = *as_global(reinterpret_cast<const f32x4_t*>(a.stats + row * 4));
-    float x[NC][VEC], dy[NC][VEC], dr[NC][VEC], h[NC][VEC];
+  Raw<TR, VEC> lx[NC], lr[NC];
+  Raw<TH, VEC> ly[NC], lh[NC];
+  f32x4_t lst;
+  auto read = [&](int64_t row) {
+    lst = *as_global(reinterpret_cast<const f32x4_t*>(a.stats + row * 4));
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int col = col_of<VEC>(c, tid, nt);
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) x[c][k] = dy[c][k] = dr[c][k] = h[c][k] = 0.f;
-      if (col < a.cols) {
-        if (a.d_y.p) {
-          load_vals<TR, VEC>(a.resid_out.p, row * a.resid_out.ld + col, x[c]);
-          load_vals<TH, VEC>(a.d_y.p, row * a.d_y.ld + col, dy[c]);
-        }
-        if (a.d_resid_out.p) load_vals<TR, VEC>(a.d_resid_out.p, row * a.d_resid_out.ld + col, dr[c]);
-        if (have_h) load_vals<TH, VEC>(a.h.p, row * a.h.ld + col, h[c]);
+      if (col >= a.cols) continue;
+      if (have_y) {
+        lx[c].load(a.resid_out.p, row * a.resid_out.ld + col);
+        ly[c].load(a.d_y.p, row * a.d_y.ld + col);
       }
+      if (have_r) lr[c].load(a.d_resid_out.p, row * a.d_resid_out.ld + col);
+      if (have_h) lh[c].load(a.h.p, row * a.h.ld + col);
     }
-    if (a.d_y.p) {
+  };
+#pragma unroll
+  for (int c = 0; c < NC; ++c) { lx[c].clear(); lr[c].clear(); ly[c].clear(); lh[c].clear(); }
+  if (AHEAD && first < end) read(first);
+  for (int64_t row = first; row < end; ++row) {
+    if (!AHEAD) read(row);
+    const f32x4_t st = lst;
+    float x[NC][VEC], dy[NC][VEC], dr[NC][VEC], h[NC][VEC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      lx[c].get(x[c]);
+      ly[c].get(dy[c]);
+      lr[c].get(dr[c]);
+      lh[c].get(h[c]);
+    }
+    if (AHEAD) read(min(row + 1, end - 1));
+    if (have_y) {
       float t[2] = {0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
@@ -226,7 +284,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_bwd_kernel(NormDev a, 
           t[1] = fmaf(dy[c][k], x[c][k], t[1]);
         }
       }
-      row_sum<2, WAVE>(t, red, phase, nt >> 6);
+      if (a.pre_kind) row_sum<2, WAVE>(t, red, phase, nt >> 6);
       t[0] *= kpre;
       t[1] *= npre;
 #pragma unroll
@@ -349,19 +407,31 @@ Shape shape_of(int cols, bool vec) {
   return {threads, nc, threads == 64 && nc == (vec ? 1 : 4)};
 }
 
-#define NORM_KERNEL(K, TR, TH)                                                                       \
-  (vec ? (sh.wave ? K<TR, TH, 8, 1, true> : sh.nc == 1 ? K<TR, TH, 8, 1, false> : K<TR, TH, 8, 2, false>) \
-       : (sh.wave ? K<TR, TH, 1, 4, true> : sh.nc == 4 ? K<TR, TH, 1, 4, false> : K<TR, TH, 1, 16, false>))
-#define NORM_PICK(K)                                                                   \
-  (a.resid_out.dt ? (hdt ? NORM_KERNEL(K, uint16_t, uint16_t) : NORM_KERNEL(K, uint16_t, float)) \
-                  : (hdt ? NORM_KERNEL(K, float, uint16_t) : NORM_KERNEL(K, float, float)))
+#define FWD_KERNEL(TR, TH)                                                                                   \
+  (vec ? (sh.wave ? norm_fwd_kernel<TR, TH, 8, 1, true> : sh.nc == 1 ? norm_fwd_kernel<TR, TH, 8, 1, false>     \
+                                                                     : norm_fwd_kernel<TR, TH, 8, 2, false>)    \
+       : (sh.wave ? norm_fwd_kernel<TR, TH, 1, 4, true> : sh.nc == 4 ? norm_fwd_kernel<TR, TH, 1, 4, false>     \
+                                                                     : norm_fwd_kernel<TR, TH, 1, 16, false>))
+#define BWD_KERNEL(TR, TH)                                                                                   \
+  (vec ? (sh.wave           ? norm_bwd_kernel<TR, TH, 8, 1, true, true>                                         \
+          : sh.nc == 2        ? norm_bwd_kernel<TR, TH, 8, 2, false, false>                                     \
+          : sh.threads <= 640 ? norm_bwd_kernel<TR, TH, 8, 1, false, true>                                      \
+                              : norm_bwd_kernel<TR, TH, 8, 1, false, false>)                                    \
+       : (sh.wave      ? norm_bwd_kernel<TR, TH, 1, 4, true, false>                                             \
+          : sh.nc == 4 ? norm_bwd_kernel<TR, TH, 1, 4, false, false>                                            \
+                       : norm_bwd_kernel<TR, TH, 1, 16, false, false>))
+#define BY_TYPES(K)                                                                                 \
+  (a.resid_out.dt ? (hdt ? K(uint16_t, uint16_t) : K(uint16_t, float)) : (hdt ? K(float, uint16_t) : K(float, float)))
 
 }  // namespace
 
-int norm_splits(int64_t groups, int64_t group_rows) {
-  // About 512 shares in all (two workgroups on each of 256 CUs), of at least
-  // eight rows: a share costs one write and one read of its column sums.
-  const int64_t want = (512 + groups - 1) / groups;
+int norm_splits(int64_t groups, int64_t group_rows, int cols) {
+  // About ten waves of shares on each of 256 CUs (one workgroup at 5120
+  // columns, where 512 shares measured 3% slower: a share costs one write and
+  // one read of its column sums), of at least eight rows.
+  const int64_t waves = (cols + 511) / 512;
+  const int64_t total = waves < 10 ? 2560 / waves : 256;
+  const int64_t want = (total + groups - 1) / groups;
   const int64_t most = (group_rows + 7) / 8;
   const int64_t n = want < most ? want : most;
   return int(n < 1 ? 1 : n);
@@ -370,7 +440,7 @@ int norm_splits(int64_t groups, int64_t group_rows) {
 hipError_t launch_norm_fwd(hipStream_t s, const NormDev& a, bool vec) {
   const Shape sh = shape_of(a.cols, vec);
   const int hdt = a.h.p ? a.h.dt : a.y.dt;
-  auto* k = NORM_PICK(norm_fwd_kernel);
+  auto* k = BY_TYPES(FWD_KERNEL);
   const int64_t grid = sh.wave ? (a.rows + 3) / 4 : a.rows;
   hipLaunchKernelGGL(k, dim3(unsigned(grid)), dim3(sh.wave ? 256 : sh.threads), 0, s, a);
   return hipGetLastError();
@@ -380,7 +450,7 @@ hipError_t launch_norm_bwd(hipStream_t s, const NormDev& a, bool vec, bool sums)
   const Shape sh = shape_of(a.cols, vec);
   const int hdt = a.h.p ? a.h.dt : a.d_y.dt;
   const int64_t groups = a.rows / a.group_rows, shares = groups * a.splits;
-  auto* k = NORM_PICK(norm_bwd_kernel);
+  auto* k = BY_TYPES(BWD_KERNEL);
   const int64_t grid = sh.wave ? (shares + 3) / 4 : shares;
   hipLaunchKernelGGL(k, dim3(unsigned(grid)), dim3(sh.wave ? 256 : sh.threads), 0, s, a, shares);
   hipError_t e = hipGetLastError();
