@@ -19,7 +19,7 @@ from .binding import (  # noqa: F401
 
 # The transformer-block operators need torch at import; the optimizer's C ABI
 # does not, so they are looked up on first use.
-_BLOCK = ("norm_fwd", "norm_bwd", "residual_norm", "attn_fwd", "attn_bwd", "attention", "ffn_fwd", "ffn_bwd",
+_BLOCK = ("norm_fwd", "norm_bwd", "residual_norm", "attn_fwd", "attn_bwd", "attention", "attention_qkv", "ffn_fwd", "ffn_bwd",
           "gated_ffn")
 
 

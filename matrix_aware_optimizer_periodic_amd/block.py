@@ -163,7 +163,7 @@ def _norm_kinds(post: str, pre: str):
 
 
 def norm_fwd(resid, h=None, gate=None, post_weight=None, pre_weight=None, scale=None, shift=None, *,
-             post: str = "none", pre: str = "layer", alpha: float = 1.0, eps: float = 1e-6):
+             post: str = "none", pre: str = "layer", alpha: float = 1.0, eps: float = 1e-6, y_dtype=None):
     """resid_out = resid + alpha gate N_post(h) post_weight;
     y = N_pre(resid_out) pre_weight (1 + scale) + shift.
 
@@ -175,11 +175,14 @@ def norm_fwd(resid, h=None, gate=None, post_weight=None, pre_weight=None, scale=
     dev = _device(resid, h, gate, post_weight, pre_weight, scale, shift)
     rows, cols, group = _norm_shape(resid)
     k_post, k_pre = _norm_kinds(post, pre)
-    if h is not None and h.shape != resid.shape:
-        raise ValueError(f"h {tuple(h.shape)} and resid {tuple(resid.shape)}")
+    if h is not None and (h.shape != resid.shape or y_dtype not in (None, h.dtype)):
+        raise ValueError(f"h {tuple(h.shape)} {h.dtype}, resid {tuple(resid.shape)}, y_dtype {y_dtype}")
     want_y = k_pre != 0 or pre_weight is not None or scale is not None or shift is not None
     out = resid if h is None else _out(resid)
-    y = _out(resid if h is None else h) if want_y else None
+    y = None
+    if want_y:
+        y = _out(h) if h is not None else _out(resid) if y_dtype in (None, resid.dtype) else \
+            torch.empty(resid.shape, dtype=y_dtype, device=dev)
     stats = torch.empty((rows, 4), dtype=torch.float32, device=dev)
     if rows == 0 or cols == 0:
         return out, y, stats
@@ -206,6 +209,7 @@ def norm_bwd(d_resid_out, d_y, resid_out, h, stats, gate=None, post_weight=None,
     k_post, k_pre = _norm_kinds(post, pre)
     if stats.dtype != torch.float32 or not stats.is_contiguous() or stats.shape != (rows, 4):
         raise ValueError("stats is norm_fwd's third result")
+    # (a missing d_y is taken as zeros of h's type)
     if d_y is None and (k_pre != 0 or pre_weight is not None or scale is not None or shift is not None):
         d_y = torch.zeros(x.shape, dtype=(x if h is None else h).dtype, device=dev)
     d_h = None if h is None else _out(h)
@@ -232,8 +236,8 @@ def norm_bwd(d_resid_out, d_y, resid_out, h, stats, gate=None, post_weight=None,
 
 class _ResidualNorm(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, resid, h, gate, post_weight, pre_weight, scale, shift, how):
-        out, y, stats = norm_fwd(resid, h, gate, post_weight, pre_weight, scale, shift, **how)
+    def forward(ctx, resid, h, gate, post_weight, pre_weight, scale, shift, how, y_dtype):
+        out, y, stats = norm_fwd(resid, h, gate, post_weight, pre_weight, scale, shift, y_dtype=y_dtype, **how)
         if h is None:
             out = resid.view_as(resid)
         ctx.how = how
@@ -245,18 +249,18 @@ class _ResidualNorm(torch.autograd.Function):
     def backward(ctx, d_out, d_y):
         out, h, stats, gate, post_weight, pre_weight, scale, shift = ctx.saved_tensors
         if d_out is None and d_y is None:
-            return (None,) * 8
+            return (None,) * 9
         d_out = None if d_out is None else d_out.contiguous()
         d_y = None if d_y is None else d_y.contiguous()
         g = norm_bwd(d_out, d_y, out, h, stats, gate, post_weight, pre_weight, scale, shift, **ctx.how)
-        return (g["resid"], g["h"], g["gate"], g["post_weight"], g["pre_weight"], g["scale"], g["shift"], None)
+        return (g["resid"], g["h"], g["gate"], g["post_weight"], g["pre_weight"], g["scale"], g["shift"], None, None)
 
 
 def residual_norm(resid, h=None, gate=None, post_weight=None, pre_weight=None, scale=None, shift=None, *,
-                  post: str = "none", pre: str = "layer", alpha: float = 1.0, eps: float = 1e-6):
+                  post: str = "none", pre: str = "layer", alpha: float = 1.0, eps: float = 1e-6, y_dtype=None):
     """norm_fwd for autograd; returns (resid_out, y)."""
     return _ResidualNorm.apply(resid, h, gate, post_weight, pre_weight, scale, shift,
-                               {"post": post, "pre": pre, "alpha": alpha, "eps": eps})
+                               {"post": post, "pre": pre, "alpha": alpha, "eps": eps}, y_dtype)
 
 
 # ---------------------------------------------------------------- attention
@@ -312,16 +316,24 @@ def attn_fwd(q, k, v, *, causal: bool = False, offset: int = 0, q_lens=None, k_l
 
 
 def attn_bwd(d_o, q, k, v, o, lse, *, causal: bool = False, offset: int = 0, q_lens=None, k_lens=None,
-             scale: float | None = None):
+             scale: float | None = None, out=None):
     """Gradients (d_q, d_k, d_v) of attn_fwd's o, from d_o and what attn_fwd
-    took and gave; contiguous, zero past the lengths."""
+    took and gave, zero past the lengths.  They are written to `out`, three
+    tensors of q's, k's and v's shapes (slices of a packed projection's
+    gradient, say), or to new contiguous ones."""
     dev = _device(q, d_o, k, v, o, lse, q_lens, k_lens)
     b, m, n, h, g, d, scale = _attn_dims(q, k, v, q_lens, k_lens, scale)
     if d_o.shape != q.shape or o.shape != q.shape or lse.shape != (b, h, m):
         raise ValueError(f"d_o {tuple(d_o.shape)}, o {tuple(o.shape)}, lse {tuple(lse.shape)} for q {tuple(q.shape)}")
     if lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse is attn_fwd's second result")
-    d_q, d_k, d_v = _out(q), _out(k), _out(v)
+    if out is None:
+        out = _out(q), _out(k), _out(v)
+    else:
+        _device(q, *out)
+        if tuple(t.shape for t in out) != (q.shape, k.shape, v.shape):
+            raise ValueError(f"out: shapes {[tuple(t.shape) for t in out]}")
+    d_q, d_k, d_v = out
     args = ATTN_ARGS.pack(b, m, n, h, g, d, int(causal), offset, scale, 0, _ptr(q_lens), _ptr(k_lens),
                           *_heads(q, "q"), *_heads(k, "k"), *_heads(v, "v"), *_heads(o, "o"), lse.data_ptr(),
                           *_heads(d_o, "d_o"), *_heads(d_q, "d_q"), *_heads(d_k, "d_k"), *_heads(d_v, "d_v"))
@@ -341,6 +353,31 @@ class _Attention(torch.autograd.Function):
     def backward(ctx, d_o):
         q, k, v, o, lse = ctx.saved_tensors
         return (*attn_bwd(d_o.contiguous(), q, k, v, o, lse, **ctx.how), None)
+
+
+class _PackedAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, qkv, how):
+        q, k, v = qkv.unbind(2)
+        o, lse = attn_fwd(q, k, v, **how)
+        ctx.how = how
+        ctx.save_for_backward(qkv, o, lse)
+        return o
+
+    @staticmethod
+    def backward(ctx, d_o):
+        qkv, o, lse = ctx.saved_tensors
+        d_qkv = torch.empty_like(qkv, memory_format=torch.contiguous_format)
+        attn_bwd(d_o.contiguous(), *qkv.unbind(2), o, lse, out=d_qkv.unbind(2), **ctx.how)
+        return d_qkv, None
+
+
+def attention_qkv(qkv, *, causal: bool = False, offset: int = 0, q_lens=None, k_lens=None,
+                  scale: float | None = None):
+    """attention of a packed projection's output (batch, len, 3, heads, dim),
+    whose gradient comes out packed alike; returns o."""
+    return _PackedAttention.apply(qkv, {"causal": causal, "offset": offset, "q_lens": q_lens, "k_lens": k_lens,
+                                        "scale": scale})
 
 
 def attention(q, k, v, *, causal: bool = False, offset: int = 0, q_lens=None, k_lens=None,
