@@ -223,19 +223,36 @@ __device__ __forceinline__ void emit_rows(const Prod& p, const f32x4_t (*acc)[BT
 #pragma unroll 1
   for (int it = 0; it < NIT; it += GRP) {
     if (it > 0) load_gu(it);
+    // all of a group's reads go out at once (pinned: they would be sunk into
+    // the branches below, each to be waited for there)
+    f32x4_t w[GRP][EPI == EPI_GATE ? 4 : 2];
+#pragma unroll
+    for (int j = 0; j < GRP; ++j) {
+      const MUON_LOCAL f32x4_t* q =
+          (const MUON_LOCAL f32x4_t*)(const MUON_LOCAL float*)(er + (lane / CPR + (it + j) * (64 / CPR)) * LDR + lane % CPR * 8);
+      w[j][0] = q[0];
+      w[j][1] = q[1];
+      if constexpr (EPI == EPI_GATE) {
+        w[j][2] = q[WOUT / 4];
+        w[j][3] = q[WOUT / 4 + 1];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < GRP; ++j)
+#pragma unroll
+      for (int k = 0; k < (EPI == EPI_GATE ? 4 : 2); ++k) asm volatile("" : "+v"(w[j][k]));
 #pragma unroll
     for (int j = 0; j < GRP; ++j) {
       const int row = lane / CPR + (it + j) * (64 / CPR);
       const int64_t m = mrow + row;
       float v[8];
-      const MUON_LOCAL float* q = (const MUON_LOCAL float*)(er + row * LDR + lane % CPR * 8);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = q[k];
+      for (int k = 0; k < 8; ++k) v[k] = w[j][k / 4][k % 4];
       if (!n_ok || m >= p.m) continue;
       if constexpr (EPI == EPI_GATE) {
         float u[8], h[8], d;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) u[k] = q[WOUT + k];
+        for (int k = 0; k < 8; ++k) u[k] = w[j][2 + k / 4][k % 4];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           act_of<ACT>(v[k], h[k], d);
