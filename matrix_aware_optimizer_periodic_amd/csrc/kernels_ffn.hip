@@ -539,10 +539,121 @@ ProdArgs weight_sizes(int64_t t, int64_t d, int64_t h) {
   return g;
 }
 
+// ---- few rows -----------------------------------------------------------------
+// Up to 16 MT rows of x against row operands, bound by reading the weights
+// once: 16 output columns (with GATE of both matrices) per workgroup, whose
+// waves divide the sum over k among them; weights and x go from memory to
+// registers as MFMA fragments, 16 weight rows down and the x rows across.
+// One launch without partial sums in memory: one row of 2048 x 8192 takes 13
+// and 11 us (5.2 and 3.1 TB/s), where 128-tiles divided along k took 15 + 5 and
+// 10 + 6 us with their joins.
+template <int MT, bool GATE, int ACT, int NW>
+__global__ __launch_bounds__(64 * NW, NW / 8) void ffn_few_rows_kernel(Prod p) {
+  constexpr int NB = GATE ? 2 : 1, STEPS = 8 / MT;   // k steps of 32 whose loads go out together
+  __shared__ f32x4_t red[NW][NB][MT][64];
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t n0 = int64_t(xcd_item(blockIdx.x, gridDim.x)) * 16;
+  // Rows past the end repeat the last one: their results are not stored.
+  const int64_t wrow = min(n0 + r, int64_t(p.n) - 1);
+  const uint16_t* w[2] = {static_cast<const uint16_t*>(p.b) + wrow * p.ldb,
+                          static_cast<const uint16_t*>(p.b2) + (GATE ? wrow * p.ldb2 : 0)};
+  const uint16_t* x[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) x[t] = static_cast<const uint16_t*>(p.a) + min(16 * t + r, p.m - 1) * p.lda;
+  f32x4_t acc[NB][MT];
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int t = 0; t < MT; ++t) acc[i][t] = (f32x4_t)(0.f);
+  // The waves take turns along k, STEPS steps each.
+  const int steps = (p.k + 31) / 32;
+  for (int s0 = wave * STEPS; s0 < steps; s0 += NW * STEPS) {
+    u32x4_t fw[STEPS][NB], fx[STEPS][MT];
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      const int k = (s0 + s) * 32 + 8 * q;
+      const bool ok = k < p.k;              // k is a multiple of 8: whole groups
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        fw[s][i] = u32x4_t{0, 0, 0, 0};
+        if (ok) fw[s][i] = *as_global(reinterpret_cast<const u32x4_t*>(w[i] + k));
+      }
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        fx[s][t] = u32x4_t{0, 0, 0, 0};
+        if (ok) fx[s][t] = *as_global(reinterpret_cast<const u32x4_t*>(x[t] + k));
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) acc[i][t] = mfma16(fw[s][i], fx[s][t], acc[i][t]);
+  }
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int t = 0; t < MT; ++t) red[wave][i][t][lane] = acc[i][t];
+  __syncthreads();
+  // Wave t finishes rows 16 t ..: a lane has columns n0 + 4 q .. + 3 of one.
+  if (wave >= MT) return;
+  f32x4_t sum[NB];
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    sum[i] = red[0][i][wave][lane];
+#pragma unroll
+    for (int v = 1; v < NW; ++v) sum[i] += red[v][i][wave][lane];
+  }
+  const int64_t m = 16 * wave + r, n = n0 + 4 * q;
+  if (m >= p.m || n >= p.n) return;         // p.n is a multiple of 8
+  auto store4 = [](void* c, int64_t e, f32x4_t v) {
+    *as_global(reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(c) + e)) =
+        u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+  };
+  if constexpr (GATE) {
+    f32x4_t h;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float av, d;
+      act_of<ACT>(sum[0][k], av, d);
+      h[k] = av * sum[1][k];
+    }
+    if (p.c2) {
+      store4(p.c2, m * p.ldc2 + n, sum[0]);
+      store4(p.c2, m * p.ldc2 + p.n + n, sum[1]);
+    }
+    store4(p.c, m * p.ldc + n, h);
+  } else {
+    store4(p.c, m * p.ldc + n, sum[0]);
+  }
+}
+
+// Every workgroup reads all of x, from L2 at about 7 TB/s; the tiled kernels
+// take 8 us and an eighth of the weights' time longer than reading them.  (At
+// 2048 x 8192: 24 us against 37 for one row, 31 against 37 for 16, 42 against
+// 39 for 32; at 5120 x 20480 143 against 165 for one, 204 against 172 for 16.)
+bool few_rows(int64_t t, int64_t d, int64_t h) {
+  const double dh = double(d) * h, again_us = t * dh * (4.0 / 16) / 7e6, weights_us = 6 * dh / 5.1e6;
+  return t <= 64 && again_us <= 8 + weights_us / 8;
+}
+
+template <bool GATE, int ACT>
+hipError_t run_few_rows(hipStream_t s, const Prod& p) {
+  const unsigned grid = unsigned((p.n + 15) / 16);
+  const bool wide = grid < 256;       // fewer workgroups than CUs: more waves to each
+  auto* k = p.m <= 16   ? (wide ? ffn_few_rows_kernel<1, GATE, ACT, 16> : ffn_few_rows_kernel<1, GATE, ACT, 8>)
+            : p.m <= 32 ? (wide ? ffn_few_rows_kernel<2, GATE, ACT, 16> : ffn_few_rows_kernel<2, GATE, ACT, 8>)
+                        : (wide ? ffn_few_rows_kernel<4, GATE, ACT, 16> : ffn_few_rows_kernel<4, GATE, ACT, 8>);
+  hipLaunchKernelGGL(k, dim3(grid), dim3(wide ? 1024 : 512), 0, s, p);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 size_t ffn_fwd_part_bytes(int64_t t, int64_t d, int64_t h) {
-  if (t == 0) return 0;
+  if (t == 0 || few_rows(t, d, h)) return 0;
   const size_t a = part_bytes(plan_of(sizes(t, h, d, 1), true)), b = part_bytes(plan_of(sizes(t, d, h, 1), false));
   return a > b ? a : b;
 }
@@ -564,14 +675,16 @@ hipError_t launch_ffn_fwd(hipStream_t s, const FfnDev& f) {
   p.b = f.w_gate; p.ldb = f.ld_wg; p.b2 = f.w_up; p.ldb2 = f.ld_wu;
   p.c = f.hid; p.ldc = h; p.c2 = f.gu; p.ldc2 = f.ld_gu;
   p.m = t; p.n = h; p.k = d;
-  hipError_t e = f.act ? run_prod<false, false, EPI_GATE, 1>(s, g) : run_prod<false, false, EPI_GATE, 0>(s, g);
+  const bool few = few_rows(t, d, h);
+  hipError_t e = few ? (f.act ? run_few_rows<true, 1>(s, p) : run_few_rows<true, 0>(s, p))
+                 : f.act ? run_prod<false, false, EPI_GATE, 1>(s, g) : run_prod<false, false, EPI_GATE, 0>(s, g);
   if (e != hipSuccess) return e;
   p = Prod{};
   p.a = f.hid; p.lda = h;
   p.b = f.w_down; p.ldb = f.ld_wd;
   p.c = f.y; p.ldc = f.ld_y;
   p.m = t; p.n = d; p.k = h;
-  return run_prod<false, false, EPI_BF16>(s, g);
+  return few ? run_few_rows<false, 0>(s, p) : run_prod<false, false, EPI_BF16>(s, g);
 }
 
 hipError_t launch_ffn_bwd(hipStream_t s, const FfnDev& f) {

@@ -220,3 +220,52 @@ def test_graph_replays():
         g2 = b.attn_bwd(g, q, k, v, o2, lse2, k_lens=kn)
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
         assert all(torch.equal(x, y) for x, y in zip(grads, g2)), n
+
+
+def test_offsets_past_32_bits():
+    """Keys whose rows lie 2^15 values apart, more than 2^31 values in all."""
+    b = block()
+    n = 70_000
+    cache = torch.empty(n * 32768, dtype=BF16, device="cuda").view(1, n, 32768)
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    k1, v1 = (torch.randn(1, n, 1, 64, generator=gen, device="cuda").to(BF16) for _ in range(2))
+    k, v = cache[:, :, 64:128].unflatten(2, (1, 64)), cache[:, :, 128:192].unflatten(2, (1, 64))
+    k.copy_(k1)
+    v.copy_(v1)
+    q, g = (torch.randn(1, 3, 2, 64, generator=gen, device="cuda").to(BF16) for _ in range(2))
+    o, lse = b.attn_fwd(q, k, v)
+    o1, lse1 = b.attn_fwd(q, k1, v1)
+    assert torch.equal(o, o1) and torch.equal(lse, lse1)
+    for x, y in zip(b.attn_bwd(g, q, k, v, o, lse), b.attn_bwd(g, q, k1, v1, o, lse)):
+        assert torch.equal(x, y)
+
+
+def test_gradients_into_given_tensors():
+    b = block()
+    qkv = make(2, 77, 77, 2, 2, 64)[0].repeat(1, 1, 3, 1).view(2, 77, 3, 2, 64)
+    q, k, v = qkv.unbind(2)
+    o, lse = b.attn_fwd(q, k, v, causal=True)
+    g = make(2, 77, 77, 2, 2, 64, seed=1)[3]
+    packed = torch.full_like(qkv, float("nan"))
+    b.attn_bwd(g, q, k, v, o, lse, causal=True, out=packed.unbind(2))
+    for x, y in zip(packed.unbind(2), b.attn_bwd(g, q, k, v, o, lse, causal=True)):
+        assert torch.equal(x, y)
+    leaf = qkv.clone().requires_grad_(True)
+    b.attention_qkv(leaf, causal=True).backward(g)
+    assert torch.equal(leaf.grad, packed)
+    with pytest.raises(ValueError):
+        b.attn_bwd(g, q, k, v, o, lse, out=(q, k, v[:1]))
+
+
+def test_another_stream():
+    b = block()
+    q, k, v, g = make(1, 2, 6000, 4, 2, 128)       # few queries: takes a workspace
+    o, lse = b.attn_fwd(q, k, v)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        o2, lse2 = b.attn_fwd(q, k, v)
+        grads = b.attn_bwd(g, q, k, v, o2, lse2)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert all(torch.equal(x, y) for x, y in zip(grads, b.attn_bwd(g, q, k, v, o, lse)))

@@ -150,3 +150,34 @@ def test_graph_replays(t):
         y2, gu2 = b.ffn_fwd(x, wg, wu, wd)
         d2 = b.ffn_bwd(dy, x, wg, wu, wd, gu2)
         assert torch.equal(y, y2) and all(torch.equal(p, q) for p, q in zip(d, d2))
+
+
+@pytest.mark.parametrize("t", [70_000])
+def test_offsets_past_32_bits(t):
+    """Rows 2^15 values apart, more than 2^31 values in all, on every side."""
+    b = block()
+    x1, wg, wu, wd, dy1 = make(t, 64, 128)
+    x, dy = (torch.empty(t * 32768, dtype=BF16, device="cuda").view(t, 32768)[:, 64:128] for _ in range(2))
+    x.copy_(x1)
+    dy.copy_(dy1)
+    y, gu = b.ffn_fwd(x, wg, wu, wd)
+    y1, gu1 = b.ffn_fwd(x1, wg, wu, wd)
+    assert torch.equal(y, y1) and torch.equal(gu, gu1)
+    wide = torch.empty(t * 32768, dtype=BF16, device="cuda").view(t, 32768)[:, 8:264]
+    wide.copy_(gu)
+    for p, q in zip(b.ffn_bwd(dy, x, wg, wu, wd, wide), b.ffn_bwd(dy1, x1, wg, wu, wd, gu)):
+        assert torch.equal(p, q)
+
+
+def test_another_stream():
+    b = block()
+    x, wg, wu, wd, dy = make(700, 256, 512)
+    y, gu = b.ffn_fwd(x, wg, wu, wd)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        y2, gu2 = b.ffn_fwd(x, wg, wu, wd)
+        d2 = b.ffn_bwd(dy, x, wg, wu, wd, gu2)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(y, y2)
+    assert all(torch.equal(p, q) for p, q in zip(d2, b.ffn_bwd(dy, x, wg, wu, wd, gu)))

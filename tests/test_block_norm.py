@@ -209,3 +209,14 @@ def test_side_stream_and_graph_replays():
         assert torch.equal(o, eo) and torch.equal(y, ey)
         assert all(torch.equal(d[n], ed[n]) for n in NAMES), k
     assert gr["resid"].shape == o.shape
+
+
+def test_offsets_past_32_bits():
+    """A row more than 2^31 values into its tensor."""
+    b = block()
+    rows, cols = 280_000, 8192
+    x = torch.zeros(rows, cols, dtype=BF16, device="cuda")
+    x[-3:] = torch.randn(3, cols, generator=torch.Generator(device="cuda").manual_seed(0), device="cuda").to(BF16)
+    out, y, _ = b.norm_fwd(x, pre="rms")
+    want = b.norm_fwd(x[-3:].clone(), pre="rms")[1]
+    assert torch.equal(y[-3:], want) and bool((y[:5] == 0).all())
