@@ -15,11 +15,12 @@
 // Fusions: one product forms g and u side by side (the B tile takes 16 rows
 // of Wg and 16 of Wu in turn, so a lane holds both for the same columns) and
 // writes h; the dh product's epilogue reads g and u and writes dg, du and h;
-// dx is one product over 2 f; the three weights' gradients are one launch.
+// dx, one product over 2 f, and the three weights' gradients are one launch.
 //
 // Bound by the matrix cores from some hundreds of rows on, by reading the
 // weights below.  Roundings to bf16: g and u as stored, h and dg, du as the
 // next product's operands, and the results.
+#include <algorithm>
 #include <type_traits>
 
 #include "block_mfma.h"
@@ -57,21 +58,26 @@ struct Prod {
   const void* gu;       // EPI_DGATE
   int64_t lda, ldb, ldb2, ldc, ldc2, ldgu;
   int32_t m, n, k;      // k of one segment
-  int32_t mt, nt;       // tiles
-};
-struct ProdArgs {
-  Prod p[3];
-  int32_t count;
   int32_t segments;     // 1, or 2: the sum goes on over a second k range (A's
                         // columns k .. 2 k - 1, B in b2)
+  int32_t acols;        // A lies along m (launches that mix both)
+  int32_t f32;          // EPI_PLAIN: C is fp32, not bf16
+  int32_t mt, nt;       // tiles
   // The first `full` tiles are one workgroup each; the others' sums are cut
   // into `splits` ranges of split_stages stages, a workgroup each, whose fp32
-  // results go to part and are added by a second kernel.
+  // results go to the launch's part and are added by a second kernel.
   int32_t full, splits, split_stages;
+  int32_t item0, part0, join0;   // its first workgroup, range and tile to join
+};
+constexpr int kProds = 4;
+struct ProdArgs {
+  Prod p[kProds];
+  int32_t count;
   float* part;
 };
 
-enum { EPI_BF16 = 0, EPI_F32 = 1, EPI_GATE = 2, EPI_DGATE = 3 };
+enum { EPI_PLAIN = 0, EPI_GATE = 1, EPI_DGATE = 2 };
+enum { ROWS_ROWS = 0, ROWS_COLS = 1, MIXED_COLS = 2 };   // how A and B lie
 
 // One operand's side of a stage: 32 k of BT rows (64 bytes each in LDS), or
 // COLS, BT columns of 32 rows of k (2 BT bytes each).
@@ -161,20 +167,13 @@ struct Frag {
   }
 };
 
-// Tile `item` of the list: its product and place.  Bands of 8 tile rows,
-// walked column by column, so that tiles near each other share operands in
-// their XCD's L2.
-struct Tile { int which, tm, tn; };
-__device__ __forceinline__ Tile tile_of(const ProdArgs& g, int item) {
-  int which = 0;
-  while (which + 1 < g.count && item >= g.p[which].mt * g.p[which].nt) {
-    item -= g.p[which].mt * g.p[which].nt;
-    ++which;
-  }
-  const Prod& p = g.p[which];
+// Place of a product's tile.  Bands of 8 tile rows, walked column by column,
+// so that tiles near each other share operands in their XCD's L2.
+struct Tile { int tm, tn; };
+__device__ __forceinline__ Tile tile_of(const Prod& p, int item) {
   const int band = item / (8 * p.nt), inb = item - band * 8 * p.nt;
   const int bh = min(8, p.mt - band * 8);
-  return Tile{which, band * 8 + inb % bh, inb / bh};
+  return Tile{band * 8 + inb % bh, inb / bh};
 }
 
 // Output columns of a tile.
@@ -279,7 +278,7 @@ __device__ __forceinline__ void emit_rows(const Prod& p, const f32x4_t (*acc)[BT
         store_vals<uint16_t, 8>(p.c, m * p.ldc + n, dg);
         store_vals<uint16_t, 8>(p.c, m * p.ldc + p.n + n, v);
         store_vals<uint16_t, 8>(p.c2, m * p.ldc2 + n, h);
-      } else if constexpr (EPI == EPI_F32) {
+      } else if (p.f32) {
         store_vals<float, 8>(p.c, m * p.ldc + n, v);
       } else {
         store_vals<uint16_t, 8>(p.c, m * p.ldc + n, v);
@@ -289,6 +288,10 @@ __device__ __forceinline__ void emit_rows(const Prod& p, const f32x4_t (*acc)[BT
   __builtin_amdgcn_wave_barrier();
 }
 
+// Stages in the LDS ring: 128 KB, or 80 KB for two workgroups per CU.
+template <int BT>
+constexpr int ring_stages() { return BT == 256 ? 4 : 5; }
+
 // One BT x BT tile per workgroup of four waves, each (BT / 2) x (BT / 2).
 // Software pipeline over a ring of stages: the fragments of one stage are in
 // registers while its MFMAs run; each fragment is refilled with the next
@@ -297,26 +300,11 @@ __device__ __forceinline__ void emit_rows(const Prod& p, const f32x4_t (*acc)[BT
 // MFMAs of a stage, makes the next stage visible and says that the previous
 // one's buffer is free (its fragments are in registers everywhere).
 template <int BT, bool ACOLS, bool BCOLS, int EPI, int ACT>
-__global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void ffn_gemm_kernel(ProdArgs g) {
+__device__ __forceinline__ void run_tile(const Prod& p, Tile tile, int range, float* part, unsigned char* smem, int lane,
+                                         int wave) {
   constexpr int F = BT / 32;                       // fragments per wave and side
-  constexpr int STAGE = 2 * BT * kStageK * 2;
-  constexpr int NSTAGE = BT == 256 ? 4 : 5;        // 128 KB, or 80 KB for two workgroups per CU
-  __shared__ __attribute__((aligned(1024))) unsigned char smem[NSTAGE * STAGE];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  constexpr int STAGE = 2 * BT * kStageK * 2, NSTAGE = ring_stages<BT>();
   const int wm = wave >> 1, wn = wave & 1;
-
-  // Whole tiles first, then the ranges of the split ones.
-  const int id = int(blockIdx.x);
-  int item, range = -1;
-  if (id < g.full) {
-    item = int(xcd_item(unsigned(id), unsigned(g.full)));
-  } else {
-    range = int(xcd_item(unsigned(id - g.full), gridDim.x - unsigned(g.full)));
-    item = g.full + range / g.splits;
-  }
-  const Tile tile = tile_of(g, item);
-  const Prod& p = g.p[tile.which];
   constexpr int NSTEP = tile_cols<BT, EPI>();
   const int64_t m0 = int64_t(tile.tm) * BT, n0 = int64_t(tile.tn) * NSTEP;
 
@@ -333,15 +321,15 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void ffn_gemm_kernel(ProdAr
   fa.init(wm, lane);
   fb.init(wn, lane);
 
-  const int per = (p.k + kStageK - 1) / kStageK, all = per * g.segments;
-  const int first = range < 0 ? 0 : range % g.splits * g.split_stages;
-  const int stages = range < 0 ? all : max(0, min(all - first, g.split_stages));
+  const int per = (p.k + kStageK - 1) / kStageK, all = per * p.segments;
+  const int first = range < 0 ? 0 : range % p.splits * p.split_stages;
+  const int stages = range < 0 ? all : max(0, min(all - first, p.split_stages));
   const unsigned lds = lds_offset(smem);
   // Stages past the end are issued as a reload of the last one, so that every
   // stage waits for the same number of DMAs; nothing reads them.
   auto issue_one = [&](int s, int i) {
     const int sc = first + min(s, stages - 1);
-    const int seg = EPI == EPI_BF16 && BCOLS && sc >= per ? 1 : 0;
+    const int seg = EPI == EPI_PLAIN && BCOLS && !ACOLS && sc >= per ? 1 : 0;
     const int ks = sc - seg * per, left = p.k - ks * kStageK;
     const unsigned at = lds + unsigned(s % NSTAGE) * STAGE;
     if (i < sa.DMA) {
@@ -401,7 +389,7 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void ffn_gemm_kernel(ProdAr
   barrier();
 
   if (range >= 0) {
-    float* o = g.part + (int64_t(range) * 4 + wave) * (F * F * 256) + lane * 4;
+    float* o = part + (int64_t(p.part0 + range) * 4 + wave) * (F * F * 256) + lane * 4;
     // blocks of 16 rows that the matrix has
 #pragma unroll
     for (int x = 0; x < F; ++x)
@@ -418,6 +406,33 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void ffn_gemm_kernel(ProdAr
     emit_rows<BT, EPI, ACT, XB>(p, &acc[x], er, m0 + wm * (BT / 2) + x * 16, n0 + wn * (NSTEP / 2), lane);
 }
 
+// MIXED_COLS: products of both kinds of A in one launch.
+template <int BT, int LIE, int EPI, int ACT>
+__global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void ffn_gemm_kernel(ProdArgs g) {
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[ring_stages<BT>() * 2 * BT * kStageK * 2];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int id = int(blockIdx.x), which = 0;
+  while (which + 1 < g.count && id >= g.p[which + 1].item0) ++which;
+  const Prod& p = g.p[which];
+  id -= p.item0;
+  // Whole tiles first, then the ranges of the split ones.
+  int item, range = -1;
+  if (id < p.full) {
+    item = int(xcd_item(unsigned(id), unsigned(p.full)));
+  } else {
+    range = int(xcd_item(unsigned(id - p.full), unsigned((p.mt * p.nt - p.full) * p.splits)));
+    item = p.full + range / p.splits;
+  }
+  const Tile tile = tile_of(p, item);
+  if constexpr (LIE == MIXED_COLS) {
+    if (p.acols) run_tile<BT, true, true, EPI, ACT>(p, tile, range, g.part, smem, lane, wave);
+    else run_tile<BT, false, true, EPI, ACT>(p, tile, range, g.part, smem, lane, wave);
+  } else {
+    run_tile<BT, false, LIE == ROWS_COLS, EPI, ACT>(p, tile, range, g.part, smem, lane, wave);
+  }
+}
+
 // Adds the ranges of one split tile, 16 rows of each wave's part per
 // workgroup, and finishes them as the product's own epilogue would.
 template <int BT, int EPI, int ACT>
@@ -426,16 +441,19 @@ __global__ __launch_bounds__(256) void ffn_join_kernel(ProdArgs g) {
   __shared__ float rows[4 * 16 * (BT / 2 + 4)];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int tile = blockIdx.x / F, x = blockIdx.x % F;
-  const Tile t = tile_of(g, g.full + tile);
-  const Prod& p = g.p[t.which];
+  int tile = blockIdx.x / F, which = 0;
+  const int x = blockIdx.x % F;
+  while (which + 1 < g.count && tile >= g.p[which + 1].join0) ++which;
+  const Prod& p = g.p[which];
+  tile -= p.join0;
+  const Tile t = tile_of(p, p.full + tile);
   if (int64_t(t.tm) * BT + (wave >> 1) * (BT / 2) + x * 16 >= p.m) return;   // a whole wave, no barrier follows
   f32x4_t acc[1][F];
 #pragma unroll
   for (int y = 0; y < F; ++y) acc[0][y] = (f32x4_t)(0.f);
 #pragma unroll 4
-  for (int i = 0; i < g.splits; ++i) {
-    const float* o = g.part + (int64_t(tile * g.splits + i) * 4 + wave) * (F * F * 256) + lane * 4;
+  for (int i = 0; i < p.splits; ++i) {
+    const float* o = g.part + (int64_t(p.part0 + tile * p.splits + i) * 4 + wave) * (F * F * 256) + lane * 4;
 #pragma unroll
     for (int y = 0; y < F; ++y) acc[0][y] += *as_global(reinterpret_cast<const f32x4_t*>(o + (x * F + y) * 256));
   }
@@ -446,45 +464,59 @@ __global__ __launch_bounds__(256) void ffn_join_kernel(ProdArgs g) {
 
 
 // How a list of products is run.  A workgroup of a 256-tile takes a CU, of
-// 128-tiles two fit.  Tiles beyond the last whole round over the CUs would
-// leave most of them idle; where that is worth a second kernel, their sums
-// over k are divided so that they fill one more, shorter round.
+// 128-tiles two fit.  Where a product's tiles do not fill a round over the
+// CUs, or take much longer than the launch's others, their sums over k are
+// divided, if that is worth a second kernel.
 //
 // The choice goes by the time of each way, from what was measured on this
 // card: a stage takes 0.78 us in 256-tiles and 0.6 us in two 128-tiles of a CU
-// (which do half the work), a tile's start and epilogue 11 and 7 us, and a
-// join 4 us and its partial sums' writing and reading at 4.5 TB/s.
+// (which do half the work), a tile's start and epilogue 11 and 5 us, a launch
+// of 256-tiles 8 us more until its first stages are in, and a join 4 us and its
+// partial sums' writing and reading at 4.5 TB/s.  (dx and the weights'
+// gradients of 777 x 1000 x 2728: 128-tiles with dx in three ranges 50 us,
+// 256-tiles in four 58.)
 struct Plan {
-  int bt, tiles, full, splits, split_stages;
+  int bt;
   double us;
+  struct { int tiles, full, splits, split_stages; } p[kProds];
 };
+int stages_of(const Prod& p) { return (p.k + kStageK - 1) / kStageK * p.segments; }
+
 Plan plan_with(const ProdArgs& g, int bt, bool gate) {
   Plan q{};
   q.bt = bt;
   const int nstep = gate ? bt / 2 : bt, slots = bt == 256 ? 256 : 512;
-  const double stage_us = bt == 256 ? 0.78 : 0.6, tile_us = bt == 256 ? 11 : 7;
-  int stages = 0, rows = 0;
+  const double stage_us = bt == 256 ? 0.78 : 0.6, tile_us = bt == 256 ? 11 : 5;
+  const double launch_us = bt == 256 ? 8 : 0;
+  double others = 0, longest = 0, shortest = 1e30;    // of the products after the first
   for (int i = 0; i < g.count; ++i) {
-    q.tiles += ((g.p[i].m + bt - 1) / bt) * ((g.p[i].n + nstep - 1) / nstep);
-    const int st = (g.p[i].k + kStageK - 1) / kStageK * g.segments;
-    stages = st > stages ? st : stages;
-    rows = g.p[i].m > rows ? g.p[i].m : rows;
+    const int st = stages_of(g.p[i]), tiles = ((g.p[i].m + bt - 1) / bt) * ((g.p[i].n + nstep - 1) / nstep);
+    q.p[i] = {tiles, tiles, 1, st};
+    const double us = st * stage_us + tile_us;
+    if (i > 0) {
+      others += tiles * us;
+      longest = us > longest ? us : longest;
+      shortest = us < shortest ? us : shortest;
+    }
   }
-  const int rem = q.tiles % slots, whole = q.tiles / slots;
-  const double tile = stages * stage_us + tile_us;
-  q.full = q.tiles;
-  q.splits = 1;
-  q.split_stages = stages;
-  q.us = (whole + (rem > 0)) * tile;
-  const double part_mb = double(bt) * (rows < bt ? (rows + 15) / 16 * 16 : bt) * 4e-6;
-  for (int n = 2; rem > 0 && n <= slots / rem && n <= stages / 4; ++n) {
+  // The first product, alone or ahead of the others, undivided or in n ranges.
+  const int stages = stages_of(g.p[0]), tiles = q.p[0].tiles, rows = g.p[0].m;
+  const int rem = g.count > 1 ? tiles : tiles % slots, whole = g.count > 1 ? 0 : tiles / slots;
+  const double part_mb = double(bt) * (rows < bt ? (rows + 15) / 16 * 16 : bt) * 4e-6, tile = stages * stage_us + tile_us;
+  for (int n = 1; n == 1 || (rem > 0 && n <= stages / 4 && n <= (g.count > 1 ? 32 : slots / rem)); ++n) {
     const int per = (stages + n - 1) / n, got = (stages + per - 1) / per;
-    const double us = whole * tile + per * stage_us + tile_us + 4 + 2 * rem * got * part_mb / 4.5;
-    if (us < q.us) {
+    const double one = per * stage_us + tile_us, join = got > 1 ? 4 + 2 * rem * got * part_mb / 4.5 : 0;
+    double us;
+    if (g.count == 1) {
+      us = whole * tile + (rem > 0 ? one : 0) + join + launch_us;
+    } else {
+      // workgroups of unequal length, the long ones first
+      const double even = (others + rem * got * one) / slots, least = one < shortest ? one : shortest;
+      us = std::max(std::max(one, longest), even + 0.5 * least) + join + launch_us;
+    }
+    if (n == 1 || us < q.us) {
       q.us = us;
-      q.splits = got;
-      q.split_stages = per;
-      q.full = q.tiles - rem;
+      q.p[0] = {tiles, got > 1 ? tiles - rem : tiles, got, per};
     }
   }
   return q;
@@ -493,49 +525,63 @@ Plan plan_of(const ProdArgs& g, bool gate) {
   const Plan big = plan_with(g, 256, gate), small = plan_with(g, 128, gate);
   return big.us <= small.us ? big : small;
 }
-size_t part_bytes(const Plan& q) {
-  return q.full == q.tiles ? 0 : size_t(q.tiles - q.full) * q.splits * q.bt * q.bt * 4;
+size_t part_bytes(const ProdArgs& g, const Plan& q) {
+  size_t ranges = 0;
+  for (int i = 0; i < g.count; ++i) ranges += size_t(q.p[i].tiles - q.p[i].full) * q.p[i].splits;
+  return ranges * q.bt * q.bt * 4;
 }
 
-template <int BT, bool ACOLS, bool BCOLS, int EPI, int ACT>
+template <int BT, int LIE, int EPI, int ACT>
 hipError_t launch_prod(hipStream_t s, ProdArgs g, const Plan& q) {
   constexpr int NSTEP = tile_cols<BT, EPI>();
+  int items = 0, ranges = 0, joins = 0;
   for (int i = 0; i < g.count; ++i) {
-    g.p[i].mt = (g.p[i].m + BT - 1) / BT;
-    g.p[i].nt = (g.p[i].n + NSTEP - 1) / NSTEP;
+    Prod& p = g.p[i];
+    p.mt = (p.m + BT - 1) / BT;
+    p.nt = (p.n + NSTEP - 1) / NSTEP;
+    p.full = q.p[i].full;
+    p.splits = q.p[i].splits;
+    p.split_stages = q.p[i].split_stages;
+    p.item0 = items;
+    p.part0 = ranges;
+    p.join0 = joins;
+    const int split = q.p[i].tiles - p.full;
+    items += p.full + split * p.splits;
+    ranges += split * p.splits;
+    joins += split;
   }
-  g.full = q.full;
-  g.splits = q.splits;
-  g.split_stages = q.split_stages;
-  const int rem = q.tiles - q.full;
-  hipLaunchKernelGGL((ffn_gemm_kernel<BT, ACOLS, BCOLS, EPI, ACT>), dim3(unsigned(q.full + rem * q.splits)), dim3(256),
-                     0, s, g);
+  hipLaunchKernelGGL((ffn_gemm_kernel<BT, LIE, EPI, ACT>), dim3(unsigned(items)), dim3(256), 0, s, g);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || rem == 0) return e;
-  hipLaunchKernelGGL((ffn_join_kernel<BT, EPI, ACT>), dim3(unsigned(rem * (BT / 32))), dim3(256), 0, s, g);
+  if (e != hipSuccess || joins == 0) return e;
+  hipLaunchKernelGGL((ffn_join_kernel<BT, EPI, ACT>), dim3(unsigned(joins * (BT / 32))), dim3(256), 0, s, g);
   return hipGetLastError();
 }
 
-template <bool ACOLS, bool BCOLS, int EPI, int ACT = 0>
+template <int LIE, int EPI, int ACT = 0>
 hipError_t run_prod(hipStream_t s, const ProdArgs& g) {
   const Plan q = plan_of(g, EPI == EPI_GATE);
-  return q.bt == 256 ? launch_prod<256, ACOLS, BCOLS, EPI, ACT>(s, g, q)
-                     : launch_prod<128, ACOLS, BCOLS, EPI, ACT>(s, g, q);
+  return q.bt == 256 ? launch_prod<256, LIE, EPI, ACT>(s, g, q) : launch_prod<128, LIE, EPI, ACT>(s, g, q);
 }
 
-// Sizes of the products, for the workspace.
-ProdArgs sizes(int64_t m, int64_t n, int64_t k, int segments) {
+// Sizes of the launches, for their choice and the workspace.
+Prod sizes(int64_t m, int64_t n, int64_t k, int segments = 1) {
+  Prod p{};
+  p.m = int32_t(m); p.n = int32_t(n); p.k = int32_t(k);
+  p.segments = segments;
+  return p;
+}
+ProdArgs alone(const Prod& p) {
   ProdArgs g{};
+  g.p[0] = p;
   g.count = 1;
-  g.segments = segments;
-  g.p[0].m = int32_t(m); g.p[0].n = int32_t(n); g.p[0].k = int32_t(k);
   return g;
 }
-ProdArgs weight_sizes(int64_t t, int64_t d, int64_t h) {
-  ProdArgs g = sizes(h, d, t, 1);
-  g.count = 3;
-  g.p[1] = g.p[2] = g.p[0];
-  g.p[2].m = int32_t(d); g.p[2].n = int32_t(h);
+ProdArgs backward_sizes(int64_t t, int64_t d, int64_t h) {
+  ProdArgs g{};
+  g.p[0] = sizes(t, d, h, 2);
+  g.p[1] = g.p[2] = sizes(h, d, t);
+  g.p[3] = sizes(d, h, t);
+  g.count = 4;
   return g;
 }
 
@@ -654,79 +700,66 @@ hipError_t run_few_rows(hipStream_t s, const Prod& p) {
 
 size_t ffn_fwd_part_bytes(int64_t t, int64_t d, int64_t h) {
   if (t == 0 || few_rows(t, d, h)) return 0;
-  const size_t a = part_bytes(plan_of(sizes(t, h, d, 1), true)), b = part_bytes(plan_of(sizes(t, d, h, 1), false));
-  return a > b ? a : b;
+  const ProdArgs up = alone(sizes(t, h, d)), down = alone(sizes(t, d, h));
+  return std::max(part_bytes(up, plan_of(up, true)), part_bytes(down, plan_of(down, false)));
 }
 size_t ffn_bwd_part_bytes(int64_t t, int64_t d, int64_t h) {
   if (t == 0) return 0;
-  const size_t a = part_bytes(plan_of(sizes(t, h, d, 1), false)), b = part_bytes(plan_of(sizes(t, d, h, 2), false));
-  const size_t c = part_bytes(plan_of(weight_sizes(t, d, h), false));
-  return a > b ? (a > c ? a : c) : (b > c ? b : c);
+  const ProdArgs dh = alone(sizes(t, h, d)), rest = backward_sizes(t, d, h);
+  return std::max(part_bytes(dh, plan_of(dh, false)), part_bytes(rest, plan_of(rest, false)));
 }
 
 hipError_t launch_ffn_fwd(hipStream_t s, const FfnDev& f) {
-  const int32_t t = int32_t(f.rows), d = int32_t(f.cols), h = int32_t(f.hidden);
-  ProdArgs g{};
-  g.count = 1;
-  g.segments = 1;
+  const int64_t t = f.rows, d = f.cols, h = f.hidden;
+  ProdArgs g = alone(sizes(t, h, d));
   g.part = f.part;
   Prod& p = g.p[0];
   p.a = f.x; p.lda = f.ld_x;
   p.b = f.w_gate; p.ldb = f.ld_wg; p.b2 = f.w_up; p.ldb2 = f.ld_wu;
   p.c = f.hid; p.ldc = h; p.c2 = f.gu; p.ldc2 = f.ld_gu;
-  p.m = t; p.n = h; p.k = d;
   const bool few = few_rows(t, d, h);
   hipError_t e = few ? (f.act ? run_few_rows<true, 1>(s, p) : run_few_rows<true, 0>(s, p))
-                 : f.act ? run_prod<false, false, EPI_GATE, 1>(s, g) : run_prod<false, false, EPI_GATE, 0>(s, g);
+                 : f.act ? run_prod<ROWS_ROWS, EPI_GATE, 1>(s, g) : run_prod<ROWS_ROWS, EPI_GATE, 0>(s, g);
   if (e != hipSuccess) return e;
-  p = Prod{};
+  p = sizes(t, d, h);
   p.a = f.hid; p.lda = h;
   p.b = f.w_down; p.ldb = f.ld_wd;
   p.c = f.y; p.ldc = f.ld_y;
-  p.m = t; p.n = d; p.k = h;
-  return few ? run_few_rows<false, 0>(s, p) : run_prod<false, false, EPI_BF16>(s, g);
+  return few ? run_few_rows<false, 0>(s, p) : run_prod<ROWS_ROWS, EPI_PLAIN>(s, g);
 }
 
 hipError_t launch_ffn_bwd(hipStream_t s, const FfnDev& f) {
-  const int32_t t = int32_t(f.rows), d = int32_t(f.cols), h = int32_t(f.hidden);
-  ProdArgs g{};
-  g.count = 1;
-  g.segments = 1;
+  const int64_t t = f.rows, d = f.cols, h = f.hidden;
+  ProdArgs g = alone(sizes(t, h, d));
   g.part = f.part;
   Prod& p = g.p[0];
   p.a = f.d_y; p.lda = f.ld_dy;
   p.b = f.w_down; p.ldb = f.ld_wd;
-  p.c = f.dgu; p.ldc = 2 * int64_t(h); p.c2 = f.hid; p.ldc2 = h;
+  p.c = f.dgu; p.ldc = 2 * h; p.c2 = f.hid; p.ldc2 = h;
   p.gu = f.gu; p.ldgu = f.ld_gu;
-  p.m = t; p.n = h; p.k = d;
-  hipError_t e = f.act ? run_prod<false, true, EPI_DGATE, 1>(s, g) : run_prod<false, true, EPI_DGATE, 0>(s, g);
+  const hipError_t e = f.act ? run_prod<ROWS_COLS, EPI_DGATE, 1>(s, g) : run_prod<ROWS_COLS, EPI_DGATE, 0>(s, g);
   if (e != hipSuccess) return e;
-  // dx, over the k range of dg and then that of du
-  p = Prod{};
-  g.segments = 2;
-  p.a = f.dgu; p.lda = 2 * int64_t(h);
+  // dx, over the k range of dg and then that of du, and the weights' gradients
+  g = backward_sizes(t, d, h);
+  g.part = f.part;
+  p.a = f.dgu; p.lda = 2 * h;
   p.b = f.w_gate; p.ldb = f.ld_wg; p.b2 = f.w_up; p.ldb2 = f.ld_wu;
   p.c = f.d_x; p.ldc = f.ld_dx;
-  p.m = t; p.n = d; p.k = h;
-  e = run_prod<false, true, EPI_BF16>(s, g);
-  if (e != hipSuccess) return e;
-  g = ProdArgs{};
-  g.count = 3;
-  g.segments = 1;
-  g.part = f.part;
-  for (int i = 0; i < 2; ++i) {
-    Prod& w = g.p[i];
-    w.a = static_cast<const uint16_t*>(f.dgu) + i * int64_t(h); w.lda = 2 * int64_t(h);
-    w.b = f.x; w.ldb = f.ld_x;
-    w.c = i ? f.d_wu : f.d_wg; w.ldc = i ? f.ld_dwu : f.ld_dwg;
-    w.m = h; w.n = d; w.k = t;
+  for (int i = 0; i < 3; ++i) {
+    Prod& w = g.p[1 + i];
+    w.acols = 1;
+    w.f32 = !f.grad_bf16;
+    if (i < 2) {
+      w.a = static_cast<const uint16_t*>(f.dgu) + i * h; w.lda = 2 * h;
+      w.b = f.x; w.ldb = f.ld_x;
+      w.c = i ? f.d_wu : f.d_wg; w.ldc = i ? f.ld_dwu : f.ld_dwg;
+    } else {
+      w.a = f.d_y; w.lda = f.ld_dy;
+      w.b = f.hid; w.ldb = h;
+      w.c = f.d_wd; w.ldc = f.ld_dwd;
+    }
   }
-  Prod& w = g.p[2];
-  w.a = f.d_y; w.lda = f.ld_dy;
-  w.b = f.hid; w.ldb = h;
-  w.c = f.d_wd; w.ldc = f.ld_dwd;
-  w.m = d; w.n = h; w.k = t;
-  return f.grad_bf16 ? run_prod<true, true, EPI_BF16>(s, g) : run_prod<true, true, EPI_F32>(s, g);
+  return run_prod<MIXED_COLS, EPI_PLAIN>(s, g);
 }
 
 }  // namespace muon
