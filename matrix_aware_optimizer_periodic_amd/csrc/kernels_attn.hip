@@ -298,11 +298,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnDev a, unsigned it
              wave);
   };
 
-  if (tiles > 0) {
-    fetch_k(0);
-    fetch_v(0);
-    if (tiles > 1) fetch_k(1);
-  }
+  if (tiles > 0) fetch_k(0);
   u32x4_t q[2 * DB];
   const uint16_t* qrow = static_cast<const uint16_t*>(a.q.p) + r.b * a.q.sb + r.qi * a.q.sl + r.head * a.q.sh;
   load_rows<DB>(q, qrow, r.live, a.dim, half);
@@ -343,9 +339,11 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnDev a, unsigned it
 
   f32x16_t s0[2], s1[2];
   wait_vm<0>();
-  barrier();
   arrived(q);
+  barrier();
   if (tiles > 0) {
+    fetch_v(0);
+    if (tiles > 1) fetch_k(1);
     if (work) {
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
@@ -364,11 +362,10 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnDev a, unsigned it
   // tile from what is in LDS, and unused).
   auto step = [&](int t, auto odd, f32x16_t (&s)[2], f32x16_t (&sn)[2]) {
     constexpr int ODD = decltype(odd)::value;
-    if (t > 0) {
-      wait_vm<0>();
-      barrier();
-    }
-    // k of tile t was read in the step before, v of tile t - 1 too
+    // The next k and this v are in, and every wave has read k of tile t (in the
+    // step before) and v of tile t - 1, whose buffers are refilled.
+    wait_vm<0>();
+    barrier();
     if (t + 2 < tiles) fetch_k(t + 2);
     if (t + 1 < tiles) fetch_v(t + 1);
     if (!work) return;
