@@ -269,3 +269,11 @@ def test_another_stream():
     torch.cuda.current_stream().wait_stream(s)
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
     assert all(torch.equal(x, y) for x, y in zip(grads, b.attn_bwd(g, q, k, v, o, lse)))
+
+
+@pytest.mark.parametrize("b,m,n,h,g,d", [(9, 600, 65, 16, 16, 64), (9, 600, 128, 16, 16, 128), (33, 130, 190, 16, 8, 64),
+                                         (10, 500, 257, 14, 14, 72), (3, 2000, 320, 12, 12, 32)])
+def test_more_row_blocks_than_fit_at_once(b, m, n, h, g, d):
+    """More workgroups than the card holds, with two, three, five key tiles,
+    whole and not."""
+    check(*make(b, m, n, h, g, d, seed=n))
