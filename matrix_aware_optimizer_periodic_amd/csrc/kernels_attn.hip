@@ -897,16 +897,19 @@ int attn_splits(const AttnDev& a, int* split_keys) {
 
 int attn_parts(const AttnDev& a) {
   // The time of the dk, dv kernel in tiles of one workgroup per CU: whole
-  // rounds of workgroups, or under a causal border, where their work differs,
-  // the average plus the last one's.  A divided block's part costs about as
-  // much as four tiles more, to write its sums and read them back.
+  // rounds of workgroups, or under a causal border, where their work differs
+  // and the long ones go first, the average and a little of the longest.  A
+  // divided block's part costs about as much as six tiles more, to write its
+  // sums and read them back.  (8192 keys and queries, 16 heads over 4: the
+  // whole backward pass took 1152, 1023, 961, 1005 and 1000 us with 2, 3, 4, 5
+  // and 8 parts.)
   const double items = double(key_blocks(a)) * a.batch * a.kv_heads;
   const double tiles = double((a.q_len + kTile - 1) / kTile) * (a.heads / a.kv_heads);
   int best = 1;
   double least = 0;
   for (int p = 1; p <= 16 && (p == 1 || tiles / p >= 4); ++p) {
-    const double one = tiles / p + (p > 1 ? 4 : 0);
-    const double time = a.causal ? std::max(one, items * p * (0.55 * tiles / p + (p > 1 ? 4 : 0)) / 256 + 0.5 * one)
+    const double cost = p > 1 ? 6 : 0, one = tiles / p + cost;
+    const double time = a.causal ? std::max(one, items * p * (0.55 * tiles / p + cost) / 256 + 0.1 * one)
                                  : std::ceil(items * p / 256) * one;
     if (p == 1 || time < 0.97 * least) {
       best = p;
