@@ -26,6 +26,12 @@
 // Rows of the forward and dq kernels are the (query, head) pairs that share a
 // key head, the heads of one query next to each other: grouped heads and few
 // queries share the key tiles of one workgroup.
+//
+// Measured on one MI355X (a large library product runs at 1460 TFLOP/s), head
+// size 128: forward 156 us at 16 x 1024, 16 heads (880 TFLOP/s), 985 us at 2 x
+// 8192 (1117); dq 136 us and dk, dv 204 us at 4 x 1024, 40 heads (948 and 842
+// on the products they form), 1230 TFLOP/s for both at 16384; one query of 4 x
+// 32 heads over 8191 keys of 8 24 us (134 MB, 5.5 TB/s) and 5 us for the join.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -271,7 +277,10 @@ __device__ __forceinline__ int seen_most(const AttnDev& a, const Rows& r) {
 // with v, so that the matrix cores and the vector units work at once.  The
 // order within a slot (one product, its fragment's successor, a piece of
 // arithmetic) is fixed; left to itself the compiler waits for each read at
-// once.
+// once.  Two workgroups of four waves and 128 rows per CU: eight waves and 256
+// rows, which bring in half as much, measured 5% slower (the waves meet at
+// every tile), and what a longer way between asking for a tile and using it, or
+// several row blocks per workgroup, could hide measured nothing.
 template <int DB, bool SPLIT>
 __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnDev a, unsigned items) {
   using G = Geo<DB>;
@@ -495,8 +504,9 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnDev a) {
 
 // ---------------------------------------------------------------------------
 // dq, and per row delta = do . o and the exponent's offset for the dk, dv
-// kernel.  Per tile of 64 keys, 32 at a time: s^T = k q^T, dp^T = v do^T,
-// ds^T = p^T (dp^T - delta), dq^T += k^T ds^T.
+// kernel.  Per tile of 64 keys: s^T = k q^T, dp^T = v do^T,
+// ds^T = p^T (dp^T - delta), dq^T += k^T ds^T.  Both halves of the tile run
+// side by side, so that no product waits for the one before it.
 template <int DB>
 __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnDev a, unsigned items) {
   using G = Geo<DB>;
@@ -640,8 +650,11 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnDev a, unsigned ite
 // heads of the group and tiles of 64 queries, 32 at a time: s = q k^T,
 // dp = do v^T (a lane has one key), then dv^T += do^T p, dk^T += q^T ds.
 // The accumulators (2 x 32 keys x dim) and k take 160 of the 256 registers at
-// 128 dims; with v there too they would spill.  256 keys share a tile, since
-// a CU takes in only some 25 bytes per cycle on the way into LDS.
+// 128 dims; with v there too 64 registers spilled (427 us where this takes
+// 204), and 64 keys per wave in 512 registers, one wave per SIMD, took 295: the
+// compiler then puts every product's result into accumulation registers and
+// moves the scores back and forth.  256 keys share a tile, since a CU takes in
+// only some 25 bytes per cycle on the way into LDS.
 //
 // The (head, query tile) pairs of a key block may be divided over several
 // workgroups (a.parts), whose fp32 sums a second kernel adds.

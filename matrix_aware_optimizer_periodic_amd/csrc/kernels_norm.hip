@@ -24,6 +24,11 @@
 // A workgroup keeps the three sums of its share of one sample's rows in
 // registers and writes them once; a second kernel adds the shares in order
 // (no atomics).
+//
+// Measured on one MI355X, where a large copy moves 5.1 TB/s: forward 16384 x
+// 2048, fp32 stream and bf16 branch, modulated, 79 us (403 MB, 5.1 TB/s);
+// backward 8192 x 5120 with every gradient 157 us for the rows (756 MB, 4.8
+// TB/s) and 7 + 5 us for the sums; seven rows of 1001 columns 5.5 us.
 #include <type_traits>
 
 #include "block_device.h"
