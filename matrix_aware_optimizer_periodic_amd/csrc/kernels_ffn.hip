@@ -595,38 +595,46 @@ ProdArgs backward_sizes(int64_t t, int64_t d, int64_t h) {
 
 // ---- few rows -----------------------------------------------------------------
 // Up to 16 MT rows of x against row operands, bound by reading the weights
-// once: 16 output columns (with GATE of both matrices) per workgroup, whose
+// once: a few output columns (with GATE of both matrices) per workgroup, whose
 // waves divide the sum over k among them; weights and x go from memory to
-// registers as MFMA fragments, 16 weight rows down and the x rows across.
-// One launch without partial sums in memory: one row of 2048 x 8192 takes 13
-// and 11 us (5.2 and 3.1 TB/s), where 128-tiles divided along k took 15 + 5 and
-// 10 + 6 us with their joins.
+// registers as MFMA fragments, weight rows down and the x rows across.
+//
+// With up to 8 rows (MT = 0) a fragment has 8 weight rows at 64 consecutive k:
+// rows 8 .. 15 are the same weights 32 k further on, and columns 8 .. 15 the
+// same x there, so that the two diagonal quarters of the result are the two
+// halves of the sum (the others are not used).  Twice the workgroups then
+// read, and whole 128-byte lines: one row of 2048 x 8192 takes 16.6 and 7.8 us
+// (4.0 and 4.3 TB/s, weights from memory) where 16 columns and 32 k take 17.3
+// and 12.0, and 5120 x 20480 takes 71 and 40 (5.9 and 5.2) for 85 and 58.
 template <int MT, bool GATE, int ACT, int NW>
 __global__ __launch_bounds__(64 * NW, NW / 8) void ffn_few_rows_kernel(Prod p) {
-  constexpr int NB = GATE ? 2 : 1, STEPS = 8 / MT;   // k steps of 32 whose loads go out together
-  __shared__ f32x4_t red[NW][NB][MT][64];
-  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  constexpr bool PAIR = MT == 0;
+  constexpr int NB = GATE ? 2 : 1, T = PAIR ? 1 : MT, COLS = PAIR ? 8 : 16;
+  constexpr int STEPS = 8 / T, STEPK = PAIR ? 64 : 32;      // k steps whose loads go out together
+  __shared__ f32x4_t red[NW][NB][T][64];
+  const int lane = threadIdx.x & 63, q = lane >> 4;
+  const int r = PAIR ? lane & 7 : lane & 15, k0 = 8 * q + (PAIR ? 4 * (lane & 8) : 0);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t n0 = int64_t(xcd_item(blockIdx.x, gridDim.x)) * 16;
+  const int64_t n0 = int64_t(xcd_item(blockIdx.x, gridDim.x)) * COLS;
   // Rows past the end repeat the last one: their results are not stored.
   const int64_t wrow = min(n0 + r, int64_t(p.n) - 1);
   const uint16_t* w[2] = {static_cast<const uint16_t*>(p.b) + wrow * p.ldb,
                           static_cast<const uint16_t*>(p.b2) + (GATE ? wrow * p.ldb2 : 0)};
-  const uint16_t* x[MT];
+  const uint16_t* x[T];
 #pragma unroll
-  for (int t = 0; t < MT; ++t) x[t] = static_cast<const uint16_t*>(p.a) + min(16 * t + r, p.m - 1) * p.lda;
-  f32x4_t acc[NB][MT];
+  for (int t = 0; t < T; ++t) x[t] = static_cast<const uint16_t*>(p.a) + min(16 * t + r, p.m - 1) * p.lda;
+  f32x4_t acc[NB][T];
 #pragma unroll
   for (int i = 0; i < NB; ++i)
 #pragma unroll
-    for (int t = 0; t < MT; ++t) acc[i][t] = (f32x4_t)(0.f);
+    for (int t = 0; t < T; ++t) acc[i][t] = (f32x4_t)(0.f);
   // The waves take turns along k, STEPS steps each.
-  const int steps = (p.k + 31) / 32;
+  const int steps = (p.k + STEPK - 1) / STEPK;
   for (int s0 = wave * STEPS; s0 < steps; s0 += NW * STEPS) {
-    u32x4_t fw[STEPS][NB], fx[STEPS][MT];
+    u32x4_t fw[STEPS][NB], fx[STEPS][T];
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
-      const int k = (s0 + s) * 32 + 8 * q;
+      const int k = (s0 + s) * STEPK + k0;
       const bool ok = k < p.k;              // k is a multiple of 8: whole groups
 #pragma unroll
       for (int i = 0; i < NB; ++i) {
@@ -634,7 +642,7 @@ __global__ __launch_bounds__(64 * NW, NW / 8) void ffn_few_rows_kernel(Prod p) {
         if (ok) fw[s][i] = *as_global(reinterpret_cast<const u32x4_t*>(w[i] + k));
       }
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
+      for (int t = 0; t < T; ++t) {
         fx[s][t] = u32x4_t{0, 0, 0, 0};
         if (ok) fx[s][t] = *as_global(reinterpret_cast<const u32x4_t*>(x[t] + k));
       }
@@ -644,21 +652,24 @@ __global__ __launch_bounds__(64 * NW, NW / 8) void ffn_few_rows_kernel(Prod p) {
 #pragma unroll
       for (int i = 0; i < NB; ++i)
 #pragma unroll
-        for (int t = 0; t < MT; ++t) acc[i][t] = mfma16(fw[s][i], fx[s][t], acc[i][t]);
+        for (int t = 0; t < T; ++t) acc[i][t] = mfma16(fw[s][i], fx[s][t], acc[i][t]);
   }
 #pragma unroll
   for (int i = 0; i < NB; ++i)
 #pragma unroll
-    for (int t = 0; t < MT; ++t) red[wave][i][t][lane] = acc[i][t];
+    for (int t = 0; t < T; ++t) red[wave][i][t][lane] = acc[i][t];
   __syncthreads();
   // Wave t finishes rows 16 t ..: a lane has columns n0 + 4 q .. + 3 of one.
-  if (wave >= MT) return;
+  if (wave >= T || (PAIR && (q > 1 || (lane & 8)))) return;
   f32x4_t sum[NB];
 #pragma unroll
   for (int i = 0; i < NB; ++i) {
-    sum[i] = red[0][i][wave][lane];
+    sum[i] = (f32x4_t)(0.f);
 #pragma unroll
-    for (int v = 1; v < NW; ++v) sum[i] += red[v][i][wave][lane];
+    for (int v = 0; v < NW; ++v) {
+      sum[i] += red[v][i][wave][lane];
+      if constexpr (PAIR) sum[i] += red[v][i][wave][lane + 40];    // column + 8, rows + 8
+    }
   }
   const int64_t m = 16 * wave + r, n = n0 + 4 * q;
   if (m >= p.m || n >= p.n) return;         // p.n is a multiple of 8
@@ -685,19 +696,24 @@ __global__ __launch_bounds__(64 * NW, NW / 8) void ffn_few_rows_kernel(Prod p) {
 }
 
 // Every workgroup reads all of x, from L2 at about 7 TB/s; the tiled kernels
-// take 8 us and an eighth of the weights' time longer than reading them.  (At
-// 2048 x 8192: 24 us against 37 for one row, 31 against 37 for 16, 42 against
-// 39 for 32; at 5120 x 20480 143 against 165 for one, 204 against 172 for 16.)
+// take 8 us and an eighth of the weights' time longer than reading them.  The
+// whole call in us, here against tiles, with weights from memory: 2048 x 8192
+// 27 against 42 for one row, 31 against 42 for 8, 40 against 43 for 16, 50
+// against 47 for 32; 5120 x 20480 121 against 173 for one, 150 against 176 for
+// 8, 186 against 177 for 9; 8192 x 28672 286 against 288 for 8, 305 against
+// 287 for 9.
 bool few_rows(int64_t t, int64_t d, int64_t h) {
   const double dh = double(d) * h, again_us = t * dh * (4.0 / 16) / 7e6, weights_us = 6 * dh / 5.1e6;
-  return t <= 64 && again_us <= 8 + weights_us / 8;
+  return t <= 8 || (t <= 64 && again_us <= 8 + weights_us / 8);
 }
 
 template <bool GATE, int ACT>
 hipError_t run_few_rows(hipStream_t s, const Prod& p) {
-  const unsigned grid = unsigned((p.n + 15) / 16);
-  const bool wide = grid < 256;       // fewer workgroups than CUs: more waves to each
-  auto* k = p.m <= 16   ? (wide ? ffn_few_rows_kernel<1, GATE, ACT, 16> : ffn_few_rows_kernel<1, GATE, ACT, 8>)
+  const int cols = p.m <= 8 ? 8 : 16;
+  const unsigned grid = unsigned((p.n + cols - 1) / cols);
+  const bool wide = grid <= 256;      // a workgroup per CU at most: more waves to each
+  auto* k = p.m <= 8    ? (wide ? ffn_few_rows_kernel<0, GATE, ACT, 16> : ffn_few_rows_kernel<0, GATE, ACT, 8>)
+            : p.m <= 16 ? (wide ? ffn_few_rows_kernel<1, GATE, ACT, 16> : ffn_few_rows_kernel<1, GATE, ACT, 8>)
             : p.m <= 32 ? (wide ? ffn_few_rows_kernel<2, GATE, ACT, 16> : ffn_few_rows_kernel<2, GATE, ACT, 8>)
                         : (wide ? ffn_few_rows_kernel<4, GATE, ACT, 16> : ffn_few_rows_kernel<4, GATE, ACT, 8>);
   hipLaunchKernelGGL(k, dim3(grid), dim3(wide ? 1024 : 512), 0, s, p);

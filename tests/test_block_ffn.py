@@ -181,3 +181,17 @@ def test_another_stream():
     torch.cuda.current_stream().wait_stream(s)
     assert torch.equal(y, y2)
     assert all(torch.equal(p, q) for p, q in zip(d2, b.ffn_bwd(dy, x, wg, wu, wd, gu)))
+
+
+@pytest.mark.parametrize("t,d,f", [(200, 4096, 128), (70, 2048, 64), (4096, 2048, 4096)])
+def test_few_tiles_and_long_sums(t, d, f):
+    """Sums over k divided over several workgroups, in every kind of product."""
+    check(*make(t, d, f, seed=d + t), kind="gelu")
+
+
+@pytest.mark.parametrize("t", [1, 8, 9, 33])
+@pytest.mark.parametrize("d,f", [(4072, 136), (4104, 72), (136, 4072), (72, 4104), (5128, 20488)])
+def test_few_rows_and_many_columns(t, d, f):
+    """Each form of the few-row products on both sides of the limits of its
+    rows and columns, where the last group of columns is cut."""
+    check(*make(t, d, f, seed=d + t), grads=False)
