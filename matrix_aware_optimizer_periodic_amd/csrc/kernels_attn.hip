@@ -280,9 +280,12 @@ __device__ __forceinline__ int seen_most(const AttnDev& a, const Rows& r) {
 // once.  Two workgroups of four waves and 128 rows per CU: eight waves and 256
 // rows, which bring in half as much, measured 5% slower (the waves meet at
 // every tile), and what a longer way between asking for a tile and using it, or
-// several row blocks per workgroup, could hide measured nothing.
+// several row blocks per workgroup, could hide measured nothing.  Up to 64 dims
+// three workgroups fit (168 registers, one of them spilled): 98 us against 107
+// for 16 samples of 1024 queries and keys with 16 heads of 64, 591 against 619
+// for 2 of 8192.  The dq kernel gains 1% at most from that, with four spilled.
 template <int DB, bool SPLIT>
-__global__ __launch_bounds__(256, 2) void attn_fwd_kernel(AttnDev a, unsigned items) {
+__global__ __launch_bounds__(256, DB <= 2 ? 3 : 2) void attn_fwd_kernel(AttnDev a, unsigned items) {
   using G = Geo<DB>;
   constexpr int KS = G::KS, AHEAD = 3;
   __shared__ __attribute__((aligned(1024))) unsigned char smem[4 * G::TILEB];   // two of k, two of v
@@ -893,7 +896,7 @@ unsigned key_blocks(const AttnDev& a) { return unsigned((a.k_len + 255) / 256); 
 #define COMMA ,
 
 int attn_splits(const AttnDev& a, int* split_keys) {
-  // Two workgroups fit on each of 256 CUs.  With fewer than half of that,
+  // At least two workgroups fit on each of 256 CUs.  With fewer than half of that,
   // the keys are divided, in ranges of at least four tiles.
   const int64_t items = int64_t(row_blocks(a)) * a.batch * a.kv_heads;
   const int tiles = (a.k_len + kTile - 1) / kTile;
