@@ -47,6 +47,7 @@ __device__ __forceinline__ void dma4(u32x4_t rsrc, unsigned lds_addr, unsigned v
 #pragma clang diagnostic pop
 template <int N>
 __device__ __forceinline__ void wait_vm() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 // A bare barrier: __syncthreads() would also wait for the DMA in flight.
 __device__ __forceinline__ void barrier() {
   asm volatile("" ::: "memory");

@@ -8,9 +8,10 @@
 // C[m][n] = sum_k A(m, k) B(n, k); an operand lies in memory either along k
 // ("rows": x, h, dy, dg | du, and the weights of the forward pass) or along
 // m / n ("cols": the weights in dh and dx, both operands of the weights'
-// gradients).  Row operands are staged as rows of 32 k values and read as
-// they are, column operands as 32 rows of the tile's width and read through
-// the transposing LDS read, so that nothing is transposed in memory.
+// gradients).  Row operands are staged as rows of 32 k values (64 where both
+// are rows) and read as they are, column operands as 32 rows of the tile's
+// width and read through the transposing LDS read, so that nothing is
+// transposed in memory.
 //
 // Fusions: one product forms g and u side by side (the B tile takes 16 rows
 // of Wg and 16 of Wu in turn, so a lane holds both for the same columns) and
@@ -22,9 +23,10 @@
 // next product's operands, and the results.
 //
 // Measured on one MI355X (a large library product runs at 1460 TFLOP/s): 4096
-// rows, 2048 x 8192, gate and up 272 us (1010 TFLOP/s), down 128 + 14 us; 4096
-// rows, 5120 x 20480, dh 869 us (988; 160 us of it would take its epilogue's
-// 0.84 GB alone), dx and the weights' gradients 3470 us (1238).  Matrix cores
+// rows, 2048 x 8192, gate and up 252 - 268 us (1030 - 1090 TFLOP/s), down
+// 113 - 121 + 14 us; 4096 rows, 5120 x 20480, dh 869 us (988; 160 us of it
+// would take its epilogue's 0.84 GB alone), dx and the weights' gradients
+// 3470 us (1238).  Matrix cores
 // busy 44 - 60% of the cycles at 1.9 - 2.1 GHz.
 #include <algorithm>
 #include <type_traits>
@@ -99,19 +101,16 @@ struct Side {
   unsigned limit;            // rows: bytes of the rows that are there
   int chunk;
 
-  // first: first row (column) of the tile; there: how many there are;
-  // alternate: every other block of 16 LDS rows is another matrix's (waves 0
-  // and 2 bring one, 1 and 3 the other).
-  __device__ __forceinline__ void init(const void* p, int64_t ld, int64_t first, int there, int wave, int lane,
-                                       bool alternate) {
+  // first: first row (column) of the tile; there: how many there are.
+  __device__ __forceinline__ void init(const void* p, int64_t ld, int64_t first, int there, int wave, int lane) {
     ldbytes = ld * 2;
     if constexpr (!COLS) {
       base = static_cast<const char*>(p) + first * ldbytes;
-      const int row = (alternate ? 16 * (wave >> 1) : 16 * wave) + (lane >> 2);   // + i * step rows
+      const int row = 16 * wave + (lane >> 2);                                    // + i * step rows
       chunk = (lane & 3) ^ ((lane >> 3) & 3);                                     // swizzle (row / 2) % 4
       v0 = unsigned(row * ldbytes + chunk * 16);
-      step = unsigned((alternate ? 32 : 64) * ldbytes);
-      limit = unsigned(min(there, alternate ? BT / 2 : BT) * ldbytes);
+      step = unsigned(64 * ldbytes);
+      limit = unsigned(min(there, BT) * ldbytes);
       kbytes = kStageK * 2;
       v1 = 0;
     } else {
@@ -294,11 +293,13 @@ __device__ __forceinline__ void emit_rows(const Prod& p, const f32x4_t (*acc)[BT
   __builtin_amdgcn_wave_barrier();
 }
 
-// Stages in the LDS ring: 128 KB, or 80 KB for two workgroups per CU.
-template <int BT>
-constexpr int ring_stages() { return BT == 256 ? 4 : 5; }
+// Bytes of the LDS ring.  256-tiles: 128 KB, one workgroup per CU (160 KB
+// with units); 128-tiles: 80 KB, two.
+template <int BT, int LIE>
+constexpr int ring_bytes() { return (BT == 128 || LIE == ROWS_ROWS ? 5 : 4) * 2 * BT * kStageK * 2; }
 
-// One BT x BT tile per workgroup of four waves, each (BT / 2) x (BT / 2).
+// The sums of one BT x BT tile, four waves of (BT / 2) x (BT / 2) each, over
+// `stages` stages from stage `first` on, where B at least lies along n.
 // Software pipeline over a ring of stages (with two stages of 64 k instead,
 // twice as wide, everything took twice as long: a stage then has one stage's
 // time to arrive): the fragments of one stage are in
@@ -307,37 +308,28 @@ constexpr int ring_stages() { return BT == 256 ? 4 : 5; }
 // NSTAGE - 1 ahead goes out between MFMAs.  The barrier, behind the first two
 // MFMAs of a stage, makes the next stage visible and says that the previous
 // one's buffer is free (its fragments are in registers everywhere).
-template <int BT, bool ACOLS, bool BCOLS, int EPI, int ACT>
-__device__ __forceinline__ void run_tile(const Prod& p, Tile tile, int range, float* part, unsigned char* smem, int lane,
-                                         int wave) {
+template <int BT, bool ACOLS, bool BCOLS>
+__device__ __forceinline__ void sum_cols(f32x4_t (&acc)[BT / 32][BT / 32], const Prod& p, int64_t m0, int64_t n0, int first,
+                                         int stages, unsigned char* smem, int lane, int wave) {
   constexpr int F = BT / 32;                       // fragments per wave and side
-  constexpr int STAGE = 2 * BT * kStageK * 2, NSTAGE = ring_stages<BT>();
-  const int wm = wave >> 1, wn = wave & 1;
-  constexpr int NSTEP = tile_cols<BT, EPI>();
-  const int64_t m0 = int64_t(tile.tm) * BT, n0 = int64_t(tile.tn) * NSTEP;
-
+  constexpr int STAGE = 2 * BT * kStageK * 2, NSTAGE = ring_bytes<BT, ROWS_COLS>() / STAGE;
   Side<BT, ACOLS> sa;
   Side<BT, BCOLS> sb;
-  sa.init(p.a, p.lda, m0, int(min(int64_t(BT), p.m - m0)), wave, lane, false);
-  // EPI_GATE: waves 0 and 2 bring rows of Wg, 1 and 3 those of Wu, which land
-  // 16 rows of each in turn.
-  sb.init(EPI == EPI_GATE && (wave & 1) ? p.b2 : p.b, EPI == EPI_GATE && (wave & 1) ? p.ldb2 : p.ldb, n0,
-          int(min(int64_t(NSTEP), p.n - n0)), wave, lane, EPI == EPI_GATE);
-  const char* b2 = static_cast<const char*>(p.b2) + (BCOLS ? n0 * 2 : n0 * p.ldb2 * 2);
+  sa.init(p.a, p.lda, m0, int(min(int64_t(BT), p.m - m0)), wave, lane);
+  sb.init(p.b, p.ldb, n0, int(min(int64_t(BT), p.n - n0)), wave, lane);
+  const char* b2 = static_cast<const char*>(p.b2) + n0 * 2;
   Frag<BT, ACOLS> fa;
   Frag<BT, BCOLS> fb;
-  fa.init(wm, lane);
-  fb.init(wn, lane);
+  fa.init(wave >> 1, lane);
+  fb.init(wave & 1, lane);
 
-  const int per = (p.k + kStageK - 1) / kStageK, all = per * p.segments;
-  const int first = range < 0 ? 0 : range % p.splits * p.split_stages;
-  const int stages = range < 0 ? all : max(0, min(all - first, p.split_stages));
+  const int per = (p.k + kStageK - 1) / kStageK;
   const unsigned lds = lds_offset(smem);
   // Stages past the end are issued as a reload of the last one, so that every
   // stage waits for the same number of DMAs; nothing reads them.
   auto issue_one = [&](int s, int i) {
     const int sc = first + min(s, stages - 1);
-    const int seg = EPI == EPI_PLAIN && BCOLS && !ACOLS && sc >= per ? 1 : 0;
+    const int seg = !ACOLS && sc >= per ? 1 : 0;
     const int ks = sc - seg * per, left = p.k - ks * kStageK;
     const unsigned at = lds + unsigned(s % NSTAGE) * STAGE;
     if (i < sa.DMA) {
@@ -347,12 +339,6 @@ __device__ __forceinline__ void run_tile(const Prod& p, Tile tile, int range, fl
     }
   };
   constexpr int DMA = Side<BT, ACOLS>::DMA + Side<BT, BCOLS>::DMA;
-
-  f32x4_t acc[F][F];
-#pragma unroll
-  for (int x = 0; x < F; ++x)
-#pragma unroll
-    for (int y = 0; y < F; ++y) acc[x][y] = (f32x4_t)(0.f);
   u32x4_t a[F], b[F];
 
   for (int s = 0; s < NSTAGE - 1; ++s)
@@ -392,6 +378,120 @@ __device__ __forceinline__ void run_tile(const Prod& p, Tile tile, int range, fl
     }
     static_assert(DMA <= (NXY - PRE) / 2, "a slot for every DMA");
   }
+}
+
+// The same where both operands are rows.  A stage's 64 bytes of a row are half
+// a line, and the caches take as long for that as for a whole one.  So 64 k
+// (a unit, of two stages) of A come in one stage and of B in the next, through
+// a ring of five units: A and B of the stages worked on and of the next two, and
+// the one under way.  Stage s asks for unit s + 4; units s + 1 and s + 2 are
+// wanted when an odd stage begins to read ahead.
+//
+// A unit is last read in the stage before its last one, so an odd stage waits
+// for its own reads before the barrier, which then says that the two units of
+// its pair are free: A's is refilled at once, B's in the next stage, which has
+// no barrier.  The reads are behind the first PRE MFMAs by then (6, 12, 18 and
+// 26 of 64 before them: 384, 385, 378 and 383 us for the call below).
+//
+// 4096 rows, 2048 x 8192, the whole forward call: 382 us where both operands
+// came as half lines, 32 KB a stage all the same, in 407.
+template <int BT, int EPI>
+__device__ __forceinline__ void sum_rows(f32x4_t (&acc)[BT / 32][BT / 32], const Prod& p, int64_t m0, int64_t n0, int first,
+                                         int stages, unsigned char* smem, int lane, int wave) {
+  constexpr bool GATE = EPI == EPI_GATE;
+  constexpr int F = BT / 32, UNIT = BT * 128, UNITS = 5, DMA = UNIT / 1024 / 4;
+  // A DMA brings 8 rows.  16-byte chunk c of row r is at chunk c ^ (r / 2) % 8.
+  const int row = 8 * wave + (lane >> 3), chunk = (lane & 7) ^ ((row >> 1) & 7);
+  // EPI_GATE: 16 rows of Wg and 16 of Wu in turn, by waves 0 and 1 and by 2 and 3.
+  const bool up = GATE && wave >= 2;
+  const int64_t a_ld = p.lda * 2, b_ld = (up ? p.ldb2 : p.ldb) * 2;
+  const char* const a_base = static_cast<const char*>(p.a) + m0 * a_ld;
+  const char* const b_base = static_cast<const char*>(up ? p.b2 : p.b) + n0 * b_ld;
+  const unsigned a_limit = unsigned(min(int64_t(BT), p.m - m0) * a_ld);
+  const unsigned b_limit = unsigned(min(int64_t(GATE ? BT / 2 : BT), p.n - n0) * b_ld);
+  const unsigned a_step = unsigned(32 * a_ld), b_step = unsigned((GATE ? 16 : 32) * b_ld);
+  const unsigned a_v = unsigned(row * a_ld + chunk * 16);
+  const unsigned b_v = unsigned((GATE ? 8 * (wave & 1) + (lane >> 3) : row) * b_ld + chunk * 16);
+  const unsigned lds = lds_offset(smem);
+  const int last = (stages + 1) / 2 - 1;
+  // Units past the end are issued as a reload of the last pair, as above.
+  auto issue_one = [&](int u, int i) {
+    const bool is_b = u & 1;
+    const int k0 = (first + 2 * min(u >> 1, last)) * kStageK;
+    u32x4_t r = buffer_at((is_b ? b_base : a_base) + int64_t(k0) * 2);
+    r[2] = is_b ? b_limit : a_limit;
+    unsigned v = (is_b ? b_v : a_v) + unsigned(i) * (is_b ? b_step : a_step);
+    if (p.k - k0 < 64 && chunk * 8 >= p.k - k0) v = kBufNone;
+    dma16(r, lds + unsigned(u % UNITS) * UNIT + unsigned(wave + 4 * i) * 1024u, v);
+  };
+  const int r16 = lane & 15;
+  const unsigned in_row = unsigned(((lane >> 4) ^ ((r16 >> 1) & 7)) << 4);
+  const unsigned a_off = unsigned(((wave >> 1) * (BT / 2) + r16) * 128) + in_row;
+  const unsigned b_off = unsigned(((wave & 1) * (BT / 2) + r16) * 128) + in_row;
+  u32x4_t a[F], b[F];
+
+#pragma unroll
+  for (int u = 0; u < UNITS - 1; ++u)
+#pragma unroll
+    for (int i = 0; i < DMA; ++i) issue_one(u, i);
+  wait_vm<2 * DMA>();
+  barrier();
+#pragma unroll
+  for (int f = 0; f < F; ++f) a[f] = lds_read16(smem, a_off + unsigned(f * 2048));
+#pragma unroll
+  for (int f = 0; f < F; ++f) b[f] = lds_read16(smem + UNIT, b_off + unsigned(f * 2048));
+
+  constexpr int NXY = F * F, HB = F / 2, PRE = F == 8 ? 18 : 6;
+  for (int s = 0; s < stages; ++s) {
+    auto mma = [&](int i) {
+      const int x = (i % (F * HB)) / HB, y = (i / (F * HB)) * HB + i % HB;
+      acc[x][y] = mfma16(b[y], a[x], acc[x][y]);
+    };
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < PRE; ++i) mma(i);
+    __builtin_amdgcn_sched_barrier(0);
+    if (s & 1) {
+      wait_vm<DMA>();
+      wait_lds();
+      barrier();
+    }
+    const unsigned pair = unsigned(s + 1) & ~1u, half = unsigned(s + 1) & 1u;
+    const unsigned char* sA = smem + (pair % UNITS) * UNIT;
+    const unsigned char* sB = smem + ((pair + 1) % UNITS) * UNIT;
+    const unsigned ao = a_off ^ (half * 64), bo = b_off ^ (half * 64);
+    int nd = 0;
+#pragma unroll
+    for (int i = PRE; i < NXY; ++i) {
+      mma(i);
+      const int x = (i % (F * HB)) / HB, y = (i / (F * HB)) * HB + i % HB;
+      if (nd < DMA && i % 2 == 0) issue_one(s + UNITS - 1, nd++);
+      if (x == F - 1) b[y] = lds_read16(sB, bo + unsigned(y * 2048));
+      if (y == F - 1) a[x] = lds_read16(sA, ao + unsigned(x * 2048));
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    static_assert(PRE <= F * HB - HB && DMA <= (NXY - PRE) / 2, "no read before the barrier, a slot for every DMA");
+  }
+}
+
+// One BT x BT tile per workgroup of four waves.
+template <int BT, bool ACOLS, bool BCOLS, int EPI, int ACT>
+__device__ __forceinline__ void run_tile(const Prod& p, Tile tile, int range, float* part, unsigned char* smem, int lane,
+                                         int wave) {
+  constexpr int F = BT / 32, NSTEP = tile_cols<BT, EPI>();
+  constexpr int LIE = !ACOLS && !BCOLS ? ROWS_ROWS : ROWS_COLS;
+  const int wm = wave >> 1, wn = wave & 1;
+  const int64_t m0 = int64_t(tile.tm) * BT, n0 = int64_t(tile.tn) * NSTEP;
+  const int all = (p.k + kStageK - 1) / kStageK * p.segments;
+  const int first = range < 0 ? 0 : range % p.splits * p.split_stages;
+  const int stages = range < 0 ? all : max(0, min(all - first, p.split_stages));
+  f32x4_t acc[F][F];
+#pragma unroll
+  for (int x = 0; x < F; ++x)
+#pragma unroll
+    for (int y = 0; y < F; ++y) acc[x][y] = (f32x4_t)(0.f);
+  if constexpr (LIE == ROWS_ROWS) sum_rows<BT, EPI>(acc, p, m0, n0, first, stages, smem, lane, wave);
+  else sum_cols<BT, ACOLS, BCOLS>(acc, p, m0, n0, first, stages, smem, lane, wave);
   // The reloads of the last stage may still be on their way into LDS.
   wait_vm<0>();
   barrier();
@@ -407,7 +507,7 @@ __device__ __forceinline__ void run_tile(const Prod& p, Tile tile, int range, fl
     return;
   }
   constexpr int XB = 2;
-  static_assert(4 * 16 * XB * (BT / 2 + 4) * 4 <= NSTAGE * STAGE, "epilogue rows fit");
+  static_assert(4 * 16 * XB * (BT / 2 + 4) * 4 <= ring_bytes<BT, LIE>(), "epilogue rows fit");
   float* er = reinterpret_cast<float*>(smem) + wave * 16 * XB * (BT / 2 + 4);
 #pragma unroll
   for (int x = 0; x < F; x += XB)
@@ -417,7 +517,7 @@ __device__ __forceinline__ void run_tile(const Prod& p, Tile tile, int range, fl
 // MIXED_COLS: products of both kinds of A in one launch.
 template <int BT, int LIE, int EPI, int ACT>
 __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void ffn_gemm_kernel(ProdArgs g) {
-  __shared__ __attribute__((aligned(1024))) unsigned char smem[ring_stages<BT>() * 2 * BT * kStageK * 2];
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[ring_bytes<BT, LIE>()];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int id = int(blockIdx.x), which = 0;
@@ -512,7 +612,7 @@ Plan plan_with(const ProdArgs& g, int bt, bool gate) {
   const int rem = g.count > 1 ? tiles : tiles % slots, whole = g.count > 1 ? 0 : tiles / slots;
   const double part_mb = double(bt) * (rows < bt ? (rows + 15) / 16 * 16 : bt) * 4e-6, tile = stages * stage_us + tile_us;
   for (int n = 1; n == 1 || (rem > 0 && n <= stages / 4 && n <= (g.count > 1 ? 32 : slots / rem)); ++n) {
-    const int per = (stages + n - 1) / n, got = (stages + per - 1) / per;
+    const int per = ((stages + n - 1) / n + 1) & ~1, got = (stages + per - 1) / per;   // whole lines of row operands
     const double one = per * stage_us + tile_us, join = got > 1 ? 4 + 2 * rem * got * part_mb / 4.5 : 0;
     double us;
     if (g.count == 1) {
