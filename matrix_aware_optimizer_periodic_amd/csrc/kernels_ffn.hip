@@ -8,10 +8,9 @@
 // C[m][n] = sum_k A(m, k) B(n, k); an operand lies in memory either along k
 // ("rows": x, h, dy, dg | du, and the weights of the forward pass) or along
 // m / n ("cols": the weights in dh and dx, both operands of the weights'
-// gradients).  Row operands are staged as rows of 32 k values (64 where both
-// are rows) and read as they are, column operands as 32 rows of the tile's
-// width and read through the transposing LDS read, so that nothing is
-// transposed in memory.
+// gradients).  Row operands are staged as rows of 64 k values and read as
+// they are, column operands as 64 rows of the tile's width and read through the
+// transposing LDS read, so that nothing is transposed in memory.
 //
 // Fusions: one product forms g and u side by side (the B tile takes 16 rows
 // of Wg and 16 of Wu in turn, so a lane holds both for the same columns) and
@@ -26,8 +25,7 @@
 // rows, 2048 x 8192, gate and up 252 - 268 us (1030 - 1090 TFLOP/s), down
 // 113 - 121 + 14 us; 4096 rows, 5120 x 20480, dh 869 us (988; 160 us of it
 // would take its epilogue's 0.84 GB alone), dx and the weights' gradients
-// 3470 us (1238).  Matrix cores
-// busy 44 - 60% of the cycles at 1.9 - 2.1 GHz.
+// 3470 us (1238).  Matrix cores busy 44 - 60% of the cycles at 1.9 - 2.1 GHz.
 #include <algorithm>
 #include <type_traits>
 
@@ -36,7 +34,7 @@
 namespace muon {
 namespace {
 
-constexpr int kStageK = 32;   // k values per LDS stage: one MFMA deep
+constexpr int kStageK = 32;   // k values per stage: one MFMA deep
 
 // ---- activation -------------------------------------------------------------
 // SiLU g / (1 + e^-g); GELU in its tanh form, 0.5 g (1 + tanh z) = g / (1 + e^-2z)
@@ -84,73 +82,70 @@ struct ProdArgs {
   float* part;
 };
 
+// Stages of a tile's whole sum; a first segment's last unit is a whole one.
+__host__ __device__ inline int stages_of(const Prod& p) {
+  return (p.segments - 1) * ((p.k + 63) / 64) * 2 + (p.k + kStageK - 1) / kStageK;
+}
+
 enum { EPI_PLAIN = 0, EPI_GATE = 1, EPI_DGATE = 2 };
 enum { ROWS_ROWS = 0, ROWS_COLS = 1, MIXED_COLS = 2 };   // how A and B lie
 
-// One operand's side of a stage: 32 k of BT rows (64 bytes each in LDS), or
-// COLS, BT columns of 32 rows of k (2 BT bytes each).
-template <int BT, bool COLS>
-struct Side {
-  static constexpr int BYTES = BT * kStageK * 2;
-  static constexpr int DMA = BYTES / 1024 / 4;               // per wave and stage
-  static constexpr int CH = BT / 8;                          // COLS: 16-byte chunks per row
-  unsigned v0, v1, step;
-  const char* base;
-  int64_t kbytes;            // bytes per stage along k
-  int64_t ldbytes;
-  unsigned limit;            // rows: bytes of the rows that are there
-  int chunk;
+// One operand's units: 64 k of BT rows (128 bytes each in LDS), or COLS, BT
+// columns of 64 rows of k (2 BT bytes each).  Both are BT / 32 DMAs per wave, of
+// 1 KB each, whose lanes' offsets differ by a step (COLS with BT = 256: from
+// one of two starts in turn).
+constexpr int kUnitK = 2 * kStageK;
+template <int BT> constexpr int unit_bytes() { return BT * kUnitK * 2; }
 
-  // first: first row (column) of the tile; there: how many there are.
-  __device__ __forceinline__ void init(const void* p, int64_t ld, int64_t first, int there, int wave, int lane) {
-    ldbytes = ld * 2;
+struct Side {
+  const char* base;
+  int64_t kbytes;            // bytes per k
+  int64_t kspan;             // bytes per k of what a buffer covers: 0, a row's k are beside each other
+  unsigned limit;            // rows: bytes of the rows that are there
+  unsigned v0, v1, step;
+  int chunk;                 // rows: the lane's chunk of 8 k; COLS: 0
+
+  // first: first row (column) of the tile; there: how many there are;
+  // turns: every other block of 16 LDS rows is another matrix's (waves 0 and 1
+  // bring one, 2 and 3 the other).
+  template <int BT, bool COLS>
+  __device__ __forceinline__ void init(const void* p, int64_t ld, int64_t first, int there, int wave, int lane,
+                                       bool turns) {
+    const int64_t ldbytes = ld * 2;
     if constexpr (!COLS) {
       base = static_cast<const char*>(p) + first * ldbytes;
-      const int row = 16 * wave + (lane >> 2);                                    // + i * step rows
-      chunk = (lane & 3) ^ ((lane >> 3) & 3);                                     // swizzle (row / 2) % 4
-      v0 = unsigned(row * ldbytes + chunk * 16);
-      step = unsigned(64 * ldbytes);
-      limit = unsigned(min(there, BT) * ldbytes);
-      kbytes = kStageK * 2;
-      v1 = 0;
+      const int lds_row = 8 * wave + (lane >> 3);                   // + 32 per DMA
+      const int row = turns ? 8 * (wave & 1) + (lane >> 3) : lds_row;
+      chunk = (lane & 7) ^ ((lds_row >> 1) & 7);
+      v0 = v1 = unsigned(row * ldbytes + chunk * 16);
+      step = unsigned((turns ? 16 : 32) * ldbytes);
+      limit = unsigned(min(there, turns ? BT / 2 : BT) * ldbytes);
+      kbytes = 2;
+      kspan = 0;
     } else {
       base = static_cast<const char*>(p) + first * 2;
-      constexpr int RPB = 64 / CH;                       // rows per 1 KB block
-      const int row = RPB * wave + lane / CH;
+      constexpr int CH = BT / 8, RPB = 64 / CH;                     // chunks per row, rows per DMA
+      const int row = RPB * wave + lane / CH;                       // + 4 RPB per DMA
       const int sw = ((row & 3) << 2) ^ (RPB * 4 == 8 ? 0 : ((row >> 3) & 1) << 1);
       const int c0 = (lane % CH) ^ sw, c1 = c0 ^ 2;
       v0 = c0 * 8 < there ? unsigned(row * ldbytes + c0 * 16) : kBufNone;
       v1 = RPB * 4 == 8 ? (c1 * 8 < there ? unsigned(row * ldbytes + c1 * 16) : kBufNone) : v0;
       step = unsigned(4 * RPB * ldbytes);
-      kbytes = kStageK * ldbytes;
+      kbytes = kspan = ldbytes;
       limit = 0;
       chunk = 0;
     }
   }
-  // DMA i of a stage that starts at `at` and has `left` k to go.
-  __device__ __forceinline__ void issue(int i, const char* at, int left, unsigned lds, int wave) const {
-    u32x4_t r = buffer_at(at);
-    unsigned v;
-    if constexpr (!COLS) {
-      r[2] = limit;
-      v = v0 + unsigned(i) * step;
-      if (left < kStageK && chunk * 8 >= left) v = kBufNone;
-    } else {
-      r[2] = unsigned(min(int64_t(min(left, kStageK)) * ldbytes, int64_t(kBufNone)));
-      v = ((i & 1) ? v1 : v0) + unsigned(i) * step;
-    }
-    dma16(r, lds + unsigned(wave + 4 * i) * 1024u, v);
-  }
 };
 
-// Fragment reads (16 rows or columns, 32 k) of one operand.
+// Fragment reads (16 rows or columns, 32 k: a half of a unit) of one operand.
 template <int BT, bool COLS>
 struct Frag {
   unsigned off[COLS ? BT / 32 : 1];
   __device__ __forceinline__ void init(int wpos, int lane) {
     const int r = lane & 15, q = lane >> 4;
     if constexpr (!COLS) {
-      off[0] = unsigned((wpos * (BT / 2) + r) * 64 + ((q ^ ((r >> 1) & 3)) << 4));
+      off[0] = unsigned((wpos * (BT / 2) + r) * 128 + ((q ^ ((r >> 1) & 7)) << 4));
     } else {
       const int row = 8 * q + (r >> 2);
       const int sw = ((row & 3) << 2) ^ (((row >> 3) & 1) << 1);
@@ -161,10 +156,12 @@ struct Frag {
       }
     }
   }
-  __device__ __forceinline__ void read(u32x4_t& o, const unsigned char* s, int f) const {
+  // The second half of a row's chunks has bit 2 of the chunk's number flipped.
+  __device__ __forceinline__ void read(u32x4_t& o, const unsigned char* s, unsigned half, int f) const {
     if constexpr (!COLS) {
-      o = lds_read16(s, off[0] + unsigned(f * 1024));
+      o = lds_read16(s, (off[0] ^ (half * 64u)) + unsigned(f * 2048));
     } else {
+      s += half * unsigned(kStageK * 2 * BT);
       const u32x2_t x = lds_read_tr(s, off[f]);
       const u32x2_t y = lds_read_tr(s, off[f] + unsigned(4 * 2 * BT));
       o = u32x4_t{x[0], x[1], y[0], y[1]};
@@ -293,99 +290,23 @@ __device__ __forceinline__ void emit_rows(const Prod& p, const f32x4_t (*acc)[BT
   __builtin_amdgcn_wave_barrier();
 }
 
-// Bytes of the LDS ring.  256-tiles: 128 KB, one workgroup per CU (160 KB
-// with units); 128-tiles: 80 KB, two.
-template <int BT, int LIE>
-constexpr int ring_bytes() { return (BT == 128 || LIE == ROWS_ROWS ? 5 : 4) * 2 * BT * kStageK * 2; }
+// Units in the LDS ring: all 160 KB with 256-tiles, 80 KB with 128-tiles, of
+// which two workgroups run per CU.
+constexpr int kUnits = 5;
 
 // The sums of one BT x BT tile, four waves of (BT / 2) x (BT / 2) each, over
-// `stages` stages from stage `first` on, where B at least lies along n.
-// Software pipeline over a ring of stages (with two stages of 64 k instead,
-// twice as wide, everything took twice as long: a stage then has one stage's
-// time to arrive): the fragments of one stage are in
-// registers while its MFMAs run; each fragment is refilled with the next
-// stage's once its last MFMA has been issued, and the DMA of the stage
-// NSTAGE - 1 ahead goes out between MFMAs.  The barrier, behind the first two
-// MFMAs of a stage, makes the next stage visible and says that the previous
-// one's buffer is free (its fragments are in registers everywhere).
-template <int BT, bool ACOLS, bool BCOLS>
-__device__ __forceinline__ void sum_cols(f32x4_t (&acc)[BT / 32][BT / 32], const Prod& p, int64_t m0, int64_t n0, int first,
-                                         int stages, unsigned char* smem, int lane, int wave) {
-  constexpr int F = BT / 32;                       // fragments per wave and side
-  constexpr int STAGE = 2 * BT * kStageK * 2, NSTAGE = ring_bytes<BT, ROWS_COLS>() / STAGE;
-  Side<BT, ACOLS> sa;
-  Side<BT, BCOLS> sb;
-  sa.init(p.a, p.lda, m0, int(min(int64_t(BT), p.m - m0)), wave, lane);
-  sb.init(p.b, p.ldb, n0, int(min(int64_t(BT), p.n - n0)), wave, lane);
-  const char* b2 = static_cast<const char*>(p.b2) + n0 * 2;
-  Frag<BT, ACOLS> fa;
-  Frag<BT, BCOLS> fb;
-  fa.init(wave >> 1, lane);
-  fb.init(wave & 1, lane);
-
-  const int per = (p.k + kStageK - 1) / kStageK;
-  const unsigned lds = lds_offset(smem);
-  // Stages past the end are issued as a reload of the last one, so that every
-  // stage waits for the same number of DMAs; nothing reads them.
-  auto issue_one = [&](int s, int i) {
-    const int sc = first + min(s, stages - 1);
-    const int seg = !ACOLS && sc >= per ? 1 : 0;
-    const int ks = sc - seg * per, left = p.k - ks * kStageK;
-    const unsigned at = lds + unsigned(s % NSTAGE) * STAGE;
-    if (i < sa.DMA) {
-      sa.issue(i, sa.base + ks * sa.kbytes + (ACOLS ? 0 : int64_t(seg) * p.k * 2), left, at, wave);
-    } else {
-      sb.issue(i - sa.DMA, (seg ? b2 : sb.base) + ks * sb.kbytes, left, at + Side<BT, ACOLS>::BYTES, wave);
-    }
-  };
-  constexpr int DMA = Side<BT, ACOLS>::DMA + Side<BT, BCOLS>::DMA;
-  u32x4_t a[F], b[F];
-
-  for (int s = 0; s < NSTAGE - 1; ++s)
-#pragma unroll
-    for (int i = 0; i < DMA; ++i) issue_one(s, i);
-  wait_vm<(NSTAGE - 2) * DMA>();
-  barrier();
-#pragma unroll
-  for (int f = 0; f < F; ++f) fa.read(a[f], smem, f);
-#pragma unroll
-  for (int f = 0; f < F; ++f) fb.read(b[f], smem + Side<BT, ACOLS>::BYTES, f);
-
-  constexpr int NXY = F * F, HB = F / 2, PRE = 2;
-  for (int s = 0; s < stages; ++s) {
-    auto mma = [&](int i) {
-      const int x = (i % (F * HB)) / HB, y = (i / (F * HB)) * HB + i % HB;
-      // operands swapped: a lane then holds four consecutive n of one m
-      acc[x][y] = mfma16(b[y], a[x], acc[x][y]);
-    };
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int i = 0; i < PRE; ++i) mma(i);
-    __builtin_amdgcn_sched_barrier(0);
-    wait_vm<(NSTAGE - 3) * DMA>();
-    barrier();
-    const unsigned char* sA = smem + ((s + 1) % NSTAGE) * STAGE;
-    const unsigned char* sB = sA + Side<BT, ACOLS>::BYTES;
-    int nd = 0;
-#pragma unroll
-    for (int i = PRE; i < NXY; ++i) {
-      mma(i);
-      const int x = (i % (F * HB)) / HB, y = (i / (F * HB)) * HB + i % HB;
-      if (nd < DMA && i % 2 == 0) issue_one(s + NSTAGE - 1, nd++);
-      if (x == F - 1) fb.read(b[y], sB, y);
-      if (y == F - 1) fa.read(a[x], sA, x);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    static_assert(DMA <= (NXY - PRE) / 2, "a slot for every DMA");
-  }
-}
-
-// The same where both operands are rows.  A stage's 64 bytes of a row are half
-// a line, and the caches take as long for that as for a whole one.  So 64 k
-// (a unit, of two stages) of A come in one stage and of B in the next, through
-// a ring of five units: A and B of the stages worked on and of the next two, and
-// the one under way.  Stage s asks for unit s + 4; units s + 1 and s + 2 are
-// wanted when an odd stage begins to read ahead.
+// `stages` stages of 32 k from stage `first`, an even one, on.
+//
+// Software pipeline: the fragments of one stage are in registers while its
+// MFMAs run; each fragment is refilled with the next stage's once its last
+// MFMA has been issued, and the DMA goes out between MFMAs.  A stage's 64 bytes
+// of a row are half a line, and the caches take as long for that as for a
+// whole one.  So 64 k (a unit, of two stages) of A come in one stage and of B in
+// the next, through a ring of five units: A and B of the stages worked on and of
+// the next two, and the one under way.  Stage s asks for unit s + 4; units
+// s + 1 and s + 2 are wanted when an odd stage begins to read ahead.  (With A
+// and B of 64 k in one stage and two such stages in LDS everything took twice
+// as long: they then have one stage's time to arrive.)
 //
 // A unit is last read in the stage before its last one, so an odd stage waits
 // for its own reads before the barrier, which then says that the two units of
@@ -393,58 +314,93 @@ __device__ __forceinline__ void sum_cols(f32x4_t (&acc)[BT / 32][BT / 32], const
 // no barrier.  The reads are behind the first PRE MFMAs by then (6, 12, 18 and
 // 26 of 64 before them: 384, 385, 378 and 383 us for the call below).
 //
-// 4096 rows, 2048 x 8192, the whole forward call: 382 us where both operands
-// came as half lines, 32 KB a stage all the same, in 407.
-template <int BT, int EPI>
-__device__ __forceinline__ void sum_rows(f32x4_t (&acc)[BT / 32][BT / 32], const Prod& p, int64_t m0, int64_t n0, int first,
+// 4096 rows, 2048 x 8192, the whole forward call: 378 us where the rows of both
+// operands came as half lines, 32 KB a stage all the same, in 407.  The backward
+// call of 777 rows, 1000 x 2728, 70 us for 79.
+template <int BT, bool ACOLS, bool BCOLS, int EPI>
+__device__ __forceinline__ void sum_tile(f32x4_t (&acc)[BT / 32][BT / 32], const Prod& p, int64_t m0, int64_t n0, int first,
                                          int stages, unsigned char* smem, int lane, int wave) {
   constexpr bool GATE = EPI == EPI_GATE;
-  constexpr int F = BT / 32, UNIT = BT * 128, UNITS = 5, DMA = UNIT / 1024 / 4;
-  // A DMA brings 8 rows.  16-byte chunk c of row r is at chunk c ^ (r / 2) % 8.
-  const int row = 8 * wave + (lane >> 3), chunk = (lane & 7) ^ ((row >> 1) & 7);
-  // EPI_GATE: 16 rows of Wg and 16 of Wu in turn, by waves 0 and 1 and by 2 and 3.
-  const bool up = GATE && wave >= 2;
-  const int64_t a_ld = p.lda * 2, b_ld = (up ? p.ldb2 : p.ldb) * 2;
-  const char* const a_base = static_cast<const char*>(p.a) + m0 * a_ld;
-  const char* const b_base = static_cast<const char*>(up ? p.b2 : p.b) + n0 * b_ld;
-  const unsigned a_limit = unsigned(min(int64_t(BT), p.m - m0) * a_ld);
-  const unsigned b_limit = unsigned(min(int64_t(GATE ? BT / 2 : BT), p.n - n0) * b_ld);
-  const unsigned a_step = unsigned(32 * a_ld), b_step = unsigned((GATE ? 16 : 32) * b_ld);
-  const unsigned a_v = unsigned(row * a_ld + chunk * 16);
-  const unsigned b_v = unsigned((GATE ? 8 * (wave & 1) + (lane >> 3) : row) * b_ld + chunk * 16);
-  const unsigned lds = lds_offset(smem);
-  const int last = (stages + 1) / 2 - 1;
-  // Units past the end are issued as a reload of the last pair, as above.
-  auto issue_one = [&](int u, int i) {
-    const bool is_b = u & 1;
-    const int k0 = (first + 2 * min(u >> 1, last)) * kStageK;
-    u32x4_t r = buffer_at((is_b ? b_base : a_base) + int64_t(k0) * 2);
-    r[2] = is_b ? b_limit : a_limit;
-    unsigned v = (is_b ? b_v : a_v) + unsigned(i) * (is_b ? b_step : a_step);
-    if (p.k - k0 < 64 && chunk * 8 >= p.k - k0) v = kBufNone;
-    dma16(r, lds + unsigned(u % UNITS) * UNIT + unsigned(wave + 4 * i) * 1024u, v);
+  constexpr int F = BT / 32;                       // fragments per wave and side
+  constexpr int UNIT = unit_bytes<BT>(), DMA = UNIT / 1024 / 4;
+  const bool up = GATE && wave >= 2;               // brings rows of Wu, not of Wg
+  Side sa, sb;
+  sa.init<BT, ACOLS>(p.a, p.lda, m0, int(min(int64_t(BT), p.m - m0)), wave, lane, false);
+  sb.init<BT, BCOLS>(up ? p.b2 : p.b, up ? p.ldb2 : p.ldb, n0, int(min(int64_t(BT), p.n - n0)), wave, lane, GATE);
+  Frag<BT, ACOLS> fa;
+  Frag<BT, BCOLS> fb;
+  fa.init(wave >> 1, lane);
+  fb.init(wave & 1, lane);
+
+  // The next unit to ask for: where the pair's A and B are, what is left of k,
+  // pairs to go (past the end the last one is loaded again, so that every
+  // stage waits for the same number of DMAs; nothing reads it), the unit's
+  // place in the ring.  Kept up in registers: worked out from the arguments in
+  // each stage, these are read again and waited for.
+  constexpr bool TWO = EPI == EPI_PLAIN && BCOLS && !ACOLS;
+  const int per = (p.k + kUnitK - 1) / kUnitK, at = first / 2, seg = TWO && at >= per ? 1 : 0;
+  const int k0 = (at - seg * per) * kUnitK;
+  const uint64_t pa2 = uint64_t(sa.base) + uint64_t(p.k) * 2;
+  const uint64_t pb2 = uint64_t(p.b2) + uint64_t(n0) * 2;
+  uint64_t pa = (seg ? pa2 : uint64_t(sa.base)) + uint64_t(k0 * sa.kbytes);
+  uint64_t pb = (seg ? pb2 : uint64_t(sb.base)) + uint64_t(k0 * sb.kbytes);
+  const unsigned a_pair = unsigned(kUnitK * sa.kbytes), b_pair = unsigned(kUnitK * sb.kbytes);
+  const int k_all = p.k;
+  int left = p.k - k0, to_go = (stages + 1) / 2 - 1;
+  unsigned ring = 0;
+  const unsigned lds = lds_offset(smem) + unsigned(wave) * 1024u;
+  u32x4_t rsrc;
+  unsigned v0, v1, step, to;
+  auto place = [&](bool is_b) {
+    const uint64_t from = is_b ? pb : pa;
+    const unsigned rows = unsigned(min(left, kUnitK));
+    const unsigned covers = is_b ? (BCOLS ? rows * unsigned(sb.kspan) : sb.limit)
+                                 : (ACOLS ? rows * unsigned(sa.kspan) : sa.limit);
+    rsrc = u32x4_t{unsigned(__builtin_amdgcn_readfirstlane(int(from))),
+                   unsigned(__builtin_amdgcn_readfirstlane(int(from >> 32))) & 0xffffu,
+                   unsigned(__builtin_amdgcn_readfirstlane(int(covers))), 0x00020000u};
+    to = lds + ring;
+    ring = ring == (kUnits - 1) * UNIT ? 0 : ring + UNIT;
   };
-  const int r16 = lane & 15;
-  const unsigned in_row = unsigned(((lane >> 4) ^ ((r16 >> 1) & 7)) << 4);
-  const unsigned a_off = unsigned(((wave >> 1) * (BT / 2) + r16) * 128) + in_row;
-  const unsigned b_off = unsigned(((wave & 1) * (BT / 2) + r16) * 128) + in_row;
+  auto starts = [&](bool is_b) {
+    v0 = is_b ? sb.v0 : sa.v0;
+    v1 = is_b ? sb.v1 : sa.v1;
+    step = is_b ? sb.step : sa.step;
+    if ((is_b ? sb.chunk : sa.chunk) * 8 >= left) v0 = v1 = kBufNone;
+    if (is_b && to_go > 0) {
+      --to_go;
+      pa += a_pair;
+      pb += b_pair;
+      left -= kUnitK;
+      if (TWO && left <= 0) {
+        pa = pa2;
+        pb = pb2;
+        left = k_all;
+      }
+    }
+  };
+  auto issue_one = [&](int i) { dma16(rsrc, to + unsigned(i) * 4096u, ((i & 1) ? v1 : v0) + unsigned(i) * step); };
   u32x4_t a[F], b[F];
 
 #pragma unroll
-  for (int u = 0; u < UNITS - 1; ++u)
+  for (int u = 0; u < kUnits - 1; ++u) {
+    place(u & 1);
+    starts(u & 1);
 #pragma unroll
-    for (int i = 0; i < DMA; ++i) issue_one(u, i);
+    for (int i = 0; i < DMA; ++i) issue_one(i);
+  }
   wait_vm<2 * DMA>();
   barrier();
 #pragma unroll
-  for (int f = 0; f < F; ++f) a[f] = lds_read16(smem, a_off + unsigned(f * 2048));
+  for (int f = 0; f < F; ++f) fa.read(a[f], smem, 0, f);
 #pragma unroll
-  for (int f = 0; f < F; ++f) b[f] = lds_read16(smem + UNIT, b_off + unsigned(f * 2048));
+  for (int f = 0; f < F; ++f) fb.read(b[f], smem + UNIT, 0, f);
 
   constexpr int NXY = F * F, HB = F / 2, PRE = F == 8 ? 18 : 6;
   for (int s = 0; s < stages; ++s) {
     auto mma = [&](int i) {
       const int x = (i % (F * HB)) / HB, y = (i / (F * HB)) * HB + i % HB;
+      // operands swapped: a lane then holds four consecutive n of one m
       acc[x][y] = mfma16(b[y], a[x], acc[x][y]);
     };
     __builtin_amdgcn_sched_barrier(0);
@@ -457,20 +413,21 @@ __device__ __forceinline__ void sum_rows(f32x4_t (&acc)[BT / 32][BT / 32], const
       barrier();
     }
     const unsigned pair = unsigned(s + 1) & ~1u, half = unsigned(s + 1) & 1u;
-    const unsigned char* sA = smem + (pair % UNITS) * UNIT;
-    const unsigned char* sB = smem + ((pair + 1) % UNITS) * UNIT;
-    const unsigned ao = a_off ^ (half * 64), bo = b_off ^ (half * 64);
+    const unsigned char* sA = smem + (pair % kUnits) * UNIT;
+    const unsigned char* sB = smem + ((pair + 1) % kUnits) * UNIT;
     int nd = 0;
 #pragma unroll
     for (int i = PRE; i < NXY; ++i) {
       mma(i);
       const int x = (i % (F * HB)) / HB, y = (i / (F * HB)) * HB + i % HB;
-      if (nd < DMA && i % 2 == 0) issue_one(s + UNITS - 1, nd++);
-      if (x == F - 1) b[y] = lds_read16(sB, bo + unsigned(y * 2048));
-      if (y == F - 1) a[x] = lds_read16(sA, ao + unsigned(x * 2048));
+      if (i == PRE) place(s & 1);
+      if (i == PRE + 1) starts(s & 1);
+      if (i >= PRE + 2 && nd < DMA && i % 2 == 0) issue_one(nd++);
+      if (x == F - 1) fb.read(b[y], sB, half, y);
+      if (y == F - 1) fa.read(a[x], sA, half, x);
       __builtin_amdgcn_sched_barrier(0);
     }
-    static_assert(PRE <= F * HB - HB && DMA <= (NXY - PRE) / 2, "no read before the barrier, a slot for every DMA");
+    static_assert(PRE <= F * HB - HB && DMA <= (NXY - PRE - 2) / 2, "no read before the barrier, a slot for every DMA");
   }
 }
 
@@ -479,10 +436,9 @@ template <int BT, bool ACOLS, bool BCOLS, int EPI, int ACT>
 __device__ __forceinline__ void run_tile(const Prod& p, Tile tile, int range, float* part, unsigned char* smem, int lane,
                                          int wave) {
   constexpr int F = BT / 32, NSTEP = tile_cols<BT, EPI>();
-  constexpr int LIE = !ACOLS && !BCOLS ? ROWS_ROWS : ROWS_COLS;
   const int wm = wave >> 1, wn = wave & 1;
   const int64_t m0 = int64_t(tile.tm) * BT, n0 = int64_t(tile.tn) * NSTEP;
-  const int all = (p.k + kStageK - 1) / kStageK * p.segments;
+  const int all = stages_of(p);
   const int first = range < 0 ? 0 : range % p.splits * p.split_stages;
   const int stages = range < 0 ? all : max(0, min(all - first, p.split_stages));
   f32x4_t acc[F][F];
@@ -490,8 +446,7 @@ __device__ __forceinline__ void run_tile(const Prod& p, Tile tile, int range, fl
   for (int x = 0; x < F; ++x)
 #pragma unroll
     for (int y = 0; y < F; ++y) acc[x][y] = (f32x4_t)(0.f);
-  if constexpr (LIE == ROWS_ROWS) sum_rows<BT, EPI>(acc, p, m0, n0, first, stages, smem, lane, wave);
-  else sum_cols<BT, ACOLS, BCOLS>(acc, p, m0, n0, first, stages, smem, lane, wave);
+  sum_tile<BT, ACOLS, BCOLS, EPI>(acc, p, m0, n0, first, stages, smem, lane, wave);
   // The reloads of the last stage may still be on their way into LDS.
   wait_vm<0>();
   barrier();
@@ -507,7 +462,7 @@ __device__ __forceinline__ void run_tile(const Prod& p, Tile tile, int range, fl
     return;
   }
   constexpr int XB = 2;
-  static_assert(4 * 16 * XB * (BT / 2 + 4) * 4 <= ring_bytes<BT, LIE>(), "epilogue rows fit");
+  static_assert(4 * 16 * XB * (BT / 2 + 4) * 4 <= kUnits * unit_bytes<BT>(), "epilogue rows fit");
   float* er = reinterpret_cast<float*>(smem) + wave * 16 * XB * (BT / 2 + 4);
 #pragma unroll
   for (int x = 0; x < F; x += XB)
@@ -517,7 +472,7 @@ __device__ __forceinline__ void run_tile(const Prod& p, Tile tile, int range, fl
 // MIXED_COLS: products of both kinds of A in one launch.
 template <int BT, int LIE, int EPI, int ACT>
 __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void ffn_gemm_kernel(ProdArgs g) {
-  __shared__ __attribute__((aligned(1024))) unsigned char smem[ring_bytes<BT, LIE>()];
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[kUnits * unit_bytes<BT>()];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int id = int(blockIdx.x), which = 0;
@@ -588,8 +543,6 @@ struct Plan {
   double us;
   struct { int tiles, full, splits, split_stages; } p[kProds];
 };
-int stages_of(const Prod& p) { return (p.k + kStageK - 1) / kStageK * p.segments; }
-
 Plan plan_with(const ProdArgs& g, int bt, bool gate) {
   Plan q{};
   q.bt = bt;
@@ -612,7 +565,7 @@ Plan plan_with(const ProdArgs& g, int bt, bool gate) {
   const int rem = g.count > 1 ? tiles : tiles % slots, whole = g.count > 1 ? 0 : tiles / slots;
   const double part_mb = double(bt) * (rows < bt ? (rows + 15) / 16 * 16 : bt) * 4e-6, tile = stages * stage_us + tile_us;
   for (int n = 1; n == 1 || (rem > 0 && n <= stages / 4 && n <= (g.count > 1 ? 32 : slots / rem)); ++n) {
-    const int per = ((stages + n - 1) / n + 1) & ~1, got = (stages + per - 1) / per;   // whole lines of row operands
+    const int per = ((stages + n - 1) / n + 1) & ~1, got = (stages + per - 1) / per;   // whole units
     const double one = per * stage_us + tile_us, join = got > 1 ? 4 + 2 * rem * got * part_mb / 4.5 : 0;
     double us;
     if (g.count == 1) {
