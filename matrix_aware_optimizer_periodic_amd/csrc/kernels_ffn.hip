@@ -311,8 +311,9 @@ constexpr int kUnits = 5;
 // A unit is last read in the stage before its last one, so an odd stage waits
 // for its own reads before the barrier, which then says that the two units of
 // its pair are free: A's is refilled at once, B's in the next stage, which has
-// no barrier.  The reads are behind the first PRE MFMAs by then (6, 12, 18 and
-// 26 of 64 before them: 384, 385, 378 and 383 us for the call below).
+// no barrier.  The reads are behind the first PRE MFMAs by then (10, 13, 18 and
+// 26 of 64: 4330, 4380, 4380 and 4390 us for the backward call of 4096 rows,
+// 5120 x 20480; fewer than 10 change nothing).
 //
 // 4096 rows, 2048 x 8192, the whole forward call: 378 us where the rows of both
 // operands came as half lines, 32 KB a stage all the same, in 407.  The backward
@@ -396,7 +397,7 @@ __device__ __forceinline__ void sum_tile(f32x4_t (&acc)[BT / 32][BT / 32], const
 #pragma unroll
   for (int f = 0; f < F; ++f) fb.read(b[f], smem + UNIT, 0, f);
 
-  constexpr int NXY = F * F, HB = F / 2, PRE = F == 8 ? 18 : 6;
+  constexpr int NXY = F * F, HB = F / 2, PRE = F == 8 ? 10 : 6;
   for (int s = 0; s < stages; ++s) {
     auto mma = [&](int i) {
       const int x = (i % (F * HB)) / HB, y = (i / (F * HB)) * HB + i % HB;
