@@ -22,10 +22,10 @@
 // next product's operands, and the results.
 //
 // Measured on one MI355X (a large library product runs at 1460 TFLOP/s): 4096
-// rows, 2048 x 8192, gate and up 252 - 268 us (1030 - 1090 TFLOP/s), down
-// 113 - 121 + 14 us; 4096 rows, 5120 x 20480, dh 869 us (988; 160 us of it
-// would take its epilogue's 0.84 GB alone), dx and the weights' gradients
-// 3470 us (1238).  Matrix cores busy 44 - 60% of the cycles at 1.9 - 2.1 GHz.
+// rows, 2048 x 8192, gate and up 250 - 264 us (1040 - 1100 TFLOP/s), down
+// 111 - 116 + 14 us; 4096 rows, 5120 x 20480, dh 870 - 907 us (950 - 990; 160 us
+// of it would take its epilogue's 0.84 GB alone), dx and the weights' gradients
+// 3300 - 3430 us (1250 - 1300).
 #include <algorithm>
 #include <type_traits>
 
@@ -533,12 +533,13 @@ __global__ __launch_bounds__(256) void ffn_join_kernel(ProdArgs g) {
 // divided, if that is worth a second kernel.
 //
 // The choice goes by the time of each way, from what was measured on this
-// card: a stage takes 0.78 us in 256-tiles and 0.6 us in two 128-tiles of a CU
+// card: a stage takes 0.78 us in 256-tiles and 0.58 us in two 128-tiles of a CU
 // (which do half the work), a tile's start and epilogue 11 and 5 us, a launch
 // of 256-tiles 8 us more until its first stages are in, and a join 4 us and its
-// partial sums' writing and reading at 4.5 TB/s.  (dx and the weights'
-// gradients of 777 x 1000 x 2728: 128-tiles with dx in three ranges 50 us,
-// 256-tiles in four 58.)
+// partial sums' writing and reading at 4.5 TB/s.  (The backward call of 777 x
+// 1000 x 2728: 128-tiles with dx in three ranges 70 us, 256-tiles in four 76.
+// Forward at 2048 x 8192: 256 rows 49 us in 128-tiles, 57 in 256-tiles; down
+// product of 4096 rows 116 + 14 us in halves of 256-tiles, 6 more in 128-tiles.)
 struct Plan {
   int bt;
   double us;
@@ -548,7 +549,7 @@ Plan plan_with(const ProdArgs& g, int bt, bool gate) {
   Plan q{};
   q.bt = bt;
   const int nstep = gate ? bt / 2 : bt, slots = bt == 256 ? 256 : 512;
-  const double stage_us = bt == 256 ? 0.78 : 0.6, tile_us = bt == 256 ? 11 : 5;
+  const double stage_us = bt == 256 ? 0.78 : 0.58, tile_us = bt == 256 ? 11 : 5;
   const double launch_us = bt == 256 ? 8 : 0;
   double others = 0, longest = 0, shortest = 1e30;    // of the products after the first
   for (int i = 0; i < g.count; ++i) {
@@ -749,16 +750,17 @@ __global__ __launch_bounds__(64 * NW, NW / 8) void ffn_few_rows_kernel(Prod p) {
   }
 }
 
-// Every workgroup reads all of x, from L2 at about 7 TB/s; the tiled kernels
-// take 8 us and an eighth of the weights' time longer than reading them.  The
-// whole call in us, here against tiles, with weights from memory: 2048 x 8192
-// 27 against 42 for one row, 31 against 42 for 8, 40 against 43 for 16, 50
-// against 47 for 32; 5120 x 20480 121 against 173 for one, 150 against 176 for
-// 8, 186 against 177 for 9; 8192 x 28672 286 against 288 for 8, 305 against
-// 287 for 9.
+// Every workgroup reads all of x: up to 8 rows at about 23 TB/s, as they are
+// shared in L1, more at about 7 from L2; the tiled kernels take 25 us, and 8 us
+// and an eighth of the weights' time, longer than reading them.  The whole call
+// in us, here against tiles, with weights from memory: 2048 x 8192 27 against
+// 41 for one row, 31 against 41 for 8, 40 against 42 for 16, 50 against 44 for
+// 32; 5120 x 20480 121 against 150 for one, 148 against 150 for 8, 184 against
+// 151 for 9; 8192 x 28672 254 against 261 for 4, 266 against 261 for 6.
 bool few_rows(int64_t t, int64_t d, int64_t h) {
-  const double dh = double(d) * h, again_us = t * dh * (4.0 / 16) / 7e6, weights_us = 6 * dh / 5.1e6;
-  return t <= 8 || (t <= 64 && again_us <= 8 + weights_us / 8);
+  const double dh = double(d) * h, weights_us = 6 * dh / 5.1e6;
+  if (t <= 8) return t * dh * (4.0 / 8) / 23e6 <= 25;
+  return t <= 64 && t * dh * (4.0 / 16) / 7e6 <= 8 + weights_us / 8;
 }
 
 template <bool GATE, int ACT>
