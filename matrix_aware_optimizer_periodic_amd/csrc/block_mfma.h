@@ -32,16 +32,19 @@ __device__ __forceinline__ u32x4_t buffer_at(const void* p) {
 // 16 (or 4) bytes per lane from a raw buffer straight into LDS: lane l lands
 // at lds_addr + 16 l (4 l).  Inline asm without outputs, so that the compiler
 // does not drain it before unrelated LDS reads; the kernels order it with
-// wait_vm() and barriers.
+// wait_vm() and barriers.  The compiler does not see the load's operands either
+// and puts no wait states between a vector instruction that writes one of its
+// scalar registers (a spilled one's reload, say) and the load, which needs five:
+// the write of m0 and the nop are those.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"   // m0 is reserved; naming it is what is meant
 // soff is added to every lane's offset; kBufNone stays out of range with it.
 __device__ __forceinline__ void dma16(u32x4_t rsrc, unsigned lds_addr, unsigned voff, unsigned soff = 0) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :: "s"(lds_addr), "v"(voff), "s"(rsrc), "s"(__builtin_amdgcn_readfirstlane(int(soff))) : "m0", "memory");
 }
 __device__ __forceinline__ void dma4(u32x4_t rsrc, unsigned lds_addr, unsigned voff) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dword %1, %2, 0 offen lds"
                :: "s"(lds_addr), "v"(voff), "s"(rsrc) : "m0", "memory");
 }
 #pragma clang diagnostic pop
