@@ -324,10 +324,12 @@ __device__ __forceinline__ void sum_tile(f32x4_t (&acc)[BT / 32][BT / 32], const
   constexpr bool GATE = EPI == EPI_GATE;
   constexpr int F = BT / 32;                       // fragments per wave and side
   constexpr int UNIT = unit_bytes<BT>(), DMA = UNIT / 1024 / 4;
-  const bool up = GATE && wave >= 2;               // brings rows of Wu, not of Wg
+  constexpr bool TWO = EPI == EPI_PLAIN && BCOLS && !ACOLS;
+  const int per = (p.k + kUnitK - 1) / kUnitK, at = first / 2, seg = TWO && at >= per ? 1 : 0;
+  const bool second = (GATE && wave >= 2) || seg;  // brings rows of Wu, not of Wg
   Side sa, sb;
   sa.init<BT, ACOLS>(p.a, p.lda, m0, int(min(int64_t(BT), p.m - m0)), wave, lane, false);
-  sb.init<BT, BCOLS>(up ? p.b2 : p.b, up ? p.ldb2 : p.ldb, n0, int(min(int64_t(BT), p.n - n0)), wave, lane, GATE);
+  sb.init<BT, BCOLS>(second ? p.b2 : p.b, second ? p.ldb2 : p.ldb, n0, int(min(int64_t(BT), p.n - n0)), wave, lane, GATE);
   Frag<BT, ACOLS> fa;
   Frag<BT, BCOLS> fb;
   fa.init(wave >> 1, lane);
@@ -338,14 +340,13 @@ __device__ __forceinline__ void sum_tile(f32x4_t (&acc)[BT / 32][BT / 32], const
   // stage waits for the same number of DMAs; nothing reads it), the unit's
   // place in the ring.  Kept up in registers: worked out from the arguments in
   // each stage, these are read again and waited for.
-  constexpr bool TWO = EPI == EPI_PLAIN && BCOLS && !ACOLS;
-  const int per = (p.k + kUnitK - 1) / kUnitK, at = first / 2, seg = TWO && at >= per ? 1 : 0;
   const int k0 = (at - seg * per) * kUnitK;
   const uint64_t pa2 = uint64_t(sa.base) + uint64_t(p.k) * 2;
-  const uint64_t pb2 = uint64_t(p.b2) + uint64_t(n0) * 2;
+  const uint64_t pb2 = TWO ? uint64_t(p.b2) + uint64_t(n0) * 2 : 0;
   uint64_t pa = (seg ? pa2 : uint64_t(sa.base)) + uint64_t(k0 * sa.kbytes);
-  uint64_t pb = (seg ? pb2 : uint64_t(sb.base)) + uint64_t(k0 * sb.kbytes);
-  const unsigned a_pair = unsigned(kUnitK * sa.kbytes), b_pair = unsigned(kUnitK * sb.kbytes);
+  uint64_t pb = uint64_t(sb.base) + uint64_t(k0 * sb.kbytes);
+  const unsigned a_pair = unsigned(kUnitK * sa.kbytes);
+  unsigned b_pair = unsigned(kUnitK * sb.kbytes);
   const int k_all = p.k;
   int left = p.k - k0, to_go = (stages + 1) / 2 - 1;
   unsigned ring = 0;
@@ -377,6 +378,9 @@ __device__ __forceinline__ void sum_tile(f32x4_t (&acc)[BT / 32][BT / 32], const
         pa = pa2;
         pb = pb2;
         left = k_all;
+        // the second matrix's rows lie ldb2 apart
+        sb.init<BT, BCOLS>(p.b2, p.ldb2, n0, int(min(int64_t(BT), p.n - n0)), wave, lane, false);
+        b_pair = unsigned(kUnitK * sb.kbytes);
       }
     }
   };
