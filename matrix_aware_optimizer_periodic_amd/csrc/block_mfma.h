@@ -35,13 +35,17 @@ __device__ __forceinline__ u32x4_t buffer_at(const void* p) {
 // wait_vm() and barriers.  The compiler does not see the load's operands either
 // and puts no wait states between a vector instruction that writes one of its
 // scalar registers (a spilled one's reload, say) and the load, which needs five:
-// the write of m0 and the nop are those.
+// the write of m0 and 1 + NOP more.  A kernel that gives a smaller NOP has to
+// have its scalar operands that far ahead; the scan of the compiled code among
+// the tests holds it to that.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"   // m0 is reserved; naming it is what is meant
 // soff is added to every lane's offset; kBufNone stays out of range with it.
+template <int NOP = 3>
 __device__ __forceinline__ void dma16(u32x4_t rsrc, unsigned lds_addr, unsigned voff, unsigned soff = 0) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-               :: "s"(lds_addr), "v"(voff), "s"(rsrc), "s"(__builtin_amdgcn_readfirstlane(int(soff))) : "m0", "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop %4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :: "s"(lds_addr), "v"(voff), "s"(rsrc), "s"(__builtin_amdgcn_readfirstlane(int(soff))), "n"(NOP)
+               : "m0", "memory");
 }
 __device__ __forceinline__ void dma4(u32x4_t rsrc, unsigned lds_addr, unsigned voff) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dword %1, %2, 0 offen lds"

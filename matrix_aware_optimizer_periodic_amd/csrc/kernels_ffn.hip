@@ -384,7 +384,12 @@ __device__ __forceinline__ void sum_tile(f32x4_t (&acc)[BT / 32][BT / 32], const
       }
     }
   };
-  auto issue_one = [&](int i) { dma16(rsrc, to + unsigned(i) * 4096u, ((i & 1) ? v1 : v0) + unsigned(i) * step); };
+  // Among the MFMAs the descriptor is formed two of them ahead of its first
+  // load, which then waits for nothing more: five wait states in each load took
+  // 4440 us for 4330 in the backward call of 4096 rows, 5120 x 20480.
+  auto issue_one = [&](int i, auto ahead) {
+    dma16<decltype(ahead)::value ? 0 : 3>(rsrc, to + unsigned(i) * 4096u, ((i & 1) ? v1 : v0) + unsigned(i) * step);
+  };
   u32x4_t a[F], b[F];
 
 #pragma unroll
@@ -392,7 +397,7 @@ __device__ __forceinline__ void sum_tile(f32x4_t (&acc)[BT / 32][BT / 32], const
     place(u & 1);
     starts(u & 1);
 #pragma unroll
-    for (int i = 0; i < DMA; ++i) issue_one(i);
+    for (int i = 0; i < DMA; ++i) issue_one(i, std::false_type{});
   }
   wait_vm<2 * DMA>();
   barrier();
@@ -427,7 +432,7 @@ __device__ __forceinline__ void sum_tile(f32x4_t (&acc)[BT / 32][BT / 32], const
       const int x = (i % (F * HB)) / HB, y = (i / (F * HB)) * HB + i % HB;
       if (i == PRE) place(s & 1);
       if (i == PRE + 1) starts(s & 1);
-      if (i >= PRE + 2 && nd < DMA && i % 2 == 0) issue_one(nd++);
+      if (i >= PRE + 2 && nd < DMA && i % 2 == 0) issue_one(nd++, std::true_type{});
       if (x == F - 1) fb.read(b[y], sB, half, y);
       if (y == F - 1) fa.read(a[x], sA, half, x);
       __builtin_amdgcn_sched_barrier(0);
