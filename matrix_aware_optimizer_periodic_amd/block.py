@@ -11,10 +11,11 @@ read raises.  Tensors made on another stream need the caller's wait (and
 ``record_stream``), as with PyTorch's own operators.  All six may be captured
 into a HIP graph.
 
-``residual_norm``, ``attention`` and ``gated_ffn`` wrap them for autograd.  To
-capture a training step into a graph, call the forward and backward functions
-themselves: an autograd graph that shares leaves with a captured backward pass
-must not be alive during the capture.
+``residual_norm``, ``attention`` and ``gated_ffn`` wrap them for autograd, once:
+gradients of their gradients raise.  To capture a training step into a graph,
+call the forward and backward functions themselves: an autograd graph that
+shares leaves with a captured backward pass must not be alive during the
+capture.
 """
 
 from __future__ import annotations
@@ -23,6 +24,7 @@ import ctypes
 import struct
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from .binding import MUON_OK, MuonError, lib
 
@@ -246,6 +248,7 @@ class _ResidualNorm(torch.autograd.Function):
         return out, y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_out, d_y):
         out, h, stats, gate, post_weight, pre_weight, scale, shift = ctx.saved_tensors
         if d_out is None and d_y is None:
@@ -350,6 +353,7 @@ class _Attention(torch.autograd.Function):
         return o
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_o):
         q, k, v, o, lse = ctx.saved_tensors
         return (*attn_bwd(d_o.contiguous(), q, k, v, o, lse, **ctx.how), None)
@@ -365,6 +369,7 @@ class _PackedAttention(torch.autograd.Function):
         return o
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_o):
         qkv, o, lse = ctx.saved_tensors
         d_qkv = torch.empty_like(qkv, memory_format=torch.contiguous_format)
@@ -453,6 +458,7 @@ class _GatedFfn(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_y):
         return (*ffn_bwd(d_y.contiguous(), *ctx.saved_tensors, act=ctx.act), None)
 

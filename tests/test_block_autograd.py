@@ -1,0 +1,111 @@
+"""What the block operators' autograd functions do around the library's calls,
+on the CPU with stand-ins for these: the plain formulas, outside autograd as
+the library's results are."""
+
+import pytest
+import torch
+
+pytest.importorskip("matrix_aware_optimizer_periodic_amd")
+from matrix_aware_optimizer_periodic_amd import block  # noqa: E402
+
+
+def softmax_attention(q, k, v, causal=False, offset=0, q_lens=None, k_lens=None, scale=None):
+    """(o, lse) of (batch, len, heads, dim), every key seen."""
+    s = torch.einsum("bmhd,bnhd->bhmn", q, k) * (q.shape[-1] ** -0.5 if scale is None else scale)
+    return torch.einsum("bhmn,bnhd->bmhd", torch.softmax(s, -1), v), torch.logsumexp(s, -1)
+
+
+@pytest.fixture
+def stand_ins(monkeypatch):
+    """Stand-ins for the six calls; `calls` lists the names of those made."""
+    calls = []
+
+    def outside(name, forward):
+        def call(*args, **how):
+            calls.append(name)
+            with torch.no_grad():
+                return forward(*args, **how)
+        monkeypatch.setattr(block, name, call)
+
+    def gradients(fn, inputs, d_out):
+        with torch.enable_grad():
+            leaves = [t.detach().requires_grad_(True) for t in inputs]
+            return torch.autograd.grad(fn(*leaves), leaves, d_out)
+
+    def attn_bwd(d_o, q, k, v, o, lse, out=None, **how):
+        g = gradients(lambda *t: softmax_attention(*t, **how)[0], (q, k, v), d_o)
+        if out is None:
+            return g
+        for t, x in zip(out, g):
+            t.copy_(x)
+        return out
+
+    def ffn(x, wg, wu, wd):
+        return (torch.nn.functional.silu(x @ wg.T) * (x @ wu.T)) @ wd.T
+
+    def ffn_fwd(x, wg, wu, wd, act="silu", save=True):
+        calls.append("saved" if save else "not saved")
+        return ffn(x, wg, wu, wd), torch.cat([x @ wg.T, x @ wu.T], 1) if save else None
+
+    def norm(resid, h, gate, post_weight, pre_weight, scale, shift):
+        return resid + h * gate[:, None], (resid + h * gate[:, None]).sin()
+
+    def norm_fwd(*args, y_dtype=None, **how):
+        return (*norm(*args), torch.zeros(args[0].shape[:-1].numel(), 4))
+
+    def norm_bwd(d_out, d_y, out, h, stats, gate, *rest, **how):
+        d = d_out + d_y * out.cos()
+        return {"resid": d, "h": d * gate[:, None], "gate": (d * h).sum(1), "post_weight": None, "pre_weight": None,
+                "scale": None, "shift": None}
+    outside("attn_fwd", softmax_attention)
+    outside("attn_bwd", attn_bwd)
+    outside("ffn_fwd", ffn_fwd)
+    outside("ffn_bwd", lambda d_y, x, wg, wu, wd, gu, act="silu": gradients(ffn, (x, wg, wu, wd), d_y))
+    outside("norm_fwd", norm_fwd)
+    outside("norm_bwd", norm_bwd)
+    return calls
+
+
+def leaves(*shapes):
+    gen = torch.Generator().manual_seed(0)
+    return [torch.randn(s, generator=gen, dtype=torch.float64).requires_grad_(True) for s in shapes]
+
+
+def through_attention():
+    q, k, v = leaves((2, 3, 2, 8), (2, 5, 2, 8), (2, 5, 2, 8))
+    return [q, k, v], block.attention(q, k, v)
+
+
+def through_packed_attention():
+    qkv, = leaves((2, 4, 3, 2, 8))
+    return [qkv], block.attention_qkv(qkv)
+
+
+def through_ffn():
+    t = leaves((3, 8), (16, 8), (16, 8), (8, 16))
+    return t, block.gated_ffn(*t)
+
+
+def through_norm():
+    resid, h, gate = leaves((2, 3, 8), (2, 3, 8), (2, 8))
+    out, y = block.residual_norm(resid, h, gate)
+    return [resid, h, gate], out + y
+
+
+@pytest.mark.parametrize("through", [through_attention, through_packed_attention, through_ffn, through_norm])
+def test_second_derivatives_are_refused(stand_ins, through):
+    """The backward passes are not recorded: a gradient penalty through one
+    would take the first gradients as constants."""
+    inputs, y = through()
+    first = torch.autograd.grad(y.square().sum(), inputs, create_graph=True)
+    assert all(bool(torch.isfinite(g).all()) for g in first)
+    penalty = sum(g.square().sum() for g in first) + sum(t.square().sum() for t in inputs)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        penalty.backward()
+
+
+@pytest.mark.parametrize("through", [through_attention, through_packed_attention, through_ffn, through_norm])
+def test_first_derivatives_reach_every_input(stand_ins, through):
+    inputs, y = through()
+    y.square().sum().backward()
+    assert all(t.grad is not None and bool((t.grad != 0).any()) for t in inputs)
