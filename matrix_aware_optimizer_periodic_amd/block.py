@@ -344,19 +344,25 @@ def attn_bwd(d_o, q, k, v, o, lse, *, causal: bool = False, offset: int = 0, q_l
     return d_q, d_k, d_v
 
 
+def _keep(ctx, how, *tensors):
+    """Saves what the backward pass reads, the lengths with it: written again
+    before that pass, they then raise as any saved tensor does."""
+    ctx.how = {name: value for name, value in how.items() if name not in ("q_lens", "k_lens")}
+    ctx.save_for_backward(*tensors, how["q_lens"], how["k_lens"])
+
+
 class _Attention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, how):
         o, lse = attn_fwd(q, k, v, **how)
-        ctx.how = how
-        ctx.save_for_backward(q, k, v, o, lse)
+        _keep(ctx, how, q, k, v, o, lse)
         return o
 
     @staticmethod
     @once_differentiable
     def backward(ctx, d_o):
-        q, k, v, o, lse = ctx.saved_tensors
-        return (*attn_bwd(d_o.contiguous(), q, k, v, o, lse, **ctx.how), None)
+        q, k, v, o, lse, q_lens, k_lens = ctx.saved_tensors
+        return (*attn_bwd(d_o.contiguous(), q, k, v, o, lse, q_lens=q_lens, k_lens=k_lens, **ctx.how), None)
 
 
 class _PackedAttention(torch.autograd.Function):
@@ -364,16 +370,15 @@ class _PackedAttention(torch.autograd.Function):
     def forward(ctx, qkv, how):
         q, k, v = qkv.unbind(2)
         o, lse = attn_fwd(q, k, v, **how)
-        ctx.how = how
-        ctx.save_for_backward(qkv, o, lse)
+        _keep(ctx, how, qkv, o, lse)
         return o
 
     @staticmethod
     @once_differentiable
     def backward(ctx, d_o):
-        qkv, o, lse = ctx.saved_tensors
+        qkv, o, lse, q_lens, k_lens = ctx.saved_tensors
         d_qkv = torch.empty_like(qkv, memory_format=torch.contiguous_format)
-        attn_bwd(d_o.contiguous(), *qkv.unbind(2), o, lse, out=d_qkv.unbind(2), **ctx.how)
+        attn_bwd(d_o.contiguous(), *qkv.unbind(2), o, lse, q_lens=q_lens, k_lens=k_lens, out=d_qkv.unbind(2), **ctx.how)
         return d_qkv, None
 
 

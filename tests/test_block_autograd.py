@@ -109,3 +109,36 @@ def test_first_derivatives_reach_every_input(stand_ins, through):
     inputs, y = through()
     y.square().sum().backward()
     assert all(t.grad is not None and bool((t.grad != 0).any()) for t in inputs)
+
+
+@pytest.mark.parametrize("which", ["q_lens", "k_lens"])
+@pytest.mark.parametrize("packed", [False, True])
+def test_lengths_written_between_the_passes_are_noticed(stand_ins, which, packed):
+    """A length buffer refilled for the next batch before the backward pass
+    would give gradients of other lengths than the forward pass used."""
+    lens = {which: torch.tensor([3, 4], dtype=torch.int32)}
+
+    def forward():
+        if packed:
+            return block.attention_qkv(*leaves((2, 4, 3, 2, 8)), **lens)
+        return block.attention(*leaves((2, 4, 2, 8), (2, 4, 2, 8), (2, 4, 2, 8)), **lens)
+    y = forward()
+    lens[which].fill_(2)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+    forward().sum().backward()           # kept as they are, they serve
+
+
+def test_lengths_reach_the_backward_call(stand_ins, monkeypatch):
+    given = []
+    real = block.attn_bwd
+    monkeypatch.setattr(block, "attn_bwd", lambda *a, **how: given.append(how) or real(*a, **how))
+    qn, kn = torch.tensor([3, 4], dtype=torch.int32), torch.tensor([1, 2], dtype=torch.int32)
+    how = {"q_lens": qn, "k_lens": kn, "causal": True, "offset": 2, "scale": 0.5}
+    block.attention(*leaves((2, 4, 2, 8), (2, 4, 2, 8), (2, 4, 2, 8)), **how).sum().backward()
+    block.attention_qkv(*leaves((2, 4, 3, 2, 8)), **how).sum().backward()
+    for got in given:
+        got.pop("out", None)
+        assert torch.equal(got.pop("q_lens"), qn) and torch.equal(got.pop("k_lens"), kn)
+        assert got == {"causal": True, "offset": 2, "scale": 0.5}
+    assert len(given) == 2
