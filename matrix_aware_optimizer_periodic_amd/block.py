@@ -456,8 +456,8 @@ def ffn_bwd(d_y, x, w_gate, w_up, w_down, gu, *, act: str = "silu", grad_dtype=t
 
 class _GatedFfn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, w_gate, w_up, w_down, act):
-        y, gu = ffn_fwd(x, w_gate, w_up, w_down, act=act, save=any(ctx.needs_input_grad))
+    def forward(ctx, x, w_gate, w_up, w_down, act, save):
+        y, gu = ffn_fwd(x, w_gate, w_up, w_down, act=act, save=save)
         ctx.act = act
         ctx.save_for_backward(x, w_gate, w_up, w_down, gu)
         return y
@@ -465,9 +465,11 @@ class _GatedFfn(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, d_y):
-        return (*ffn_bwd(d_y.contiguous(), *ctx.saved_tensors, act=ctx.act), None)
+        return (*ffn_bwd(d_y.contiguous(), *ctx.saved_tensors, act=ctx.act), None, None)
 
 
 def gated_ffn(x, w_gate, w_up, w_down, *, act: str = "silu"):
     """ffn_fwd for autograd; returns y."""
-    return _GatedFfn.apply(x, w_gate, w_up, w_down, act)
+    # (inside forward the grad mode is off, and needs_input_grad does not know it)
+    save = torch.is_grad_enabled() and any(t.requires_grad for t in (x, w_gate, w_up, w_down))
+    return _GatedFfn.apply(x, w_gate, w_up, w_down, act, save)

@@ -142,3 +142,19 @@ def test_lengths_reach_the_backward_call(stand_ins, monkeypatch):
         assert torch.equal(got.pop("q_lens"), qn) and torch.equal(got.pop("k_lens"), kn)
         assert got == {"causal": True, "offset": 2, "scale": 0.5}
     assert len(given) == 2
+
+
+def test_projections_are_kept_where_a_backward_pass_may_follow(stand_ins):
+    t = leaves((3, 8), (16, 8), (16, 8), (8, 16))
+    frozen = [w.detach() for w in t]
+
+    def kept(call):
+        stand_ins.clear()
+        call()
+        return stand_ins[-1] == "saved"
+    assert kept(lambda: block.gated_ffn(*t))
+    assert kept(lambda: block.gated_ffn(t[0], *frozen[1:])) and kept(lambda: block.gated_ffn(frozen[0], *t[1:]))
+    assert not kept(lambda: block.gated_ffn(*frozen))
+    for off in (torch.no_grad, torch.inference_mode):
+        with off():
+            assert not kept(lambda: block.gated_ffn(*t)), off
