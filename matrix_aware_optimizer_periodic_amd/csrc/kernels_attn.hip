@@ -471,9 +471,16 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnDev a) {
   if (line >= lines) return;
   const int lane = threadIdx.x & 63, d = (lane & 15) * 8;
   float top = -INFINITY;
-  for (int i = lane; i < a.splits; i += 64) top = fmaxf(top, *as_global(a.part_lse + i * lines + line));
+  bool nan = false;
+  for (int i = lane; i < a.splits; i += 64) {
+    const float lse = *as_global(a.part_lse + i * lines + line);
+    top = fmaxf(top, lse);
+    nan |= lse != lse;
+  }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+  // The maximum leaves NaN out; a row that has one in any range is NaN.
+  if (__any(nan)) top = NAN;
   float sum = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (top != -INFINITY) {
 #pragma unroll 4
