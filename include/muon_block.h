@@ -23,7 +23,8 @@
  *   As in muon.h: a status, never an exception or abort, and nothing is
  *   enqueued when a call returns anything but MUON_OK or MUON_E_HIP.
  *   muon_block_last_error() gives the text.  NaN and infinities propagate
- *   as in the formulas, except where a length says that a value is not there.
+ *   as in the formulas, except where a length says that a value is not there
+ *   (and, near a causal border, as the attention section says).
  */
 #ifndef MUON_BLOCK_H
 #define MUON_BLOCK_H
@@ -89,9 +90,14 @@ muon_status muon_norm_bwd(const muon_norm_args* args, void* workspace, size_t wo
  * head h / (heads / kv_heads).  Key j is seen by query i of sample b when
  * i < q_lens[b], j < k_lens[b] (each q_len / k_len where absent) and, with
  * causal, j <= i + offset.  A query that sees no key has o = 0 and
- * lse = -inf, and no gradient; what lies past a length is never used, so it
- * may hold anything.  Scores, softmax and all sums are fp32; probabilities
- * and their gradients are rounded to bf16 as matrix-core operands. */
+ * lse = -inf, and no gradient; a key that no query sees has none either.
+ * What lies past a length, a key that no query sees and a query that sees no
+ * key are never used, so they may hold anything.  Between queries and keys
+ * that others do see, the causal border is kept by probabilities of 0: a NaN
+ * or infinity in a key or value (backward: also in a query or its d_o) may
+ * pass it, to positions less than 128 away from the border.  Scores, softmax
+ * and all sums are fp32; probabilities and their gradients are rounded to
+ * bf16 as matrix-core operands. */
 typedef struct muon_heads {
   void* ptr;              /* BF16 (batch, len, heads, dim), dim contiguous    */
   int64_t stride_batch, stride_len, stride_head;   /* in values, multiples of 8 */

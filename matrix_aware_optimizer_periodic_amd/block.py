@@ -306,7 +306,8 @@ def attn_fwd(q, k, v, *, causal: bool = False, offset: int = 0, q_lens=None, k_l
     and keys are there.  causal: query i sees key j for j <= i + offset.
     scale: dim ** -0.5 where None.  Returns o (batch, q_len, heads, dim) bf16
     and lse (batch, heads, q_len) fp32; a query that sees no key has o = 0 and
-    lse = -inf."""
+    lse = -inf.  What lies past a length, and keys that no query sees, may hold
+    anything."""
     dev = _device(q, k, v, q_lens, k_lens)
     b, m, n, h, g, d, scale = _attn_dims(q, k, v, q_lens, k_lens, scale)
     o = _out(q)                              # q's type is checked by _heads

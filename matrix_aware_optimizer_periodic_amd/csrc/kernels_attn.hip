@@ -303,11 +303,10 @@ __global__ __launch_bounds__(256, DB <= 2 ? 3 : 2) void attn_fwd_kernel(AttnDev 
   const TileMove<DB, 4> mk(a.k.sl, a.dim, wave, lane), mv(a.v.sl, a.dim, wave, lane);
   const unsigned lds = lds_offset(smem);
   auto fetch_k = [&](int t) {
-    mk.issue(kbase + int64_t(t) * kTile * a.k.sl, r.k_here - first - t * kTile, lds + unsigned(t & 1) * G::TILEB, wave);
+    mk.issue(kbase + int64_t(t) * kTile * a.k.sl, most - first - t * kTile, lds + unsigned(t & 1) * G::TILEB, wave);
   };
   auto fetch_v = [&](int t) {
-    mv.issue(vbase + int64_t(t) * kTile * a.v.sl, r.k_here - first - t * kTile, lds + unsigned(2 + (t & 1)) * G::TILEB,
-             wave);
+    mv.issue(vbase + int64_t(t) * kTile * a.v.sl, most - first - t * kTile, lds + unsigned(2 + (t & 1)) * G::TILEB, wave);
   };
 
   if (tiles > 0) fetch_k(0);
@@ -442,6 +441,10 @@ __global__ __launch_bounds__(256, DB <= 2 ? 3 : 2) void attn_fwd_kernel(AttnDev 
   const float inv = sum == 0.f ? 0.f : 1.0f / sum;
   const float lse = sum == 0.f ? -INFINITY : fmaf(top, a.scale, __builtin_amdgcn_logf(sum) * kLn2);
   if (!r.ok) return;
+  if (sum == 0.f) {            // sees none of these keys, whatever they hold
+#pragma unroll
+    for (int db = 0; db < DB; ++db) o[db] = (f32x16_t)(0.f);
+  }
   const int64_t line = (int64_t(r.b) * a.heads + r.head) * a.q_len + r.qi;
   if constexpr (SPLIT) {
     const int64_t at = int64_t(split) * a.batch * a.heads * a.q_len + line;
@@ -529,14 +532,14 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnDev a, unsigned ite
   const int tiles = (end + kTile - 1) / kTile;
 
   u32x4_t q[2 * DB], g[2 * DB];
-  load_rows<DB>(q, static_cast<const uint16_t*>(a.q.p) + r.b * a.q.sb + r.qi * a.q.sl + r.head * a.q.sh, r.live, a.dim,
+  load_rows<DB>(q, static_cast<const uint16_t*>(a.q.p) + r.b * a.q.sb + r.qi * a.q.sl + r.head * a.q.sh, r.see > 0, a.dim,
                 half);
-  load_rows<DB>(g, static_cast<const uint16_t*>(a.d_o.p) + r.b * a.d_o.sb + r.qi * a.d_o.sl + r.head * a.d_o.sh, r.live,
+  load_rows<DB>(g, static_cast<const uint16_t*>(a.d_o.p) + r.b * a.d_o.sb + r.qi * a.d_o.sl + r.head * a.d_o.sh, r.see > 0,
                 a.dim, half);
   float delta = 0.f;
   {
     u32x4_t o[2 * DB];
-    load_rows<DB>(o, static_cast<const uint16_t*>(a.o.p) + r.b * a.o.sb + r.qi * a.o.sl + r.head * a.o.sh, r.live,
+    load_rows<DB>(o, static_cast<const uint16_t*>(a.o.p) + r.b * a.o.sb + r.qi * a.o.sl + r.head * a.o.sh, r.see > 0,
                   a.dim, half);
     // The diagonal of o do^T, summed in the same order as do v^T below: where
     // a row's o is one row of v (one key), dp - delta is then exactly 0.
@@ -551,11 +554,10 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnDev a, unsigned ite
   // A row that sees nothing gets the offset +inf: its probabilities are 0.
   const int64_t line = (int64_t(r.b) * a.heads + r.head) * a.q_len + r.qi;
   float lse = INFINITY;
-  if (r.live) {
+  if (r.see > 0) {
     lse = *as_global(a.lse + line);
     lse = lse == -INFINITY ? INFINITY : lse * kLog2e;
   }
-  if (r.see == 0) { lse = INFINITY; delta = 0.f; }
   if (r.ok && half == 0) {
     *as_global(a.part_lse + line) = lse;
     *as_global(a.delta + line) = delta;
@@ -568,8 +570,8 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnDev a, unsigned ite
   const unsigned lds = lds_offset(smem);
   auto fetch = [&](int t) {
     const unsigned at = lds + unsigned(t & 1) * 2u * G::TILEB;
-    mk.issue(kbase + int64_t(t) * kTile * a.k.sl, r.k_here - t * kTile, at, wave);
-    mv.issue(vbase + int64_t(t) * kTile * a.v.sl, r.k_here - t * kTile, at + G::TILEB, wave);
+    mk.issue(kbase + int64_t(t) * kTile * a.k.sl, end - t * kTile, at, wave);
+    mv.issue(vbase + int64_t(t) * kTile * a.v.sl, end - t * kTile, at + G::TILEB, wave);
   };
   f32x16_t acc[DB];
 #pragma unroll
@@ -649,6 +651,10 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnDev a, unsigned ite
       slot_end(n);
     }
   }
+  if (r.see == 0) {            // no gradient, whatever the others' keys and values hold
+#pragma unroll
+    for (int db = 0; db < DB; ++db) acc[db] = (f32x16_t)(0.f);
+  }
   if (r.ok)
     store_rows<DB>(acc, a.scale, static_cast<uint16_t*>(a.d_q.p) + r.b * a.d_q.sb + r.qi * a.d_q.sl + r.head * a.d_q.sh,
                    a.dim, half);
@@ -686,14 +692,17 @@ __global__ __launch_bounds__(512, 2) void attn_dkv_kernel(AttnDev a, unsigned it
   const unsigned rest = item - up * (a.causal ? a.by_bh.by : a.key_blocks.by);
   const unsigned bh = a.causal ? rest : up, blk = a.causal ? up : rest;
   const int b = int(div_by(bh, a.by_kv_heads)), kvh = int(bh) - b * a.kv_heads, group = int(a.by_group.by);
-  const int q_here = clamp_len(a.q_lens, b, a.q_len), k_here = clamp_len(a.k_lens, b, a.k_len);
+  const int q_here = clamp_len(a.q_lens, b, a.q_len);
+  // keys that the last query sees (the most of any); the others are as if not there
+  const int k_here = q_here > 0 ? seen(a, q_here - 1, clamp_len(a.k_lens, b, a.k_len)) : 0;
   const int key0 = int(blk) * KEYS;
   const int wkey = key0 + wave * 32, key = wkey + (lane & 31);
   // First query that sees a key.
   const int64_t border = a.causal ? -a.offset : int64_t(-0x7fffffff);
   auto first_query = [&](int k) { return int(max(int64_t(0), min(int64_t(q_here), int64_t(k) + border))); };
-  const int tile0 = first_query(key0) / kTile, tile_end = (q_here + kTile - 1) / kTile;
-  const int per_head = key0 < k_here && first_query(key0) < q_here ? tile_end - tile0 : 0;
+  // The tiles begin at the first query that sees any of the block's keys.
+  const int begin = first_query(key0);
+  const int per_head = key0 < k_here ? (q_here - begin + kTile - 1) / kTile : 0;
   const int all = per_head * group, share = (all + a.parts - 1) / a.parts;
   const int t0 = min(all, int(part) * share), tiles = min(all, t0 + share) - t0;
   const int wave_first = first_query(wkey), wave_all = first_query(wkey + 31);
@@ -727,7 +736,7 @@ __global__ __launch_bounds__(512, 2) void attn_dkv_kernel(AttnDev a, unsigned it
   int head = 0, q0 = 0;                 // of the tile worked on
   if (tiles > 0) {
     head = t0 / per_head;
-    q0 = (tile0 + t0 % per_head) * kTile;
+    q0 = begin + t0 % per_head * kTile;
     const TileMove<DB, NW> mv(a.v.sl, a.dim, wave, lane);
 #pragma unroll
     for (int i = 0; i < KEYS / kTile; ++i)
@@ -741,7 +750,7 @@ __global__ __launch_bounds__(512, 2) void attn_dkv_kernel(AttnDev a, unsigned it
     wait_vm<0>();
     barrier();
     int next_head = head, next_q0 = q0 + kTile;
-    if (next_q0 >= q_here) { next_q0 = tile0 * kTile; ++next_head; }
+    if (next_q0 >= q_here) { next_q0 = begin; ++next_head; }
     if (t + 1 < tiles) fetch(next_head, next_q0, t + 1);
     const unsigned char* qt = smem + VB + (t & 1) * BUF;
     const unsigned char* gt = qt + G::TILEB;
@@ -840,7 +849,7 @@ __global__ __launch_bounds__(512, 2) void attn_dkv_kernel(AttnDev a, unsigned it
     q0 = next_q0;
   }
   if (key >= a.k_len) return;
-  if (key >= k_here) {      // a key past the length has no gradient
+  if (key >= k_here) {      // a key past the length, or that no query sees, has no gradient
 #pragma unroll
     for (int db = 0; db < DB; ++db) dk[db] = dv[db] = (f32x16_t)(0.f);
   }

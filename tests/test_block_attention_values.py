@@ -107,3 +107,69 @@ def test_keys_and_values_that_are_not_finite(n):
         (k, v)[what][1, n // 2, 1, 7] = NAN
         check(q, k, v, d_o)
         check(q, k, v, d_o, k_lens=torch.tensor([n, n // 2], dtype=torch.int32, device="cuda"))
+
+
+# A cache whose end holds anything, bounded by the causal border alone: whole
+# and part tiles past it, few queries and many, heads in groups.
+@pytest.mark.parametrize("b,m,n,h,g,d", [(1, 1, 90, 4, 2, 64), (2, 3, 2500, 4, 1, 128), (2, 70, 200, 2, 2, 128),
+                                         (3, 260, 700, 2, 1, 40), (40, 130, 300, 2, 1, 72)])
+@pytest.mark.parametrize("value", [NAN, INF])
+def test_keys_that_no_query_sees_hold_anything(b, m, n, h, g, d, value):
+    for past in (1, 29, 64, n - m):
+        q, k, v, d_o = make(b, m, n, h, g, d, seed=n + past)
+        offset = n - m - past                       # the last query sees all keys but `past`
+        k[:, n - past:] = value
+        v[:, n - past:] = -value
+        check(q, k, v, d_o, causal=True, offset=offset)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("m,n,offset", [(140, 130, -33), (140, 130, -64), (300, 90, -280), (5, 900, -3), (70, 70, -200)])
+def test_queries_that_see_no_key_hold_anything(m, n, offset, d):
+    q, k, v, d_o = make(2, m, n, 4, 2, d, seed=m)
+    q[:, :-offset] = NAN
+    d_o[:, :-offset] = INF
+    check(q, k, v, d_o, causal=True, offset=offset)
+    v[0, 1, 0, 2] = INF                             # nor does what they do not see reach them
+    k[1, 0, 1, 2] = NAN
+    b = block()
+    o, lse = b.attn_fwd(q, k, v, causal=True, offset=offset)
+    dq = b.attn_bwd(d_o, q, k, v, o, lse, causal=True, offset=offset)[0]
+    empty = slice(0, min(m, -offset))
+    assert bool((o[:, empty] == 0).all()) and bool((lse[:, :, empty] == -INF).all()) and bool((dq[:, empty] == 0).all())
+
+
+def test_rows_and_keys_that_are_there_do_not_reach_the_others():
+    """A value of infinity within a sample's lengths, beside queries and keys
+    past them and a range of keys that a row does not see."""
+    q, k, v, d_o = make(3, 150, 200, 2, 2, 64, seed=8)
+    v[:, 5, 0, 9] = INF
+    kn, qn = torch.tensor([200, 80, 6], dtype=torch.int32, device="cuda"), torch.tensor([150, 0, 3], dtype=torch.int32, device="cuda")
+    check(q, k, v, d_o, q_lens=qn, k_lens=kn)
+    q, k, v, d_o = make(1, 3, 4000, 2, 1, 128, seed=9)
+    k[0, 3000:], v[0, 3000:] = NAN, NAN
+    check(q, k, v, d_o, causal=True, offset=1000)
+    check(q, k, v, d_o, k_lens=torch.tensor([2999], dtype=torch.int32, device="cuda"))
+
+
+def test_how_far_a_key_reaches_over_the_border():
+    """A key and value that are not finite, and a d_o, may reach rows (keys)
+    on the border's other side that are less than 128 positions away."""
+    m, at = 700, 400
+    b = block()
+    q, k, v, d_o = make(1, m, m, 2, 2, 64, seed=3)
+    o, lse = b.attn_fwd(q, k, v, causal=True)
+    want = b.attn_bwd(d_o, q, k, v, o, lse, causal=True)
+    k1, v1 = k.clone(), v.clone()
+    k1[0, at], v1[0, at] = NAN, NAN
+    o1, lse1 = b.attn_fwd(q, k1, v1, causal=True)
+    assert bool(torch.isnan(o1[:, at:]).all()) and torch.equal(lse1[:, :, :at], lse[:, :, :at])
+    assert torch.equal(o1[:, :at - 127], o[:, :at - 127])
+    got = b.attn_bwd(d_o, q, k1, v1, o1, lse1, causal=True)
+    assert torch.equal(got[0][:, :at - 127], want[0][:, :at - 127])
+    g1 = d_o.clone()
+    g1[0, at] = NAN
+    got = b.attn_bwd(g1, q, k, v, o, lse, causal=True)
+    assert torch.equal(got[0][:, :at], want[0][:, :at])
+    for x, y in zip(got[1:], want[1:]):
+        assert bool(torch.isnan(x[:, :at + 1]).all()) and torch.equal(x[:, at + 128:], y[:, at + 128:])
