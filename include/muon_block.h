@@ -55,7 +55,8 @@ const char* muon_block_last_error(void);
 typedef enum muon_norm_kind { MUON_NORM_NONE = 0, MUON_NORM_RMS = 1, MUON_NORM_LAYER = 2 } muon_norm_kind;
 
 typedef struct muon_norm_args {
-  int64_t rows, cols;     /* rows >= 0; 1 <= cols <= 16384                    */
+  int64_t rows, cols;     /* 0 <= rows < 2^31; 1 <= cols <= 16384; rows /
+                           * group_rows times cols / 64 (up) below 2^31       */
   int64_t group_rows;     /* rows of one sample; divides rows                 */
   int32_t post_kind;      /* muon_norm_kind of h                              */
   int32_t pre_kind;       /* muon_norm_kind of resid_out                      */
@@ -104,7 +105,9 @@ typedef struct muon_heads {
 } muon_heads;
 
 typedef struct muon_attn_args {
-  int64_t batch, q_len, k_len;    /* >= 0                                     */
+  int64_t batch, q_len, k_len;    /* >= 0; below 2^24 batch x kv_heads, and
+                                   * those x q_len x (heads / kv_heads) / 128
+                                   * (up); backward below 2^23 x k_len / 256  */
   int32_t heads, kv_heads;        /* kv_heads divides heads                   */
   int32_t dim;                    /* multiple of 8, 8 .. 128                  */
   int32_t causal;                 /* 0 or 1                                   */
@@ -140,7 +143,9 @@ muon_status muon_attn_bwd(const muon_attn_args* args, void* workspace, size_t wo
 typedef enum muon_act { MUON_ACT_SILU = 0, MUON_ACT_GELU_TANH = 1 } muon_act;
 
 typedef struct muon_ffn_args {
-  int64_t rows, cols, hidden;     /* rows >= 0; cols, hidden multiples of 8   */
+  int64_t rows, cols, hidden;     /* rows >= 0; cols, hidden multiples of 8,
+                                   * up to 2^20; below 15 x 2^20 tiles of 128
+                                   * rows and 64 hidden or 128 other columns  */
   int32_t act;                    /* muon_act                                 */
   int32_t reserved;               /* must be 0                                */
   muon_tensor x, y;               /* rows x cols, BF16                        */

@@ -81,7 +81,8 @@ muon_status norm_dims(const muon_norm_args* a) {
     return fail(MUON_E_ARG, "unknown norm kind");
   if (!std::isfinite(a->alpha) || !(a->eps >= 0.f) || !std::isfinite(a->eps))
     return fail(MUON_E_ARG, "alpha and eps must be finite, eps >= 0");
-  // one workgroup per 64 columns and group in the sums' launch, per row in the forward's
+  // 32-bit numbers of workgroups, one per 64 columns and group in the sums'
+  // launch, per row in the forward's
   if (a->rows / a->group_rows * ((a->cols + 63) / 64) > 0x7fffffff || a->rows > 0x7fffffff)
     return fail(MUON_E_SHAPE, "too many rows for one call");
   return MUON_OK;
@@ -142,7 +143,7 @@ size_t norm_bwd_bytes(const muon_norm_args* a) {
 }
 
 // ---- attention ----------------------------------------------------------------
-muon_status attn_dims(const muon_attn_args* a) {
+muon_status attn_dims(const muon_attn_args* a, bool backward) {
   if (!a) return fail(MUON_E_ARG, "args is NULL");
   if (a->batch < 0 || a->q_len < 0 || a->k_len < 0 || a->heads < 1 || a->kv_heads < 1 || a->heads % a->kv_heads)
     return fail(MUON_E_SHAPE, "batch %lld, lengths %lld and %lld, heads %d over %d", (long long)a->batch,
@@ -150,11 +151,13 @@ muon_status attn_dims(const muon_attn_args* a) {
   if (a->dim < 8 || a->dim > 128 || a->dim % 8) return fail(MUON_E_SHAPE, "dim %d: a multiple of 8 up to 128", a->dim);
   if ((a->causal != 0 && a->causal != 1) || a->reserved != 0) return fail(MUON_E_ARG, "causal is 0 or 1, reserved 0");
   if (!std::isfinite(a->scale) || !(a->scale > 0.f)) return fail(MUON_E_ARG, "scale must be positive and finite");
-  // 32-bit row, key and workgroup numbers
-  const int64_t group = a->heads / a->kv_heads, top = 1 << 30;
-  if (a->batch > 1 << 20 || a->q_len > top || a->k_len > top || a->q_len * group > top ||
-      ((a->q_len * group + 127) / 128 + 1) * a->batch * a->kv_heads > top / 512 * 64 ||
-      ((a->k_len + 127) / 128) * a->batch * a->kv_heads > top)
+  // 32-bit row and key numbers, and fewer than 2^32 threads to a launch: 256 per
+  // 128 rows, backward 512 per 256 keys.  (Launches whose keys or key blocks are
+  // divided have far fewer.)
+  const int64_t group = a->heads / a->kv_heads, top = 1 << 30, most = 1 << 24;
+  const int64_t pairs = a->batch > 1 << 20 ? most : a->batch * a->kv_heads;
+  if (pairs >= most || a->q_len > top || a->k_len > top || a->q_len * group > top ||
+      (a->q_len * group + 127) / 128 * pairs >= most || (backward && (a->k_len + 255) / 256 * pairs >= most / 2))
     return fail(MUON_E_SHAPE, "too many rows for one call");
   return MUON_OK;
 }
@@ -202,10 +205,15 @@ muon_status ffn_dims(const muon_ffn_args* a) {
   if (!a) return fail(MUON_E_ARG, "args is NULL");
   const int64_t most = 1 << 20;    // 2 hidden and a column tile stay within kMaxLd
   if (a->rows < 0 || a->rows > (1 << 30) || a->cols < 8 || a->hidden < 8 || a->cols % 8 || a->hidden % 8 ||
-      a->cols > most || a->hidden > most ||
-      ((a->rows + 127) / 128) * ((a->cols > a->hidden ? a->cols : 2 * a->hidden) / 64 + 1) > (1 << 30))
+      a->cols > most || a->hidden > most)
     return fail(MUON_E_SHAPE, "rows %lld, cols %lld, hidden %lld: cols and hidden are multiples of 8 up to 2^20",
                 (long long)a->rows, (long long)a->cols, (long long)a->hidden);
+  // fewer than 2^32 threads to a launch: 256 per tile, of 128 x 128 results at
+  // least (64 hidden columns of g and u); divided tiles add 2^20 at most
+  const int64_t tiles = 15 << 20, rb = (a->rows + 127) / 128, cb = (a->cols + 127) / 128, hb = (a->hidden + 63) / 64;
+  if (rb * hb >= tiles || rb * cb + 2 * hb * cb >= tiles)
+    return fail(MUON_E_SHAPE, "too many rows or columns for one call: %lld x %lld x %lld", (long long)a->rows,
+                (long long)a->cols, (long long)a->hidden);
   if ((a->act != MUON_ACT_SILU && a->act != MUON_ACT_GELU_TANH) || a->reserved != 0)
     return fail(MUON_E_ARG, "unknown act, or reserved is not 0");
   return MUON_OK;
@@ -324,13 +332,13 @@ muon_status muon_norm_bwd(const muon_norm_args* a, void* ws, size_t ws_bytes, vo
 
 muon_status muon_attn_fwd_workspace(const muon_attn_args* a, size_t* bytes) {
   if (!bytes) return fail(MUON_E_ARG, "bytes is NULL");
-  CHECK(attn_dims(a));
+  CHECK(attn_dims(a, false));
   *bytes = attn_fwd_bytes(attn_dev(a));
   return MUON_OK;
 }
 
 muon_status muon_attn_fwd(const muon_attn_args* a, void* ws, size_t ws_bytes, void* hip_stream) {
-  CHECK(attn_dims(a));
+  CHECK(attn_dims(a, false));
   if (a->batch == 0 || a->q_len == 0) return MUON_OK;
   CHECK(attn_heads("q", a->q));
   if (a->k_len > 0) {
@@ -350,13 +358,13 @@ muon_status muon_attn_fwd(const muon_attn_args* a, void* ws, size_t ws_bytes, vo
 
 muon_status muon_attn_bwd_workspace(const muon_attn_args* a, size_t* bytes) {
   if (!bytes) return fail(MUON_E_ARG, "bytes is NULL");
-  CHECK(attn_dims(a));
+  CHECK(attn_dims(a, true));
   *bytes = attn_bwd_bytes(attn_dev(a));
   return MUON_OK;
 }
 
 muon_status muon_attn_bwd(const muon_attn_args* a, void* ws, size_t ws_bytes, void* hip_stream) {
-  CHECK(attn_dims(a));
+  CHECK(attn_dims(a, true));
   if (a->batch == 0 || (a->q_len == 0 && a->k_len == 0)) return MUON_OK;
   if (a->q_len > 0) {
     CHECK(attn_heads("q", a->q));

@@ -575,7 +575,9 @@ Plan plan_with(const ProdArgs& g, int bt, bool gate) {
   const int stages = stages_of(g.p[0]), tiles = q.p[0].tiles, rows = g.p[0].m;
   const int rem = g.count > 1 ? tiles : tiles % slots, whole = g.count > 1 ? 0 : tiles / slots;
   const double part_mb = double(bt) * (rows < bt ? (rows + 15) / 16 * 16 : bt) * 4e-6, tile = stages * stage_us + tile_us;
-  for (int n = 1; n == 1 || (rem > 0 && n <= stages / 4 && n <= (g.count > 1 ? 32 : slots / rem)); ++n) {
+  // (at most 2^20 ranges: a launch's workgroups are counted without them)
+  for (int n = 1; n == 1 || (rem > 0 && n <= stages / 4 && n <= (g.count > 1 ? std::min(32, (1 << 20) / rem) : slots / rem));
+       ++n) {
     const int per = ((stages + n - 1) / n + 1) & ~1, got = (stages + per - 1) / per;   // whole units
     const double one = per * stage_us + tile_us, join = got > 1 ? 4 + 2 * rem * got * part_mb / 4.5 : 0;
     double us;

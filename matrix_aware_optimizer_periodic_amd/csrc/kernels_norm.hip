@@ -96,13 +96,14 @@ __device__ __forceinline__ void row_stats(const float (&v)[NC][VEC], int kind, i
   rstd = 1.0f / sqrtf(fmaf(q[0], inv, eps));
 }
 
-// One row per wave (WAVE: four rows per workgroup) or per workgroup.
+// One row per wave (WAVE: four rows per workgroup) or per workgroup.  Every
+// kernel's first workgroup is `from`, for grids that go out in pieces.
 template <typename TR, typename TH, int VEC, int NC, bool WAVE>
-__global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_fwd_kernel(NormDev a) {
+__global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_fwd_kernel(NormDev a, int64_t from) {
   __shared__ float red[2][2][kMaxWaves];
   const int tid = WAVE ? threadIdx.x & 63 : threadIdx.x;
   const int nt = WAVE ? 64 : blockDim.x;
-  const int64_t row = WAVE ? int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  const int64_t row = WAVE ? (from + blockIdx.x) * 4 + (threadIdx.x >> 6) : from + blockIdx.x;
   if (row >= a.rows) return;          // WAVE: whole waves, no barrier follows
   int phase = 0;
   const int64_t grp = row / a.group_rows;
@@ -202,11 +203,12 @@ struct Raw<T, 1> {
 // read while this one is worked on; that takes registers which a workgroup of
 // more than 640 threads does not have.
 template <typename TR, typename TH, int VEC, int NC, bool WAVE, bool AHEAD>
-__global__ __launch_bounds__(WAVE ? 256 : AHEAD ? 640 : 1024) void norm_bwd_kernel(NormDev a, int64_t shares) {
+__global__ __launch_bounds__(WAVE ? 256 : AHEAD ? 640 : 1024) void norm_bwd_kernel(NormDev a, int64_t from,
+                                                                                   int64_t shares) {
   __shared__ float red[2][2][kMaxWaves];
   const int tid = WAVE ? threadIdx.x & 63 : threadIdx.x;
   const int nt = WAVE ? 64 : blockDim.x;
-  const int64_t share = WAVE ? int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  const int64_t share = WAVE ? (from + blockIdx.x) * 4 + (threadIdx.x >> 6) : from + blockIdx.x;
   if (share >= shares) return;
   int phase = 0;
   const int64_t grp = share / a.splits;
@@ -365,11 +367,12 @@ __device__ __forceinline__ void col_sums(const float* p, int64_t n, int64_t stri
   }
 }
 
-__global__ __launch_bounds__(1024) void norm_sums_kernel(NormDev a, int64_t groups) {
+__global__ __launch_bounds__(1024) void norm_sums_kernel(NormDev a, int64_t from, int64_t groups) {
   __shared__ float red[kNormSums][16][64];
   const int tiles = (a.cols + 63) / 64;
-  const int64_t grp = blockIdx.x / unsigned(tiles);
-  const int col = int(blockIdx.x % unsigned(tiles)) * 64 + (threadIdx.x & 63);
+  const unsigned item = unsigned(from) + blockIdx.x;      // below 2^31
+  const int64_t grp = item / unsigned(tiles);
+  const int col = int(item % unsigned(tiles)) * 64 + (threadIdx.x & 63);
   float s[kNormSums];
   col_sums<kNormSums>(a.part + grp * a.splits * kNormSums * int64_t(a.cols), a.splits, kNormSums * int64_t(a.cols),
                       a.cols, col, a.cols, s, red);
@@ -428,6 +431,19 @@ Shape shape_of(int cols, bool vec) {
 #define BY_TYPES(K)                                                                                 \
   (a.resid_out.dt ? (hdt ? K(uint16_t, uint16_t) : K(uint16_t, float)) : (hdt ? K(float, uint16_t) : K(float, float)))
 
+// A launch has fewer than 2^32 threads: a larger grid goes out in pieces.
+// launch(first workgroup, workgroups)
+template <typename F>
+hipError_t in_pieces(int64_t workgroups, int threads, F launch) {
+  const int64_t most = 0xffffffffll / threads;
+  for (int64_t from = 0; from < workgroups; from += most) {
+    launch(from, dim3(unsigned(workgroups - from < most ? workgroups - from : most)));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 }  // namespace
 
 int norm_splits(int64_t groups, int64_t group_rows, int cols) {
@@ -446,9 +462,10 @@ hipError_t launch_norm_fwd(hipStream_t s, const NormDev& a, bool vec) {
   const Shape sh = shape_of(a.cols, vec);
   const int hdt = a.h.p ? a.h.dt : a.y.dt;
   auto* k = BY_TYPES(FWD_KERNEL);
-  const int64_t grid = sh.wave ? (a.rows + 3) / 4 : a.rows;
-  hipLaunchKernelGGL(k, dim3(unsigned(grid)), dim3(sh.wave ? 256 : sh.threads), 0, s, a);
-  return hipGetLastError();
+  const int threads = sh.wave ? 256 : sh.threads;
+  return in_pieces(sh.wave ? (a.rows + 3) / 4 : a.rows, threads, [&](int64_t from, dim3 grid) {
+    hipLaunchKernelGGL(k, grid, dim3(threads), 0, s, a, from);
+  });
 }
 
 hipError_t launch_norm_bwd(hipStream_t s, const NormDev& a, bool vec, bool sums) {
@@ -456,13 +473,15 @@ hipError_t launch_norm_bwd(hipStream_t s, const NormDev& a, bool vec, bool sums)
   const int hdt = a.h.p ? a.h.dt : a.d_y.dt;
   const int64_t groups = a.rows / a.group_rows, shares = groups * a.splits;
   auto* k = BY_TYPES(BWD_KERNEL);
-  const int64_t grid = sh.wave ? (shares + 3) / 4 : shares;
-  hipLaunchKernelGGL(k, dim3(unsigned(grid)), dim3(sh.wave ? 256 : sh.threads), 0, s, a, shares);
-  hipError_t e = hipGetLastError();
+  const int threads = sh.wave ? 256 : sh.threads;
+  hipError_t e = in_pieces(sh.wave ? (shares + 3) / 4 : shares, threads, [&](int64_t from, dim3 grid) {
+    hipLaunchKernelGGL(k, grid, dim3(threads), 0, s, a, from, shares);
+  });
   if (e != hipSuccess || !sums) return e;
   const unsigned tiles = unsigned((a.cols + 63) / 64);
-  hipLaunchKernelGGL(norm_sums_kernel, dim3(unsigned(tiles * groups)), dim3(1024), 0, s, a, groups);
-  e = hipGetLastError();
+  e = in_pieces(tiles * groups, 1024, [&](int64_t from, dim3 grid) {
+    hipLaunchKernelGGL(norm_sums_kernel, grid, dim3(1024), 0, s, a, from, groups);
+  });
   if (e != hipSuccess || groups == 1 || !(a.d_pre_weight.p || a.d_post_weight.p)) return e;
   hipLaunchKernelGGL(norm_weights_kernel, dim3(tiles), dim3(1024), 0, s, a, groups);
   return hipGetLastError();
