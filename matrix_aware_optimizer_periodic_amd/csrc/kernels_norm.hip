@@ -67,6 +67,11 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[2][kMaxWaves
 template <int VEC>
 __device__ __forceinline__ int col_of(int c, int tid, int nthreads) { return (c * nthreads + tid) * VEC; }
 
+// The start of a row: with the row's number in scalar registers, so is this,
+// and a column takes one register as an offset where an address takes two.
+template <typename T>
+__device__ __forceinline__ T* row_of(const NormMat& m, int64_t row) { return static_cast<T*>(m.p) + row * m.ld; }
+
 // Mean and 1 / deviation of a row held in v (zeros past its end).
 template <int VEC, int NC, bool WAVE>
 __device__ __forceinline__ void row_stats(const float (&v)[NC][VEC], int kind, int cols, float inv, float eps,
@@ -200,8 +205,9 @@ struct Raw<T, 1> {
 
 // One share of one sample's rows per wave (WAVE: four shares per workgroup)
 // or per workgroup; share = group * splits + split.  AHEAD: the next row is
-// read while this one is worked on; that takes registers which a workgroup of
-// more than 640 threads does not have.
+// read while this one is worked on, in rows of up to 5120 columns, the widest
+// timed with it (4096 x 5120 fp32 stream, bf16 branch: 92 us; 4096 x 5128 without
+// it 106); up to 768 threads would have the registers.
 template <typename TR, typename TH, int VEC, int NC, bool WAVE, bool AHEAD>
 __global__ __launch_bounds__(WAVE ? 256 : AHEAD ? 640 : 1024) void norm_bwd_kernel(NormDev a, int64_t from,
                                                                                    int64_t shares) {
@@ -248,17 +254,19 @@ __global__ __launch_bounds__(WAVE ? 256 : AHEAD ? 640 : 1024) void norm_bwd_kern
   Raw<TH, VEC> ly[NC], lh[NC];
   f32x4_t lst;
   auto read = [&](int64_t row) {
+    const TR *px = row_of<TR>(a.resid_out, row), *pr = row_of<TR>(a.d_resid_out, row);
+    const TH *py = row_of<TH>(a.d_y, row), *ph = row_of<TH>(a.h, row);
     lst = *as_global(reinterpret_cast<const f32x4_t*>(a.stats + row * 4));
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int col = col_of<VEC>(c, tid, nt);
-      if (col >= a.cols) continue;
+      const unsigned col = unsigned(col_of<VEC>(c, tid, nt));
+      if (col >= unsigned(a.cols)) continue;
       if (have_y) {
-        lx[c].load(a.resid_out.p, row * a.resid_out.ld + col);
-        ly[c].load(a.d_y.p, row * a.d_y.ld + col);
+        lx[c].load(px, col);
+        ly[c].load(py, col);
       }
-      if (have_r) lr[c].load(a.d_resid_out.p, row * a.d_resid_out.ld + col);
-      if (have_h) lh[c].load(a.h.p, row * a.h.ld + col);
+      if (have_r) lr[c].load(pr, col);
+      if (have_h) lh[c].load(ph, col);
     }
   };
 #pragma unroll
@@ -302,9 +310,9 @@ __global__ __launch_bounds__(WAVE ? 256 : AHEAD ? 640 : 1024) void norm_bwd_kern
     float t[2] = {0.f, 0.f};
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int col = col_of<VEC>(c, tid, nt);
-      if (col >= a.cols) continue;
-      store_vals<TR, VEC>(a.d_resid.p, row * a.d_resid.ld + col, dr[c]);
+      const unsigned col = unsigned(col_of<VEC>(c, tid, nt));
+      if (col >= unsigned(a.cols)) continue;
+      store_vals<TR, VEC>(row_of<TR>(a.d_resid, row), col, dr[c]);
       if (have_h) {
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
@@ -322,11 +330,11 @@ __global__ __launch_bounds__(WAVE ? 256 : AHEAD ? 640 : 1024) void norm_bwd_kern
     t[1] *= npost;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int col = col_of<VEC>(c, tid, nt);
-      if (col >= a.cols) continue;
+      const unsigned col = unsigned(col_of<VEC>(c, tid, nt));
+      if (col >= unsigned(a.cols)) continue;
 #pragma unroll
       for (int k = 0; k < VEC; ++k) dr[c][k] = st[1] * (dr[c][k] - t[0] - h[c][k] * t[1]);
-      store_vals<TH, VEC>(a.d_h.p, row * a.d_h.ld + col, dr[c]);
+      store_vals<TH, VEC>(row_of<TH>(a.d_h, row), col, dr[c]);
     }
   }
   if (!a.part) return;
@@ -405,12 +413,15 @@ __global__ __launch_bounds__(1024) void norm_weights_kernel(NormDev a, int64_t g
 }
 
 // Threads per row and chunks per thread: eight columns per thread while a
-// row fits 1024 threads, single columns where a row is not whole aligned
-// groups of eight.
+// row fits 1024 threads, single columns (four, eight or sixteen) where a row is
+// not whole aligned groups of eight.  The backward pass holds seven values per
+// column: sixteen columns, in any form, spill some 250 registers and run at 2.1 -
+// 2.5 TB/s in whole groups, 0.9 in single columns (4096 x 10001: 789 us; x 16384:
+// 476), eight single ones none (4096 x 5001: 203 us, 963 with sixteen).
 struct Shape { int threads; int nc; bool wave; };
 Shape shape_of(int cols, bool vec) {
   const int per = (cols + (vec ? 8 : 1) - 1) / (vec ? 8 : 1);   // thread columns of a row
-  const int nc = vec ? (per <= 1024 ? 1 : 2) : (per <= 4096 ? 4 : 16);
+  const int nc = vec ? (per <= 1024 ? 1 : 2) : per <= 4096 ? 4 : per <= 8192 ? 8 : 16;
   const int threads = ((per + nc - 1) / nc + 63) / 64 * 64;
   return {threads, nc, threads == 64 && nc == (vec ? 1 : 4)};
 }
@@ -419,7 +430,7 @@ Shape shape_of(int cols, bool vec) {
   (vec ? (sh.wave ? norm_fwd_kernel<TR, TH, 8, 1, true> : sh.nc == 1 ? norm_fwd_kernel<TR, TH, 8, 1, false>     \
                                                                      : norm_fwd_kernel<TR, TH, 8, 2, false>)    \
        : (sh.wave ? norm_fwd_kernel<TR, TH, 1, 4, true> : sh.nc == 4 ? norm_fwd_kernel<TR, TH, 1, 4, false>     \
-                                                                     : norm_fwd_kernel<TR, TH, 1, 16, false>))
+          : sh.nc == 8 ? norm_fwd_kernel<TR, TH, 1, 8, false> : norm_fwd_kernel<TR, TH, 1, 16, false>))
 #define BWD_KERNEL(TR, TH)                                                                                   \
   (vec ? (sh.wave           ? norm_bwd_kernel<TR, TH, 8, 1, true, true>                                         \
           : sh.nc == 2        ? norm_bwd_kernel<TR, TH, 8, 2, false, false>                                     \
@@ -427,6 +438,7 @@ Shape shape_of(int cols, bool vec) {
                               : norm_bwd_kernel<TR, TH, 8, 1, false, false>)                                    \
        : (sh.wave      ? norm_bwd_kernel<TR, TH, 1, 4, true, false>                                             \
           : sh.nc == 4 ? norm_bwd_kernel<TR, TH, 1, 4, false, false>                                            \
+          : sh.nc == 8 ? norm_bwd_kernel<TR, TH, 1, 8, false, false>                                            \
                        : norm_bwd_kernel<TR, TH, 1, 16, false, false>))
 #define BY_TYPES(K)                                                                                 \
   (a.resid_out.dt ? (hdt ? K(uint16_t, uint16_t) : K(uint16_t, float)) : (hdt ? K(float, uint16_t) : K(float, float)))
