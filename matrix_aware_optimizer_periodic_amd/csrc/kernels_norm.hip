@@ -351,14 +351,16 @@ __global__ __launch_bounds__(WAVE ? 256 : AHEAD ? 640 : 1024) void norm_bwd_kern
 
 // Sums over `n` rows, `stride` floats apart, of 64 columns per workgroup:
 // 16 threads per column take every 16th row, then their sums are added in
-// order.  The result is in the threads of the first wave.
-template <int N>
+// order.  The result is in the threads of the first wave.  UNROLL rows are read
+// ahead of their additions.
+template <int N, int UNROLL>
 __device__ __forceinline__ void col_sums(const float* p, int64_t n, int64_t stride, int64_t next, int col, int cols,
                                          float (&v)[N], float (*red)[16][64]) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
 #pragma unroll
   for (int k = 0; k < N; ++k) v[k] = 0.f;
   if (col < cols) {
+#pragma unroll UNROLL
     for (int64_t i = w; i < n; i += 16)
 #pragma unroll
       for (int k = 0; k < N; ++k) v[k] += *as_global(p + i * stride + k * next + col);
@@ -375,16 +377,27 @@ __device__ __forceinline__ void col_sums(const float* p, int64_t n, int64_t stri
   }
 }
 
-__global__ __launch_bounds__(1024) void norm_sums_kernel(NormDev a, int64_t from, int64_t groups) {
-  __shared__ float red[kNormSums][16][64];
+// FEW: a sample has no more shares than that workgroup has waves, and a wave
+// adds one sample's 64 columns by itself, in the same order.
+template <bool FEW>
+__global__ __launch_bounds__(FEW ? 256 : 1024) void norm_sums_kernel(NormDev a, int64_t from, int64_t groups) {
   const int tiles = (a.cols + 63) / 64;
-  const unsigned item = unsigned(from) + blockIdx.x;      // below 2^31
-  const int64_t grp = item / unsigned(tiles);
-  const int col = int(item % unsigned(tiles)) * 64 + (threadIdx.x & 63);
-  float s[kNormSums];
-  col_sums<kNormSums>(a.part + grp * a.splits * kNormSums * int64_t(a.cols), a.splits, kNormSums * int64_t(a.cols),
-                      a.cols, col, a.cols, s, red);
-  if (threadIdx.x >= 64 || col >= a.cols) return;
+  const int64_t item = FEW ? (from + blockIdx.x) * 4 + (threadIdx.x >> 6) : from + blockIdx.x;   // below 2^31
+  if (FEW && item >= groups * tiles) return;
+  const int64_t grp = unsigned(item) / unsigned(tiles);
+  const int col = int(unsigned(item) % unsigned(tiles)) * 64 + (threadIdx.x & 63);
+  const float* part = a.part + grp * a.splits * kNormSums * int64_t(a.cols);
+  float s[kNormSums] = {0.f, 0.f, 0.f};
+  if constexpr (FEW) {
+    if (col >= a.cols) return;
+    for (int i = 0; i < a.splits; ++i)
+#pragma unroll
+      for (int k = 0; k < kNormSums; ++k) s[k] += *as_global(part + (i * kNormSums + k) * int64_t(a.cols) + col);
+  } else {
+    __shared__ float red[kNormSums][16][64];
+    col_sums<kNormSums, 1>(part, a.splits, kNormSums * int64_t(a.cols), a.cols, col, a.cols, s, red);
+    if (threadIdx.x >= 64 || col >= a.cols) return;
+  }
   const float wp = a.pre_weight.p ? load_any1(a.pre_weight.p, a.pre_weight.dt, col) : 1.f;
   const float wo = a.post_weight.p ? load_any1(a.post_weight.p, a.post_weight.dt, col) : 1.f;
   if (a.d_scale.p) store_any1(a.d_scale.p, a.d_scale.dt, grp * a.d_scale.ld + col, wp * s[0]);
@@ -406,7 +419,7 @@ __global__ __launch_bounds__(1024) void norm_weights_kernel(NormDev a, int64_t g
   __shared__ float red[2][16][64];
   const int col = int(blockIdx.x) * 64 + (threadIdx.x & 63);
   float s[2];
-  col_sums<2>(a.gsum, groups, 2 * int64_t(a.cols), a.cols, col, a.cols, s, red);
+  col_sums<2, 8>(a.gsum, groups, 2 * int64_t(a.cols), a.cols, col, a.cols, s, red);
   if (threadIdx.x >= 64 || col >= a.cols) return;
   if (a.d_pre_weight.p) store_any1(a.d_pre_weight.p, a.d_pre_weight.dt, col, s[0]);
   if (a.d_post_weight.p) store_any1(a.d_post_weight.p, a.d_post_weight.dt, col, s[1]);
@@ -442,6 +455,13 @@ Shape shape_of(int cols, bool vec) {
                        : norm_bwd_kernel<TR, TH, 1, 16, false, false>))
 #define BY_TYPES(K)                                                                                 \
   (a.resid_out.dt ? (hdt ? K(uint16_t, uint16_t) : K(uint16_t, float)) : (hdt ? K(float, uint16_t) : K(float, float)))
+
+// Whether a wave or a workgroup adds a sample's shares: a workgroup's 16 waves
+// read one share each where there are up to 16, so many samples wait for
+// workgroups (30000 samples of one row of 512: 818 us, 178 a wave each; 300 of 13
+// shares 11.9 and 7.6), while a wave reads them one after the other (16 samples
+// of 16 shares, 1024 columns: 8.4 us for 4.0; 64 of 8 take 6.0 both ways).
+bool sums_by_wave(int splits, int64_t items) { return splits <= 16 && items >= 128 * splits; }
 
 // A launch has fewer than 2^32 threads: a larger grid goes out in pieces.
 // launch(first workgroup, workgroups)
@@ -491,8 +511,11 @@ hipError_t launch_norm_bwd(hipStream_t s, const NormDev& a, bool vec, bool sums)
   });
   if (e != hipSuccess || !sums) return e;
   const unsigned tiles = unsigned((a.cols + 63) / 64);
-  e = in_pieces(tiles * groups, 1024, [&](int64_t from, dim3 grid) {
-    hipLaunchKernelGGL(norm_sums_kernel, grid, dim3(1024), 0, s, a, from, groups);
+  const bool few = sums_by_wave(a.splits, tiles * groups);
+  auto* sum = few ? norm_sums_kernel<true> : norm_sums_kernel<false>;
+  const int sum_threads = few ? 256 : 1024;
+  e = in_pieces(few ? (tiles * groups + 3) / 4 : tiles * groups, sum_threads, [&](int64_t from, dim3 grid) {
+    hipLaunchKernelGGL(sum, grid, dim3(sum_threads), 0, s, a, from, groups);
   });
   if (e != hipSuccess || groups == 1 || !(a.d_pre_weight.p || a.d_post_weight.p)) return e;
   hipLaunchKernelGGL(norm_weights_kernel, dim3(tiles), dim3(1024), 0, s, a, groups);

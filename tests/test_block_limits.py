@@ -93,9 +93,9 @@ def test_norm_rows_in_pieces(rows, cols, per):
 
 @pytest.mark.gpu
 def test_norm_sums_in_pieces():
-    """Modulation of its own for each of 66000 rows of 4096 columns: 64
-    workgroups of 1024 threads to a row's sums, 2^32 threads from 65536 rows
-    on.  dscale = dy xhat and dshift = dy of each row, dw their sum."""
+    """Modulation of its own for each of 66000 rows of 4096 columns: a workgroup
+    of 1024 threads to each 64 columns of a row's sums would be more than 2^32
+    threads.  dscale = dy xhat and dshift = dy of each row, dw their sum."""
     from matrix_aware_optimizer_periodic_amd import block as b
     rows, cols = 66_000, 4096
     gen = torch.Generator(device="cuda").manual_seed(1)
@@ -116,3 +116,19 @@ def test_norm_sums_in_pieces():
     # off by 2^-24 of a partial sum of random sign
     exact = sum((dy[i:i + 6000].double() * y[i:i + 6000].double()).sum((0, 1)) for i in range(0, rows, 6000))
     assert bool(((d["pre_weight"].double() - exact).abs() <= 4125 * 2.0 ** -24 * exact.abs().max()).all())
+
+
+@pytest.mark.gpu
+def test_norm_sums_of_very_many_samples():
+    """A wave to each row's sums: past 2^32 threads from 2^26 rows on."""
+    from matrix_aware_optimizer_periodic_amd import block as b
+    rows, cols = (1 << 26) + 77, 8
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.empty(rows, 1, cols, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    scale = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    _, _, stats = b.norm_fwd(x, scale=scale, pre="rms")
+    d = b.norm_bwd(None, x, x, None, stats, scale=scale, pre="rms")
+    for at in (0, rows // 2, 4 * (0xffffffff // 256) - 20, rows - 40):
+        some = slice(at, at + 40)
+        want = b.norm_bwd(None, x[some], x[some], None, stats[some], scale=scale[some], pre="rms")
+        assert torch.equal(d["scale"][some], want["scale"]) and torch.equal(d["resid"][some], want["resid"]), at

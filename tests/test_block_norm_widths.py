@@ -53,3 +53,13 @@ def test_backward_rows_up_to_8192_columns_stay_in_registers(tmp_path):
     # the widest rows of each form: 64 threads x 4, 1024 x 4, 1024 x 8 and 1024 x 8 in one chunk
     for form in ((1, 4), (1, 8), (8, 1)):
         assert found[form] <= 16, (form, found)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("samples,rows,cols", [(300, 1, 520), (2000, 3, 264), (40, 130, 1000), (129, 8, 64), (127, 9, 64),
+                                               (3, 128, 257), (70, 100, 2048)])
+def test_many_samples_of_few_rows(samples, rows, cols):
+    """Modulation that changes every few rows: the column sums of a sample by
+    one wave and by a workgroup, on both sides of what chooses between them."""
+    from test_block_norm import check, make
+    check(make(samples, rows, cols, F32, BF16, F32, seed=samples), "rms", "layer", 0.5)
