@@ -27,11 +27,12 @@
 // key head, the heads of one query next to each other: grouped heads and few
 // queries share the key tiles of one workgroup.
 //
-// Measured on one MI355X (a large library product runs at 1460 TFLOP/s), head
-// size 128: forward 156 us at 16 x 1024, 16 heads (880 TFLOP/s), 985 us at 2 x
-// 8192 (1117); dq 136 us and dk, dv 204 us at 4 x 1024, 40 heads (948 and 842
-// on the products they form), 1230 TFLOP/s for both at 16384; one query of 4 x
-// 32 heads over 8191 keys of 8 24 us (134 MB, 5.5 TB/s) and 5 us for the join.
+// Measured on one MI355X (a large library product runs at 1460 TFLOP/s), medians
+// of twelve calls, head size 128: forward 164 us at 16 x 1024, 16 heads (836
+// TFLOP/s), 1018 us at 2 x 8192 (1080); dq 153 us and dk, dv 243 us at 4 x 1024,
+// 40 heads (845 and 708 on the products they form; 138 and 203 us at best), 1213
+// TFLOP/s for both at 16384; one query of 4 x 32 heads over 8191 keys of 8 25 us
+// (134 MB, 5.3 TB/s) and 4.4 us for the join.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -281,9 +282,10 @@ __device__ __forceinline__ int seen_most(const AttnDev& a, const Rows& r) {
 // rows, which bring in half as much, measured 5% slower (the waves meet at
 // every tile), and what a longer way between asking for a tile and using it, or
 // several row blocks per workgroup, could hide measured nothing.  Up to 64 dims
-// three workgroups fit (168 registers, one of them spilled): 98 us against 107
-// for 16 samples of 1024 queries and keys with 16 heads of 64, 591 against 619
-// for 2 of 8192.  The dq kernel gains 1% at most from that, with four spilled.
+// three workgroups fit (168 registers, one of them spilled): calls of 98 us
+// against 107 for 16 samples of 1024 queries and keys with 16 heads of 64, 591
+// against 619 for 2 of 8192 (the kernel alone: 89 and 595).  The dq kernel gains
+// 1% at most from that, with four spilled.
 template <int DB, bool SPLIT>
 __global__ __launch_bounds__(256, DB <= 2 ? 3 : 2) void attn_fwd_kernel(AttnDev a, unsigned items) {
   using G = Geo<DB>;
@@ -666,8 +668,8 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnDev a, unsigned ite
 // heads of the group and tiles of 64 queries, 32 at a time: s = q k^T,
 // dp = do v^T (a lane has one key), then dv^T += do^T p, dk^T += q^T ds.
 // The accumulators (2 x 32 keys x dim) and k take 160 of the 256 registers at
-// 128 dims; with v there too 64 registers spilled (427 us where this takes
-// 204), and 64 keys per wave in 512 registers, one wave per SIMD, took 295: the
+// 128 dims; with v there too 64 registers spilled (427 us where this took
+// 206), and 64 keys per wave in 512 registers, one wave per SIMD, took 295: the
 // compiler then puts every product's result into accumulation registers and
 // moves the scores back and forth.  256 keys share a tile, since a CU takes in
 // only some 25 bytes per cycle on the way into LDS.

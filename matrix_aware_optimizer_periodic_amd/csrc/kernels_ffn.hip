@@ -21,11 +21,11 @@
 // weights below.  Roundings to bf16: g and u as stored, h and dg, du as the
 // next product's operands, and the results.
 //
-// Measured on one MI355X (a large library product runs at 1460 TFLOP/s): 4096
-// rows, 2048 x 8192, gate and up 250 - 264 us (1040 - 1100 TFLOP/s), down
-// 111 - 116 + 14 us; 4096 rows, 5120 x 20480, dh 870 - 907 us (950 - 990; 160 us
-// of it would take its epilogue's 0.84 GB alone), dx and the weights' gradients
-// 3300 - 3430 us (1250 - 1300).
+// Measured on one MI355X (a large library product runs at 1460 TFLOP/s), medians
+// of twelve calls over several cards: 4096 rows, 2048 x 8192, gate and up 255 -
+// 284 us (970 - 1080 TFLOP/s), down 118 - 124 + 14 us; 4096 rows, 5120 x 20480,
+// dh 872 - 904 us (950 - 985; 160 us of it would take its epilogue's 0.84 GB
+// alone), dx and the weights' gradients 3415 - 3450 us (1245 - 1258).
 #include <algorithm>
 #include <type_traits>
 

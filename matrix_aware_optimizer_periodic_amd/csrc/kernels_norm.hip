@@ -27,8 +27,8 @@
 //
 // Measured on one MI355X, where a large copy moves 5.1 TB/s: forward 16384 x
 // 2048, fp32 stream and bf16 branch, modulated, 79 us (403 MB, 5.1 TB/s);
-// backward 8192 x 5120 with every gradient 157 us for the rows (756 MB, 4.8
-// TB/s) and 7 + 5 us for the sums; seven rows of 1001 columns 5.5 us.
+// backward 8192 x 5120 with every gradient 156 us for the rows (756 MB, 4.8
+// TB/s) and 7.5 + 4.7 us for the sums; seven rows of 1001 columns 5.6 us.
 #include <type_traits>
 
 #include "block_device.h"
