@@ -112,7 +112,7 @@ typedef struct muon_attn_args {
   int32_t dim;                    /* multiple of 8, 8 .. 128                  */
   int32_t causal;                 /* 0 or 1                                   */
   int64_t offset;                 /* causal border: j <= i + offset           */
-  float scale;
+  float scale;                    /* finite, above 0                          */
   int32_t reserved;               /* must be 0                                */
   const int32_t* q_lens;          /* batch device integers, 0 .. q_len (values
                                    * outside are taken as the nearer end), or

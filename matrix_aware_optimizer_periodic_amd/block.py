@@ -304,7 +304,7 @@ def attn_fwd(q, k, v, *, causal: bool = False, offset: int = 0, q_lens=None, k_l
 
     q_lens, k_lens: int32 (batch,) on the GPU, how many of a sample's queries
     and keys are there.  causal: query i sees key j for j <= i + offset.
-    scale: dim ** -0.5 where None.  Returns o (batch, q_len, heads, dim) bf16
+    scale: above 0, dim ** -0.5 where None.  Returns o (batch, q_len, heads, dim) bf16
     and lse (batch, heads, q_len) fp32; a query that sees no key has o = 0 and
     lse = -inf.  What lies past a length, and keys that no query sees, may hold
     anything."""
