@@ -1,7 +1,8 @@
 /*
  * muon_block.h - C ABI of the transformer-block operators for gfx950 that
  * produce the gradients muon_step consumes: the fused residual norm, softmax
- * attention and the gated feed-forward block, each forward and backward.
+ * attention, the gated feed-forward block, linear layers with their epilogue,
+ * rotary positions and dropout, each forward and backward.
  *
  * All entries are stateless.  A call validates its arguments on the host,
  * enqueues kernels on the given stream and returns; nothing is allocated,
@@ -140,13 +141,13 @@ muon_status muon_attn_bwd(const muon_attn_args* args, void* workspace, size_t wo
  * to bf16 as operands), dx = dg w_gate + du w_up, and the weights' gradients
  * dg^T x, du^T x, dy^T (act(g) u) in the weights' own layout, F32 or BF16:
  * what muon_step takes. */
-typedef enum muon_act { MUON_ACT_SILU = 0, MUON_ACT_GELU_TANH = 1 } muon_act;
+typedef enum muon_act { MUON_ACT_SILU = 0, MUON_ACT_GELU_TANH = 1, MUON_ACT_NONE = 2 } muon_act;
 
 typedef struct muon_ffn_args {
   int64_t rows, cols, hidden;     /* rows >= 0; cols, hidden multiples of 8,
                                    * up to 2^20; below 15 x 2^20 tiles of 128
                                    * rows and 64 hidden or 128 other columns  */
-  int32_t act;                    /* muon_act                                 */
+  int32_t act;                    /* muon_act, not NONE                       */
   int32_t reserved;               /* must be 0                                */
   muon_tensor x, y;               /* rows x cols, BF16                        */
   muon_tensor w_gate, w_up;       /* hidden x cols, BF16                      */
@@ -160,6 +161,102 @@ muon_status muon_ffn_fwd_workspace(const muon_ffn_args* args, size_t* bytes);
 muon_status muon_ffn_fwd(const muon_ffn_args* args, void* workspace, size_t workspace_bytes, void* hip_stream);
 muon_status muon_ffn_bwd_workspace(const muon_ffn_args* args, size_t* bytes);
 muon_status muon_ffn_bwd(const muon_ffn_args* args, void* workspace, size_t workspace_bytes, void* hip_stream);
+
+/* ---- Dropout ----------------------------------------------------------------
+ * y = residual + keep x / (1 - p).  The mask is a function of (seed, offset) and
+ * of an element's number row * cols + column, whatever the strides, and is
+ * never stored: the gradient of x is the same call on d_y without a residual.
+ * Element i is dropped when word i % 4 of Philox4x32-10's block with key seed
+ * and counter (i / 4, offset), each number's low word first, is below p 2^32
+ * (rounded; the probability is off by 2^-33 at most).  A dropped element is 0
+ * whatever it held.  p 0 copies; p 1 drops everything. */
+typedef struct muon_rng {
+  uint64_t seed, offset;
+  const uint64_t* state;  /* two device integers that are read in their place
+                           * when the call runs (a graph's replays then differ
+                           * by what the caller writes there), or NULL        */
+} muon_rng;
+
+typedef struct muon_dropout_args {
+  int64_t rows, cols;     /* >= 0; rows x cols below 2^56                     */
+  double p;               /* 0 .. 1                                           */
+  muon_rng rng;
+  muon_tensor x;          /* rows x cols, F32 or BF16; row strides up to 2^40 */
+  muon_tensor residual;   /* may be absent; else of y's type                  */
+  muon_tensor y;          /* F32 or BF16                                      */
+} muon_dropout_args;
+
+muon_status muon_dropout(const muon_dropout_args* args, void* hip_stream);
+
+/* ---- Linear -----------------------------------------------------------------
+ * z = x weight^T + bias, y = residual + drop(act(z)), products with fp32
+ * accumulation and the epilogue in fp32.  drop is muon_dropout's, of a rows x
+ * out matrix.  z (BF16) is what the backward pass reads where act is not NONE;
+ * absent, it is not written.  The backward pass forms dz = drop(d_y) act'(z),
+ * rounded to bf16 as a matrix-core operand, and d_x = dz weight, d_weight =
+ * dz^T x, d_bias = the column sums of dz before its rounding, added in a fixed
+ * order: the same inputs give the same bits.  The gradient of the residual is
+ * d_y itself. */
+typedef struct muon_linear_args {
+  int64_t rows, cols, out;        /* rows 0 .. 2^30; cols, out multiples of 8,
+                                   * up to 2^20; below 15 x 2^20 tiles of 128 x
+                                   * 128 results                              */
+  int32_t act;                    /* muon_act                                 */
+  int32_t reserved;               /* must be 0                                */
+  double p;                       /* dropout: 0 (none) .. 1                   */
+  muon_rng rng;                   /* read where p is not 0                    */
+  muon_tensor x;                  /* rows x cols, BF16                        */
+  muon_tensor weight;             /* out x cols, BF16                         */
+  muon_tensor bias;               /* 1 x out, F32 or BF16; may be absent      */
+  muon_tensor residual;           /* rows x out, of y's type; may be absent   */
+  muon_tensor y;                  /* rows x out, F32 or BF16                  */
+  muon_tensor z;                  /* rows x out, BF16; may be absent (forward,
+                                   * and backward where act is NONE)          */
+  /* Backward only: reads d_y and, as far as they are needed, x, weight and z;
+   * writes those of the three gradients that are there. */
+  muon_tensor d_y;                /* rows x out, F32 or BF16                  */
+  muon_tensor d_x;                /* rows x cols, BF16                        */
+  muon_tensor d_weight;           /* out x cols, F32 or BF16                  */
+  muon_tensor d_bias;             /* 1 x out, F32 or BF16                     */
+} muon_linear_args;
+
+muon_status muon_linear_fwd_workspace(const muon_linear_args* args, size_t* bytes);
+muon_status muon_linear_fwd(const muon_linear_args* args, void* workspace, size_t workspace_bytes, void* hip_stream);
+muon_status muon_linear_bwd_workspace(const muon_linear_args* args, size_t* bytes);
+muon_status muon_linear_bwd(const muon_linear_args* args, void* workspace, size_t workspace_bytes, void* hip_stream);
+
+/* ---- Rotary positions ---------------------------------------------------------
+ * Pair p of a head at token i of sample b turns by t = sum_a pos[a] freqs[a][p]:
+ *   (u, v) -> scale (u cos t - v sin t, v cos t + u sin t)
+ * with (u, v) values (2 p, 2 p + 1) where interleaved, else (p, p + pairs).
+ * Values from 2 pairs on are copied.  inverse turns by -t (with the same scale):
+ * the gradient.  Angles are formed in fp64, so that far positions keep their
+ * digits.  q_out may be q itself (the same pointer and strides), and k_out k;
+ * other overlaps are not allowed. */
+typedef struct muon_rotary_args {
+  int64_t batch, len;             /* >= 0; batch x len below 2^31             */
+  int32_t heads, kv_heads;        /* of q and of k; kv_heads 0: there is no k.
+                                   * Together up to 2^16                      */
+  int32_t dim;                    /* even, 2 .. 1024                          */
+  int32_t pairs;                  /* 1 .. dim / 2                             */
+  int32_t axes;                   /* 1 .. 8; 1 where positions is NULL        */
+  int32_t interleaved, inverse;   /* 0 or 1                                   */
+  int32_t dtype;                  /* of all four tensors: F32 or BF16         */
+  float scale;                    /* finite                                   */
+  int32_t reserved;               /* must be 0                                */
+  int64_t offset;                 /* position of token 0 without positions    */
+  const double* freqs;            /* axes x pairs device values, radians per
+                                   * position                                 */
+  const int32_t* positions;       /* [sample][len][axes] device integers, or
+                                   * NULL: a token's position is its number
+                                   * in its sample, plus offset               */
+  int64_t positions_batch;        /* integers between samples (0: shared)     */
+  muon_heads q, k, q_out, k_out;  /* (batch, len, heads, dim), any strides of
+                                   * 0 or more (outputs: no two values in one
+                                   * place)                                   */
+} muon_rotary_args;
+
+muon_status muon_rotary(const muon_rotary_args* args, void* hip_stream);
 
 #ifdef __cplusplus
 }

@@ -20,7 +20,8 @@ from .binding import (  # noqa: F401
 # The transformer-block operators need torch at import; the optimizer's C ABI
 # does not, so they are looked up on first use.
 _BLOCK = ("norm_fwd", "norm_bwd", "residual_norm", "attn_fwd", "attn_bwd", "attention", "attention_qkv", "ffn_fwd", "ffn_bwd",
-          "gated_ffn")
+          "gated_ffn", "linear_fwd", "linear_bwd", "linear", "rotary_freqs", "rotary_fwd", "rotary_bwd", "rotary",
+          "dropout_fwd", "dropout_bwd", "dropout")
 
 
 def __getattr__(name: str):

@@ -1,17 +1,20 @@
 """PyTorch entry points of the transformer-block operators declared in
-include/muon_block.h: the fused residual norm, softmax attention and the gated
-feed-forward block.
+include/muon_block.h: the fused residual norm, softmax attention, the gated
+feed-forward block, linear layers with their epilogue, rotary positions and
+dropout.
 
-``norm_fwd`` / ``norm_bwd``, ``attn_fwd`` / ``attn_bwd`` and ``ffn_fwd`` /
-``ffn_bwd`` are one call of the library each: they check devices, types and
+``norm_fwd`` / ``norm_bwd``, ``attn_fwd`` / ``attn_bwd``, ``ffn_fwd`` /
+``ffn_bwd``, ``linear_fwd`` / ``linear_bwd``, ``rotary_fwd`` / ``rotary_bwd`` and
+``dropout_fwd`` / ``dropout_bwd`` are one call of the library each: they check devices, types and
 shapes, take outputs and workspace from PyTorch's allocator and enqueue the
 kernels on the current stream of the tensors' device.  Nothing is copied or
 made contiguous behind the caller's back: a layout that the kernels cannot
 read raises.  Tensors made on another stream need the caller's wait (and
-``record_stream``), as with PyTorch's own operators.  All six may be captured
-into a HIP graph.
+``record_stream``), as with PyTorch's own operators.  All of them may be
+captured into a HIP graph.
 
-``residual_norm``, ``attention`` and ``gated_ffn`` wrap them for autograd, once:
+``residual_norm``, ``attention``, ``gated_ffn``, ``linear``, ``rotary`` and
+``dropout`` wrap them for autograd, once:
 gradients of their gradients raise.  To capture a training step into a graph,
 call the forward and backward functions themselves: an autograd graph that
 shares leaves with a captured backward pass must not be alive during the
@@ -30,17 +33,24 @@ from .binding import MUON_OK, MuonError, lib
 
 NORM_KINDS = {"none": 0, "rms": 1, "layer": 2}
 ACTS = {"silu": 0, "gelu": 1}
+LINEAR_ACTS = {**ACTS, "none": 2}
 BLOCK_EXPORTED = ("muon_block_last_error", "muon_norm_fwd", "muon_norm_bwd_workspace", "muon_norm_bwd",
                   "muon_attn_fwd_workspace", "muon_attn_fwd", "muon_attn_bwd_workspace", "muon_attn_bwd",
-                  "muon_ffn_fwd_workspace", "muon_ffn_fwd", "muon_ffn_bwd_workspace", "muon_ffn_bwd")
+                  "muon_ffn_fwd_workspace", "muon_ffn_fwd", "muon_ffn_bwd_workspace", "muon_ffn_bwd",
+                  "muon_linear_fwd_workspace", "muon_linear_fwd", "muon_linear_bwd_workspace", "muon_linear_bwd",
+                  "muon_rotary", "muon_dropout")
+_NO_WORKSPACE = ("muon_norm_fwd", "muon_rotary", "muon_dropout")
 
 _TYPES = {torch.float32: 0, torch.bfloat16: 1}
 # The argument structures of muon_block.h, packed field by field (a few
 # microseconds where a ctypes.Structure of some 120 fields takes ten times that).
-_MAT, _HEADS = "Pqqqii", "Pqqq"
+_MAT, _HEADS, _RNG = "Pqqqii", "Pqqq", "QQP"
 NORM_ARGS = struct.Struct("@qqqiiff" + 9 * _MAT + "P" + 9 * _MAT)
 ATTN_ARGS = struct.Struct("@qqqiiiiqfiPP" + 4 * _HEADS + "P" + 4 * _HEADS)
 FFN_ARGS = struct.Struct("@qqqii" + 11 * _MAT)
+LINEAR_ARGS = struct.Struct("@qqqiid" + _RNG + 10 * _MAT)
+DROPOUT_ARGS = struct.Struct("@qqd" + _RNG + 3 * _MAT)
+ROTARY_ARGS = struct.Struct("@qqiiiiiiiifiqPPq" + 4 * _HEADS)
 _NO_MAT, _NO_HEADS = (0,) * 6, (0,) * 4
 
 _READY = None
@@ -57,7 +67,7 @@ def _lib():
             f.restype = ctypes.c_int
             if name.endswith("_workspace"):
                 f.argtypes = [ctypes.c_char_p, ctypes.POINTER(size)]
-            elif name == "muon_norm_fwd":
+            elif name in _NO_WORKSPACE:
                 f.argtypes = [ctypes.c_char_p, void]
             else:
                 f.argtypes = [ctypes.c_char_p, void, size, void]
@@ -368,27 +378,41 @@ class _Attention(torch.autograd.Function):
 
 class _PackedAttention(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, qkv, how):
+    def forward(ctx, qkv, how, turn):
         q, k, v = qkv.unbind(2)
+        if turn is None:
+            o, lse = attn_fwd(q, k, v, **how)
+            _keep(ctx, how, qkv, o, lse)
+            return o
+        q, k = rotary_fwd(q, k, **turn)
         o, lse = attn_fwd(q, k, v, **how)
-        _keep(ctx, how, qkv, o, lse)
+        ctx.turn = {name: value for name, value in turn.items() if name not in ("freqs", "positions")}
+        _keep(ctx, how, qkv, o, lse, q, k, turn["freqs"], turn.get("positions"))
         return o
 
     @staticmethod
     @once_differentiable
     def backward(ctx, d_o):
-        qkv, o, lse, q_lens, k_lens = ctx.saved_tensors
+        qkv, o, lse, *rotated, q_lens, k_lens = ctx.saved_tensors
+        q, k, v = qkv.unbind(2)
         d_qkv = torch.empty_like(qkv, memory_format=torch.contiguous_format)
-        attn_bwd(d_o.contiguous(), *qkv.unbind(2), o, lse, q_lens=q_lens, k_lens=k_lens, out=d_qkv.unbind(2), **ctx.how)
-        return d_qkv, None
+        d_q, d_k, d_v = d_qkv.unbind(2)
+        if rotated:
+            q, k, freqs, positions = rotated
+        attn_bwd(d_o.contiguous(), q, k, v, o, lse, q_lens=q_lens, k_lens=k_lens, out=(d_q, d_k, d_v), **ctx.how)
+        if rotated:
+            rotary_bwd(d_q, d_k, freqs, positions, out=(d_q, d_k), **ctx.turn)
+        return d_qkv, None, None
 
 
 def attention_qkv(qkv, *, causal: bool = False, offset: int = 0, q_lens=None, k_lens=None,
-                  scale: float | None = None):
+                  scale: float | None = None, rotary: dict | None = None):
     """attention of a packed projection's output (batch, len, 3, heads, dim),
-    whose gradient comes out packed alike; returns o."""
+    whose gradient comes out packed alike; returns o.  rotary: rotary_fwd's
+    arguments from freqs on, by name, where queries and keys are to be rotated
+    first."""
     return _PackedAttention.apply(qkv, {"causal": causal, "offset": offset, "q_lens": q_lens, "k_lens": k_lens,
-                                        "scale": scale})
+                                        "scale": scale}, rotary)
 
 
 def attention(q, k, v, *, causal: bool = False, offset: int = 0, q_lens=None, k_lens=None,
@@ -474,3 +498,344 @@ def gated_ffn(x, w_gate, w_up, w_down, *, act: str = "silu"):
     # (inside forward the grad mode is off, and needs_input_grad does not know it)
     save = torch.is_grad_enabled() and any(t.requires_grad for t in (x, w_gate, w_up, w_down))
     return _GatedFfn.apply(x, w_gate, w_up, w_down, act, save)
+
+
+# -------------------------------------------------------------------- dropout
+def _rng(p, rng, device):
+    """(seed, offset, address of both): two numbers, or a tensor that holds them."""
+    if not 0.0 <= p <= 1.0:
+        raise ValueError(f"p is in 0 .. 1: got {p}")
+    if p == 0.0:
+        return 0, 0, 0
+    if rng is None:
+        raise ValueError("dropout needs rng: (seed, offset), or an int64 tensor of both")
+    if isinstance(rng, torch.Tensor):
+        if rng.dtype != torch.int64 or rng.shape != (2,) or not rng.is_contiguous() or rng.device != device:
+            raise ValueError(f"rng: two contiguous int64 on {device} are wanted, got {tuple(rng.shape)} {rng.dtype} on {rng.device}")
+        return 0, 0, rng.data_ptr()
+    seed, offset = rng
+    if not (0 <= seed < 1 << 64 and 0 <= offset < 1 << 64):
+        raise ValueError(f"rng: seed and offset are 64-bit numbers, got {rng}")
+    return seed, offset, 0
+
+
+def _dropout(x, p, rng, residual, dtype):
+    dev = _device(x, residual)
+    if residual is not None and residual.shape != x.shape:
+        raise ValueError(f"residual {tuple(residual.shape)} for x {tuple(x.shape)}")
+    if x.dim() == 0:
+        raise ValueError("(..., cols) is wanted")
+    if dtype not in _TYPES:
+        raise TypeError(f"unsupported dtype {dtype}")
+    seed, offset, state = _rng(p, rng, dev)
+    y = torch.empty(x.shape, dtype=dtype, device=dev)
+    if x.numel() == 0:
+        return y
+    rows, cols = x.shape[:-1].numel(), x.shape[-1]
+    args = DROPOUT_ARGS.pack(rows, cols, p, seed, offset, state, *_mat(x, rows, cols), *_mat(residual, rows, cols),
+                             *_mat(y, rows, cols))
+    _call("muon_dropout", args, dev, workspace=False)
+    return y
+
+
+def dropout_fwd(x, p: float, rng=None, residual=None):
+    """y = residual + keep x / (1 - p), the mask formed from rng and never
+    stored.
+
+    x, residual: (..., cols), fp32 or bf16 each; y has the residual's type (x's
+    where there is none).  rng: (seed, offset), or an int64 tensor of the two on
+    the GPU that is read when the kernel runs, so that a captured graph's replays
+    differ by what is written there.  Calls whose masks are to differ take
+    different offsets; the same seed and offset give the same mask, by an
+    element's number in x.  Dropped elements count as 0 whatever they hold."""
+    return _dropout(x, p, rng, residual, x.dtype if residual is None else residual.dtype)
+
+
+def dropout_bwd(d_y, p: float, rng=None, *, dtype=None):
+    """Gradient of dropout_fwd's x, of `dtype` (x's type; d_y's where None).
+    The residual's is d_y."""
+    return _dropout(d_y, p, rng, None, d_y.dtype if dtype is None else dtype)
+
+
+def _keep_rng(ctx, rng, *tensors):
+    """Saves what the backward pass reads, numbers in a tensor with it: written
+    again before that pass, they then raise as any saved tensor does."""
+    held = isinstance(rng, torch.Tensor)
+    ctx.rng = None if held else rng
+    ctx.save_for_backward(*tensors, rng if held else None)
+
+
+class _Dropout(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, p, rng):
+        ctx.p, ctx.dtype = p, x.dtype
+        _keep_rng(ctx, rng)
+        return dropout_fwd(x, p, rng, residual)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, d_y):
+        held, = ctx.saved_tensors
+        d_x = None
+        if ctx.needs_input_grad[0]:
+            d_x = dropout_bwd(d_y.contiguous(), ctx.p, ctx.rng if held is None else held, dtype=ctx.dtype)
+        return d_x, d_y if ctx.needs_input_grad[1] else None, None, None
+
+
+def dropout(x, p: float, rng=None, residual=None):
+    """dropout_fwd for autograd; returns y."""
+    return _Dropout.apply(x, residual, p, rng)
+
+
+# --------------------------------------------------------------------- linear
+def _linear_dims(weight, act: str):
+    if act not in LINEAR_ACTS:
+        raise ValueError(f"act is one of {sorted(LINEAR_ACTS)}: got {act!r}")
+    if weight.dim() != 2:
+        raise ValueError("the weight is a matrix")
+    if weight.dtype != torch.bfloat16:
+        raise TypeError(f"weight: bf16 is wanted, got {weight.dtype}")
+    return weight.shape
+
+
+def _vec(t, n: int):
+    if t is not None and t.shape != (n,):
+        raise ValueError(f"bias: shape {tuple(t.shape)} where ({n},) is wanted")
+    return _mat(t, 1, n)
+
+
+def linear_fwd(x, weight, bias=None, residual=None, *, act: str = "none", p: float = 0.0, rng=None, save: bool = True,
+               y_dtype=None):
+    """z = x weight^T + bias; y = residual + drop(act(z)), with fp32 sums and
+    epilogue.
+
+    x (..., cols) and weight (out, cols) bf16, cols and out multiples of 8; bias
+    (out,) fp32 or bf16; residual (..., out) fp32 or bf16, whose type y has (else
+    y_dtype, bf16 where None).  act: "none", "silu", or "gelu" in its tanh form.
+    p, rng: dropout as in dropout_fwd, the same mask as it gives for y's shape.
+    Returns (y, z): z (rows, out) bf16 is what linear_bwd reads, None where act is
+    "none" or save is false."""
+    dev = _device(x, weight, bias, residual)
+    out, cols = _linear_dims(weight, act)
+    if x.dtype != torch.bfloat16:
+        raise TypeError(f"x: bf16 is wanted, got {x.dtype}")
+    if x.dim() < 1 or x.shape[-1] != cols:
+        raise ValueError(f"x {tuple(x.shape)} for a weight {tuple(weight.shape)}")
+    shape = (*x.shape[:-1], out)
+    if residual is not None and (residual.shape != shape or y_dtype not in (None, residual.dtype)):
+        raise ValueError(f"residual {tuple(residual.shape)} {residual.dtype} for {shape}, y_dtype {y_dtype}")
+    dtype = residual.dtype if residual is not None else y_dtype or torch.bfloat16
+    if dtype not in _TYPES:
+        raise TypeError(f"unsupported dtype {dtype}")
+    rows = x.shape[:-1].numel()
+    rng = _rng(p, rng, dev)
+    y = torch.empty(shape, dtype=dtype, device=dev)
+    z = torch.empty((rows, out), dtype=torch.bfloat16, device=dev) if save and act != "none" else None
+    b = _vec(bias, out)
+    if rows == 0:
+        return y, z
+    args = LINEAR_ARGS.pack(rows, cols, out, LINEAR_ACTS[act], 0, p, *rng, *_mat(x, rows, cols), *_mat(weight, out, cols),
+                            *b, *_mat(residual, rows, out), *_mat(y, rows, out), *_mat(z, rows, out),
+                            *(4 * _NO_MAT))
+    _call("muon_linear_fwd", args, dev)
+    return y, z
+
+
+def linear_bwd(d_y, x, weight, bias=None, z=None, *, act: str = "none", p: float = 0.0, rng=None,
+               grad_dtype=torch.bfloat16, need_x: bool = True, need_weight: bool = True):
+    """Gradients (d_x, d_weight, d_bias) of linear_fwd's y.
+
+    z is linear_fwd's second result, the rest its arguments (x may be None where
+    need_weight is false); d_y is fp32 or bf16.  d_weight is contiguous, of
+    grad_dtype (bf16 or fp32), d_bias of the bias's type: what muon_step reads.
+    None stands for what is not needed, d_bias where bias is None.  The
+    residual's gradient is d_y."""
+    dev = _device(d_y, x, weight, bias, z)
+    out, cols = _linear_dims(weight, act)
+    if d_y.dim() < 1 or d_y.shape[-1] != out:
+        raise ValueError(f"d_y {tuple(d_y.shape)} for a weight {tuple(weight.shape)}")
+    shape = (*d_y.shape[:-1], cols)
+    if (need_weight or x is not None) and (x is None or x.shape != shape):
+        raise ValueError(f"x {None if x is None else tuple(x.shape)} where {shape} is wanted")
+    if act != "none" and z is None:
+        raise ValueError("z is linear_fwd's second result")
+    if grad_dtype not in _TYPES:
+        raise TypeError(f"unsupported grad_dtype {grad_dtype}")
+    rows = d_y.shape[:-1].numel()
+    rng = _rng(p, rng, dev)
+    b = _vec(bias, out)
+    d_x = torch.empty(shape, dtype=torch.bfloat16, device=dev) if need_x else None
+    d_w = torch.empty((out, cols), dtype=grad_dtype, device=dev) if need_weight else None
+    d_b = None if bias is None else torch.empty((out,), dtype=bias.dtype, device=dev)
+    if rows == 0:
+        for t in (d_w, d_b):
+            if t is not None:
+                t.zero_()
+        return d_x, d_w, d_b
+    args = LINEAR_ARGS.pack(rows, cols, out, LINEAR_ACTS[act], 0, p, *rng, *_mat(x, rows, cols), *_mat(weight, out, cols),
+                            *b, *(2 * _NO_MAT), *_mat(z, rows, out), *_mat(d_y, rows, out), *_mat(d_x, rows, cols),
+                            *_mat(d_w, out, cols), *_mat(d_b, 1, out))
+    _call("muon_linear_bwd", args, dev)
+    return d_x, d_w, d_b
+
+
+class _Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, act, p, rng, y_dtype, save):
+        y, z = linear_fwd(x, weight, bias, residual, act=act, p=p, rng=rng, save=save, y_dtype=y_dtype)
+        ctx.act, ctx.p = act, p
+        _keep_rng(ctx, rng, x, weight, bias, z)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, d_y):
+        x, weight, bias, z, held = ctx.saved_tensors
+        need_x, need_w, need_b, need_r = ctx.needs_input_grad[:4]
+        d = (None,) * 3
+        if need_x or need_w or need_b:
+            d = linear_bwd(d_y.contiguous(), x, weight, bias if need_b else None, z, act=ctx.act, p=ctx.p,
+                           rng=ctx.rng if held is None else held, need_x=need_x, need_weight=need_w)
+        return (*d, d_y if need_r else None, None, None, None, None, None)
+
+
+def linear(x, weight, bias=None, residual=None, *, act: str = "none", p: float = 0.0, rng=None, y_dtype=None):
+    """linear_fwd for autograd; returns y."""
+    # (inside forward the grad mode is off, and needs_input_grad does not know it)
+    save = torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias))
+    return _Linear.apply(x, weight, bias, residual, act, p, rng, y_dtype, save)
+
+
+# ----------------------------------------------------------- rotary positions
+STRETCHES = ("none", "linear", "ntk", "yarn")
+
+
+def rotary_freqs(dim, *, base: float = 10000.0, stretch: str = "none", factor: float = 1.0, length: int | None = None,
+                 device="cuda"):
+    """Frequencies for rotary_fwd, float64 (axes, pairs): base ** (-2 i / d) for
+    the i-th pair of the d values that an axis turns.
+
+    dim: the values that are rotated, or a sequence of them, one per axis, which
+    take consecutive pairs (an image's rows and columns: (dim // 2, dim // 2)).
+    stretch, for contexts `factor` times the one trained on: "linear" divides the
+    frequencies (positions are interpolated), "ntk" raises the base by
+    factor ** (d / (d - 2)), which leaves the fastest pair and divides the slowest,
+    "yarn" divides those that turn less than once over `length` trained tokens,
+    leaves those that turn more than 32 times and goes evenly between (Peng et al.,
+    "YaRN", which also scales queries and keys, rotary_fwd's scale, by
+    0.1 log(factor) + 1)."""
+    dims = (dim,) if isinstance(dim, int) else tuple(dim)
+    if not dims or any(d < 2 or d % 2 for d in dims):
+        raise ValueError(f"each axis turns an even number of values: got {dim}")
+    if stretch not in STRETCHES or not factor > 0.0 or not base > 0.0:
+        raise ValueError(f"stretch is one of {STRETCHES}, factor and base above 0: got {stretch!r}, {factor}, {base}")
+    if stretch == "yarn" and (length is None or length < 1):
+        raise ValueError("yarn needs the length trained on")
+    out = torch.zeros((len(dims), sum(dims) // 2), dtype=torch.float64)
+    at = 0
+    for axis, d in enumerate(dims):
+        b = base * factor ** (d / (d - 2)) if stretch == "ntk" and d > 2 else base
+        f = b ** (-torch.arange(0, d, 2, dtype=torch.float64) / d)
+        if stretch == "linear":
+            f = f / factor
+        elif stretch == "yarn":
+            kept = ((length * f / (2 * torch.pi) - 1) / 31).clamp(0, 1)
+            f = f * (kept + (1 - kept) / factor)
+        out[axis, at:at + d // 2] = f
+        at += d // 2
+    return out.to(device)
+
+
+def _turned_heads(t, name: str, dtype):
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: {dtype} is wanted, got {t.dtype}")
+    b, n, h, d = t.shape
+    sb, sl, sh, sd = t.stride()
+    if sd != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return t.data_ptr(), sb if b > 1 else 0, sl if n > 1 else 0, sh if h > 1 else 0
+
+
+def _rotary(q, k, freqs, positions, offset, interleaved, scale, out, inverse):
+    dev = _device(q, k, freqs, positions)
+    if q.dim() != 4 or (k is not None and (k.dim() != 4 or k.shape[:2] != q.shape[:2] or k.shape[3] != q.shape[3])):
+        raise ValueError(f"(batch, len, heads, dim) each: q {tuple(q.shape)}, k {None if k is None else tuple(k.shape)}")
+    if q.dtype not in _TYPES:
+        raise TypeError(f"unsupported dtype {q.dtype}")
+    b, n, h, d = q.shape
+    if freqs.dtype != torch.float64 or freqs.dim() != 2 or not freqs.is_contiguous():
+        raise ValueError("freqs: contiguous float64 (axes, pairs) is wanted")
+    axes, pairs = freqs.shape
+    between = 0
+    if positions is not None:
+        if positions.dtype != torch.int32 or not positions.is_contiguous():
+            raise TypeError("positions: contiguous int32 is wanted")
+        one = (n,) if axes == 1 else (n, axes)
+        if positions.shape not in (one, (b, *one)):
+            raise ValueError(f"positions {tuple(positions.shape)} where {one} or {(b, *one)} is wanted")
+        if offset:
+            raise ValueError("offset is for tokens without positions")
+        between = n * axes if len(positions.shape) > len(one) else 0
+    made = out is None
+    if made:
+        out = _out(q), None if k is None else _out(k)
+    else:
+        _device(q, *out)
+        if len(out) != 2 or tuple(None if t is None else t.shape for t in out) != (q.shape, None if k is None else k.shape):
+            raise ValueError(f"out: shapes {[None if t is None else tuple(t.shape) for t in out]}")
+    args = ROTARY_ARGS.pack(
+        b, n, h, 0 if k is None else k.shape[2], d, pairs, axes, int(interleaved), inverse, _TYPES[q.dtype], scale, 0, offset,
+        freqs.data_ptr(), _ptr(positions), between, *_turned_heads(q, "q", q.dtype),
+        *(_NO_HEADS if k is None else _turned_heads(k, "k", q.dtype)), *_turned_heads(out[0], "out", q.dtype),
+        *(_NO_HEADS if k is None else _turned_heads(out[1], "out", q.dtype)))
+    _call("muon_rotary", args, dev, workspace=False)
+    return tuple(out)
+
+
+def rotary_fwd(q, k, freqs, positions=None, *, offset: int = 0, interleaved: bool = False, scale: float = 1.0, out=None):
+    """Rotates queries and keys by their positions: pair p of a head turns by
+    t = sum_a positions[..., a] freqs[a, p], (u, v) -> scale (u cos t - v sin t,
+    v cos t + u sin t).
+
+    q (batch, len, heads, dim) and k (batch, len, kv_heads, dim) or None, fp32 or
+    bf16, any strides with the last dimension contiguous (slices of a packed
+    projection are fine); dim even, up to 1024.  freqs: float64 (axes, pairs),
+    rotary_freqs gives some; 2 pairs values of each head are rotated, the rest is
+    copied.  interleaved: pairs of neighbours (2 p, 2 p + 1), else of halves
+    (p, p + pairs).  positions: int32, (len,) or (batch, len), with several axes
+    (len, axes) or (batch, len, axes); None: a token's number plus offset.
+
+    Returns both, written to `out`, two tensors of q's and k's shapes, or to new
+    contiguous ones.  out may be (q, k) themselves."""
+    return _rotary(q, k, freqs, positions, offset, interleaved, scale, out, 0)
+
+
+def rotary_bwd(d_q, d_k, freqs, positions=None, *, offset: int = 0, interleaved: bool = False, scale: float = 1.0, out=None):
+    """Gradients of rotary_fwd's q and k from those of its results: the inverse
+    rotation, with the same scale."""
+    return _rotary(d_q, d_k, freqs, positions, offset, interleaved, scale, out, 1)
+
+
+class _Rotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, freqs, positions, how):
+        ctx.how = how
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(freqs, positions)
+        return rotary_fwd(q, k, freqs, positions, **how)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, d_q, d_k):
+        freqs, positions = ctx.saved_tensors
+        d = [None if t is None else t.contiguous() for t in (d_q, d_k)]
+        if d[0] is None:
+            d[1] = None if d[1] is None else rotary_bwd(d[1], None, freqs, positions, **ctx.how)[0]
+        else:
+            d = rotary_bwd(*d, freqs, positions, **ctx.how)
+        return (*d, None, None, None)
+
+
+def rotary(q, k, freqs, positions=None, *, offset: int = 0, interleaved: bool = False, scale: float = 1.0):
+    """rotary_fwd for autograd; returns both rotated (None for a k that is None)."""
+    return _Rotary.apply(q, k, freqs, positions, {"offset": offset, "interleaved": interleaved, "scale": scale})

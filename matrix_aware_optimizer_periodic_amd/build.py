@@ -18,7 +18,8 @@ OUT = os.path.join(HERE, "libmuon_hip.so")
 OBJDIR = os.path.join(HERE, "_build")
 SOURCES = ["kernels_rownorm.hip", "kernels_ns5.hip", "kernels_gram_tri.hip", "kernels_misc.hip",
            "noalloc.hip", "kernels_norm.hip", "kernels_attn.hip",
-           "kernels_ffn.hip", "block_runtime.cpp", "runtime.cpp"]
+           "kernels_ffn.hip", "kernels_linear.hip", "kernels_dropout.hip", "kernels_rotary.hip", "block_runtime.cpp",
+           "runtime.cpp"]
 ARCH = os.environ.get("MUON_OFFLOAD_ARCH", "gfx950")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -103,4 +103,53 @@ hipError_t launch_ffn_bwd(hipStream_t s, const FfnDev& a);
 size_t ffn_fwd_part_bytes(int64_t rows, int64_t cols, int64_t hidden);
 size_t ffn_bwd_part_bytes(int64_t rows, int64_t cols, int64_t hidden);
 
+// ---- dropout ----------------------------------------------------------------
+struct DropDev {
+  uint64_t seed, offset;
+  const uint64_t* state;  // device: seed and offset in their place, or null
+  uint32_t last;          // words up to this one drop their element
+  int32_t on;             // 0: nothing is dropped, and last means nothing
+  float scale;            // 1 / (1 - p) of the others
+  int32_t pad;
+};
+
+struct DropoutDev {
+  int64_t rows, cols;
+  DropDev drop;
+  NormMat x, resid, y;
+};
+// vec: rows of whole groups of eight, 16-byte aligned.
+hipError_t launch_dropout(hipStream_t s, const DropoutDev& a, bool vec);
+
+// ---- linear -----------------------------------------------------------------
+struct LinearDev {
+  int64_t rows, cols, out;
+  int32_t act;            // muon_act
+  DropDev drop;
+  NormMat x, w, bias, resid, y, z, d_y, d_x, d_w, d_bias;
+  void* dz;               // rows x out bf16: the products' operand, or null where d_y is that
+  float* sums;            // [split][out] shares of d_bias
+  float* part;            // partial products of split sums
+};
+hipError_t launch_linear_fwd(hipStream_t s, const LinearDev& a);
+hipError_t launch_linear_bwd(hipStream_t s, const LinearDev& a);
+size_t linear_fwd_part_bytes(int64_t rows, int64_t cols, int64_t out);
+size_t linear_bwd_part_bytes(int64_t rows, int64_t cols, int64_t out, bool d_x, bool d_w);
+// Shares of the rows that d_bias is summed in.
+int linear_sum_splits(int64_t rows, int64_t out);
+
+// ---- rotary positions ---------------------------------------------------------
+struct RotaryDev {
+  int64_t tokens;         // batch x len
+  int64_t offset;
+  int32_t len, heads, kv_heads, dim, pairs, axes, interleaved, inverse, f32, in_place;
+  float scale;
+  const double* freqs;    // [axes][pairs], radians per position
+  const int32_t* positions;   // [batch or 1][len][axes], or null: token + offset
+  int64_t pos_batch;      // positions of a sample (0: shared)
+  HeadsDev q, k, q_out, k_out;
+  FastDiv by_len, by_heads, by_chunks;
+};
+hipError_t launch_rotary(hipStream_t s, const RotaryDev& a, int vec);
+
 }  // namespace muon

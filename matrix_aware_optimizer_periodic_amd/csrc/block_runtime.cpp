@@ -41,14 +41,15 @@ size_t type_size(int32_t dt) { return dt == MUON_F32 ? 4 : 2; }
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 // A present matrix: shape, type (dt < 0: F32 or BF16), stride, alignment.
-muon_status check_mat(const char* name, const muon_tensor& t, int64_t rows, int64_t cols, int32_t dt) {
+muon_status check_mat(const char* name, const muon_tensor& t, int64_t rows, int64_t cols, int32_t dt,
+                      int64_t max_ld = kMaxLd) {
   if (!t.ptr) return fail(MUON_E_ARG, "%s is missing", name);
   if (t.rows != rows || t.cols != cols || t.reserved != 0)
     return fail(MUON_E_SHAPE, "%s: %lld x %lld where %lld x %lld is wanted", name, (long long)t.rows,
                 (long long)t.cols, (long long)rows, (long long)cols);
   if ((t.dtype != MUON_F32 && t.dtype != MUON_BF16) || (dt >= 0 && t.dtype != dt))
     return fail(MUON_E_DTYPE, "%s: dtype %d", name, t.dtype);
-  if (t.ld < cols || t.ld > kMaxLd)
+  if (t.ld < cols || t.ld > max_ld)
     return fail(MUON_E_ALIGN, "%s: ld %lld for %lld columns", name, (long long)t.ld, (long long)cols);
   if (!aligned(t.ptr, type_size(t.dtype))) return fail(MUON_E_ALIGN, "%s: pointer not aligned to its type", name);
   return MUON_OK;
@@ -259,6 +260,89 @@ size_t ffn_bwd_bytes(const muon_ffn_args* a) {
   return 3 * ffn_hid_bytes(a) + align_up(ffn_bwd_part_bytes(a->rows, a->cols, a->hidden));
 }
 
+// ---- dropout ----------------------------------------------------------------
+// p as the last word that drops its element.
+muon_status drop_dev(double p, const muon_rng& rng, DropDev* d) {
+  *d = DropDev{};
+  if (!(p >= 0.0) || !(p <= 1.0)) return fail(MUON_E_ARG, "p must be in 0 .. 1");
+  const double words = std::nearbyint(p * 4294967296.0);
+  if (words < 1.0) return MUON_OK;
+  if (!aligned(rng.state, 8)) return fail(MUON_E_ALIGN, "rng.state not aligned");
+  d->seed = rng.seed; d->offset = rng.offset; d->state = rng.state;
+  d->last = uint32_t(uint64_t(words) - 1);
+  d->on = 1;
+  d->scale = p < 1.0 ? float(1.0 / (1.0 - p)) : 0.f;
+  return MUON_OK;
+}
+
+// ---- linear -----------------------------------------------------------------
+muon_status linear_dims(const muon_linear_args* a, DropDev* d) {
+  if (!a) return fail(MUON_E_ARG, "args is NULL");
+  const int64_t most = 1 << 20;
+  if (a->rows < 0 || a->rows > (1 << 30) || a->cols < 8 || a->out < 8 || a->cols % 8 || a->out % 8 || a->cols > most ||
+      a->out > most)
+    return fail(MUON_E_SHAPE, "rows %lld, cols %lld, out %lld: cols and out are multiples of 8 up to 2^20",
+                (long long)a->rows, (long long)a->cols, (long long)a->out);
+  // fewer than 2^32 threads to a launch, 256 per tile; divided tiles add 2^20 at most
+  const int64_t tiles = 15 << 20, rb = (a->rows + 127) / 128, cb = (a->cols + 127) / 128, ob = (a->out + 127) / 128;
+  if (rb * ob >= tiles || rb * cb + ob * cb >= tiles)
+    return fail(MUON_E_SHAPE, "too many rows or columns for one call: %lld x %lld x %lld", (long long)a->rows,
+                (long long)a->cols, (long long)a->out);
+  if ((a->act != MUON_ACT_SILU && a->act != MUON_ACT_GELU_TANH && a->act != MUON_ACT_NONE) || a->reserved != 0)
+    return fail(MUON_E_ARG, "unknown act, or reserved is not 0");
+  return drop_dev(a->p, a->rng, d);
+}
+
+LinearDev linear_dev(const muon_linear_args* a, const DropDev& drop) {
+  LinearDev d{};
+  d.rows = a->rows; d.cols = a->cols; d.out = a->out; d.act = a->act; d.drop = drop;
+  d.x = norm_mat(a->x); d.w = norm_mat(a->weight); d.bias = norm_mat(a->bias); d.resid = norm_mat(a->residual);
+  d.y = norm_mat(a->y); d.z = norm_mat(a->z); d.d_y = norm_mat(a->d_y); d.d_x = norm_mat(a->d_x);
+  d.d_w = norm_mat(a->d_weight); d.d_bias = norm_mat(a->d_bias);
+  return d;
+}
+
+// Whether the backward products' operand is formed apart from d_y.
+bool linear_forms_dz(const muon_linear_args* a, const DropDev& drop) {
+  return (a->d_x.ptr || a->d_weight.ptr) && (a->act != MUON_ACT_NONE || drop.on || a->d_y.dtype != MUON_BF16);
+}
+size_t linear_dz_bytes(const muon_linear_args* a, const DropDev& drop) {
+  return linear_forms_dz(a, drop) ? align_up(size_t(a->rows) * size_t(a->out) * 2) : 0;
+}
+size_t linear_sums_bytes(const muon_linear_args* a) {
+  if (!a->d_bias.ptr || a->rows == 0) return 0;
+  const int splits = linear_sum_splits(a->rows, a->out);
+  return splits > 1 ? align_up(size_t(splits) * size_t(a->out) * 4) : 0;
+}
+size_t linear_fwd_bytes(const muon_linear_args* a) { return align_up(linear_fwd_part_bytes(a->rows, a->cols, a->out)); }
+size_t linear_bwd_bytes(const muon_linear_args* a, const DropDev& drop) {
+  return linear_dz_bytes(a, drop) + linear_sums_bytes(a) +
+         align_up(linear_bwd_part_bytes(a->rows, a->cols, a->out, a->d_x.ptr, a->d_weight.ptr));
+}
+
+// ---- rotary positions ---------------------------------------------------------
+muon_status rotary_heads(const char* name, const muon_heads& t, int32_t dtype) {
+  if (!t.ptr) return fail(MUON_E_ARG, "%s is missing", name);
+  if (!aligned(t.ptr, type_size(dtype))) return fail(MUON_E_ALIGN, "%s: pointer not aligned to its type", name);
+  const int64_t far = int64_t(1) << 40;
+  if (t.stride_batch < 0 || t.stride_len < 0 || t.stride_head < 0 || t.stride_batch > far || t.stride_len > far ||
+      t.stride_head > far)
+    return fail(MUON_E_SHAPE, "%s: stride out of range", name);
+  return MUON_OK;
+}
+
+// Whether runs of v values of every head of t lie on the boundary their access
+// needs (16 bytes at most).
+bool rotary_runs(const muon_heads& t, int32_t dtype, int v) {
+  const size_t size = type_size(dtype), need = v * size > 16 ? 16 : v * size;
+  return aligned(t.ptr, need) && t.stride_batch * size % need == 0 && t.stride_len * size % need == 0 &&
+         t.stride_head * size % need == 0;
+}
+
+bool same_heads(const muon_heads& a, const muon_heads& b) {
+  return a.ptr == b.ptr && a.stride_batch == b.stride_batch && a.stride_len == b.stride_len && a.stride_head == b.stride_head;
+}
+
 }  // namespace
 
 extern "C" {
@@ -432,6 +516,136 @@ muon_status muon_ffn_bwd(const muon_ffn_args* a, void* ws, size_t ws_bytes, void
   d.dgu = static_cast<char*>(ws) + ffn_hid_bytes(a);
   d.part = reinterpret_cast<float*>(static_cast<char*>(ws) + 3 * ffn_hid_bytes(a));
   return launched("muon_ffn_bwd", launch_ffn_bwd(static_cast<hipStream_t>(hip_stream), d));
+}
+
+muon_status muon_dropout(const muon_dropout_args* a, void* hip_stream) {
+  if (!a) return fail(MUON_E_ARG, "args is NULL");
+  const int64_t top = int64_t(1) << 56, far = int64_t(1) << 40;
+  if (a->rows < 0 || a->cols < 0 || a->cols > far || (a->cols > 0 && a->rows > top / a->cols))
+    return fail(MUON_E_SHAPE, "rows %lld, cols %lld", (long long)a->rows, (long long)a->cols);
+  DropoutDev d{};
+  CHECK(drop_dev(a->p, a->rng, &d.drop));
+  if (a->rows == 0 || a->cols == 0) return MUON_OK;
+  CHECK(check_mat("x", a->x, a->rows, a->cols, -1, far));
+  CHECK(check_mat("y", a->y, a->rows, a->cols, -1, far));
+  if (a->residual.ptr) CHECK(check_mat("residual", a->residual, a->rows, a->cols, a->y.dtype, far));
+  d.rows = a->rows; d.cols = a->cols;
+  d.x = norm_mat(a->x); d.resid = norm_mat(a->residual); d.y = norm_mat(a->y);
+  // Rows beside each other everywhere are one row.
+  bool one = true, vec = true;
+  for (const muon_tensor* t : {&a->x, &a->residual, &a->y})
+    if (t->ptr && t->ld != a->cols) one = false;
+  if (one) { d.cols *= d.rows; d.rows = 1; }
+  for (const muon_tensor* t : {&a->x, &a->residual, &a->y})
+    if (t->ptr && (!aligned(t->ptr, 16) || (d.rows > 1 && t->ld % 8))) vec = false;
+  if (d.rows > 1 && a->cols % 8) vec = false;
+  return launched("muon_dropout", launch_dropout(static_cast<hipStream_t>(hip_stream), d, vec));
+}
+
+muon_status muon_linear_fwd_workspace(const muon_linear_args* a, size_t* bytes) {
+  if (!bytes) return fail(MUON_E_ARG, "bytes is NULL");
+  DropDev drop;
+  CHECK(linear_dims(a, &drop));
+  *bytes = linear_fwd_bytes(a);
+  return MUON_OK;
+}
+
+muon_status muon_linear_fwd(const muon_linear_args* a, void* ws, size_t ws_bytes, void* hip_stream) {
+  DropDev drop;
+  CHECK(linear_dims(a, &drop));
+  CHECK(ffn_mat("weight", a->weight, a->out, a->cols, MUON_BF16));
+  CHECK(check_opt("bias", a->bias, 1, a->out, -1));
+  if (a->rows == 0) return MUON_OK;
+  CHECK(ffn_mat("x", a->x, a->rows, a->cols, MUON_BF16));
+  CHECK(ffn_mat("y", a->y, a->rows, a->out, -1));
+  if (a->residual.ptr) CHECK(ffn_mat("residual", a->residual, a->rows, a->out, a->y.dtype));
+  if (a->z.ptr) CHECK(ffn_mat("z", a->z, a->rows, a->out, MUON_BF16));
+  CHECK(check_workspace(ws, ws_bytes, linear_fwd_bytes(a)));
+  LinearDev d = linear_dev(a, drop);
+  d.part = static_cast<float*>(ws);
+  return launched("muon_linear_fwd", launch_linear_fwd(static_cast<hipStream_t>(hip_stream), d));
+}
+
+muon_status muon_linear_bwd_workspace(const muon_linear_args* a, size_t* bytes) {
+  if (!bytes) return fail(MUON_E_ARG, "bytes is NULL");
+  DropDev drop;
+  CHECK(linear_dims(a, &drop));
+  *bytes = linear_bwd_bytes(a, drop);
+  return MUON_OK;
+}
+
+muon_status muon_linear_bwd(const muon_linear_args* a, void* ws, size_t ws_bytes, void* hip_stream) {
+  DropDev drop;
+  CHECK(linear_dims(a, &drop));
+  if (!a->d_x.ptr && !a->d_weight.ptr && !a->d_bias.ptr) return MUON_OK;
+  if (a->rows == 0 && (a->d_weight.ptr || a->d_bias.ptr))
+    return fail(MUON_E_SHAPE, "no rows: the weights' gradients have none to be summed over");
+  if (a->rows == 0) return MUON_OK;
+  CHECK(ffn_mat("d_y", a->d_y, a->rows, a->out, -1));
+  if (a->act != MUON_ACT_NONE) CHECK(ffn_mat("z", a->z, a->rows, a->out, MUON_BF16));
+  if (a->d_x.ptr) {
+    CHECK(ffn_mat("weight", a->weight, a->out, a->cols, MUON_BF16));
+    CHECK(ffn_mat("d_x", a->d_x, a->rows, a->cols, MUON_BF16));
+  }
+  if (a->d_weight.ptr) {
+    CHECK(ffn_mat("x", a->x, a->rows, a->cols, MUON_BF16));
+    CHECK(ffn_mat("d_weight", a->d_weight, a->out, a->cols, -1));
+  }
+  CHECK(check_opt("d_bias", a->d_bias, 1, a->out, -1));
+  CHECK(check_workspace(ws, ws_bytes, linear_bwd_bytes(a, drop)));
+  LinearDev d = linear_dev(a, drop);
+  char* at = static_cast<char*>(ws);
+  if (linear_forms_dz(a, drop)) d.dz = at;
+  at += linear_dz_bytes(a, drop);
+  d.sums = reinterpret_cast<float*>(at);
+  d.part = reinterpret_cast<float*>(at + linear_sums_bytes(a));
+  return launched("muon_linear_bwd", launch_linear_bwd(static_cast<hipStream_t>(hip_stream), d));
+}
+
+muon_status muon_rotary(const muon_rotary_args* a, void* hip_stream) {
+  if (!a) return fail(MUON_E_ARG, "args is NULL");
+  const int64_t top = 0x7fffffff;
+  if (a->batch < 0 || a->len < 0 || a->batch > top || a->len > top || a->batch * a->len > top || a->heads < 1 ||
+      a->kv_heads < 0 || int64_t(a->heads) + a->kv_heads > 1 << 16)
+    return fail(MUON_E_SHAPE, "batch %lld, len %lld, heads %d and %d", (long long)a->batch, (long long)a->len, a->heads,
+                a->kv_heads);
+  if (a->dim < 2 || a->dim > 1024 || a->dim % 2 || a->pairs < 1 || a->pairs > a->dim / 2)
+    return fail(MUON_E_SHAPE, "dim %d (even, up to 1024), pairs %d (up to half of that)", a->dim, a->pairs);
+  if (a->axes < 1 || a->axes > 8 || (a->axes > 1 && !a->positions))
+    return fail(MUON_E_ARG, "axes %d: 1 .. 8, and 1 without positions", a->axes);
+  if ((a->interleaved | a->inverse) & ~1 || a->reserved != 0) return fail(MUON_E_ARG, "interleaved and inverse are 0 or 1, reserved 0");
+  if (a->dtype != MUON_F32 && a->dtype != MUON_BF16) return fail(MUON_E_DTYPE, "dtype %d", a->dtype);
+  if (!std::isfinite(a->scale)) return fail(MUON_E_ARG, "scale must be finite");
+  const int64_t far = int64_t(1) << 52;
+  if (a->offset > far || a->offset < -far) return fail(MUON_E_ARG, "offset beyond 2^52");
+  if (a->batch == 0 || a->len == 0) return MUON_OK;
+  if (!a->freqs || !aligned(a->freqs, 8)) return fail(a->freqs ? MUON_E_ALIGN : MUON_E_ARG, "freqs is missing or not aligned");
+  if (!aligned(a->positions, 4)) return fail(MUON_E_ALIGN, "positions not aligned");
+  if (a->positions_batch < 0 || a->positions_batch > int64_t(1) << 40) return fail(MUON_E_SHAPE, "positions_batch out of range");
+  CHECK(rotary_heads("q", a->q, a->dtype));
+  CHECK(rotary_heads("q_out", a->q_out, a->dtype));
+  if (a->kv_heads > 0) {
+    CHECK(rotary_heads("k", a->k, a->dtype));
+    CHECK(rotary_heads("k_out", a->k_out, a->dtype));
+  }
+  RotaryDev d{};
+  d.tokens = a->batch * a->len;
+  d.offset = a->offset; d.len = int32_t(a->len); d.heads = a->heads; d.kv_heads = a->kv_heads; d.dim = a->dim;
+  d.pairs = a->pairs; d.axes = a->axes; d.interleaved = a->interleaved; d.inverse = a->inverse;
+  d.f32 = a->dtype == MUON_F32; d.scale = a->scale;
+  d.freqs = a->freqs; d.positions = a->positions; d.pos_batch = a->positions_batch;
+  d.q = heads_dev(a->q); d.k = heads_dev(a->k); d.q_out = heads_dev(a->q_out); d.k_out = heads_dev(a->k_out);
+  d.in_place = same_heads(a->q, a->q_out) && (a->kv_heads == 0 || same_heads(a->k, a->k_out));
+  // Values that move at once: whole chunks of pairs and of what is copied, and
+  // runs on their boundaries.
+  int vec = 1;
+  for (int v : {8, 4}) {
+    bool fits = vec == 1 && a->pairs % v == 0 && (a->dim - 2 * a->pairs) % (2 * v) == 0;
+    for (const muon_heads* t : {&a->q, &a->q_out, &a->k, &a->k_out})
+      fits = fits && ((a->kv_heads == 0 && (t == &a->k || t == &a->k_out)) || rotary_runs(*t, a->dtype, v));
+    if (fits) vec = v;
+  }
+  return launched("muon_rotary", launch_rotary(static_cast<hipStream_t>(hip_stream), d, vec));
 }
 
 }  // extern "C"
