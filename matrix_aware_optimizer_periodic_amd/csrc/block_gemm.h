@@ -41,21 +41,28 @@ __device__ __forceinline__ void act_of(float g, float& a, float& da) {
   da = fmaf(a * dw, 1.0f / (1.0f + __expf(w)), e);
 }
 
-// The activation chosen at run time: muon_act, 2 for none.
-__device__ __forceinline__ void act_any(int act, float g, float& a, float& da) {
-  if (act == 0) act_of<0>(g, a, da);
-  else if (act == 1) act_of<1>(g, a, da);
-  else { a = g; da = 1.f; }
+// The same in one exponential and one reciprocal (each within 2^-23 of itself),
+// as the linear kernels take it: t = e^-w, e = 1 / (1 + t), and 1 - e = t e keeps
+// its digits.  Where t overflows, e is 0 and so is all that t stands in.  w' is
+// taken of a bounded g^2, so that far values give 0 times a number.  ACT 2: none.
+template <int ACT>
+__device__ __forceinline__ float act_value(float g) {
+  if constexpr (ACT == 2) return g;
+  const float w = ACT == 1 ? 1.5957691216057308f * fmaf(0.044715f * g, g * g, g) : g;
+  return g * __builtin_amdgcn_rcpf(1.0f + __expf(-w));
 }
-
-struct NoExtra {};
-// EPI_LINEAR: y = residual + drop(act(sum + bias)); a Prod's c is y (f32: its
-// type), c2 what act is taken of, gu the residual, of y's type.
-struct LinearExtra {
-  const void* bias;     // n values, or null
-  int32_t bias_bf16, act;
-  DropDev drop;
-};
+template <int ACT>
+__device__ __forceinline__ float act_slope(float g) {
+  if constexpr (ACT == 2) return 1.f;
+  float w = g, dw = 1.f;
+  if constexpr (ACT == 1) {
+    const float c = 1.5957691216057308f, g2 = fminf(g * g, 1e12f);     // 2 sqrt(2 / pi)
+    w = c * fmaf(0.044715f * g, g * g, g);
+    dw = c * fmaf(3.f * 0.044715f, g2, 1.f);
+  }
+  const float t = __expf(-w), e = __builtin_amdgcn_rcpf(1.0f + t);
+  return fmaf(g * e * (fminf(t, 3.4e38f) * e), dw, e);
+}
 
 // ---- products ---------------------------------------------------------------
 struct Prod {
@@ -84,6 +91,27 @@ struct ProdArgs {
   int32_t count;
   float* part;
 };
+
+struct NoExtra { static constexpr bool kDrop = false; };
+// EPI_LINEAR: y = residual + drop(act(sum + bias)); a Prod's c is y (f32: its
+// type), c2 what act is taken of, gu the residual, of y's type.  ACT 2 is none.
+// The activation and whether anything is dropped are template arguments: chosen
+// at run time, the epilogue of a 256-tile outgrows what the compiler unrolls, and
+// its accumulators go through scratch memory (4096 x 2048 x 8192 with gelu 223 us
+// instead of %%).
+template <bool DROP>
+struct LinearExtra {
+  static constexpr bool kDrop = DROP;
+  const void* bias;     // n values, or null
+  int32_t bias_bf16;
+  DropDev drop;
+};
+// A lane's eight values of it.
+template <class X>
+__device__ __forceinline__ void load_bias(const X& ext, const Prod& p, int64_t n, float (&bias)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) bias[k] = ext.bias && n < p.n ? load_any1(ext.bias, ext.bias_bf16, n + k) : 0.f;
+}
 
 // Stages of a tile's whole sum; a first segment's last unit is a whole one.
 __host__ __device__ inline int stages_of(const Prod& p) {
@@ -192,22 +220,16 @@ constexpr int tile_cols() { return EPI == EPI_GATE ? BT / 2 : BT; }
 // at once, the first four before the accumulators go to LDS: read one by one,
 // the dh product of 4096 x 20480 x 5120 took 967 us instead of 876.
 template <int BT, int EPI, int ACT, int XB, class X>
-__device__ __forceinline__ void emit_rows(const Prod& p, const X& ext, const f32x4_t (*acc)[BT / 32], float* er, int64_t mrow,
-                                          int64_t ncol, int lane) {
+__device__ __forceinline__ void emit_rows(const Prod& p, const X& ext, const float (&bias)[8], const f32x4_t (*acc)[BT / 32],
+                                          float* er, int64_t mrow, int64_t ncol, int lane) {
   constexpr int F = BT / 32, W = BT / 2, LDR = W + 4;
   constexpr int WOUT = tile_cols<BT, EPI>() / 2;
   constexpr int CPR = WOUT / 8, NIT = 16 * XB * CPR / 64, GRP = NIT < 4 ? NIT : 4;
   static_assert(NIT * 64 == 16 * XB * CPR && NIT % GRP == 0, "whole pieces per lane");
   const int64_t m_at = mrow + lane / CPR, n = ncol + lane % CPR * 8;   // + 64 / CPR rows per piece
   const bool n_ok = n < p.n;
-  float bias[8] = {};
   Rng rng{};
-  if constexpr (EPI == EPI_LINEAR) {
-    if (ext.drop.on) rng = rng_of(ext.drop);
-    if (ext.bias && n_ok)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) bias[k] = load_any1(ext.bias, ext.bias_bf16, n + k);
-  }
+  if constexpr (X::kDrop) rng = rng_of(ext.drop);
   u32x4_t raw[GRP][2];
   auto load_gu = [&](int it) {
     if constexpr (EPI == EPI_DGATE) {
@@ -267,6 +289,16 @@ __device__ __forceinline__ void emit_rows(const Prod& p, const X& ext, const f32
     for (int j = 0; j < GRP; ++j)
 #pragma unroll
       for (int k = 0; k < (EPI == EPI_GATE ? 4 : 2); ++k) asm volatile("" : "+v"(w[j][k]));
+    // The group's mask, two blocks of the generator at a time: formed in a loop,
+    // as bits, for the code's size (see LinearExtra).
+    uint32_t dropped = 0;
+    if constexpr (X::kDrop) {
+#pragma unroll 1
+      for (int j = GRP - 1; j >= 0; --j) {
+        const uint64_t e = uint64_t(m_at + (it + j) * (64 / CPR)) * unsigned(p.n) + uint64_t(n);
+        dropped = dropped << 8 | dropped4(ext.drop, rng, e) | dropped4(ext.drop, rng, e + 4) << 4;
+      }
+    }
 #pragma unroll
     for (int j = 0; j < GRP; ++j) {
       const int row = lane / CPR + (it + j) * (64 / CPR);
@@ -309,14 +341,11 @@ __device__ __forceinline__ void emit_rows(const Prod& p, const X& ext, const f32
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] += bias[k];
         if (p.c2) store_vals<uint16_t, 8>(p.c2, m * p.ldc2 + n, v);
-        if (ext.act != 2) {
+        if constexpr (ACT != 2) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            float d;
-            act_any(ext.act, v[k], v[k], d);
-          }
+          for (int k = 0; k < 8; ++k) v[k] = act_value<ACT>(v[k]);
         }
-        if (ext.drop.on) drop<8>(ext.drop, rng, uint64_t(m) * unsigned(p.n) + n, v);
+        if constexpr (X::kDrop) drop_by(ext.drop, dropped >> (8 * j), v);
         if (p.gu) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
@@ -518,12 +547,14 @@ __device__ __forceinline__ void run_tile(const Prod& p, const X& ext, Tile tile,
         for (int y = 0; y < F; ++y) *as_global(reinterpret_cast<f32x4_t*>(o + (x * F + y) * 256)) = acc[x][y];
     return;
   }
+  float bias[8] = {};
+  if constexpr (EPI == EPI_LINEAR) load_bias(ext, p, n0 + wn * (NSTEP / 2) + lane % (NSTEP / 16) * 8, bias);
   constexpr int XB = 2;
   static_assert(4 * 16 * XB * (BT / 2 + 4) * 4 <= kUnits * unit_bytes<BT>(), "epilogue rows fit");
   float* er = reinterpret_cast<float*>(smem) + wave * 16 * XB * (BT / 2 + 4);
 #pragma unroll
   for (int x = 0; x < F; x += XB)
-    emit_rows<BT, EPI, ACT, XB>(p, ext, &acc[x], er, m0 + wm * (BT / 2) + x * 16, n0 + wn * (NSTEP / 2), lane);
+    emit_rows<BT, EPI, ACT, XB>(p, ext, bias, &acc[x], er, m0 + wm * (BT / 2) + x * 16, n0 + wn * (NSTEP / 2), lane);
 }
 
 // MIXED_COLS: products of both kinds of A in one launch.
@@ -577,9 +608,11 @@ __device__ __forceinline__ void product_join(const ProdArgs& g, const X& ext) {
 #pragma unroll
     for (int y = 0; y < F; ++y) acc[0][y] += *as_global(reinterpret_cast<const f32x4_t*>(o + (x * F + y) * 256));
   }
-  emit_rows<BT, EPI, ACT, 1>(p, ext, acc, rows + wave * 16 * (BT / 2 + 4),
-                          int64_t(t.tm) * BT + (wave >> 1) * (BT / 2) + x * 16,
-                          int64_t(t.tn) * tile_cols<BT, EPI>() + (wave & 1) * (tile_cols<BT, EPI>() / 2), lane);
+  const int64_t ncol = int64_t(t.tn) * tile_cols<BT, EPI>() + (wave & 1) * (tile_cols<BT, EPI>() / 2);
+  float bias[8] = {};
+  if constexpr (EPI == EPI_LINEAR) load_bias(ext, p, ncol + lane % (tile_cols<BT, EPI>() / 16) * 8, bias);
+  emit_rows<BT, EPI, ACT, 1>(p, ext, bias, acc, rows + wave * 16 * (BT / 2 + 4),
+                             int64_t(t.tm) * BT + (wave >> 1) * (BT / 2) + x * 16, ncol, lane);
 }
 
 
@@ -652,9 +685,17 @@ size_t part_bytes(const ProdArgs& g, const Plan& q) {
   return ranges * q.bt * q.bt * 4;
 }
 
+// Workgroups of a launch's tiles and ranges.
+int items_of(const ProdArgs& g, const Plan& q) {
+  int items = 0;
+  for (int i = 0; i < g.count; ++i) items += q.p[i].full + (q.p[i].tiles - q.p[i].full) * q.p[i].splits;
+  return items;
+}
+
+// `more` workgroups behind the products' own do what the kernel has them do.
 template <int BT, int EPI, class... X>
 hipError_t launch_prod(hipStream_t s, ProdArgs g, const Plan& q, void (*gemm)(ProdArgs, X...), void (*join)(ProdArgs, X...),
-                       X... ext) {
+                       unsigned more, X... ext) {
   constexpr int NSTEP = tile_cols<BT, EPI>();
   int items = 0, ranges = 0, joins = 0;
   for (int i = 0; i < g.count; ++i) {
@@ -672,7 +713,7 @@ hipError_t launch_prod(hipStream_t s, ProdArgs g, const Plan& q, void (*gemm)(Pr
     ranges += split * p.splits;
     joins += split;
   }
-  hipLaunchKernelGGL(gemm, dim3(unsigned(items)), dim3(256), 0, s, g, ext...);
+  hipLaunchKernelGGL(gemm, dim3(unsigned(items) + more), dim3(256), 0, s, g, ext...);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || joins == 0) return e;
   hipLaunchKernelGGL(join, dim3(unsigned(joins * (BT / 32))), dim3(256), 0, s, g, ext...);

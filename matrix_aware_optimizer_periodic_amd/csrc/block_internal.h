@@ -150,6 +150,7 @@ struct RotaryDev {
   HeadsDev q, k, q_out, k_out;
   FastDiv by_len, by_heads, by_chunks;
 };
+// vec: pairs that move at once, 8, 4, 2 or 1; 0: value by value.
 hipError_t launch_rotary(hipStream_t s, const RotaryDev& a, int vec);
 
 }  // namespace muon

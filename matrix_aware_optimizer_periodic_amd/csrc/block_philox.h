@@ -40,6 +40,19 @@ __device__ __forceinline__ Rng rng_of(const DropDev& d) {
   return Rng{s[0], s[1]};
 }
 
+// Bit k: whether element e + k is dropped, for four elements from e (a multiple
+// of four) on.
+__device__ __forceinline__ uint32_t dropped4(const DropDev& d, const Rng& r, uint64_t e) {
+  const u32x4_t w = philox(e / 4, r.offset, r.seed);
+  return (w[0] <= d.last ? 1u : 0u) | (w[1] <= d.last ? 2u : 0u) | (w[2] <= d.last ? 4u : 0u) | (w[3] <= d.last ? 8u : 0u);
+}
+// Dropped elements as 0, whatever they held, the others scaled.
+template <int N>
+__device__ __forceinline__ void drop_by(const DropDev& d, uint32_t dropped, float (&v)[N]) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = dropped >> k & 1u ? 0.f : v[k] * d.scale;
+}
+
 // v[0 .. N - 1], elements e .. e + N - 1 (e a multiple of four): dropped ones 0,
 // whatever they held, the others scaled.
 template <int N>

@@ -43,8 +43,8 @@ __global__ __launch_bounds__(256) void ffn_join_kernel(ProdArgs g) {
 template <int LIE, int EPI, int ACT = 0>
 hipError_t run_prod(hipStream_t s, const ProdArgs& g) {
   const Plan q = plan_of(g, EPI == EPI_GATE);
-  return q.bt == 256 ? launch_prod<256, EPI>(s, g, q, &ffn_gemm_kernel<256, LIE, EPI, ACT>, &ffn_join_kernel<256, EPI, ACT>)
-                     : launch_prod<128, EPI>(s, g, q, &ffn_gemm_kernel<128, LIE, EPI, ACT>, &ffn_join_kernel<128, EPI, ACT>);
+  return q.bt == 256 ? launch_prod<256, EPI>(s, g, q, &ffn_gemm_kernel<256, LIE, EPI, ACT>, &ffn_join_kernel<256, EPI, ACT>, 0)
+                     : launch_prod<128, EPI>(s, g, q, &ffn_gemm_kernel<128, LIE, EPI, ACT>, &ffn_join_kernel<128, EPI, ACT>, 0);
 }
 
 ProdArgs backward_sizes(int64_t t, int64_t d, int64_t h) {

@@ -14,38 +14,27 @@
 namespace muon {
 namespace {
 
-template <int BT>
-__global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void linear_kernel(ProdArgs g, LinearExtra ext) {
-  product_tile<BT, ROWS_ROWS, EPI_LINEAR, 0>(g, ext);
+template <int BT, int ACT, bool DROP>
+__global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void linear_kernel(ProdArgs g, LinearExtra<DROP> ext) {
+  product_tile<BT, ROWS_ROWS, EPI_LINEAR, ACT>(g, ext);
 }
-template <int BT>
-__global__ __launch_bounds__(256) void linear_join_kernel(ProdArgs g, LinearExtra ext) {
-  product_join<BT, EPI_LINEAR, 0>(g, ext);
+template <int BT, int ACT, bool DROP>
+__global__ __launch_bounds__(256) void linear_join_kernel(ProdArgs g, LinearExtra<DROP> ext) {
+  product_join<BT, EPI_LINEAR, ACT>(g, ext);
 }
-template <int BT>
-__global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void linear_grads_kernel(ProdArgs g) {
-  product_tile<BT, MIXED_COLS, EPI_PLAIN, 0>(g, NoExtra{});
-}
-template <int BT>
-__global__ __launch_bounds__(256) void linear_grads_join_kernel(ProdArgs g) {
-  product_join<BT, EPI_PLAIN, 0>(g, NoExtra{});
-}
-
 // ---- few rows -----------------------------------------------------------------
 template <int MT, int NW>
-__global__ __launch_bounds__(64 * NW, NW / 8) void linear_few_rows_kernel(Prod p, LinearExtra ext) {
+__global__ __launch_bounds__(64 * NW, NW / 8) void linear_few_rows_kernel(Prod p, LinearExtra<true> ext, int act) {
   f32x4_t sum[1];
   int64_t m, n;
   if (!few_rows_sums<MT, false, NW>(p, sum, m, n)) return;
+  asm volatile("" : "+v"(sum[0]));     // (nothing below moves up among the sum's reads, whose registers it would spill)
   float v[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) v[k] = sum[0][k] + (ext.bias ? load_any1(ext.bias, ext.bias_bf16, n + k) : 0.f);
   if (p.c2) store4(p.c2, m * p.ldc2 + n, f32x4_t{v[0], v[1], v[2], v[3]});
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    float d;
-    act_any(ext.act, v[k], v[k], d);
-  }
+  for (int k = 0; k < 4; ++k) v[k] = act == 0 ? act_value<0>(v[k]) : act == 1 ? act_value<1>(v[k]) : v[k];
   if (ext.drop.on) drop<4>(ext.drop, rng_of(ext.drop), uint64_t(m) * unsigned(p.n) + n, v);
   const int64_t r = m * p.ldgu + n, c = m * p.ldc + n;
   if (p.gu) {
@@ -62,7 +51,7 @@ bool few_rows(int64_t t, int64_t d, int64_t n) {
   return t <= 64 && t * dn * (2.0 / 16) / 7e6 <= 4 + weights_us / 8;
 }
 
-hipError_t run_few_rows(hipStream_t s, const Prod& p, const LinearExtra& ext) {
+hipError_t run_few_rows(hipStream_t s, const Prod& p, const LinearExtra<true>& ext, int act) {
   const int cols = p.m <= 8 ? 8 : 16;
   const unsigned grid = unsigned((p.n + cols - 1) / cols);
   const bool wide = grid <= 256;      // a workgroup per CU at most: more waves to each
@@ -70,14 +59,26 @@ hipError_t run_few_rows(hipStream_t s, const Prod& p, const LinearExtra& ext) {
             : p.m <= 16 ? (wide ? linear_few_rows_kernel<1, 16> : linear_few_rows_kernel<1, 8>)
             : p.m <= 32 ? (wide ? linear_few_rows_kernel<2, 16> : linear_few_rows_kernel<2, 8>)
                         : (wide ? linear_few_rows_kernel<4, 16> : linear_few_rows_kernel<4, 8>);
-  hipLaunchKernelGGL(k, dim3(grid), dim3(wide ? 1024 : 512), 0, s, p, ext);
+  hipLaunchKernelGGL(k, dim3(grid), dim3(wide ? 1024 : 512), 0, s, p, ext, act);
   return hipGetLastError();
+}
+
+template <int ACT, bool DROP>
+hipError_t run_linear(hipStream_t s, const ProdArgs& g, const LinearDev& f) {
+  const Plan q = plan_of(g, false);
+  const LinearExtra<DROP> ext{f.bias.p, f.bias.dt, f.drop};
+  return q.bt == 256 ? launch_prod<256, EPI_LINEAR>(s, g, q, &linear_kernel<256, ACT, DROP>, &linear_join_kernel<256, ACT, DROP>, 0, ext)
+                     : launch_prod<128, EPI_LINEAR>(s, g, q, &linear_kernel<128, ACT, DROP>, &linear_join_kernel<128, ACT, DROP>, 0, ext);
 }
 
 // ---- dz and d_bias --------------------------------------------------------------
 // A thread has eight columns of every 256 / width-th row of its workgroup's
-// share, `width` threads beside each other; the shares' column sums are added in
-// a fixed order, by the rows within a workgroup and then by the second kernel.
+// share, `width` threads beside each other, and reads kAhead rows before it works
+// on them.  The shares' column sums are added in a fixed order: by the rows
+// within a workgroup, then by the workgroups behind the gradients' products (or
+// by a kernel of their own).  Bound by memory: the slope of an activation is some
+// fifteen instructions (with divisions it was sixty, and as long as the memory).
+constexpr int kAhead = 4;
 struct DzShape {
   int width_log;         // threads along the columns: 1 << width_log
   int blocks;            // workgroups along the columns
@@ -89,15 +90,15 @@ DzShape dz_shape(int64_t rows, int64_t out) {
   const int64_t chunks = out / 8;
   while (d.width_log < 6 && (int64_t(1) << d.width_log) < chunks) ++d.width_log;
   d.blocks = int((chunks + (1 << d.width_log) - 1) >> d.width_log);
-  const int64_t turn = 256 >> d.width_log;                       // rows at a time
-  const int64_t most = (rows + 4 * turn - 1) / (4 * turn);
-  d.splits = int(std::max<int64_t>(1, std::min<int64_t>(most, std::min<int64_t>(512, 1024 / d.blocks))));
-  d.rows = (rows + d.splits - 1) / d.splits;
+  const int64_t turn = kAhead * (256 >> d.width_log);            // rows at a time
+  const int64_t turns = (rows + turn - 1) / turn;
+  d.splits = int(std::max<int64_t>(1, std::min<int64_t>(turns, std::min<int64_t>(512, 1024 / d.blocks))));
+  d.rows = (turns + d.splits - 1) / d.splits * turn;
   d.splits = int((rows + d.rows - 1) / d.rows);
   return d;
 }
 
-template <typename T>
+template <typename T, int ACT>
 __global__ __launch_bounds__(256) void linear_dz_kernel(LinearDev a, DzShape d) {
   __shared__ float red[256][9];
   const int cc = threadIdx.x & ((1 << d.width_log) - 1), rr = threadIdx.x >> d.width_log, turn = 256 >> d.width_log;
@@ -106,22 +107,26 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinearDev a, DzShape d) 
   const Rng rng = a.drop.on ? rng_of(a.drop) : Rng{};
   float sum[8] = {};
   if (n < a.out) {
-    for (int64_t r = int64_t(blockIdx.y) * d.rows + rr; r < end; r += turn) {
-      float v[8], z[8];
-      load_vals<T, 8>(a.d_y.p, r * a.d_y.ld + n, v);
-      if (a.act != 2) load_vals<uint16_t, 8>(a.z.p, r * a.z.ld + n, z);
-      if (a.drop.on) drop<8>(a.drop, rng, uint64_t(r) * uint64_t(a.out) + n, v);
-      if (a.act != 2) {
+    for (int64_t r0 = int64_t(blockIdx.y) * d.rows + rr; r0 < end; r0 += kAhead * turn) {
+      float v[kAhead][8], z[kAhead][8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          float f, df;
-          act_any(a.act, z[k], f, df);
-          v[k] *= df;
-        }
+      for (int i = 0; i < kAhead; ++i) {
+        const int64_t r = min(r0 + i * turn, end - 1);           // (past the end: the last one again)
+        load_vals<T, 8>(a.d_y.p, r * a.d_y.ld + n, v[i]);
+        if constexpr (ACT != 2) load_vals<uint16_t, 8>(a.z.p, r * a.z.ld + n, z[i]);
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) sum[k] += v[k];
-      if (a.dz) store_vals<uint16_t, 8>(a.dz, r * a.out + n, v);
+      for (int i = 0; i < kAhead; ++i) {
+        const int64_t r = r0 + i * turn;
+        if (r >= end) break;
+        if (a.drop.on) drop<8>(a.drop, rng, uint64_t(r) * uint64_t(a.out) + n, v[i]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if constexpr (ACT != 2) v[i][k] *= act_slope<ACT>(z[i][k]);
+          sum[k] += v[i][k];
+        }
+        if (a.dz) store_vals<uint16_t, 8>(a.dz, r * a.out + n, v[i]);
+      }
     }
   }
   if (!a.d_bias.p) return;
@@ -138,13 +143,32 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinearDev a, DzShape d) 
   }
 }
 
-__global__ __launch_bounds__(256) void linear_bias_kernel(LinearDev a, int splits) {
-  const int64_t n = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (n >= a.out) return;
+// The shares' sums of 256 columns: what a workgroup adds of them.
+struct BiasSums {
+  const float* sums;     // [splits][out]
+  NormMat d_bias;
+  int64_t out;
+  int32_t splits;
+  int32_t item0;         // the first workgroup of a launch that does this
+};
+__device__ __forceinline__ void add_bias_sums(const BiasSums& b, int block) {
+  const int64_t n = int64_t(block) * 256 + threadIdx.x;
+  if (n >= b.out) return;
   float s = 0.f;
 #pragma unroll 8
-  for (int i = 0; i < splits; ++i) s += a.sums[i * a.out + n];
-  store_any1(a.d_bias.p, a.d_bias.dt, n, s);
+  for (int i = 0; i < b.splits; ++i) s += as_global(b.sums)[i * b.out + n];
+  store_any1(b.d_bias.p, b.d_bias.dt, n, s);
+}
+__global__ __launch_bounds__(256) void linear_bias_kernel(BiasSums b) { add_bias_sums(b, int(blockIdx.x)); }
+
+template <int BT>
+__global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void linear_grads_kernel(ProdArgs g, BiasSums b) {
+  if (int(blockIdx.x) >= b.item0) return add_bias_sums(b, int(blockIdx.x) - b.item0);
+  product_tile<BT, MIXED_COLS, EPI_PLAIN, 0>(g, NoExtra{});
+}
+template <int BT>
+__global__ __launch_bounds__(256) void linear_grads_join_kernel(ProdArgs g, BiasSums) {
+  product_join<BT, EPI_PLAIN, 0>(g, NoExtra{});
 }
 
 // ---- the gradients' products --------------------------------------------------
@@ -181,26 +205,35 @@ hipError_t launch_linear_fwd(hipStream_t s, const LinearDev& f) {
   p.c = f.y.p; p.ldc = f.y.ld; p.f32 = f.y.dt == 0;
   p.c2 = f.z.p; p.ldc2 = f.z.ld;
   p.gu = f.resid.p; p.ldgu = f.resid.ld;
-  const LinearExtra ext{f.bias.p, f.bias.dt, f.act, f.drop};
-  if (few_rows(f.rows, f.cols, f.out)) return run_few_rows(s, p, ext);
-  const Plan q = plan_of(g, false);
-  return q.bt == 256 ? launch_prod<256, EPI_LINEAR>(s, g, q, &linear_kernel<256>, &linear_join_kernel<256>, ext)
-                     : launch_prod<128, EPI_LINEAR>(s, g, q, &linear_kernel<128>, &linear_join_kernel<128>, ext);
+  if (few_rows(f.rows, f.cols, f.out)) return run_few_rows(s, p, LinearExtra<true>{f.bias.p, f.bias.dt, f.drop}, f.act);
+  if (f.drop.on) return f.act == 0 ? run_linear<0, true>(s, g, f) : f.act == 1 ? run_linear<1, true>(s, g, f) : run_linear<2, true>(s, g, f);
+  return f.act == 0 ? run_linear<0, false>(s, g, f) : f.act == 1 ? run_linear<1, false>(s, g, f) : run_linear<2, false>(s, g, f);
+}
+
+template <typename T>
+void launch_dz(hipStream_t s, const LinearDev& f, const DzShape& d) {
+  auto* k = f.act == 0 ? linear_dz_kernel<T, 0> : f.act == 1 ? linear_dz_kernel<T, 1> : linear_dz_kernel<T, 2>;
+  hipLaunchKernelGGL(k, dim3(unsigned(d.blocks), unsigned(d.splits)), dim3(256), 0, s, f, d);
 }
 
 hipError_t launch_linear_bwd(hipStream_t s, const LinearDev& f) {
+  BiasSums b{};
+  unsigned bias_blocks = 0;
   if (f.dz || f.d_bias.p) {
     const DzShape d = dz_shape(f.rows, f.out);
-    auto* k = f.d_y.dt ? linear_dz_kernel<uint16_t> : linear_dz_kernel<float>;
-    hipLaunchKernelGGL(k, dim3(unsigned(d.blocks), unsigned(d.splits)), dim3(256), 0, s, f, d);
-    hipError_t e = hipGetLastError();
+    if (f.d_y.dt) launch_dz<uint16_t>(s, f, d);
+    else launch_dz<float>(s, f, d);
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (f.d_bias.p && d.splits > 1) {
-      hipLaunchKernelGGL(linear_bias_kernel, dim3(unsigned((f.out + 255) / 256)), dim3(256), 0, s, f, d.splits);
-      if ((e = hipGetLastError()) != hipSuccess) return e;
+      b = BiasSums{f.sums, f.d_bias, f.out, d.splits, 0};
+      bias_blocks = unsigned((f.out + 255) / 256);
     }
   }
-  if (!f.d_x.p && !f.d_w.p) return hipSuccess;
+  if (!f.d_x.p && !f.d_w.p) {
+    if (bias_blocks) hipLaunchKernelGGL(linear_bias_kernel, dim3(bias_blocks), dim3(256), 0, s, b);
+    return hipGetLastError();
+  }
   ProdArgs g = grad_sizes(f.rows, f.cols, f.out, f.d_x.p, f.d_w.p);
   g.part = f.part;
   const void* dz = f.dz ? f.dz : f.d_y.p;
@@ -217,8 +250,9 @@ hipError_t launch_linear_bwd(hipStream_t s, const LinearDev& f) {
     }
   }
   const Plan q = plan_of(g, false);
-  return q.bt == 256 ? launch_prod<256, EPI_PLAIN>(s, g, q, &linear_grads_kernel<256>, &linear_grads_join_kernel<256>)
-                     : launch_prod<128, EPI_PLAIN>(s, g, q, &linear_grads_kernel<128>, &linear_grads_join_kernel<128>);
+  b.item0 = items_of(g, q);
+  return q.bt == 256 ? launch_prod<256, EPI_PLAIN>(s, g, q, &linear_grads_kernel<256>, &linear_grads_join_kernel<256>, bias_blocks, b)
+                     : launch_prod<128, EPI_PLAIN>(s, g, q, &linear_grads_kernel<128>, &linear_grads_join_kernel<128>, bias_blocks, b);
 }
 
 }  // namespace muon

@@ -14,38 +14,46 @@ namespace {
 
 __device__ __forceinline__ uint32_t over(uint32_t n, const FastDiv& d) { return (__umulhi(n, d.mul) + n) >> d.shift; }
 
-// V consecutive values, V 8 (16-byte aligned), 4 (8-byte aligned bf16, 16-byte
-// aligned fp32) or 1.
-template <typename T, int V>
-__device__ __forceinline__ void load_run(const void* p, int64_t e, float (&v)[V]) {
-  if constexpr (V != 4) {
-    load_vals<T, V>(p, e, v);
-  } else if constexpr (sizeof(T) == 4) {
-    const f32x4_t a = *as_global(reinterpret_cast<const f32x4_t*>(static_cast<const float*>(p) + e));
+// N consecutive values, aligned to their size (to 16 bytes where that is more).
+template <typename T, int N>
+__device__ __forceinline__ void load_run(const void* p, int64_t e, float* v) {
+  if constexpr (N == 16 || N == 8 || N == 1) {
+    constexpr int M = N == 16 ? 8 : N;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = a[k];
+    for (int i = 0; i < N; i += M) load_vals<T, M>(p, e + i, *reinterpret_cast<float(*)[M]>(v + i));
   } else {
-    const u32x2_t u = *as_global(reinterpret_cast<const u32x2_t*>(static_cast<const uint16_t*>(p) + e));
+    uint32_t w[N * sizeof(T) / 4];
+    const auto* q = as_global(reinterpret_cast<const uint32_t*>(static_cast<const T*>(p) + e));
+    if constexpr (sizeof w == 16) *reinterpret_cast<u32x4_t*>(w) = *(const MUON_GLOBAL u32x4_t*)q;
+    else if constexpr (sizeof w == 8) *reinterpret_cast<u32x2_t*>(w) = *(const MUON_GLOBAL u32x2_t*)q;
+    else w[0] = q[0];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) { v[2 * k] = bf16_to_f32(u[k] & 0xffffu); v[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u); }
+    for (int k = 0; k < N; ++k) v[k] = sizeof(T) == 4 ? __uint_as_float(w[k]) : k & 1 ? __uint_as_float(w[k / 2] & 0xffff0000u) : bf16_to_f32(w[k / 2] & 0xffffu);
   }
 }
-template <typename T, int V>
-__device__ __forceinline__ void store_run(void* p, int64_t e, const float (&v)[V]) {
-  if constexpr (V != 4) {
-    store_vals<T, V>(p, e, v);
-  } else if constexpr (sizeof(T) == 4) {
-    *as_global(reinterpret_cast<f32x4_t*>(static_cast<float*>(p) + e)) = f32x4_t{v[0], v[1], v[2], v[3]};
+template <typename T, int N>
+__device__ __forceinline__ void store_run(void* p, int64_t e, const float* v) {
+  if constexpr (N == 16 || N == 8 || N == 1) {
+    constexpr int M = N == 16 ? 8 : N;
+#pragma unroll
+    for (int i = 0; i < N; i += M) store_vals<T, M>(p, e + i, *reinterpret_cast<const float(*)[M]>(v + i));
   } else {
-    *as_global(reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(p) + e)) =
-        u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    uint32_t w[N * sizeof(T) / 4];
+#pragma unroll
+    for (int k = 0; k < int(sizeof w / 4); ++k) w[k] = sizeof(T) == 4 ? __float_as_uint(v[k]) : pack_bf16x2(v[2 * k], v[2 * k + 1]);
+    auto* q = as_global(reinterpret_cast<uint32_t*>(static_cast<T*>(p) + e));
+    if constexpr (sizeof w == 16) *(MUON_GLOBAL u32x4_t*)q = *reinterpret_cast<u32x4_t*>(w);
+    else if constexpr (sizeof w == 8) *(MUON_GLOBAL u32x2_t*)q = *reinterpret_cast<u32x2_t*>(w);
+    else q[0] = w[0];
   }
 }
 
 constexpr int kAngles = 2048;          // cosines and sines of a workgroup
 
+enum { HALVES = 0, NEIGHBOURS = 1, NEIGHBOURS_APART = 2 };   // the last: pairs off their boundary, value by value
+
 // V: pairs of a thread's chunk.
-template <typename T, int V, bool PAIRED>
+template <typename T, int V, int LIE>
 __global__ __launch_bounds__(256) void rotary_kernel(RotaryDev a, int group) {
   __shared__ f32x2_t cs[kAngles];
   const int heads = a.heads + a.kv_heads, turned = a.pairs / V;
@@ -79,30 +87,33 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryDev a, int group) {
       const HeadsDev& out = is_k ? a.k_out : a.q_out;
       const int64_t from = b * in.sb + at * in.sl + h * in.sh, to = b * out.sb + at * out.sl + h * out.sh;
       const bool turn = int(c) < turned;
-      // the two runs of V values of this chunk
-      const int first = turn && !PAIRED ? int(c) * V : int(c) * 2 * V;
-      const int second = turn && !PAIRED ? first + a.pairs : first + V;
-      float u[V], v[V];
-      load_run<T, V>(in.p, from + first, u);
-      load_run<T, V>(in.p, from + second, v);
+      // this chunk's 2 V values: one run, or one of each half
+      const int first = turn && LIE == HALVES ? int(c) * V : int(c) * 2 * V;
+      const int second = turn && LIE == HALVES ? first + a.pairs : first + V;
+      float x[2 * V];
+      if constexpr (LIE == NEIGHBOURS) {
+        load_run<T, 2 * V>(in.p, from + first, x);
+      } else {
+        load_run<T, V>(in.p, from + first, x);
+        load_run<T, V>(in.p, from + second, x + V);
+      }
       if (turn) {
         const f32x2_t* w = cs + tt * a.pairs + c * V;
-        float x[2 * V];
-#pragma unroll
-        for (int k = 0; k < V; ++k) { x[k] = u[k]; x[V + k] = v[k]; }
 #pragma unroll
         for (int k = 0; k < V; ++k) {
           const f32x2_t t = w[k];
-          const int iu = PAIRED ? 2 * k : k, iv = PAIRED ? 2 * k + 1 : V + k;
+          const int iu = LIE ? 2 * k : k, iv = LIE ? 2 * k + 1 : V + k;
           const float p = x[iu], q = x[iv];
           x[iu] = fmaf(p, t[0], -(q * t[1]));
           x[iv] = fmaf(q, t[0], p * t[1]);
         }
-#pragma unroll
-        for (int k = 0; k < V; ++k) { u[k] = x[k]; v[k] = x[V + k]; }
       }
-      store_run<T, V>(out.p, to + first, u);
-      store_run<T, V>(out.p, to + second, v);
+      if constexpr (LIE == NEIGHBOURS) {
+        store_run<T, 2 * V>(out.p, to + first, x);
+      } else {
+        store_run<T, V>(out.p, to + first, x);
+        store_run<T, V>(out.p, to + second, x + V);
+      }
     }
     __syncthreads();
   }
@@ -112,7 +123,7 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryDev a, int group) {
 
 hipError_t launch_rotary(hipStream_t s, const RotaryDev& a0, int vec) {
   RotaryDev a = a0;
-  const int heads = a.heads + a.kv_heads, chunks = (a.in_place ? 2 * a.pairs : a.dim) / (2 * vec);
+  const int heads = a.heads + a.kv_heads, chunks = (a.in_place ? 2 * a.pairs : a.dim) / (vec ? 2 * vec : 2);
   a.by_len = fast_div(uint32_t(a.len));
   a.by_heads = fast_div(uint32_t(heads));
   a.by_chunks = fast_div(uint32_t(chunks));
@@ -123,8 +134,16 @@ hipError_t launch_rotary(hipStream_t s, const RotaryDev& a0, int vec) {
   const unsigned grid = unsigned(groups < (1 << 20) ? groups : 1 << 20);
   auto pick = [&](auto type) {
     using T = decltype(type);
-    return a.interleaved ? (vec == 8 ? rotary_kernel<T, 8, true> : vec == 4 ? rotary_kernel<T, 4, true> : rotary_kernel<T, 1, true>)
-                         : (vec == 8 ? rotary_kernel<T, 8, false> : vec == 4 ? rotary_kernel<T, 4, false> : rotary_kernel<T, 1, false>);
+    if (a.interleaved)
+      return vec == 8   ? rotary_kernel<T, 8, NEIGHBOURS>
+             : vec == 4 ? rotary_kernel<T, 4, NEIGHBOURS>
+             : vec == 2 ? rotary_kernel<T, 2, NEIGHBOURS>
+             : vec == 1 ? rotary_kernel<T, 1, NEIGHBOURS>
+                        : rotary_kernel<T, 1, NEIGHBOURS_APART>;
+    return vec == 8   ? rotary_kernel<T, 8, HALVES>
+           : vec == 4 ? rotary_kernel<T, 4, HALVES>
+           : vec == 2 ? rotary_kernel<T, 2, HALVES>
+                      : rotary_kernel<T, 1, HALVES>;
   };
   auto* k = a.f32 ? pick(float{}) : pick(uint16_t{});
   hipLaunchKernelGGL(k, dim3(grid), dim3(256), 0, s, a, group);
