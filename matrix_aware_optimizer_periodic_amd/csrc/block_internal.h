@@ -148,7 +148,7 @@ struct RotaryDev {
   const int32_t* positions;   // [batch or 1][len][axes], or null: token + offset
   int64_t pos_batch;      // positions of a sample (0: shared)
   HeadsDev q, k, q_out, k_out;
-  FastDiv by_len, by_heads, by_chunks;
+  FastDiv by_len, by_heads, by_kv_heads, by_chunks;
 };
 // vec: pairs that move at once, 8, 4, 2 or 1; 0: value by value.
 hipError_t launch_rotary(hipStream_t s, const RotaryDev& a, int vec);

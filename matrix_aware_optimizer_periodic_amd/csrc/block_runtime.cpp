@@ -636,11 +636,12 @@ muon_status muon_rotary(const muon_rotary_args* a, void* hip_stream) {
   d.freqs = a->freqs; d.positions = a->positions; d.pos_batch = a->positions_batch;
   d.q = heads_dev(a->q); d.k = heads_dev(a->k); d.q_out = heads_dev(a->q_out); d.k_out = heads_dev(a->k_out);
   d.in_place = same_heads(a->q, a->q_out) && (a->kv_heads == 0 || same_heads(a->k, a->k_out));
-  // Pairs that move at once: whole chunks of them and of what is copied, and
-  // runs on their boundaries (0: not even a pair of neighbours is).
+  // Pairs that move at once: whole chunks of a head (of halves, all of whose pairs
+  // turn or none), and runs on their boundaries (0: not even a pair of neighbours
+  // is).
   int vec = 0;
   for (int v : {8, 4, 2, 1}) {
-    bool fits = vec == 0 && a->pairs % v == 0 && (a->dim - 2 * a->pairs) % (2 * v) == 0;
+    bool fits = vec == 0 && a->dim % (2 * v) == 0 && (a->interleaved || a->pairs % v == 0);
     for (const muon_heads* t : {&a->q, &a->q_out, &a->k, &a->k_out})
       fits = fits && ((a->kv_heads == 0 && (t == &a->k || t == &a->k_out)) || rotary_runs(*t, a->dtype, a->interleaved ? 2 * v : v));
     if (fits) vec = v;
