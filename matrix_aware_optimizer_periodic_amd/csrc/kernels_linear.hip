@@ -45,10 +45,18 @@ __global__ __launch_bounds__(64 * NW, NW / 8) void linear_few_rows_kernel(Prod p
   else store4(p.c, c, f32x4_t{v[0], v[1], v[2], v[3]});
 }
 
+// Every workgroup reads all of x, so the time grows with rows x cols x out where
+// tiles take the weights' time and 8 to 12 us.  In us, here against tiles, with
+// weights from memory: 256 -> 2048 columns 4 against 8 for 64 rows; 2048 -> 2048 5
+// against 12 for one row, 12.2 against 13.8 for 64; 2048 -> 12288 11 against 19,
+// 16 against 19 for 16, 20 against 20 for 24; 8192 -> 2048 18 against 19 for 12;
+// 5120 -> 5120 17 against 19 for 8, 24 against 19 for 12; 5120 -> 20480 43 against
+// 44.5 for 4, 53 against 45 for 8; 5120 -> 30720 62 against 64 for 4, 76 against
+// 64 for 8.
 bool few_rows(int64_t t, int64_t d, int64_t n) {
-  const double dn = double(d) * n, weights_us = 2 * dn / 5.1e6;
-  if (t <= 8) return t * dn * (2.0 / 8) / 23e6 <= 12;
-  return t <= 64 && t * dn * (2.0 / 16) / 7e6 <= 4 + weights_us / 8;
+  const double dn = double(d) * n;
+  if (t <= 8) return t * dn <= 4.6e8;
+  return t <= 64 && (t * dn <= 2.7e8 || (t * d <= 50000 && dn <= 3e7));
 }
 
 hipError_t run_few_rows(hipStream_t s, const Prod& p, const LinearExtra<true>& ext, int act) {
@@ -171,6 +179,128 @@ __global__ __launch_bounds__(256) void linear_grads_join_kernel(ProdArgs g, Bias
   product_join<BT, EPI_PLAIN, 0>(g, NoExtra{});
 }
 
+// ---- the weight's gradient from few rows ----------------------------------------
+// dW = dz^T x of up to 16 rows, bound by writing dW.  A wave keeps the x of 256
+// columns as fragments and goes down the columns of dz, four at a time, with
+// MFMAs of 16 blocks of 4 x 4: a block's rows are columns of x, so that a lane ends
+// with eight consecutive values of a row of dW and 16 lanes write 256 bytes beside
+// each other (512 in fp32).  MFMAs of one 16 x 16 block leave 64 bytes to four
+// lanes: 8 rows of 5120 -> 30720 columns, both gradients, 187 us.  The stores are
+// non-temporal: as others they leave the caches full of dW, and reading W for d_x
+// next to it takes 98 us instead of 57 (in all 159, now 132: 4.8 TB/s; as tiles of
+// one launch with d_x 158).  d_bias, where it is wanted here, comes from the same
+// columns of dz.
+constexpr int kOuterCols = 256;          // of a wave, four waves beside each other
+constexpr int kOuterGroups = 1024;       // workgroups of a launch, about
+constexpr int kOuterRows = 256;          // columns of dz that a workgroup holds
+struct Outer {
+  const void *dz, *x;
+  int64_t ld_dz, ld_x, n, d;
+  NormMat dw, d_bias;
+  int32_t rows, span;                    // columns of dz to a workgroup, a multiple of four
+};
+
+// v_mfma_f32_4x4x4_16b_bf16: lane 4 b + i gives row (A) or column (B) i of block b,
+// four k; result v of lane 4 b + j is row v, column j of block b.
+__device__ __forceinline__ f32x4_t mfma4(u32x2_t a, u32x2_t b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(__builtin_bit_cast(s16x4_t, a), __builtin_bit_cast(s16x4_t, b), c, 0, 0, 0);
+}
+
+// Lane i of four holds row i of a 4 x 4 block of bf16; afterwards column i.
+__device__ __forceinline__ u32x2_t turned4(u32x2_t a, int i) {
+  unsigned v[4];
+  auto from = [&](auto j) {
+    constexpr int J = decltype(j)::value;
+    const unsigned lo = unsigned(__builtin_amdgcn_mov_dpp(int(a[0]), J * 0x55, 0xf, 0xf, true));
+    const unsigned hi = unsigned(__builtin_amdgcn_mov_dpp(int(a[1]), J * 0x55, 0xf, 0xf, true));
+    v[J] = ((i & 2 ? hi : lo) >> (16 * (i & 1))) & 0xffffu;
+  };
+  from(std::integral_constant<int, 0>{});
+  from(std::integral_constant<int, 1>{});
+  from(std::integral_constant<int, 2>{});
+  from(std::integral_constant<int, 3>{});
+  return u32x2_t{v[0] | v[1] << 16, v[2] | v[3] << 16};
+}
+
+// KT: steps of four rows.
+template <bool F32, int KT>
+__global__ __launch_bounds__(256) void linear_outer_kernel(Outer o) {
+  __shared__ __attribute__((aligned(16))) uint16_t z[kOuterRows * 4 * KT];        // [column of dz][row]
+  const int lane = threadIdx.x & 63, b = lane >> 2, i = lane & 3;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t n0 = int64_t(blockIdx.x) * o.span, c0 = (int64_t(blockIdx.y) * 4 + wave) * kOuterCols;
+  const int here = int(min(int64_t(o.span), o.n - n0));
+  const auto* dz = as_global(static_cast<const uint16_t*>(o.dz));
+  const auto* x = as_global(static_cast<const uint16_t*>(o.x));
+  for (int t = wave; t < 4 * KT; t += 4)
+    for (int n = lane; n < here; n += 64) z[n * 4 * KT + t] = t < o.rows ? dz[t * o.ld_dz + n0 + n] : uint16_t(0);
+  constexpr int G = kOuterCols / 128;
+  u32x2_t fx[G][2][KT];
+#pragma unroll
+  for (int g = 0; g < G; ++g)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int k = 0; k < KT; ++k) {
+        const int64_t c = c0 + 128 * g + 8 * b + 4 * h;
+        u32x2_t v{0, 0};
+        if (c < o.d && 4 * k + i < o.rows) v = *reinterpret_cast<const MUON_GLOBAL u32x2_t*>(x + (4 * k + i) * o.ld_x + c);
+        fx[g][h][k] = turned4(v, i);
+      }
+  __syncthreads();
+  if (blockIdx.y == 0 && o.d_bias.p && int(threadIdx.x) < here) {
+    float s = 0.f;
+#pragma unroll
+    for (int t = 0; t < 4 * KT; ++t) s += bf16_to_f32(z[threadIdx.x * 4 * KT + t]);
+    store_any1(o.d_bias.p, o.d_bias.dt, n0 + threadIdx.x, s);
+  }
+  if (c0 >= o.d) return;
+  for (int n = i; n < here; n += 4) {        // (here is a multiple of four)
+    u32x2_t fz[KT];
+#pragma unroll
+    for (int k = 0; k < KT; ++k) fz[k] = *(const MUON_LOCAL u32x2_t*)(const MUON_LOCAL uint16_t*)(z + n * 4 * KT + 4 * k);
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      f32x4_t acc[2] = {(f32x4_t)(0.f), (f32x4_t)(0.f)};
+#pragma unroll
+      for (int k = 0; k < KT; ++k) {
+        acc[0] = mfma4(fx[g][0][k], fz[k], acc[0]);
+        acc[1] = mfma4(fx[g][1][k], fz[k], acc[1]);
+      }
+      const int64_t c = c0 + 128 * g + 8 * b;
+      if (c < o.d) {
+        const int64_t at = (n0 + n) * o.dw.ld + c;
+        if constexpr (F32) {
+          auto* w = as_global(reinterpret_cast<f32x4_t*>(static_cast<float*>(o.dw.p) + at));
+          __builtin_nontemporal_store(acc[0], w);
+          __builtin_nontemporal_store(acc[1], w + 1);
+        } else {
+          const u32x4_t w{pack_bf16x2(acc[0][0], acc[0][1]), pack_bf16x2(acc[0][2], acc[0][3]),
+                          pack_bf16x2(acc[1][0], acc[1][1]), pack_bf16x2(acc[1][2], acc[1][3])};
+          __builtin_nontemporal_store(w, as_global(reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(o.dw.p) + at)));
+        }
+      }
+    }
+  }
+}
+
+// In us, both gradients, here against tiles: 8 rows 5120 -> 5120 34 against 37, 20480
+// -> 5120 95 against 103, 2048 -> 8192 32 against 29; 16 rows 5120 -> 30720 135
+// against 159, 20480 -> 5120 98 against 104, 5120 -> 5120 41 against 37; 24 rows
+// 5120 -> 30720 157 against 160 and elsewhere slower.
+bool outer_rows(int64_t t, int64_t d, int64_t n) { return t <= 8 ? d * n >= 25000000 : t <= 16 && d * n >= 100000000; }
+
+hipError_t run_outer(hipStream_t s, const Outer& o0) {
+  Outer o = o0;
+  const int64_t groups = (o.d + 4 * kOuterCols - 1) / (4 * kOuterCols);
+  o.span = int32_t(std::min<int64_t>(kOuterRows, std::max<int64_t>(16, (o.n * groups / kOuterGroups + 3) / 4 * 4)));
+  const dim3 grid(unsigned((o.n + o.span - 1) / o.span), unsigned(groups));
+  auto* k = o.rows <= 8 ? (o.dw.dt ? linear_outer_kernel<false, 2> : linear_outer_kernel<true, 2>)
+                        : (o.dw.dt ? linear_outer_kernel<false, 4> : linear_outer_kernel<true, 4>);
+  hipLaunchKernelGGL(k, grid, dim3(256), 0, s, o);
+  return hipGetLastError();
+}
+
 // ---- the gradients' products --------------------------------------------------
 ProdArgs grad_sizes(int64_t t, int64_t d, int64_t n, bool d_x, bool d_w) {
   ProdArgs g{};
@@ -191,8 +321,8 @@ size_t linear_fwd_part_bytes(int64_t t, int64_t d, int64_t n) {
 }
 size_t linear_bwd_part_bytes(int64_t t, int64_t d, int64_t n, bool d_x, bool d_w) {
   if (t == 0 || !(d_x || d_w)) return 0;
-  const ProdArgs g = grad_sizes(t, d, n, d_x, d_w);
-  return part_bytes(g, plan_of(g, false));
+  const ProdArgs g = grad_sizes(t, d, n, d_x, d_w && !outer_rows(t, d, n));
+  return g.count ? part_bytes(g, plan_of(g, false)) : 0;
 }
 int linear_sum_splits(int64_t rows, int64_t out) { return dz_shape(rows, out).splits; }
 
@@ -219,7 +349,8 @@ void launch_dz(hipStream_t s, const LinearDev& f, const DzShape& d) {
 hipError_t launch_linear_bwd(hipStream_t s, const LinearDev& f) {
   BiasSums b{};
   unsigned bias_blocks = 0;
-  if (f.dz || f.d_bias.p) {
+  const bool outer = f.d_w.p && outer_rows(f.rows, f.cols, f.out), bias_there = outer && !f.dz;
+  if (f.dz || (f.d_bias.p && !bias_there)) {
     const DzShape d = dz_shape(f.rows, f.out);
     if (f.d_y.dt) launch_dz<uint16_t>(s, f, d);
     else launch_dz<float>(s, f, d);
@@ -230,11 +361,17 @@ hipError_t launch_linear_bwd(hipStream_t s, const LinearDev& f) {
       bias_blocks = unsigned((f.out + 255) / 256);
     }
   }
-  if (!f.d_x.p && !f.d_w.p) {
+  if (outer) {
+    const Outer o{f.dz ? f.dz : f.d_y.p, f.x.p, f.dz ? f.out : f.d_y.ld, f.x.ld, f.out, f.cols, f.d_w,
+                  bias_there ? f.d_bias : NormMat{}, int32_t(f.rows), 0};
+    const hipError_t e = run_outer(s, o);
+    if (e != hipSuccess) return e;
+  }
+  if (!f.d_x.p && (!f.d_w.p || outer)) {
     if (bias_blocks) hipLaunchKernelGGL(linear_bias_kernel, dim3(bias_blocks), dim3(256), 0, s, b);
     return hipGetLastError();
   }
-  ProdArgs g = grad_sizes(f.rows, f.cols, f.out, f.d_x.p, f.d_w.p);
+  ProdArgs g = grad_sizes(f.rows, f.cols, f.out, f.d_x.p, f.d_w.p && !outer);
   g.part = f.part;
   const void* dz = f.dz ? f.dz : f.d_y.p;
   const int64_t ld = f.dz ? f.out : f.d_y.ld;

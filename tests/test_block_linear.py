@@ -314,3 +314,20 @@ def test_numbers_of_dropped_elements_past_32_bits():
     for first in (0, 1 << 29, (1 << 29) + 32):
         part = min(40, t - first)
         assert torch.equal(y[first:first + part] != 0, kept((part, n), 0.5, RNG, first=first * n))
+
+
+@pytest.mark.parametrize("t", [1, 3, 4, 5, 8, 9, 13, 16, 17])
+@pytest.mark.parametrize("d,n", [(4096, 6144), (5000, 5048), (16392, 6104), (24, 1048568), (1048568, 104)])
+@pytest.mark.parametrize("exact", [False, True])
+def test_large_gradients_from_few_rows(t, d, n, exact):
+    """On both sides of the limits of the weight's gradient from few rows, last
+    columns cut both ways, with dz formed and as it comes."""
+    x, w, bias, _, dy = make(t, d, n, seed=t, resid=None if exact else F32)
+    how = dict(grad_dtype=F32) if exact else dict(kind="silu")
+    check(x, w, bias, None, dy, **how)
+    if t == 5:
+        b = block()
+        got = b.linear_bwd(dy, x, w, bias, torch.zeros(t, n, dtype=BF16, device="cuda"), act="silu", need_x=False)
+        # act'(0) = 1/2, which every type holds
+        close(got[1], (dy.double() / 2).T @ x.double(), "d_weight:bf16", inner=0.0 if exact else ROUND)
+        close(got[2], dy.double().sum(0) / 2, "d_bias:f32")
