@@ -49,9 +49,11 @@ NORM_ARGS = struct.Struct("@qqqiiff" + 9 * _MAT + "P" + 9 * _MAT)
 ATTN_ARGS = struct.Struct("@qqqiiiiqfiPP" + 4 * _HEADS + "P" + 4 * _HEADS)
 FFN_ARGS = struct.Struct("@qqqii" + 11 * _MAT)
 LINEAR_ARGS = struct.Struct("@qqqiid" + _RNG + 10 * _MAT)
+LINEAR_FWD_ARGS = struct.Struct("@qqqiid" + _RNG + 6 * _MAT)      # what comes before the backward call's own
+_NO_LINEAR_BWD = bytes(LINEAR_ARGS.size - LINEAR_FWD_ARGS.size)
 DROPOUT_ARGS = struct.Struct("@qqd" + _RNG + 3 * _MAT)
 ROTARY_ARGS = struct.Struct("@qqiiiiiiiifiqPPq" + 4 * _HEADS)
-_NO_MAT, _NO_HEADS = (0,) * 6, (0,) * 4
+_NO_MAT, _NO_HEADS, _NO_RNG = (0,) * 6, (0,) * 4, (0,) * 3
 
 _READY = None
 
@@ -87,12 +89,13 @@ def _stream(index: int) -> int:
 # The handle of the current stream without the Python object around it (2 us
 # of a call's 15), where this torch has it.
 _stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _call(name: str, args: bytes, device, workspace: bool = True) -> None:
     L = _READY or _lib()
     index = device.index
-    if index != torch.cuda.current_device():
+    if index != _current_device():
         with torch.cuda.device(device):
             return _call(name, args, device, workspace)
     if not workspace:
@@ -506,7 +509,7 @@ def _rng(p, rng, device):
     if not 0.0 <= p <= 1.0:
         raise ValueError(f"p is in 0 .. 1: got {p}")
     if p == 0.0:
-        return 0, 0, 0
+        return _NO_RNG
     if rng is None:
         raise ValueError("dropout needs rng: (seed, offset), or an int64 tensor of both")
     if isinstance(rng, torch.Tensor):
@@ -528,12 +531,13 @@ def _dropout(x, p, rng, residual, dtype):
     if dtype not in _TYPES:
         raise TypeError(f"unsupported dtype {dtype}")
     seed, offset, state = _rng(p, rng, dev)
-    y = torch.empty(x.shape, dtype=dtype, device=dev)
+    y = _out(x) if dtype == x.dtype else torch.empty(x.shape, dtype=dtype, device=dev)
     if x.numel() == 0:
         return y
     rows, cols = x.shape[:-1].numel(), x.shape[-1]
-    args = DROPOUT_ARGS.pack(rows, cols, p, seed, offset, state, *_mat(x, rows, cols), *_mat(residual, rows, cols),
-                             *_mat(y, rows, cols))
+    args = DROPOUT_ARGS.pack(rows, cols, p, seed, offset, state, *_mat(x, rows, cols),
+                             *(_NO_MAT if residual is None else _mat(residual, rows, cols)),
+                             y.data_ptr(), rows, cols, cols, _TYPES[dtype], 0)
     _call("muon_dropout", args, dev, workspace=False)
     return y
 
@@ -599,7 +603,7 @@ def _linear_dims(weight, act: str):
 
 
 def _vec(t, n: int):
-    if t is not None and t.shape != (n,):
+    if t.shape != (n,):
         raise ValueError(f"bias: shape {tuple(t.shape)} where ({n},) is wanted")
     return _mat(t, 1, n)
 
@@ -628,15 +632,16 @@ def linear_fwd(x, weight, bias=None, residual=None, *, act: str = "none", p: flo
     if dtype not in _TYPES:
         raise TypeError(f"unsupported dtype {dtype}")
     rows = x.shape[:-1].numel()
-    rng = _rng(p, rng, dev)
-    y = torch.empty(shape, dtype=dtype, device=dev)
-    z = torch.empty((rows, out), dtype=torch.bfloat16, device=dev) if save and act != "none" else None
-    b = _vec(bias, out)
+    rng = _rng(p, rng, dev) if p != 0.0 else _NO_RNG
+    y = x.new_empty(shape) if dtype == torch.bfloat16 else torch.empty(shape, dtype=dtype, device=dev)
+    z = x.new_empty((rows, out)) if save and act != "none" else None
+    b = _NO_MAT if bias is None else _vec(bias, out)
     if rows == 0:
         return y, z
-    args = LINEAR_ARGS.pack(rows, cols, out, LINEAR_ACTS[act], 0, p, *rng, *_mat(x, rows, cols), *_mat(weight, out, cols),
-                            *b, *_mat(residual, rows, out), *_mat(y, rows, out), *_mat(z, rows, out),
-                            *(4 * _NO_MAT))
+    args = LINEAR_FWD_ARGS.pack(rows, cols, out, LINEAR_ACTS[act], 0, p, *rng, *_mat(x, rows, cols),
+                                *_mat(weight, out, cols), *b, *(_NO_MAT if residual is None else _mat(residual, rows, out)),
+                                y.data_ptr(), rows, out, out, _TYPES[dtype], 0,
+                                *(_NO_MAT if z is None else (z.data_ptr(), rows, out, out, 1, 0))) + _NO_LINEAR_BWD
     _call("muon_linear_fwd", args, dev)
     return y, z
 
@@ -662,9 +667,9 @@ def linear_bwd(d_y, x, weight, bias=None, z=None, *, act: str = "none", p: float
     if grad_dtype not in _TYPES:
         raise TypeError(f"unsupported grad_dtype {grad_dtype}")
     rows = d_y.shape[:-1].numel()
-    rng = _rng(p, rng, dev)
-    b = _vec(bias, out)
-    d_x = torch.empty(shape, dtype=torch.bfloat16, device=dev) if need_x else None
+    rng = _rng(p, rng, dev) if p != 0.0 else _NO_RNG
+    b = _NO_MAT if bias is None else _vec(bias, out)
+    d_x = weight.new_empty(shape) if need_x else None
     d_w = torch.empty((out, cols), dtype=grad_dtype, device=dev) if need_weight else None
     d_b = None if bias is None else torch.empty((out,), dtype=bias.dtype, device=dev)
     if rows == 0:
@@ -747,21 +752,34 @@ def rotary_freqs(dim, *, base: float = 10000.0, stretch: str = "none", factor: f
 
 
 def _turned_heads(t, name: str, dtype):
+    """Descriptor of (batch, len, heads, dim), any strides."""
+    if t is None:
+        return _NO_HEADS
     if t.dtype != dtype:
         raise TypeError(f"{name}: {dtype} is wanted, got {t.dtype}")
-    b, n, h, d = t.shape
+    b, n, h, _ = t.shape
     sb, sl, sh, sd = t.stride()
     if sd != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
     return t.data_ptr(), sb if b > 1 else 0, sl if n > 1 else 0, sh if h > 1 else 0
 
 
+def _new_heads(t):
+    """A contiguous tensor of t's shape and its descriptor."""
+    if t is None:
+        return None, _NO_HEADS
+    o = _out(t)
+    _, n, h, d = t.shape
+    return o, (o.data_ptr(), n * h * d, h * d, d)
+
+
 def _rotary(q, k, freqs, positions, offset, interleaved, scale, out, inverse):
     dev = _device(q, k, freqs, positions)
     if q.dim() != 4 or (k is not None and (k.dim() != 4 or k.shape[:2] != q.shape[:2] or k.shape[3] != q.shape[3])):
         raise ValueError(f"(batch, len, heads, dim) each: q {tuple(q.shape)}, k {None if k is None else tuple(k.shape)}")
-    if q.dtype not in _TYPES:
-        raise TypeError(f"unsupported dtype {q.dtype}")
+    dtype = q.dtype
+    if dtype not in _TYPES:
+        raise TypeError(f"unsupported dtype {dtype}")
     b, n, h, d = q.shape
     if freqs.dtype != torch.float64 or freqs.dim() != 2 or not freqs.is_contiguous():
         raise ValueError("freqs: contiguous float64 (axes, pairs) is wanted")
@@ -776,20 +794,20 @@ def _rotary(q, k, freqs, positions, offset, interleaved, scale, out, inverse):
         if offset:
             raise ValueError("offset is for tokens without positions")
         between = n * axes if len(positions.shape) > len(one) else 0
-    made = out is None
-    if made:
-        out = _out(q), None if k is None else _out(k)
+    hq, hk = _turned_heads(q, "q", dtype), _turned_heads(k, "k", dtype)
+    if out is None:
+        (oq, to_q), (ok, to_k) = _new_heads(q), _new_heads(k)
     else:
         _device(q, *out)
         if len(out) != 2 or tuple(None if t is None else t.shape for t in out) != (q.shape, None if k is None else k.shape):
             raise ValueError(f"out: shapes {[None if t is None else tuple(t.shape) for t in out]}")
+        oq, ok = out
+        to_q, to_k = _turned_heads(oq, "out", dtype), _turned_heads(ok, "out", dtype)
     args = ROTARY_ARGS.pack(
-        b, n, h, 0 if k is None else k.shape[2], d, pairs, axes, int(interleaved), inverse, _TYPES[q.dtype], scale, 0, offset,
-        freqs.data_ptr(), _ptr(positions), between, *_turned_heads(q, "q", q.dtype),
-        *(_NO_HEADS if k is None else _turned_heads(k, "k", q.dtype)), *_turned_heads(out[0], "out", q.dtype),
-        *(_NO_HEADS if k is None else _turned_heads(out[1], "out", q.dtype)))
+        b, n, h, 0 if k is None else k.shape[2], d, pairs, axes, int(interleaved), inverse, _TYPES[dtype], scale, 0, offset,
+        freqs.data_ptr(), _ptr(positions), between, *hq, *hk, *to_q, *to_k)
     _call("muon_rotary", args, dev, workspace=False)
-    return tuple(out)
+    return oq, ok
 
 
 def rotary_fwd(q, k, freqs, positions=None, *, offset: int = 0, interleaved: bool = False, scale: float = 1.0, out=None):
