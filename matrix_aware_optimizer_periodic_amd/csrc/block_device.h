@@ -65,6 +65,19 @@ __device__ __forceinline__ void store_vals(void* p, int64_t e, const float (&v)[
   }
 }
 
+// Eight values past the caches, for what is not read again soon.
+template <typename T>
+__device__ __forceinline__ void store_vals_past(void* p, int64_t e, const float (&v)[8]) {
+  if constexpr (sizeof(T) == 4) {
+    auto* q = as_global(reinterpret_cast<f32x4_t*>(static_cast<float*>(p) + e));
+    __builtin_nontemporal_store(f32x4_t{v[0], v[1], v[2], v[3]}, q);
+    __builtin_nontemporal_store(f32x4_t{v[4], v[5], v[6], v[7]}, q + 1);
+  } else {
+    const u32x4_t w{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+    __builtin_nontemporal_store(w, as_global(reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(p) + e)));
+  }
+}
+
 // The same with the type chosen at run time (vectors read once per row).
 template <int VEC>
 __device__ __forceinline__ void load_any(const void* p, int dt, int64_t e, float (&v)[VEC]) {

@@ -340,7 +340,7 @@ __device__ __forceinline__ void emit_rows(const Prod& p, const X& ext, const flo
       } else if constexpr (EPI == EPI_LINEAR) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] += bias[k];
-        if (p.c2) store_vals<uint16_t, 8>(p.c2, m * p.ldc2 + n, v);
+        if (p.c2) store_vals_past<uint16_t>(p.c2, m * p.ldc2 + n, v);
         if constexpr (ACT != 2) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) v[k] = act_value<ACT>(v[k]);

@@ -268,18 +268,9 @@ __global__ __launch_bounds__(256) void linear_outer_kernel(Outer o) {
         acc[1] = mfma4(fx[g][1][k], fz[k], acc[1]);
       }
       const int64_t c = c0 + 128 * g + 8 * b;
-      if (c < o.d) {
-        const int64_t at = (n0 + n) * o.dw.ld + c;
-        if constexpr (F32) {
-          auto* w = as_global(reinterpret_cast<f32x4_t*>(static_cast<float*>(o.dw.p) + at));
-          __builtin_nontemporal_store(acc[0], w);
-          __builtin_nontemporal_store(acc[1], w + 1);
-        } else {
-          const u32x4_t w{pack_bf16x2(acc[0][0], acc[0][1]), pack_bf16x2(acc[0][2], acc[0][3]),
-                          pack_bf16x2(acc[1][0], acc[1][1]), pack_bf16x2(acc[1][2], acc[1][3])};
-          __builtin_nontemporal_store(w, as_global(reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(o.dw.p) + at)));
-        }
-      }
+      const float v[8] = {acc[0][0], acc[0][1], acc[0][2], acc[0][3], acc[1][0], acc[1][1], acc[1][2], acc[1][3]};
+      using T = std::conditional_t<F32, float, uint16_t>;
+      if (c < o.d) store_vals_past<T>(o.dw.p, (n0 + n) * o.dw.ld + c, v);
     }
   }
 }
