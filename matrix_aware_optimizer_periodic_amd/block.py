@@ -670,16 +670,22 @@ def linear_bwd(d_y, x, weight, bias=None, z=None, *, act: str = "none", p: float
     rng = _rng(p, rng, dev) if p != 0.0 else _NO_RNG
     b = _NO_MAT if bias is None else _vec(bias, out)
     d_x = weight.new_empty(shape) if need_x else None
-    d_w = torch.empty((out, cols), dtype=grad_dtype, device=dev) if need_weight else None
-    d_b = None if bias is None else torch.empty((out,), dtype=bias.dtype, device=dev)
+    d_w = None
+    if need_weight:
+        d_w = weight.new_empty((out, cols)) if grad_dtype == torch.bfloat16 else \
+            torch.empty((out, cols), dtype=grad_dtype, device=dev)
+    d_b = None if bias is None else _out(bias)
     if rows == 0:
         for t in (d_w, d_b):
             if t is not None:
                 t.zero_()
         return d_x, d_w, d_b
-    args = LINEAR_ARGS.pack(rows, cols, out, LINEAR_ACTS[act], 0, p, *rng, *_mat(x, rows, cols), *_mat(weight, out, cols),
-                            *b, *(2 * _NO_MAT), *_mat(z, rows, out), *_mat(d_y, rows, out), *_mat(d_x, rows, cols),
-                            *_mat(d_w, out, cols), *_mat(d_b, 1, out))
+    args = LINEAR_ARGS.pack(rows, cols, out, LINEAR_ACTS[act], 0, p, *rng,
+                            *(_NO_MAT if x is None else _mat(x, rows, cols)), *_mat(weight, out, cols), *b, *_NO_MAT, *_NO_MAT,
+                            *(_NO_MAT if z is None else _mat(z, rows, out)), *_mat(d_y, rows, out),
+                            *((d_x.data_ptr(), rows, cols, cols, 1, 0) if need_x else _NO_MAT),
+                            *((d_w.data_ptr(), out, cols, cols, _TYPES[grad_dtype], 0) if need_weight else _NO_MAT),
+                            *(_NO_MAT if d_b is None else (d_b.data_ptr(), 1, out, out, _TYPES[d_b.dtype], 0)))
     _call("muon_linear_bwd", args, dev)
     return d_x, d_w, d_b
 

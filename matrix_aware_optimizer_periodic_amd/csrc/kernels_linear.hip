@@ -151,22 +151,32 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinearDev a, DzShape d) 
   }
 }
 
-// The shares' sums of 256 columns: what a workgroup adds of them.
+// Column sums of a few rows, 256 columns to a workgroup: of the shares' sums, or
+// of dy itself where that is dz and has few rows.
 struct BiasSums {
-  const float* sums;     // [splits][out]
+  const void* rows;
+  int64_t ld;
   NormMat d_bias;
   int64_t out;
-  int32_t splits;
+  int32_t count, bf16;
   int32_t item0;         // the first workgroup of a launch that does this
 };
 __device__ __forceinline__ void add_bias_sums(const BiasSums& b, int block) {
   const int64_t n = int64_t(block) * 256 + threadIdx.x;
   if (n >= b.out) return;
   float s = 0.f;
+  if (b.bf16) {
 #pragma unroll 8
-  for (int i = 0; i < b.splits; ++i) s += as_global(b.sums)[i * b.out + n];
+    for (int i = 0; i < b.count; ++i) s += load_any1(b.rows, 1, i * b.ld + n);
+  } else {
+#pragma unroll 8
+    for (int i = 0; i < b.count; ++i) s += load_any1(b.rows, 0, i * b.ld + n);
+  }
   store_any1(b.d_bias.p, b.d_bias.dt, n, s);
 }
+// (a thread reads eight rows at a time; a launch less: 32 rows of 2048 -> 2048, both
+// gradients and d_bias, 17.4 -> 14 us)
+bool bias_from_rows(const LinearDev& f) { return f.d_bias.p && !f.dz && f.act == 2 && !f.drop.on && f.d_y.dt && f.rows <= 64; }
 __global__ __launch_bounds__(256) void linear_bias_kernel(BiasSums b) { add_bias_sums(b, int(blockIdx.x)); }
 
 template <int BT>
@@ -275,11 +285,11 @@ __global__ __launch_bounds__(256) void linear_outer_kernel(Outer o) {
   }
 }
 
-// In us, both gradients, here against tiles: 8 rows 5120 -> 5120 34 against 37, 20480
-// -> 5120 95 against 103, 2048 -> 8192 32 against 29; 16 rows 5120 -> 30720 135
-// against 159, 20480 -> 5120 98 against 104, 5120 -> 5120 41 against 37; 24 rows
-// 5120 -> 30720 157 against 160 and elsewhere slower.
-bool outer_rows(int64_t t, int64_t d, int64_t n) { return t <= 8 ? d * n >= 25000000 : t <= 16 && d * n >= 100000000; }
+// In us, both gradients and d_bias, here against tiles: 8 rows 5120 -> 30720 131
+// against 155, 20480 -> 5120 94 against 99, 5120 -> 5120 34 against 32, 2048 ->
+// 12288 38 against 33; 16 rows 5120 -> 30720 136 against 155, 20480 -> 5120 98
+// against 100; 24 rows 5120 -> 30720 157 against 155.
+bool outer_rows(int64_t t, int64_t d, int64_t n) { return t <= 16 && d * n >= 100000000; }
 
 hipError_t run_outer(hipStream_t s, const Outer& o0) {
   Outer o = o0;
@@ -340,15 +350,18 @@ void launch_dz(hipStream_t s, const LinearDev& f, const DzShape& d) {
 hipError_t launch_linear_bwd(hipStream_t s, const LinearDev& f) {
   BiasSums b{};
   unsigned bias_blocks = 0;
-  const bool outer = f.d_w.p && outer_rows(f.rows, f.cols, f.out), bias_there = outer && !f.dz;
-  if (f.dz || (f.d_bias.p && !bias_there)) {
+  const bool outer = f.d_w.p && outer_rows(f.rows, f.cols, f.out), bias_there = outer && !f.dz && f.act == 2 && !f.drop.on && f.d_y.dt;
+  if (!bias_there && bias_from_rows(f)) {
+    b = BiasSums{f.d_y.p, f.d_y.ld, f.d_bias, f.out, int32_t(f.rows), 1, 0};
+    bias_blocks = unsigned((f.out + 255) / 256);
+  } else if (f.dz || (f.d_bias.p && !bias_there)) {
     const DzShape d = dz_shape(f.rows, f.out);
     if (f.d_y.dt) launch_dz<uint16_t>(s, f, d);
     else launch_dz<float>(s, f, d);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (f.d_bias.p && d.splits > 1) {
-      b = BiasSums{f.sums, f.d_bias, f.out, d.splits, 0};
+      b = BiasSums{f.sums, f.out, f.d_bias, f.out, d.splits, 0, 0};
       bias_blocks = unsigned((f.out + 255) / 256);
     }
   }

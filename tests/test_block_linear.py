@@ -317,7 +317,7 @@ def test_numbers_of_dropped_elements_past_32_bits():
 
 
 @pytest.mark.parametrize("t", [1, 3, 4, 5, 8, 9, 13, 16, 17])
-@pytest.mark.parametrize("d,n", [(4096, 6144), (5000, 5048), (16392, 6104), (24, 1048568), (1048568, 104)])
+@pytest.mark.parametrize("d,n", [(4096, 24504), (16392, 6104), (5128, 19504), (104, 1048568), (1048568, 104)])
 @pytest.mark.parametrize("exact", [False, True])
 def test_large_gradients_from_few_rows(t, d, n, exact):
     """On both sides of the limits of the weight's gradient from few rows, last
