@@ -414,6 +414,8 @@ def attention_qkv(qkv, *, causal: bool = False, offset: int = 0, q_lens=None, k_
     whose gradient comes out packed alike; returns o.  rotary: rotary_fwd's
     arguments from freqs on, by name, where queries and keys are to be rotated
     first."""
+    if rotary is not None and "out" in rotary:
+        raise ValueError("rotary: queries and keys are rotated into tensors of their own")
     return _PackedAttention.apply(qkv, {"causal": causal, "offset": offset, "q_lens": q_lens, "k_lens": k_lens,
                                         "scale": scale}, rotary)
 
@@ -808,6 +810,9 @@ def _rotary(q, k, freqs, positions, offset, interleaved, scale, out, inverse):
         if len(out) != 2 or tuple(None if t is None else t.shape for t in out) != (q.shape, None if k is None else k.shape):
             raise ValueError(f"out: shapes {[None if t is None else tuple(t.shape) for t in out]}")
         oq, ok = out
+        for t in out:
+            if t is not None and any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
+                raise ValueError("out: values on top of each other")
         to_q, to_k = _turned_heads(oq, "out", dtype), _turned_heads(ok, "out", dtype)
     args = ROTARY_ARGS.pack(
         b, n, h, 0 if k is None else k.shape[2], d, pairs, axes, int(interleaved), inverse, _TYPES[dtype], scale, 0, offset,

@@ -255,7 +255,9 @@ def test_rotary_checks_its_arguments(packed):
            lambda: m.rotary_fwd(q, k, f2, pos), lambda: m.rotary_fwd(q, k, f, pos, offset=1),
            lambda: m.rotary_fwd(q, k, f, pos.T.contiguous().T), lambda: m.rotary_fwd(q, k, f, out=(q,)),
            lambda: m.rotary_fwd(q, k, f, out=(q, q)), lambda: m.rotary_fwd(q, k, f, out=(q, None)),
-           lambda: m.rotary_fwd(q, k, f, out=(q.to(BF16), k)), lambda: m.rotary_fwd(q.transpose(2, 3), None, f)]
+           lambda: m.rotary_fwd(q, k, f, out=(q.to(BF16), k)), lambda: m.rotary_fwd(q.transpose(2, 3), None, f),
+           lambda: m.rotary_fwd(q, k, f, out=(q, k[:, :, :1].expand(-1, -1, 2, -1))),
+           lambda: m.attention_qkv(torch.zeros(2, 5, 3, 4, 16), rotary={"freqs": f, "out": (q, q)})]
     for i, call in enumerate(bad):
         with pytest.raises((ValueError, TypeError)):
             call()
