@@ -697,7 +697,7 @@ class _Linear(torch.autograd.Function):
     def forward(ctx, x, weight, bias, residual, act, p, rng, y_dtype, save):
         y, z = linear_fwd(x, weight, bias, residual, act=act, p=p, rng=rng, save=save, y_dtype=y_dtype)
         ctx.act, ctx.p = act, p
-        _keep_rng(ctx, rng, x, weight, bias, z)
+        _keep_rng(ctx, rng, x if ctx.needs_input_grad[1] else None, weight, bias, z)
         return y
 
     @staticmethod
@@ -818,6 +818,11 @@ def _rotary(q, k, freqs, positions, offset, interleaved, scale, out, inverse):
         b, n, h, 0 if k is None else k.shape[2], d, pairs, axes, int(interleaved), inverse, _TYPES[dtype], scale, 0, offset,
         freqs.data_ptr(), _ptr(positions), between, *hq, *hk, *to_q, *to_k)
     _call("muon_rotary", args, dev, workspace=False)
+    if out is not None:
+        # autograd is told, so that a backward pass that saved them raises
+        for t in out:
+            if t is not None and not t.is_inference():
+                torch.autograd.graph.increment_version(t)
     return oq, ok
 
 

@@ -634,7 +634,7 @@ struct Plan {
   double us;
   struct { int tiles, full, splits, split_stages; } p[kProds];
 };
-Plan plan_with(const ProdArgs& g, int bt, bool gate) {
+Plan plan_with(const ProdArgs& g, int bt, bool gate, double each_us) {
   Plan q{};
   q.bt = bt;
   const int nstep = gate ? bt / 2 : bt, slots = bt == 256 ? 256 : 512;
@@ -659,7 +659,7 @@ Plan plan_with(const ProdArgs& g, int bt, bool gate) {
   for (int n = 1; n == 1 || (rem > 0 && n <= stages / 4 && n <= (g.count > 1 ? std::min(32, (1 << 20) / rem) : slots / rem));
        ++n) {
     const int per = ((stages + n - 1) / n + 1) & ~1, got = (stages + per - 1) / per;   // whole units
-    const double one = per * stage_us + tile_us, join = got > 1 ? 4 + 2 * rem * got * part_mb / 4.5 : 0;
+    const double one = per * stage_us + tile_us, join = got > 1 ? 4 + 2 * rem * got * part_mb / 4.5 + each_us * got : 0;
     double us;
     if (g.count == 1) {
       us = whole * tile + (rem > 0 ? one : 0) + join + launch_us;
@@ -675,8 +675,11 @@ Plan plan_with(const ProdArgs& g, int bt, bool gate) {
   }
   return q;
 }
-Plan plan_of(const ProdArgs& g, bool gate) {
-  const Plan big = plan_with(g, 256, gate), small = plan_with(g, 128, gate);
+// each_us: a join's time for each range of a tile, which it reads one after the
+// other (0.14 us: 365 ranges of one tile took 51; it tells where few tiles have long
+// sums, which the feed-forward's do not).
+Plan plan_of(const ProdArgs& g, bool gate, double each_us = 0) {
+  const Plan big = plan_with(g, 256, gate, each_us), small = plan_with(g, 128, gate, each_us);
   return big.us <= small.us ? big : small;
 }
 size_t part_bytes(const ProdArgs& g, const Plan& q) {

@@ -22,6 +22,8 @@
 namespace muon {
 namespace {
 
+constexpr double kEachUs = 0.14;       // plan_of
+
 template <int BT, int ACT, bool DROP>
 __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void linear_kernel(ProdArgs g, LinearExtra<DROP> ext) {
   product_tile<BT, ROWS_ROWS, EPI_LINEAR, ACT>(g, ext);
@@ -81,7 +83,7 @@ hipError_t run_few_rows(hipStream_t s, const Prod& p, const LinearExtra<true>& e
 
 template <int ACT, bool DROP>
 hipError_t run_linear(hipStream_t s, const ProdArgs& g, const LinearDev& f) {
-  const Plan q = plan_of(g, false);
+  const Plan q = plan_of(g, false, kEachUs);
   const LinearExtra<DROP> ext{f.bias.p, f.bias.dt, f.drop};
   return q.bt == 256 ? launch_prod<256, EPI_LINEAR>(s, g, q, &linear_kernel<256, ACT, DROP>, &linear_join_kernel<256, ACT, DROP>, 0, ext)
                      : launch_prod<128, EPI_LINEAR>(s, g, q, &linear_kernel<128, ACT, DROP>, &linear_join_kernel<128, ACT, DROP>, 0, ext);
@@ -303,14 +305,43 @@ hipError_t run_outer(hipStream_t s, const Outer& o0) {
 }
 
 // ---- the gradients' products --------------------------------------------------
-ProdArgs grad_sizes(int64_t t, int64_t d, int64_t n, bool d_x, bool d_w) {
-  ProdArgs g{};
-  if (d_x) g.p[g.count++] = sizes(t, d, n);
-  if (d_w) {
-    g.p[g.count] = sizes(n, d, t);
-    g.p[g.count++].acols = 1;
-  }
-  return g;
+// dx, dW or both, in one launch or two.  Only a launch's first product is divided
+// where its sums are long for the tiles it has, so the one that needs it comes
+// first, or each is launched alone (an allowance of 4 us), where that is a fifth
+// less by the estimate: 16384 rows of 2048 -> 32 columns, whose dW has 16 tiles of
+// 512 stages, 175 us with dW behind dx and 47 in two launches; 4096 rows of 2048 ->
+// 8192, where the estimates are close, 235 with dx first and 255 turned.
+struct GradPlan {
+  ProdArgs g[2];
+  Plan q[2];
+  int launches;
+};
+GradPlan grad_plan(int64_t t, int64_t d, int64_t n, bool d_x, bool d_w) {
+  const Prod dx = sizes(t, d, n);
+  Prod dw = sizes(n, d, t);
+  dw.acols = 1;
+  auto one = [](const Prod& a, const Prod* b) {
+    ProdArgs g = alone(a);
+    if (b) g.p[g.count++] = *b;
+    return g;
+  };
+  GradPlan best{};
+  if (!d_x && !d_w) return best;
+  best.launches = 1;
+  best.g[0] = d_x && d_w ? one(dx, &dw) : one(d_x ? dx : dw, nullptr);
+  best.q[0] = plan_of(best.g[0], false, kEachUs);
+  if (!d_x || !d_w) return best;
+  const ProdArgs turned = one(dw, &dx);
+  const Plan q = plan_of(turned, false, kEachUs);
+  if (q.us < 0.8 * best.q[0].us) { best.g[0] = turned; best.q[0] = q; }
+  GradPlan apart{{one(dx, nullptr), one(dw, nullptr)}, {}, 2};
+  for (int i = 0; i < 2; ++i) apart.q[i] = plan_of(apart.g[i], false, kEachUs);
+  return apart.q[0].us + apart.q[1].us + 4 < 0.8 * best.q[0].us ? apart : best;
+}
+size_t grad_part_bytes(const GradPlan& p) {
+  size_t most = 0;
+  for (int i = 0; i < p.launches; ++i) most = std::max(most, part_bytes(p.g[i], p.q[i]));
+  return most;
 }
 
 }  // namespace
@@ -318,12 +349,11 @@ ProdArgs grad_sizes(int64_t t, int64_t d, int64_t n, bool d_x, bool d_w) {
 size_t linear_fwd_part_bytes(int64_t t, int64_t d, int64_t n) {
   if (t == 0 || few_rows(t, d, n)) return 0;
   const ProdArgs g = alone(sizes(t, n, d));
-  return part_bytes(g, plan_of(g, false));
+  return part_bytes(g, plan_of(g, false, kEachUs));
 }
 size_t linear_bwd_part_bytes(int64_t t, int64_t d, int64_t n, bool d_x, bool d_w) {
   if (t == 0 || !(d_x || d_w)) return 0;
-  const ProdArgs g = grad_sizes(t, d, n, d_x, d_w && !outer_rows(t, d, n));
-  return g.count ? part_bytes(g, plan_of(g, false)) : 0;
+  return grad_part_bytes(grad_plan(t, d, n, d_x, d_w && !outer_rows(t, d, n)));
 }
 int linear_sum_splits(int64_t rows, int64_t out) { return dz_shape(rows, out).splits; }
 
@@ -375,25 +405,31 @@ hipError_t launch_linear_bwd(hipStream_t s, const LinearDev& f) {
     if (bias_blocks) hipLaunchKernelGGL(linear_bias_kernel, dim3(bias_blocks), dim3(256), 0, s, b);
     return hipGetLastError();
   }
-  ProdArgs g = grad_sizes(f.rows, f.cols, f.out, f.d_x.p, f.d_w.p && !outer);
-  g.part = f.part;
+  GradPlan plan = grad_plan(f.rows, f.cols, f.out, f.d_x.p, f.d_w.p && !outer);
   const void* dz = f.dz ? f.dz : f.d_y.p;
   const int64_t ld = f.dz ? f.out : f.d_y.ld;
-  for (int i = 0; i < g.count; ++i) {
-    Prod& p = g.p[i];
-    p.a = dz; p.lda = ld;
-    if (p.acols) {
-      p.b = f.x.p; p.ldb = f.x.ld;
-      p.c = f.d_w.p; p.ldc = f.d_w.ld; p.f32 = f.d_w.dt == 0;
-    } else {
-      p.b = f.w.p; p.ldb = f.w.ld;
-      p.c = f.d_x.p; p.ldc = f.d_x.ld;
+  hipError_t e = hipSuccess;
+  for (int k = 0; k < plan.launches && e == hipSuccess; ++k) {
+    ProdArgs& g = plan.g[k];
+    const Plan& q = plan.q[k];
+    g.part = f.part;                     // (a launch's join has read it before the next one begins)
+    for (int i = 0; i < g.count; ++i) {
+      Prod& p = g.p[i];
+      p.a = dz; p.lda = ld;
+      if (p.acols) {
+        p.b = f.x.p; p.ldb = f.x.ld;
+        p.c = f.d_w.p; p.ldc = f.d_w.ld; p.f32 = f.d_w.dt == 0;
+      } else {
+        p.b = f.w.p; p.ldb = f.w.ld;
+        p.c = f.d_x.p; p.ldc = f.d_x.ld;
+      }
     }
+    b.item0 = items_of(g, q);
+    e = q.bt == 256 ? launch_prod<256, EPI_PLAIN>(s, g, q, &linear_grads_kernel<256>, &linear_grads_join_kernel<256>, bias_blocks, b)
+                    : launch_prod<128, EPI_PLAIN>(s, g, q, &linear_grads_kernel<128>, &linear_grads_join_kernel<128>, bias_blocks, b);
+    bias_blocks = 0;
   }
-  const Plan q = plan_of(g, false);
-  b.item0 = items_of(g, q);
-  return q.bt == 256 ? launch_prod<256, EPI_PLAIN>(s, g, q, &linear_grads_kernel<256>, &linear_grads_join_kernel<256>, bias_blocks, b)
-                     : launch_prod<128, EPI_PLAIN>(s, g, q, &linear_grads_kernel<128>, &linear_grads_join_kernel<128>, bias_blocks, b);
+  return e;
 }
 
 }  // namespace muon

@@ -107,6 +107,16 @@ def test_few_tiles_and_long_sums(t, d, n):
     check(*make(t, d, n, seed=d + t, resid=BF16), kind="gelu", p=0.5, rng=RNG)
 
 
+@pytest.mark.parametrize("t,d,n", [(20000, 256, 32), (3000, 24, 16), (16400, 136, 4096), (40, 16, 16384), (9000, 8, 8),
+                                   (5000, 1152, 32)])
+def test_one_product_with_few_tiles(t, d, n):
+    """The weight's gradient, the input's or both have few tiles of long sums:
+    divided first, second or in launches of their own.  fp32 sums of 20000 terms,
+    32 at a time: 625 additions of 2^-24 of random sign, within 1e-5."""
+    check(*make(t, d, n, seed=d + t), grad_dtype=F32)
+    check(*make(t, d, n, seed=d + t, resid=F32), kind="silu")
+
+
 @pytest.mark.parametrize("t", [1, 8, 9, 33])
 @pytest.mark.parametrize("d,n", [(4072, 136), (4104, 72), (136, 4072), (72, 4104), (2048, 12288)])
 def test_few_rows_and_many_columns(t, d, n):

@@ -262,6 +262,11 @@ def test_rotary_checks_its_arguments(packed):
         with pytest.raises((ValueError, TypeError)):
             call()
         assert not packed, i
+    saved = (q.clone().requires_grad_(True) * q).sum()
+    m.rotary_fwd(q, None, f, out=(q, None))
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        saved.backward()
+    packed.clear()
     m.rotary_fwd(q, k, f, pos, interleaved=True, scale=0.5)
     m.rotary_bwd(q, None, f2, torch.zeros(5, 2, dtype=torch.int32))
     first, second = (b.ROTARY_ARGS.unpack(a) for _, a in packed)
