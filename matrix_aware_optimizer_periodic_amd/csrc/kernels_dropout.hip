@@ -14,18 +14,25 @@ namespace {
 // aligned groups; an element's number goes by its row and column, not by where
 // it lies.
 template <typename TX, typename TY>
-__device__ void drop_one(const DropoutDev& a, const Rng& rng, int64_t row, int64_t col) {
-  float v[1], r[1] = {0.f};
-  load_vals<TX, 1>(a.x.p, row * a.x.ld + col, v);
-  if (a.resid.p) load_vals<TY, 1>(a.resid.p, row * a.resid.ld + col, r);
-  if (a.drop.on) {
-    const uint64_t e = uint64_t(row) * uint64_t(a.cols) + uint64_t(col);
-    const u32x4_t w = philox(e / 4, rng.offset, rng.seed);
-    const uint32_t mine = e % 4 == 0 ? w[0] : e % 4 == 1 ? w[1] : e % 4 == 2 ? w[2] : w[3];
-    v[0] = mine <= a.drop.last ? 0.f : v[0] * a.drop.scale;
+__device__ __forceinline__ void drop_some(const DropoutDev& a, const Rng& rng, int64_t row, int64_t col, int64_t end) {
+  uint64_t group = ~uint64_t(0);
+  u32x4_t w{0, 0, 0, 0};
+  for (; col < end; ++col) {
+    float v[1], r[1] = {0.f};
+    load_vals<TX, 1>(a.x.p, row * a.x.ld + col, v);
+    if (a.resid.p) load_vals<TY, 1>(a.resid.p, row * a.resid.ld + col, r);
+    if (a.drop.on) {
+      const uint64_t e = uint64_t(row) * uint64_t(a.cols) + uint64_t(col);
+      if (e / 4 != group) {              // four columns are in two groups at most
+        group = e / 4;
+        w = philox(group, rng.offset, rng.seed);
+      }
+      const uint32_t mine = e % 4 == 0 ? w[0] : e % 4 == 1 ? w[1] : e % 4 == 2 ? w[2] : w[3];
+      v[0] = mine <= a.drop.last ? 0.f : v[0] * a.drop.scale;
+    }
+    v[0] += r[0];
+    store_vals<TY, 1>(a.y.p, row * a.y.ld + col, v);
   }
-  v[0] += r[0];
-  store_vals<TY, 1>(a.y.p, row * a.y.ld + col, v);
 }
 
 template <typename TX, typename TY, bool VEC>
@@ -47,7 +54,7 @@ __global__ __launch_bounds__(256) void dropout_kernel(DropoutDev a) {
         continue;
       }
     }
-    for (int64_t c = col; c < min(col + N, a.cols); ++c) drop_one<TX, TY>(a, rng, row, c);
+    drop_some<TX, TY>(a, rng, row, col, min(col + N, a.cols));
   }
 }
 
