@@ -813,6 +813,8 @@ def _rotary(q, k, freqs, positions, offset, interleaved, scale, out, inverse):
         for t in out:
             if t is not None and any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
                 raise ValueError("out: values on top of each other")
+        if ok is not None and oq.numel() and oq.data_ptr() == ok.data_ptr():
+            raise ValueError("out: both in one place")
         to_q, to_k = _turned_heads(oq, "out", dtype), _turned_heads(ok, "out", dtype)
     args = ROTARY_ARGS.pack(
         b, n, h, 0 if k is None else k.shape[2], d, pairs, axes, int(interleaved), inverse, _TYPES[dtype], scale, 0, offset,

@@ -627,6 +627,7 @@ muon_status muon_rotary(const muon_rotary_args* a, void* hip_stream) {
   if (a->kv_heads > 0) {
     CHECK(rotary_heads("k", a->k, a->dtype));
     CHECK(rotary_heads("k_out", a->k_out, a->dtype));
+    if (a->q_out.ptr == a->k_out.ptr) return fail(MUON_E_ARG, "q_out and k_out are in one place");
   }
   RotaryDev d{};
   d.tokens = a->batch * a->len;

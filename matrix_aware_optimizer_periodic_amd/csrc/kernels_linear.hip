@@ -111,7 +111,7 @@ DzShape dz_shape(int64_t rows, int64_t out) {
   d.blocks = int((chunks + (1 << d.width_log) - 1) >> d.width_log);
   const int64_t turn = 256 >> d.width_log;                       // rows at a time
   const int64_t turns = (rows + turn - 1) / turn;
-  d.splits = int(std::max<int64_t>(1, std::min<int64_t>(turns, std::min<int64_t>(512, 1024 / d.blocks))));
+  d.splits = int(std::max<int64_t>(1, std::min<int64_t>(turns, std::min<int64_t>(256, 1024 / d.blocks))));
   d.rows = (turns + d.splits - 1) / d.splits * turn;
   d.splits = int((rows + d.rows - 1) / d.rows);
   return d;

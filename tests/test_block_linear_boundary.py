@@ -148,7 +148,7 @@ def test_dropout_refuses(over, status):
 # ------------------------------------------------------------------- rotary
 def rotary_args(**over):
     v = dict(batch=2, len=10, heads=4, kv_heads=2, dim=64, pairs=32, axes=1, interleaved=0, inverse=0, dtype=1, scale=1.0,
-             reserved=0, offset=0, freqs=FAKE, positions=FAKE, between=0, q=heads(), k=heads(), q_out=heads(), k_out=heads())
+             reserved=0, offset=0, freqs=FAKE, positions=FAKE, between=0, q=heads(), k=heads(), q_out=heads(), k_out=heads(ptr=2 * FAKE))
     v.update(over)
     return b.ROTARY_ARGS.pack(*(v[k] for k in ("batch", "len", "heads", "kv_heads", "dim", "pairs", "axes", "interleaved",
                                                "inverse", "dtype", "scale", "reserved", "offset", "freqs", "positions",
@@ -168,7 +168,7 @@ def rotary_args(**over):
     (dict(between=-1), E.MUON_E_SHAPE), (dict(q=heads(ptr=0)), E.MUON_E_ARG), (dict(k=heads(ptr=0)), E.MUON_E_ARG),
     (dict(q_out=heads(ptr=0)), E.MUON_E_ARG), (dict(k_out=heads(ptr=0)), E.MUON_E_ARG),
     (dict(q=heads(ptr=FAKE + 1)), E.MUON_E_ALIGN), (dict(k=heads(sl=-8)), E.MUON_E_SHAPE),
-    (dict(q_out=heads(sb=(1 << 40) + 8)), E.MUON_E_SHAPE), (dict(batch=0), E.MUON_OK), (dict(len=0), E.MUON_OK),
+    (dict(q_out=heads(sb=(1 << 40) + 8)), E.MUON_E_SHAPE), (dict(k_out=heads()), E.MUON_E_ARG), (dict(batch=0), E.MUON_OK), (dict(len=0), E.MUON_OK),
 ])
 def test_rotary_refuses(over, status):
     assert b._lib().muon_rotary(rotary_args(**over), None) == status
@@ -257,6 +257,7 @@ def test_rotary_checks_its_arguments(packed):
            lambda: m.rotary_fwd(q, k, f, out=(q, q)), lambda: m.rotary_fwd(q, k, f, out=(q, None)),
            lambda: m.rotary_fwd(q, k, f, out=(q.to(BF16), k)), lambda: m.rotary_fwd(q.transpose(2, 3), None, f),
            lambda: m.rotary_fwd(q, k, f, out=(q, k[:, :, :1].expand(-1, -1, 2, -1))),
+           lambda: m.rotary_fwd(q, q, f, out=(q, q)),
            lambda: m.attention_qkv(torch.zeros(2, 5, 3, 4, 16), rotary={"freqs": f, "out": (q, q)})]
     for i, call in enumerate(bad):
         with pytest.raises((ValueError, TypeError)):
