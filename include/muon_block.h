@@ -193,7 +193,8 @@ muon_status muon_dropout(const muon_dropout_args* args, void* hip_stream);
  * accumulation and the epilogue in fp32.  drop is muon_dropout's, of a rows x
  * out matrix.  z (BF16) is what the backward pass reads where act is not NONE;
  * absent, it is not written.  The backward pass forms dz = drop(d_y) act'(z),
- * rounded to bf16 as a matrix-core operand, and d_x = dz weight, d_weight =
+ * rounded to bf16 as a matrix-core operand (kept in fp32 by small calls, which
+ * take no workspace), and d_x = dz weight, d_weight =
  * dz^T x, d_bias = the column sums of dz before its rounding, added in a fixed
  * order: the same inputs give the same bits.  The gradient of the residual is
  * d_y itself. */

@@ -135,6 +135,8 @@ hipError_t launch_linear_fwd(hipStream_t s, const LinearDev& a);
 hipError_t launch_linear_bwd(hipStream_t s, const LinearDev& a);
 size_t linear_fwd_part_bytes(int64_t rows, int64_t cols, int64_t out);
 size_t linear_bwd_part_bytes(int64_t rows, int64_t cols, int64_t out, bool d_x, bool d_w);
+// Whether the backward call is one launch without a workspace.
+bool linear_small_grads(int64_t rows, int64_t cols, int64_t out);
 // Shares of the rows that d_bias is summed in.
 int linear_sum_splits(int64_t rows, int64_t out);
 

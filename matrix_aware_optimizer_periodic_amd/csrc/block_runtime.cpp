@@ -316,6 +316,7 @@ size_t linear_sums_bytes(const muon_linear_args* a) {
 }
 size_t linear_fwd_bytes(const muon_linear_args* a) { return align_up(linear_fwd_part_bytes(a->rows, a->cols, a->out)); }
 size_t linear_bwd_bytes(const muon_linear_args* a, const DropDev& drop) {
+  if (linear_small_grads(a->rows, a->cols, a->out)) return 0;
   return linear_dz_bytes(a, drop) + linear_sums_bytes(a) +
          align_up(linear_bwd_part_bytes(a->rows, a->cols, a->out, a->d_x.ptr, a->d_weight.ptr));
 }
@@ -592,10 +593,11 @@ muon_status muon_linear_bwd(const muon_linear_args* a, void* ws, size_t ws_bytes
     CHECK(ffn_mat("d_weight", a->d_weight, a->out, a->cols, -1));
   }
   CHECK(check_opt("d_bias", a->d_bias, 1, a->out, -1));
-  CHECK(check_workspace(ws, ws_bytes, linear_bwd_bytes(a, drop)));
+  const size_t need = linear_bwd_bytes(a, drop);
+  CHECK(check_workspace(ws, ws_bytes, need));
   LinearDev d = linear_dev(a, drop);
   char* at = static_cast<char*>(ws);
-  if (linear_forms_dz(a, drop)) d.dz = at;
+  if (need > 0 && linear_forms_dz(a, drop)) d.dz = at;
   at += linear_dz_bytes(a, drop);
   d.sums = reinterpret_cast<float*>(at);
   d.part = reinterpret_cast<float*>(at + linear_sums_bytes(a));

@@ -5,8 +5,9 @@
 //
 // Forward: one product; bias, activation, dropout and the residual's addition
 // are its epilogue, on the fp32 sums.  Backward: one pass over dy and z forms dz
-// and the column sums, then dx and dW are one launch of products.  (The pass is
-// left out where dz is dy itself: bf16, no activation, no dropout, no bias.)
+// and the column sums, then dx and dW are one launch of products, or two.  (The
+// pass is left out where dz is dy itself, bf16 without activation and dropout, and
+// there is no bias or rows are few.)  Small calls are one launch in fp32.
 // Roundings to bf16: z as stored, dz as the products' operand, and the results.
 // d_bias is summed from the unrounded dz.
 //
@@ -191,6 +192,113 @@ __global__ __launch_bounds__(256) void linear_grads_join_kernel(ProdArgs g, Bias
   product_join<BT, EPI_PLAIN, 0>(g, NoExtra{});
 }
 
+// ---- small backward calls ---------------------------------------------------------
+// Every gradient in one launch, in fp32 throughout: dz is formed where it is used and
+// not rounded.  A workgroup has 32 x 32 results of dx or dW, each thread 2 x 2,
+// and goes over 32 values of the sum at a time, the next ones read ahead; those of
+// dW's first columns add up d_bias.  A turn of 32 takes about 1.4 us, the loads'
+// latency, so sums are kept short.
+//
+// In us, both gradients and d_bias with gelu, here against two or three launches of
+// the other forms, replayed and (called from Python): 5 rows 608 -> 104 columns 7.9
+// against 7.8 (13.6 against 18.4), 41 rows 144 -> 40 5.8 against 7.6 (13.3 against
+// 18.2), 64 rows 4096 -> 64 6.7 against 8.0 (13.6 against 18.4); 64 rows 256 -> 256
+// 14.6 against 9.7 (14.7 against 18.3), 440 rows 64 -> 184 27 against 11.
+struct SmallGrads {
+  LinearDev f;
+  int32_t col_blocks, dx_tiles, dw_cols;     // dw_cols: column blocks of dW (1 for d_bias alone)
+};
+bool small_grads(int64_t t, int64_t d, int64_t n) { return t <= 128 && n <= 128 && t * d * n <= 20000000; }
+
+// Four values at element e, a multiple of four of rows that are 16-byte aligned.
+__device__ __forceinline__ void load4(const void* p, int dt, int64_t e, float (&v)[4]) {
+  if (dt) {
+    const u32x2_t u = *as_global(reinterpret_cast<const u32x2_t*>(static_cast<const uint16_t*>(p) + e));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = k & 1 ? __uint_as_float(u[k / 2] & 0xffff0000u) : bf16_to_f32(u[k / 2] & 0xffffu);
+  } else {
+    const f32x4_t u = *as_global(reinterpret_cast<const f32x4_t*>(static_cast<const float*>(p) + e));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = u[k];
+  }
+}
+
+// Four values of dz, row r, columns n .. n + 3, fp32.
+__device__ __forceinline__ void dz4(const LinearDev& f, const Rng& rng, int64_t r, int64_t n, float (&v)[4]) {
+  float z[4];
+  load4(f.d_y.p, f.d_y.dt, r * f.d_y.ld + n, v);
+  if (f.act != 2) load4(f.z.p, 1, r * f.z.ld + n, z);
+  if (f.drop.on) drop<4>(f.drop, rng, uint64_t(r) * uint64_t(f.out) + uint64_t(n), v);
+  if (f.act == 2) return;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] *= f.act == 0 ? act_slope<0>(z[k]) : act_slope<1>(z[k]);
+}
+
+__global__ __launch_bounds__(256) void linear_small_grads_kernel(SmallGrads a) {
+  __shared__ float sa[32][36], sb[32][36];             // [k][row of the result], [k][column]
+  const LinearDev& f = a.f;
+  const int id = int(blockIdx.x), tid = threadIdx.x;
+  const bool is_w = id >= a.dx_tiles;
+  const int blocks = is_w ? a.dw_cols : a.col_blocks, tile = is_w ? id - a.dx_tiles : id;
+  const int64_t m0 = int64_t(tile / blocks) * 32, c0 = int64_t(tile % blocks) * 32;
+  const int64_t rows = is_w ? f.out : f.rows, depth = is_w ? f.rows : f.out;
+  const NormMat& o = is_w ? f.d_w : f.d_x;             // absent where dW's tiles are there for d_bias
+  const Rng rng = f.drop.on ? rng_of(f.drop) : Rng{};
+  const int i8 = tid >> 3, q4 = (tid & 7) * 4;         // this thread's four values of each operand
+  float va[4], vb[4];
+  auto fetch = [&](int64_t k0) {
+    // dz: columns are k for dx, rows are k for dW
+    const int64_t r = is_w ? k0 + i8 : m0 + i8, n = is_w ? m0 + q4 : k0 + q4;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) va[k] = vb[k] = 0.f;
+    if (r < f.rows && n < f.out) dz4(f, rng, r, n, va);
+    const NormMat& b = is_w ? f.x : f.w;
+    if (o.p && k0 + i8 < depth && c0 + q4 < f.cols) load4(b.p, 1, (k0 + i8) * b.ld + c0 + q4, vb);
+  };
+  const int ty = (tid >> 4) * 2, tx = (tid & 15) * 2;
+  float acc[2][2] = {}, sum = 0.f;
+  const bool bias = is_w && c0 == 0 && f.d_bias.p && tid < 32;
+  fetch(0);
+  for (int64_t k0 = 0; k0 < depth; k0 += 32) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (is_w) sa[i8][q4 + k] = va[k];
+      else sa[q4 + k][i8] = va[k];
+      sb[i8][q4 + k] = vb[k];
+    }
+    __syncthreads();
+    if (k0 + 32 < depth) fetch(k0 + 32);
+#pragma unroll 8
+    for (int k = 0; k < 32; ++k) {
+      const float a0 = sa[k][ty], a1 = sa[k][ty + 1], b0 = sb[k][tx], b1 = sb[k][tx + 1];
+      acc[0][0] = fmaf(a0, b0, acc[0][0]);
+      acc[0][1] = fmaf(a0, b1, acc[0][1]);
+      acc[1][0] = fmaf(a1, b0, acc[1][0]);
+      acc[1][1] = fmaf(a1, b1, acc[1][1]);
+    }
+    if (bias)
+#pragma unroll 8
+      for (int k = 0; k < 32; ++k) sum += sa[k][tid];
+    __syncthreads();
+  }
+  if (bias && m0 + tid < f.out) store_any1(f.d_bias.p, f.d_bias.dt, m0 + tid, sum);
+  if (!o.p || c0 + tx >= f.cols) return;
+#pragma unroll
+  for (int y = 0; y < 2; ++y)
+    if (m0 + ty + y < rows)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) store_any1(o.p, o.dt, (m0 + ty + y) * o.ld + c0 + tx + x, acc[y][x]);
+}
+
+hipError_t run_small_grads(hipStream_t s, const LinearDev& f) {
+  SmallGrads a{f, int32_t((f.cols + 31) / 32), 0, 0};
+  if (f.d_x.p) a.dx_tiles = int32_t((f.rows + 31) / 32) * a.col_blocks;
+  a.dw_cols = f.d_w.p ? a.col_blocks : f.d_bias.p ? 1 : 0;
+  const unsigned grid = unsigned(a.dx_tiles + int32_t((f.out + 31) / 32) * a.dw_cols);
+  hipLaunchKernelGGL(linear_small_grads_kernel, dim3(grid), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
 // ---- the weight's gradient from few rows ----------------------------------------
 // dW = dz^T x of up to 16 rows, bound by writing dW.  A wave keeps the x of 256
 // columns as fragments and goes down the columns of dz, four at a time, with
@@ -355,6 +463,7 @@ size_t linear_bwd_part_bytes(int64_t t, int64_t d, int64_t n, bool d_x, bool d_w
   if (t == 0 || !(d_x || d_w)) return 0;
   return grad_part_bytes(grad_plan(t, d, n, d_x, d_w && !outer_rows(t, d, n)));
 }
+bool linear_small_grads(int64_t rows, int64_t cols, int64_t out) { return small_grads(rows, cols, out); }
 int linear_sum_splits(int64_t rows, int64_t out) { return dz_shape(rows, out).splits; }
 
 hipError_t launch_linear_fwd(hipStream_t s, const LinearDev& f) {
@@ -378,6 +487,7 @@ void launch_dz(hipStream_t s, const LinearDev& f, const DzShape& d) {
 }
 
 hipError_t launch_linear_bwd(hipStream_t s, const LinearDev& f) {
+  if (small_grads(f.rows, f.cols, f.out)) return run_small_grads(s, f);
   BiasSums b{};
   unsigned bias_blocks = 0;
   const bool outer = f.d_w.p && outer_rows(f.rows, f.cols, f.out), bias_there = outer && !f.dz && f.act == 2 && !f.drop.on && f.d_y.dt;

@@ -36,6 +36,12 @@ def wide(t):
     return None if t is None else t.double()
 
 
+def small(x, w):
+    """Whether the backward call keeps dz in fp32."""
+    t, (n, d) = x.shape[0], w.shape
+    return t <= 128 and n <= 128 and t * d * n <= 20_000_000
+
+
 def check(x, w, bias, res, dy, kind="none", p=0.0, rng=None, grads=True, grad_dtype=BF16):
     b = block()
     y, z = b.linear_fwd(x, w, bias, res, act=kind, p=p, rng=rng)
@@ -57,7 +63,7 @@ def check(x, w, bias, res, dy, kind="none", p=0.0, rng=None, grads=True, grad_dt
     if kind != "none":
         leaf = wide(z).requires_grad_(True)
         dz, = torch.autograd.grad(acted(leaf, kind), leaf, dz)
-    exact = kind == "none" and p == 0.0 and dy.dtype == BF16
+    exact = kind == "none" and p == 0.0 and dy.dtype == BF16 or small(x, w)
     inner = 0.0 if exact else ROUND
     close(got[0], dz @ wide(w), "d_x:bf16", inner=inner)
     close(got[1], dz.T @ wide(x), "d_weight:" + name_of(got[1]), inner=inner)
@@ -74,8 +80,9 @@ def test_row_counts(t):
 
 
 @pytest.mark.parametrize("d,n", [(8, 8), (8, 264), (264, 8), (56, 72), (64, 64), (120, 136), (128, 128), (136, 120),
-                                 (200, 1000), (1000, 200), (256, 256), (512, 520)])
-@pytest.mark.parametrize("t", [3, 150])
+                                 (200, 1000), (1000, 200), (256, 256), (512, 520), (8, 520), (24, 528), (72, 584),
+                                 (120, 640), (136, 1032), (520, 8), (2056, 24)])
+@pytest.mark.parametrize("t", [3, 150, 600])
 def test_widths(t, d, n):
     check(*make(t, d, n, seed=d + n, resid=BF16), kind="silu", p=0.1, rng=RNG)
 
@@ -341,3 +348,23 @@ def test_large_gradients_from_few_rows(t, d, n, exact):
         # act'(0) = 1/2, which every type holds
         close(got[1], (dy.double() / 2).T @ x.double(), "d_weight:bf16", inner=0.0 if exact else ROUND)
         close(got[2], dy.double().sum(0) / 2, "d_bias:f32")
+
+
+@pytest.mark.parametrize("t", [1, 31, 32, 33, 128, 129])
+@pytest.mark.parametrize("d,n", [(8, 8), (40, 24), (1216, 128), (1224, 128), (144, 136), (4096, 32)])
+@pytest.mark.parametrize("kind,p", [("none", 0.0), ("gelu", 0.0), ("silu", 0.3)])
+def test_small_gradients(t, d, n, kind, p):
+    """On both sides of the small form's limits, its blocks of 32 cut every way,
+    each gradient alone and together."""
+    x, w, bias, _, dy = make(t, d, n, seed=t + n, resid=F32 if p else None)
+    rng = RNG if p else None
+    check(x, w, bias, None, dy, kind=kind, p=p, rng=rng, grad_dtype=F32)
+    if not small(x, w):
+        return
+    b = block()
+    z = b.linear_fwd(x, w, bias, act=kind, p=p, rng=rng)[1]
+    how = dict(act=kind, p=p, rng=rng)
+    every = b.linear_bwd(dy, x, w, bias, z, **how)
+    assert torch.equal(b.linear_bwd(dy, None, w, None, z, need_weight=False, **how)[0], every[0])
+    assert torch.equal(b.linear_bwd(dy, x, w, None, z, need_x=False, **how)[1], every[1])
+    assert torch.equal(b.linear_bwd(dy, x, w, bias, z, need_x=False, need_weight=False, **how)[2], every[2])

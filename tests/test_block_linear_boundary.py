@@ -94,14 +94,16 @@ def test_linear_bwd_refuses(over, status):
 @needs_lib
 def test_linear_workspace():
     L = b._lib()
-    st, n = need("muon_linear_bwd", linear_args())
-    assert st == E.MUON_OK and n >= 40 * 96 * 2
-    assert L.muon_linear_bwd(linear_args(), FAKE, n - 1, None) == E.MUON_E_WORKSPACE
-    assert L.muon_linear_bwd(linear_args(), None, n, None) == E.MUON_E_WORKSPACE
-    assert L.muon_linear_bwd(linear_args(), FAKE + 16, n, None) == E.MUON_E_ALIGN
+    big = dict(rows=700, x=mat(700, 64), z=mat(700, 96), d_y=mat(700, 96, 0), d_x=mat(700, 64))
+    st, n = need("muon_linear_bwd", linear_args(**big))
+    assert st == E.MUON_OK and n >= 700 * 96 * 2
+    assert L.muon_linear_bwd(linear_args(**big), FAKE, n - 1, None) == E.MUON_E_WORKSPACE
+    assert L.muon_linear_bwd(linear_args(**big), None, n, None) == E.MUON_E_WORKSPACE
+    assert L.muon_linear_bwd(linear_args(**big), FAKE + 16, n, None) == E.MUON_E_ALIGN
+    assert need("muon_linear_bwd", linear_args()) == (E.MUON_OK, 0)      # a small call forms dz where it is used
     # dz is dy itself: bf16, no activation, no dropout
-    same = dict(act=2, p=0.0, d_y=mat(40, 96), d_bias=NONE, d_weight=NONE, d_x=NONE)
-    assert need("muon_linear_bwd", linear_args(**same)) == (E.MUON_OK, 0)
+    same = dict(act=2, p=0.0, d_y=mat(700, 96), d_bias=NONE, d_weight=NONE, d_x=NONE)
+    assert need("muon_linear_bwd", linear_args(**dict(big, **same))) == (E.MUON_OK, 0)
     assert L.muon_linear_bwd(linear_args(**same), None, 0, None) == E.MUON_OK       # nothing is wanted
     assert L.muon_linear_fwd(linear_args(rows=0), None, 0, None) == E.MUON_OK
     assert L.muon_linear_bwd(linear_args(rows=0, d_weight=NONE, d_bias=NONE), None, 0, None) == E.MUON_OK
