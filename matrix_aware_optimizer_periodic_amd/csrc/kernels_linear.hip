@@ -16,7 +16,7 @@
 // library product runs at 1520 - 1590 TFLOP/s, a copy at 4.9 - 5.5 TB/s), kernels
 // alone: 4096 rows, 2048 -> 8192, bias, gelu and z 137 us (1006 TFLOP/s; all tiles
 // of a round end together and then write 67 MB); 8192 -> 2048 with dropout and fp32
-// residual 114 + 26 us (tiles in halves, joined: 134 MB at 5.2 TB/s); backward of
+// residual 114 - 122 + 27 us (tiles in halves, joined: 134 MB at 5 TB/s); backward of
 // 5120 -> 20480 dz 94 us (5.4 TB/s), products 1280 - 1380 (1240 - 1340 TFLOP/s).
 #include "block_gemm.h"
 
