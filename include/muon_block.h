@@ -233,7 +233,8 @@ muon_status muon_linear_bwd(const muon_linear_args* args, void* workspace, size_
  * Values from 2 pairs on are copied.  inverse turns by -t (with the same scale):
  * the gradient.  Angles are formed in fp64, so that far positions keep their
  * digits.  q_out may be q itself (the same pointer and strides), and k_out k;
- * other overlaps are not allowed. */
+ * outputs that share a value's place with each other, within themselves or
+ * otherwise with q or k are refused (slices of one buffer need not). */
 typedef struct muon_rotary_args {
   int64_t batch, len;             /* >= 0; batch x len below 2^31             */
   int32_t heads, kv_heads;        /* of q and of k; kv_heads 0: there is no k.

@@ -842,7 +842,8 @@ def rotary_fwd(q, k, freqs, positions=None, *, offset: int = 0, interleaved: boo
     (len, axes) or (batch, len, axes); None: a token's number plus offset.
 
     Returns both, written to `out`, two tensors of q's and k's shapes, or to new
-    contiguous ones.  out may be (q, k) themselves."""
+    contiguous ones.  out may be (q, k) themselves; one that holds a value of q or
+    k in any other way, or two values in one place, raises."""
     return _rotary(q, k, freqs, positions, offset, interleaved, scale, out, 0)
 
 

@@ -4,6 +4,7 @@
 // state is a fixed buffer of error text per thread.
 #include "../../include/muon_block.h"
 #include "block_internal.h"
+#include "block_overlap.h"
 
 #include <cmath>
 #include <cstdarg>
@@ -340,8 +341,8 @@ bool rotary_runs(const muon_heads& t, int32_t dtype, int v) {
          t.stride_head * size % need == 0;
 }
 
-bool same_heads(const muon_heads& a, const muon_heads& b) {
-  return a.ptr == b.ptr && a.stride_batch == b.stride_batch && a.stride_len == b.stride_len && a.stride_head == b.stride_head;
+Places rotary_places(const muon_rotary_args* a, const muon_heads& t, int32_t heads) {
+  return Places{t.ptr, {t.stride_batch, t.stride_len, t.stride_head, 1}, {a->batch, a->len, heads, a->dim}};
 }
 
 }  // namespace
@@ -629,8 +630,19 @@ muon_status muon_rotary(const muon_rotary_args* a, void* hip_stream) {
   if (a->kv_heads > 0) {
     CHECK(rotary_heads("k", a->k, a->dtype));
     CHECK(rotary_heads("k_out", a->k_out, a->dtype));
-    if (a->q_out.ptr == a->k_out.ptr) return fail(MUON_E_ARG, "q_out and k_out are in one place");
   }
+  // Workgroups turn the tokens in any order, so that a value that is written is
+  // read by its own thread alone, which reads it first, or by none.
+  const Places q = rotary_places(a, a->q, a->heads), q_out = rotary_places(a, a->q_out, a->heads);
+  const Places k = rotary_places(a, a->k, a->kv_heads), k_out = rotary_places(a, a->k_out, a->kv_heads);
+  const int64_t size = int64_t(type_size(a->dtype));
+  const bool q_same = same_places(q, q_out), k_same = same_places(k, k_out);      // (no k meets nothing)
+  if (places_repeat(q_out) || places_repeat(k_out)) return fail(MUON_E_ARG, "an output has two values in one place");
+  if (places_meet(q_out, k_out, size)) return fail(MUON_E_ARG, "q_out and k_out overlap");
+  if ((!q_same && places_meet(q_out, q, size)) || (!k_same && places_meet(k_out, k, size)))
+    return fail(MUON_E_ARG, "an output overlaps its input and is not the same tensor");
+  if (places_meet(q_out, k, size) || places_meet(k_out, q, size))
+    return fail(MUON_E_ARG, "an output overlaps the other tensor's input");
   RotaryDev d{};
   d.tokens = a->batch * a->len;
   d.offset = a->offset; d.len = int32_t(a->len); d.heads = a->heads; d.kv_heads = a->kv_heads; d.dim = a->dim;
@@ -638,7 +650,7 @@ muon_status muon_rotary(const muon_rotary_args* a, void* hip_stream) {
   d.f32 = a->dtype == MUON_F32; d.scale = a->scale;
   d.freqs = a->freqs; d.positions = a->positions; d.pos_batch = a->positions_batch;
   d.q = heads_dev(a->q); d.k = heads_dev(a->k); d.q_out = heads_dev(a->q_out); d.k_out = heads_dev(a->k_out);
-  d.in_place = same_heads(a->q, a->q_out) && (a->kv_heads == 0 || same_heads(a->k, a->k_out));
+  d.in_place = q_same && (a->kv_heads == 0 || k_same);
   // Pairs that move at once: whole chunks of a head (of halves, all of whose pairs
   // turn or none), and runs on their boundaries (0: not even a pair of neighbours
   // is).
