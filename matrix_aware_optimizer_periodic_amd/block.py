@@ -416,6 +416,8 @@ def attention_qkv(qkv, *, causal: bool = False, offset: int = 0, q_lens=None, k_
     first."""
     if rotary is not None and "out" in rotary:
         raise ValueError("rotary: queries and keys are rotated into tensors of their own")
+    if rotary is not None:
+        _no_learned(rotary.get("freqs"))
     return _PackedAttention.apply(qkv, {"causal": causal, "offset": offset, "q_lens": q_lens, "k_lens": k_lens,
                                         "scale": scale}, rotary)
 
@@ -853,6 +855,11 @@ def rotary_bwd(d_q, d_k, freqs, positions=None, *, offset: int = 0, interleaved:
     return _rotary(d_q, d_k, freqs, positions, offset, interleaved, scale, out, 1)
 
 
+def _no_learned(freqs):
+    if isinstance(freqs, torch.Tensor) and freqs.requires_grad and torch.is_grad_enabled():
+        raise ValueError("freqs: no gradient is formed for frequencies (detach them)")
+
+
 class _Rotary(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, freqs, positions, how):
@@ -874,5 +881,7 @@ class _Rotary(torch.autograd.Function):
 
 
 def rotary(q, k, freqs, positions=None, *, offset: int = 0, interleaved: bool = False, scale: float = 1.0):
-    """rotary_fwd for autograd; returns both rotated (None for a k that is None)."""
+    """rotary_fwd for autograd; returns both rotated (None for a k that is None).
+    Frequencies get no gradient: those that want one raise."""
+    _no_learned(freqs)
     return _Rotary.apply(q, k, freqs, positions, {"offset": offset, "interleaved": interleaved, "scale": scale})
