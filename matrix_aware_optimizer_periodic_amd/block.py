@@ -872,7 +872,9 @@ class _Rotary(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, d_q, d_k):
         freqs, positions = ctx.saved_tensors
-        d = [None if t is None or not need else t.contiguous() for t, need in zip((d_q, d_k), ctx.needs_input_grad)]
+        # (any strides will do, but for an expanded last dimension)
+        d = [None if t is None or not need else t if t.stride(-1) == 1 else t.contiguous()
+             for t, need in zip((d_q, d_k), ctx.needs_input_grad)]
         if d[0] is None:
             d[1] = None if d[1] is None else rotary_bwd(d[1], None, freqs, positions, **ctx.how)[0]
         else:
