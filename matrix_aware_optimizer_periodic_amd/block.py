@@ -577,7 +577,7 @@ class _Dropout(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, residual, p, rng):
         ctx.p, ctx.dtype = p, x.dtype
-        _keep_rng(ctx, rng)
+        _keep_rng(ctx, rng if p != 0.0 and ctx.needs_input_grad[0] else None)
         return dropout_fwd(x, p, rng, residual)
 
     @staticmethod
@@ -699,17 +699,23 @@ class _Linear(torch.autograd.Function):
     def forward(ctx, x, weight, bias, residual, act, p, rng, y_dtype, save):
         y, z = linear_fwd(x, weight, bias, residual, act=act, p=p, rng=rng, save=save, y_dtype=y_dtype)
         ctx.act, ctx.p = act, p
-        _keep_rng(ctx, rng, x if ctx.needs_input_grad[1] else None, weight, bias, z)
+        need_x, need_w, need_b = ctx.needs_input_grad[:3]
+        # What the backward pass reads, and no more: anything else may be written
+        # before it.  Of a weight without d_x, and of the bias, shape and type count.
+        ctx.shapes = None if need_x else weight.detach(), bias.detach() if need_b else None
+        _keep_rng(ctx, rng if p != 0.0 and (need_x or need_w or need_b) else None, x if need_w else None,
+                  weight if need_x else None, z)
         return y
 
     @staticmethod
     @once_differentiable
     def backward(ctx, d_y):
-        x, weight, bias, z, held = ctx.saved_tensors
+        x, weight, z, held = ctx.saved_tensors
+        shape, bias = ctx.shapes
         need_x, need_w, need_b, need_r = ctx.needs_input_grad[:4]
         d = (None,) * 3
         if need_x or need_w or need_b:
-            d = linear_bwd(d_y.contiguous(), x, weight, bias if need_b else None, z, act=ctx.act, p=ctx.p,
+            d = linear_bwd(d_y.contiguous(), x, shape if weight is None else weight, bias, z, act=ctx.act, p=ctx.p,
                            rng=ctx.rng if held is None else held, need_x=need_x, need_weight=need_w)
         return (*d, d_y if need_r else None, None, None, None, None, None)
 

@@ -79,3 +79,38 @@ def test_rotary_gradients_of_any_strides():
     leaf = q.clone().requires_grad_(True)
     b.rotary(leaf, None, f)[0].backward(w[:1].expand_as(w))
     assert torch.equal(leaf.grad, want[:1].expand_as(w))
+
+
+def test_what_no_backward_pass_reads_may_be_written(stand_ins):  # noqa: F811
+    """Weights and biases of an optimizer step between the passes, and random
+    numbers that nothing was dropped by."""
+    x, w, bias, res = leaves((3, 8), (16, 8), (16,), (3, 16))
+    state = torch.tensor([1, 2])
+
+    def write(*tensors):
+        with torch.no_grad():
+            for t in tensors:
+                t.add_(1)
+    y = b.linear(x.detach(), w, bias, res, act="gelu", rng=state)      # weight and bias: from x, z and d_y
+    write(w, bias, res, state)
+    y.sum().backward()
+    assert torch.equal(w.grad, x.detach().sum(0).expand(16, 8)) and torch.equal(bias.grad, torch.full_like(bias, 3.0))
+    y = b.linear(x, w.detach().clone(), bias, p=0.5, rng=(1, 2))       # x: from the weight
+    write(x, bias)
+    y.sum().backward()
+    y = b.linear(x, w, bias.detach().clone(), res)
+    write(bias, res)
+    y.sum().backward()
+    y = b.dropout(x, 0.0, state)
+    write(state)
+    y.sum().backward()
+    y = b.dropout(x.detach(), 0.5, state, x) + b.linear(x.detach(), w.detach()[:8], None, x, p=0.5, rng=state)
+    write(state)
+    y.sum().backward()
+    # what is read is still noticed
+    for write_to, call in ((w, lambda: b.linear(x, w)), (x, lambda: b.linear(x, w)), (state, lambda: b.dropout(x, 0.5, state)),
+                           (state, lambda: b.linear(x, w, p=0.5, rng=state))):
+        y = call()
+        write(write_to)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.sum().backward()
