@@ -358,6 +358,13 @@ def attn_bwd(d_o, q, k, v, o, lse, *, causal: bool = False, offset: int = 0, q_l
     return d_q, d_k, d_v
 
 
+def _gradient(t):
+    """t contiguous and on the 16-byte boundary that matrix operands need: autograd
+    may pass a run out of a larger gradient, from any value on."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _keep(ctx, how, *tensors):
     """Saves what the backward pass reads, the lengths with it: written again
     before that pass, they then raise as any saved tensor does."""
@@ -376,7 +383,7 @@ class _Attention(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, d_o):
         q, k, v, o, lse, q_lens, k_lens = ctx.saved_tensors
-        return (*attn_bwd(d_o.contiguous(), q, k, v, o, lse, q_lens=q_lens, k_lens=k_lens, **ctx.how), None)
+        return (*attn_bwd(_gradient(d_o), q, k, v, o, lse, q_lens=q_lens, k_lens=k_lens, **ctx.how), None)
 
 
 class _PackedAttention(torch.autograd.Function):
@@ -402,7 +409,7 @@ class _PackedAttention(torch.autograd.Function):
         d_q, d_k, d_v = d_qkv.unbind(2)
         if rotated:
             q, k, freqs, positions = rotated
-        attn_bwd(d_o.contiguous(), q, k, v, o, lse, q_lens=q_lens, k_lens=k_lens, out=(d_q, d_k, d_v), **ctx.how)
+        attn_bwd(_gradient(d_o), q, k, v, o, lse, q_lens=q_lens, k_lens=k_lens, out=(d_q, d_k, d_v), **ctx.how)
         if rotated:
             rotary_bwd(d_q, d_k, freqs, positions, out=(d_q, d_k), **ctx.turn)
         return d_qkv, None, None
@@ -497,7 +504,7 @@ class _GatedFfn(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, d_y):
-        return (*ffn_bwd(d_y.contiguous(), *ctx.saved_tensors, act=ctx.act), None, None)
+        return (*ffn_bwd(_gradient(d_y), *ctx.saved_tensors, act=ctx.act), None, None)
 
 
 def gated_ffn(x, w_gate, w_up, w_down, *, act: str = "silu"):
@@ -715,7 +722,7 @@ class _Linear(torch.autograd.Function):
         need_x, need_w, need_b, need_r = ctx.needs_input_grad[:4]
         d = (None,) * 3
         if need_x or need_w or need_b:
-            d = linear_bwd(d_y.contiguous(), x, shape if weight is None else weight, bias, z, act=ctx.act, p=ctx.p,
+            d = linear_bwd(_gradient(d_y), x, shape if weight is None else weight, bias, z, act=ctx.act, p=ctx.p,
                            rng=ctx.rng if held is None else held, need_x=need_x, need_weight=need_w)
         return (*d, d_y if need_r else None, None, None, None, None, None)
 

@@ -1,10 +1,12 @@
-"""What the autograd functions of linear, rotary and dropout take, save and form, on
-the CPU with stand-ins for the library's calls."""
+"""What the autograd functions of the block operators take, save and form, on the CPU
+with stand-ins for the library's calls, and on the GPU where strides decide."""
 
 import pytest
 import torch
 
-from test_block_linear_boundary import b, leaves, stand_ins  # noqa: F401
+from test_block_autograd import stand_ins as block_stand_ins  # noqa: F401
+from test_block_autograd import through_attention, through_ffn, through_packed_attention
+from test_block_linear_boundary import b, leaves, stand_ins, through_linear  # noqa: F401
 
 BF16 = torch.bfloat16
 
@@ -114,3 +116,45 @@ def test_what_no_backward_pass_reads_may_be_written(stand_ins):  # noqa: F811
         write(write_to)
         with pytest.raises(RuntimeError, match="modified by an inplace operation"):
             y.sum().backward()
+
+
+def off_the_boundary(y):
+    """y beside one other value, whose gradient has y's begin one value further on."""
+    return torch.cat([torch.ones(1, dtype=y.dtype, device=y.device, requires_grad=True), y.flatten()]).square().sum()
+
+
+@pytest.mark.parametrize("call,through", [("linear_bwd", through_linear), ("attn_bwd", through_attention),
+                                          ("attn_bwd", through_packed_attention), ("ffn_bwd", through_ffn)])
+def test_gradients_come_on_their_boundary(stand_ins, block_stand_ins, monkeypatch, call, through):  # noqa: F811
+    """A run out of a larger gradient is contiguous, and may begin at any value: the
+    library takes rows on 16 bytes only."""
+    got = []
+    plain = getattr(b, call)
+    monkeypatch.setattr(b, call, lambda d, *a, **how: (got.append(d), plain(d, *a, **how))[1])
+    _, y = through()
+    off_the_boundary(y).backward()
+    assert got[0].is_contiguous() and got[0].data_ptr() % 16 == 0
+    assert torch.equal(got[0], 2 * y)
+    got.clear()
+    _, y = through()
+    mine = torch.randn(y.shape, dtype=y.dtype)
+    assert mine.data_ptr() % 16 == 0
+    y.backward(mine)
+    assert got[0].data_ptr() == mine.data_ptr()                 # (and is not copied for nothing)
+
+
+@pytest.mark.gpu
+def test_gradients_off_their_boundary():
+    gen = torch.Generator(device="cuda").manual_seed(3)
+
+    def r(*shape):
+        return (0.3 * torch.randn(shape, generator=gen, device="cuda")).to(BF16).requires_grad_(True)
+    ways = {"linear": lambda: (b.linear, (r(20, 64), r(72, 64), r(72)), {"act": "gelu"}),
+            "attention": lambda: (b.attention, (r(2, 9, 2, 64), r(2, 11, 2, 64), r(2, 11, 2, 64)), {}),
+            "packed": lambda: (b.attention_qkv, (r(2, 9, 3, 2, 64),), {}),
+            "ffn": lambda: (b.gated_ffn, (r(20, 64), r(72, 64), r(72, 64), r(64, 72)), {})}
+    for name, way in ways.items():
+        call, given, how = way()
+        got = torch.autograd.grad(off_the_boundary(call(*given, **how)), given)
+        want = torch.autograd.grad(call(*given, **how).square().sum(), given)
+        assert all(torch.equal(p, q) for p, q in zip(got, want)), name
