@@ -24,6 +24,7 @@ capture.
 from __future__ import annotations
 
 import ctypes
+import operator
 import struct
 
 import torch
@@ -527,7 +528,7 @@ def _rng(p, rng, device):
         if rng.dtype != torch.int64 or rng.shape != (2,) or not rng.is_contiguous() or rng.device != device:
             raise ValueError(f"rng: two contiguous int64 on {device} are wanted, got {tuple(rng.shape)} {rng.dtype} on {rng.device}")
         return 0, 0, rng.data_ptr()
-    seed, offset = rng
+    seed, offset = map(operator.index, rng)
     if not (0 <= seed < 1 << 64 and 0 <= offset < 1 << 64):
         raise ValueError(f"rng: seed and offset are 64-bit numbers, got {rng}")
     return seed, offset, 0
@@ -817,6 +818,8 @@ def _rotary(q, k, freqs, positions, offset, interleaved, scale, out, inverse):
         if offset:
             raise ValueError("offset is for tokens without positions")
         between = n * axes if len(positions.shape) > len(one) else 0
+    if not -1 << 63 <= operator.index(offset) < 1 << 63:
+        raise ValueError(f"offset is a 64-bit number, got {offset}")
     hq, hk = _turned_heads(q, "q", dtype), _turned_heads(k, "k", dtype)
     if out is None:
         (oq, to_q), (ok, to_k) = _new_heads(q), _new_heads(k)
