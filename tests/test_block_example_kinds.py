@@ -74,3 +74,30 @@ def test_dropout_differs_by_step():
     net = train_dit.Dit(128, 2, 344, 2, seed=3, dropout=0.2)
     x, cond, _ = train_dit.batch(3, 50, 128, 0)
     assert torch.equal(net(x, cond, 1), net(x, cond, 1)) and not torch.equal(net(x, cond, 1), net(x, cond, 2))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_training_moves_every_weight(kind, monkeypatch):
+    """Every weight and bias goes somewhere in each of the first steps (refresh and
+    between), and the leaves are what the optimizer's weights round to."""
+    import train_dit
+    nets, seen = [], []
+
+    class Kept(train_dit.Dit):
+        def __init__(self, *args, **how):
+            super().__init__(*args, **how)
+            nets.append(self)
+
+        def __call__(self, *args):
+            seen.append([t.detach().clone() for t in self.leaf])
+            return super().__call__(*args)
+    monkeypatch.setattr(train_dit, "Dit", Kept)
+    train_dit.train(dim=128, heads=2, hidden=344, blocks=2, samples=4, tokens=64, steps=4, report=None, **kind)
+    net, = nets
+    seen.append([t.detach() for t in net.leaf])
+    assert len(seen) == 5 and ({"b1", "b2"} <= {n for _, n in net.names}) == (kind.get("mlp") == "gelu")
+    for step, (before, after) in enumerate(zip(seen, seen[1:])):
+        for name, p, q in zip(net.names, before, after):
+            assert not torch.equal(p, q) and bool(torch.isfinite(q).all()), (step, name)
+    for name, leaf, master in zip(net.names, net.leaf, net.master):
+        assert torch.equal(leaf, master.to(leaf.dtype)), name
