@@ -666,7 +666,12 @@ def linear_bwd(d_y, x, weight, bias=None, z=None, *, act: str = "none", p: float
     need_weight is false); d_y is fp32 or bf16.  d_weight is contiguous, of
     grad_dtype (bf16 or fp32), d_bias of the bias's type: what muon_step reads.
     None stands for what is not needed, d_bias where bias is None.  The
-    residual's gradient is d_y."""
+    residual's gradient is d_y.
+
+    drop(d_y) act'(z) is rounded to bf16 as an operand of both products, unless it
+    is a bf16 d_y itself: d_x and d_weight are off by some 1.7e-3 of their norm for
+    that, in fp32 too.  Calls of at most 128 rows and 128 outputs (and rows x cols x
+    out of 2e7) keep it in fp32; d_bias is summed from fp32 always."""
     dev = _device(d_y, x, weight, bias, z)
     out, cols = _linear_dims(weight, act)
     if d_y.dim() < 1 or d_y.shape[-1] != out:
