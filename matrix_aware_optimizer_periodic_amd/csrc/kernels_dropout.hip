@@ -2,9 +2,17 @@
 // mask formed from the element's number (block_philox.h) and never stored.  The
 // gradient is the same call on dy.
 //
-// Bound by memory, and only just: ten rounds of two 64-bit products for four
-// elements take about as long as four bytes of an element.  16384 x 2048 bf16 onto
-// an fp32 residual 57 us (5.9 TB/s).
+// Whole aligned groups of eight are bound by memory, and only just: ten rounds of
+// two 64-bit products for four elements take about as long as four bytes of an
+// element.  16384 x 2048 bf16 onto an fp32 residual 57 us (5.9 TB/s), 20000 x 1000
+// bf16 17.5 (4.6).
+//
+// Rows off the groups (a width or stride that is no multiple of eight, rows apart)
+// are not: a lane's four columns are loaded and stored one value at a time, and lie
+// in two of the generator's blocks where they cross a group.  20000 x 1001 with rows
+// 1004 apart in bf16 41 us (1.9 TB/s), onto an fp32 residual 56 (3.6); 300000 x 33
+// with rows 40 apart in bf16 27 (1.5), in fp32 26 (3.0).  Rows beside each other
+// count as one row, whatever their width: 300000 x 33 so 9.7 (4.1).
 #include "block_philox.h"
 
 namespace muon {
