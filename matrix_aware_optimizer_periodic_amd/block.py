@@ -755,9 +755,11 @@ def rotary_freqs(dim, *, base: float = 10000.0, stretch: str = "none", factor: f
     frequencies (positions are interpolated), "ntk" raises the base by
     factor ** (d / (d - 2)), which leaves the fastest pair and divides the slowest,
     "yarn" divides those that turn less than once over `length` trained tokens,
-    leaves those that turn more than 32 times and goes evenly between (Peng et al.,
-    "YaRN", which also scales queries and keys, rotary_fwd's scale, by
-    0.1 log(factor) + 1)."""
+    leaves those that turn more than 32 times and goes between by their turns, as the
+    paper has it (Peng et al., "YaRN", which also scales queries and keys, rotary_fwd's
+    scale, by 0.1 log(factor) + 1).  Programs that go between by a pair's number
+    instead give other frequencies there: weights trained with those need them as
+    they are, in a tensor of one's own."""
     dims = (dim,) if isinstance(dim, int) else tuple(dim)
     if not dims or any(d < 2 or d % 2 for d in dims):
         raise ValueError(f"each axis turns an even number of values: got {dim}")
