@@ -47,9 +47,9 @@ __device__ __forceinline__ void act_of(float g, float& a, float& da) {
 // that is rounded to fp32 after the product with log2 e (and, of GELU, after w's own
 // roundings), so that t is off by some 2^-24 |w| and more far out.  On the side where
 // t is small that does not show; on the other the value has t's error, and is small
-// itself.  Over every bf16 value, relative: 2^-22 for |w| up to 2 and on the positive
-// side, then SiLU 2^-21 at w = -8, 2^-20 at -20, 2^-18 at -80, GELU twice that; no
-// more than 4e-8 of an absolute error on the negative side, and 1.6e-7 of a slope's.
+// itself.  Over every bf16 value, relative: 2.5e-7 for |w| up to 2 and on the positive
+// side, then SiLU 2^-21 at w = -8, 2^-20 at -20, 2^-18 at -80, GELU twice that; the
+// absolute error is 6e-8 at most on the negative side, and a slope's 1.6e-7 anywhere.
 // Where t overflows (w below -88.7), e is 0 and so is all that t stands in: of values
 // below 1e-36.  w' is taken of a bounded g^2, so that far values give 0 times a
 // number.  ACT 2: none.
